@@ -279,6 +279,147 @@ qmoe_status qmoe_decode_step(qmoe_ctx* ctx, const qmoe_layer_weights* layers, in
 qmoe_status qmoe_prefill(qmoe_ctx* ctx, const qmoe_layer_weights* layers, int n_layers,
                          int n_tokens, int pos0, float* hidden, int32_t* ids_out);
 
+/* ------------------------------------------------------------------ paged 4-bit KV cache
+ *
+ * Several sequences share one pool of KV pages per layer, held in NVFP4 (the
+ * format of qmoe_forward_nvfp4): E2M1 codes two per byte with the even element
+ * in the low nibble, one E4M3 scale per 16 consecutive elements of a head, one
+ * fp32 scale per kv head.  A position of a kv head takes head_dim * 9/16 bytes
+ * for K and as much for V (144 B together at head_dim 128, against 512 B in the
+ * fp16 cache of qmoe_decode_step).  One layer's cache:
+ *   codes  [n_pages][n_kv_heads][page_size][head_dim/2]   bytes
+ *   scales [n_pages][n_kv_heads][page_size][head_dim/16]  E4M3 codes, not NaN
+ *   value (page, kv head, slot, d) = e2m1(code) * e4m3(scale[d/16]) * global[kv head]
+ * A slot is page * page_size + offset (int64).  Position p of sequence s lives in
+ * page block_table[s][p / page_size] at offset p % page_size.
+ *
+ * A serving step is qmoe_kv4_plan once, then per layer qmoe_kv4_append and
+ * qmoe_kv4_attention (qmoe_step_kv4 runs whole decoder layers that way).  All
+ * lengths, tables and slots stay on the device, so a step can be captured into a
+ * graph and replayed while the lengths change.
+ *
+ * Conventions as above.  A qmoe_kv4 handle has its own stream, workspace, status
+ * word and error text; a call runs on the device the handle was created on,
+ * whichever device is current.  Calls that share a handle share its workspace:
+ * they must be ordered (graphs captured from one handle must not run at the same
+ * time).  Contents of device arrays are checked on the device: an index outside
+ * its range is never followed, and sets the status word (QMOE_ERR_DEVICE_CHECK). */
+typedef enum { QMOE_F32 = 0, QMOE_F16 = 1, QMOE_BF16 = 2 } qmoe_dtype;
+
+typedef struct qmoe_kv4 qmoe_kv4;
+
+typedef struct {
+    int n_heads;            /* q heads, 1..1024 */
+    int n_kv_heads;         /* kv heads, divides n_heads */
+    int head_dim;           /* 64, 128 or 256 */
+    int page_size;          /* positions per page: 16, 32, 64, 128 or 256 */
+    int n_pages;            /* pages of each layer's cache, 1..2^30 */
+    int max_seqs;           /* largest n_seqs of a call, 1..4096 */
+    int max_tokens;         /* largest n_tokens of a call, 1..2^20 */
+    int max_pages_per_seq;  /* row length of the block table; times page_size at most 2^30 */
+    void* stream;           /* cudaStream_t the work is enqueued on (NULL = legacy default) */
+} qmoe_kv4_config;
+
+/* One layer's cache (all device pointers; codes and scales 16-byte aligned). */
+typedef struct {
+    void* k_codes;
+    void* k_scales;
+    void* v_codes;
+    void* v_scales;
+    const float* k_global;  /* [n_kv_heads], finite; rows of a head whose global is not
+                               positive are appended as zeros */
+    const float* v_global;  /* [n_kv_heads] */
+} qmoe_kv4_cache;
+
+/* Create a handle on the current device and allocate its workspace.  On failure
+ * qmoe_last_error(NULL) tells why. */
+qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out);
+void qmoe_kv4_destroy(qmoe_kv4* kv);
+qmoe_status qmoe_kv4_set_stream(qmoe_kv4* kv, void* stream);
+size_t qmoe_kv4_workspace_bytes(const qmoe_kv4_config* cfg);   /* 0 on bad config */
+
+/* As qmoe_get_status and qmoe_last_error, for a handle. */
+qmoe_status qmoe_kv4_get_status(qmoe_kv4* kv);
+const char* qmoe_kv4_last_error(qmoe_kv4* kv);
+
+/* Block tables and slot maps of one step, from the requests' lengths (one launch).
+ *  seq_len     : int32 [n_seqs] positions each request has cached.
+ *  new_len     : int32 [n_seqs] tokens that arrive in this step, 0 for none;
+ *                negative: the request has finished and returns its pages.
+ *  block_table : int32 [n_seqs][max_pages_per_seq], in/out.  Columns below
+ *                ceil(seq_len/page_size) are read; the columns that the new tokens
+ *                reach are written; every other entry is left as it was.
+ *  free_pages  : int32 [n_pages], in/out, a stack whose first *n_free entries are
+ *                the free pages.  The pages of finished requests are pushed in
+ *                the order of requests and columns, then the pages that new tokens
+ *                need are popped in that order.  Entries below the final height
+ *                are as after those pushes and pops, those above unspecified.
+ *  n_free      : int32 [1].
+ *  cap_tokens  : entries of positions and slots, 1..max_tokens.
+ * Outputs (device):
+ *  seq_len_out : int32 [n_seqs] lengths after the step (0 for a finished request);
+ *                may be seq_len.
+ *  n_free_out  : int32 [1]; may be n_free.
+ *  cu_tokens   : int32 [n_seqs+1], the new tokens of request s are the rows
+ *                cu_tokens[s] .. cu_tokens[s+1]-1 of the step's batch.
+ *  positions   : int32 [cap_tokens], slots: int64 [cap_tokens], of each row; -1 in
+ *                the rows behind the last token.
+ * A step that cannot be served changes nothing: cu_tokens is all zero, positions
+ * and slots are -1, lengths, tables and the free list stay, and the status word
+ * says why: QMOE_ERR_DEVICE_CHECK (a length or n_free out of range, more pages
+ * free than exist), QMOE_ERR_SHAPE (more than cap_tokens new tokens, or a request
+ * longer than its table row), QMOE_ERR_NO_MEMORY (too few free pages). */
+qmoe_status qmoe_kv4_plan(qmoe_kv4* kv, int n_seqs, const int32_t* seq_len, const int32_t* new_len,
+                          int32_t* block_table, int32_t* free_pages, const int32_t* n_free,
+                          int cap_tokens, int32_t* seq_len_out, int32_t* n_free_out,
+                          int32_t* cu_tokens, int32_t* positions, int64_t* slots);
+
+/* Quantise n_tokens K and V rows into their slots (one launch).  Row t of kv head h
+ * starts at k + t*k_stride + h*head_dim (elements of dtype; 0: n_kv_heads*head_dim),
+ * so rows may be read in place from side-by-side Q/K/V rows.  Per 16 elements, in
+ * fp32 (as qmoe_nvfp4_quantize, the global scale being given):
+ *   s = E4M3 nearest to max|x| / (6 * global), ties to even, saturating at 448;
+ *   d = e4m3(s) * global;  code = E2M1 nearest to x / d, ties to even, saturating
+ *   at 6; all zero where d = 0.
+ *  slots       : int64 [n_tokens]; a row whose slot is negative goes nowhere.  Slots
+ *                that occur twice end up with an unspecified mixture of their rows;
+ *                a slot past the cache is skipped (QMOE_ERR_DEVICE_CHECK).
+ *  k_hat, v_hat: F32 [n_tokens][n_kv_heads*head_dim] or NULL: the values the cache
+ *                holds for each row (also for rows that go nowhere).
+ * Row base addresses, strides in bytes, k_hat and v_hat 16-byte aligned.  Inputs
+ * must be finite (the codes of a 16-element block with NaN or infinity are
+ * unspecified; its scale is never NaN). */
+qmoe_status qmoe_kv4_append(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const void* k, const void* v,
+                            qmoe_dtype dtype, int n_tokens, int64_t k_stride, int64_t v_stride,
+                            const int64_t* slots, float* k_hat, float* v_hat);
+
+/* Causal GQA attention of a ragged batch of tokens over the cache.
+ *  q           : n_tokens rows of n_heads*head_dim elements of q_t, q_stride elements
+ *                apart (0: contiguous).  Rows cu_tokens[s] .. cu_tokens[s+1]-1 are the
+ *                last cu_tokens[s+1]-cu_tokens[s] positions of sequence s; row i of the
+ *                N rows of a sequence of seq_len[s] positions sees the positions
+ *                0 .. seq_len[s]-N+i (their K and V appended before this call).
+ *  max_new     : no sequence has more new tokens than this (1..n_tokens).
+ *  seq_len     : int32 [n_seqs] lengths with the new tokens (qmoe_kv4_plan's output).
+ *  scale       : softmax scale, finite, e.g. 1/sqrt(head_dim).
+ *  out         : rows of n_heads*head_dim elements of out_t, out_stride apart (0:
+ *                contiguous); sum over visible p of softmax(scale * q.k_p) v_p.
+ *  lse         : F32 [n_tokens][n_heads] or NULL: log of the sum of exp(scale * q.k_p).
+ * A row that sees no position is 0 with lse -inf.  Rows behind cu_tokens[n_seqs] are
+ * left as they were.  q head h reads kv head h / (n_heads/n_kv_heads).  Products
+ * have fp32 accumulators and the running maximum and sum are fp32; F32 rows enter
+ * the tensor cores as two fp16 terms each, F16 and BF16 rows as one (K and V are
+ * exact in fp16).  A sequence whose offsets, length or new tokens are out of range
+ * (negative, past the table row, n_tokens or max_new) is skipped, and a position
+ * whose page id is out of range counts as not visible; both set
+ * QMOE_ERR_DEVICE_CHECK.  Row addresses, strides in bytes and out 16-byte aligned;
+ * out must not overlap q. */
+qmoe_status qmoe_kv4_attention(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const void* q,
+                               qmoe_dtype q_t, int64_t q_stride, int n_seqs, int n_tokens,
+                               int max_new, const int32_t* cu_tokens, const int32_t* seq_len,
+                               const int32_t* block_table, float scale, void* out,
+                               qmoe_dtype out_t, int64_t out_stride, float* lse);
+
 /* Allocation-free variant of qmoe_forward for decode-sized calls.  The pages
  * have no counterpart to this entry point; it exists for callers that cannot
  * allocate device memory: processes whose device memory is owned by their own

@@ -23,6 +23,8 @@ STATUS_NAMES = {0: "QMOE_OK", 1: "QMOE_ERR_INVALID_ARG", 2: "QMOE_ERR_MISALIGNED
                 6: "QMOE_ERR_CUDA", 7: "QMOE_ERR_TIMEOUT", 8: "QMOE_ERR_DEVICE_CHECK"}
 QMOE_Q4_K, QMOE_Q6_K = 1, 2
 QTYPE = {"Q4_K": QMOE_Q4_K, "Q6_K": QMOE_Q6_K}
+QMOE_F32, QMOE_F16, QMOE_BF16 = 0, 1, 2
+DTYPE = {"F32": QMOE_F32, "F16": QMOE_F16, "BF16": QMOE_BF16}
 
 # kernels one qmoe_forward enqueues on the decode path (n_tokens <= 8): the
 # whole layer is one kernel (the batch-1 kernel for one token, the fused
@@ -64,7 +66,10 @@ EXPORTED = ["qmoe_create", "qmoe_destroy", "qmoe_set_stream", "qmoe_forward", "q
             "qmoe_workspace_bytes", "qmoe_expert_stride", "qmoe_forward_noalloc",
             "qmoe_fused_decode_available", "qmoe_forward_q8k", "qmoe_forward_fp8", "qmoe_forward_nvfp4",
             "qmoe_nvfp4_quantize", "qmoe_noalloc_status",
-            "qmoe_debug_stall_next", "qmoe_debug_fail_alloc"]
+            "qmoe_debug_stall_next", "qmoe_debug_fail_alloc",
+            "qmoe_kv4_create", "qmoe_kv4_destroy", "qmoe_kv4_set_stream", "qmoe_kv4_workspace_bytes",
+            "qmoe_kv4_get_status", "qmoe_kv4_last_error", "qmoe_kv4_plan", "qmoe_kv4_append",
+            "qmoe_kv4_attention"]
 
 
 class qmoe_config(C.Structure):
@@ -81,6 +86,17 @@ class qmoe_layer_weights(C.Structure):
                 ("k_norm", C.c_void_p), ("ffn_norm", C.c_void_p), ("router_w", C.c_void_p),
                 ("gate_exps", C.c_void_p), ("up_exps", C.c_void_p), ("down_exps", C.c_void_p),
                 ("down_t", C.c_int), ("k_cache", C.c_void_p), ("v_cache", C.c_void_p)]
+
+
+class qmoe_kv4_config(C.Structure):
+    _fields_ = [("n_heads", C.c_int), ("n_kv_heads", C.c_int), ("head_dim", C.c_int),
+                ("page_size", C.c_int), ("n_pages", C.c_int), ("max_seqs", C.c_int),
+                ("max_tokens", C.c_int), ("max_pages_per_seq", C.c_int), ("stream", C.c_void_p)]
+
+
+class qmoe_kv4_cache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_codes", C.c_void_p),
+                ("v_scales", C.c_void_p), ("k_global", C.c_void_p), ("v_global", C.c_void_p)]
 
 
 class QmoeError(RuntimeError):
@@ -138,6 +154,26 @@ def _load():
     L.qmoe_debug_stall_next.restype = i
     L.qmoe_debug_fail_alloc.argtypes = [i]
     L.qmoe_debug_fail_alloc.restype = None
+    i64 = C.c_int64
+    L.qmoe_kv4_create.argtypes = [C.POINTER(qmoe_kv4_config), C.POINTER(C.c_void_p)]
+    L.qmoe_kv4_create.restype = i
+    L.qmoe_kv4_destroy.argtypes = [vp]
+    L.qmoe_kv4_destroy.restype = None
+    L.qmoe_kv4_set_stream.argtypes = [vp, vp]
+    L.qmoe_kv4_set_stream.restype = i
+    L.qmoe_kv4_workspace_bytes.argtypes = [C.POINTER(qmoe_kv4_config)]
+    L.qmoe_kv4_workspace_bytes.restype = C.c_size_t
+    L.qmoe_kv4_get_status.argtypes = [vp]
+    L.qmoe_kv4_get_status.restype = i
+    L.qmoe_kv4_last_error.argtypes = [vp]
+    L.qmoe_kv4_last_error.restype = C.c_char_p
+    L.qmoe_kv4_plan.argtypes = [vp, i, ip, ip, ip, ip, ip, i, ip, ip, ip, ip, vp]
+    L.qmoe_kv4_plan.restype = i
+    L.qmoe_kv4_append.argtypes = [vp, C.POINTER(qmoe_kv4_cache), vp, vp, i, i, i64, i64, vp, fp, fp]
+    L.qmoe_kv4_append.restype = i
+    L.qmoe_kv4_attention.argtypes = [vp, C.POINTER(qmoe_kv4_cache), vp, i, i64, i, i, i, ip, ip, ip,
+                                     C.c_float, vp, i, i64, fp]
+    L.qmoe_kv4_attention.restype = i
     return L
 
 
@@ -278,6 +314,69 @@ def qmoe_fused_decode_available(ctx, n_tokens: int, gate_t: int, up_t: int, down
 
 def qmoe_expert_stride(qtype: int, rows: int, cols: int) -> int:
     return lib.qmoe_expert_stride(qtype, rows, cols)
+
+
+def _check_kv4(kv, status):
+    if status != QMOE_OK:
+        raise QmoeError(status, lib.qmoe_kv4_last_error(kv).decode())
+
+
+def qmoe_kv4_create(cfg: qmoe_kv4_config):
+    h = C.c_void_p()
+    _check_kv4(None, lib.qmoe_kv4_create(C.byref(cfg), C.byref(h)))
+    return h
+
+
+def qmoe_kv4_destroy(kv):
+    lib.qmoe_kv4_destroy(kv)
+
+
+def qmoe_kv4_set_stream(kv, stream: int):
+    _check_kv4(kv, lib.qmoe_kv4_set_stream(kv, stream))
+
+
+def qmoe_kv4_workspace_bytes(cfg: qmoe_kv4_config) -> int:
+    return lib.qmoe_kv4_workspace_bytes(C.byref(cfg))
+
+
+def qmoe_kv4_get_status(kv) -> int:
+    return lib.qmoe_kv4_get_status(kv)
+
+
+def qmoe_kv4_last_error(kv) -> str:
+    return lib.qmoe_kv4_last_error(kv).decode()
+
+
+def qmoe_kv4_plan(kv, n_seqs, seq_len, new_len, block_table, free_pages, n_free, cap_tokens,
+                  seq_len_out, n_free_out, cu_tokens, positions, slots):
+    _check_kv4(kv, lib.qmoe_kv4_plan(kv, n_seqs, _ptr(seq_len), _ptr(new_len), _ptr(block_table),
+                                     _ptr(free_pages), _ptr(n_free), cap_tokens, _ptr(seq_len_out),
+                                     _ptr(n_free_out), _ptr(cu_tokens), _ptr(positions), _ptr(slots)))
+
+
+def qmoe_kv4_append(kv, cache, k, v, dtype, n_tokens, k_stride, v_stride, slots, k_hat=None,
+                    v_hat=None):
+    _check_kv4(kv, lib.qmoe_kv4_append(kv, C.byref(cache), _ptr(k), _ptr(v), dtype, n_tokens,
+                                       k_stride, v_stride, _ptr(slots), _ptr(k_hat), _ptr(v_hat)))
+
+
+def qmoe_kv4_attention(kv, cache, q, q_t, q_stride, n_seqs, n_tokens, max_new, cu_tokens, seq_len,
+                       block_table, scale, out, out_t, out_stride, lse=None):
+    _check_kv4(kv, lib.qmoe_kv4_attention(kv, C.byref(cache), _ptr(q), q_t, q_stride, n_seqs,
+                                          n_tokens, max_new, _ptr(cu_tokens), _ptr(seq_len),
+                                          _ptr(block_table), scale, _ptr(out), out_t, out_stride,
+                                          _ptr(lse)))
+
+
+def make_kv4_config(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_seqs, max_tokens,
+                    max_pages_per_seq, stream=0) -> qmoe_kv4_config:
+    return qmoe_kv4_config(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_seqs, max_tokens,
+                           max_pages_per_seq, stream or None)
+
+
+def make_kv4_cache(k_codes, k_scales, v_codes, v_scales, k_global, v_global) -> qmoe_kv4_cache:
+    return qmoe_kv4_cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
+                          _ptr(k_global), _ptr(v_global))
 
 
 def make_config(hidden, n_experts, top_k, ffn, max_tokens, norm_topk_prob=1, stream=0,

@@ -1,0 +1,114 @@
+// kv4.cuh -- the paged 4-bit KV cache: what its kernels and the C ABI share.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "lowbit.cuh"
+#include "pdl.cuh"
+
+namespace qmoe {
+
+enum : int { KV4_F32 = 0, KV4_F16 = 1, KV4_BF16 = 2 };
+
+// Geometry of every layer's cache and the table that maps positions to pages.
+struct Kv4Shape {
+    int nq, nkv, hd, page, n_pages, width;   // width: columns of the block table
+};
+
+// One layer's cache.  codes [n_pages][nkv][page][hd/2], scales [n_pages][nkv][page][hd/16]
+struct Kv4Cache {
+    uint8_t* kc;
+    uint8_t* ks;
+    uint8_t* vc;
+    uint8_t* vs;
+    const float* kg;
+    const float* vg;
+};
+
+struct Kv4PlanArgs {
+    int n, page, n_pages, width, cap;
+    const int32_t* seq_len;
+    const int32_t* new_len;
+    int32_t* table;
+    int32_t* free_pages;
+    const int32_t* n_free;
+    int32_t* seq_len_out;
+    int32_t* n_free_out;
+    int32_t* cu;
+    int32_t* positions;
+    int64_t* slots;
+    unsigned* arrive;     // zero between launches
+    int* status;
+};
+cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, int num_sms, cudaStream_t st);
+
+struct Kv4AppendArgs {
+    Kv4Shape s;
+    Kv4Cache c;
+    const void* k;
+    const void* v;
+    int dtype, n_tokens;
+    int64_t k_stride, v_stride;   // elements between rows
+    const int64_t* slots;
+    float* k_hat;
+    float* v_hat;
+    int* status;
+};
+cudaError_t launch_kv4_append(const Kv4AppendArgs& a, cudaStream_t st);
+
+struct Kv4AttnArgs {
+    Kv4Shape s;
+    Kv4Cache c;
+    const void* q;
+    int q_t, out_t;
+    int64_t q_stride, out_stride;
+    int n_seqs, n_tokens, max_new;
+    const int32_t* cu;
+    const int32_t* seq_len;
+    const int32_t* table;
+    float scale;
+    void* out;
+    float* lse;
+    int* status;
+};
+cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st);
+
+__device__ __forceinline__ float kv4_load(const void* p, size_t i, int t) {
+    return t == KV4_F32 ? static_cast<const float*>(p)[i]
+         : t == KV4_F16 ? __half2float(static_cast<const __half*>(p)[i])
+                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+__device__ __forceinline__ void kv4_store(void* p, size_t i, int t, float v) {
+    if (t == KV4_F32) static_cast<float*>(p)[i] = v;
+    else if (t == KV4_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// nearest E2M1 code of v (ties to the even code), saturating at 6
+__device__ __forceinline__ uint32_t kv4_e2m1_code(float v) {
+    const float a = fabsf(v);
+    const uint32_t m = a <= 0.25f ? 0u : a < 0.75f ? 1u : a <= 1.25f ? 2u : a < 1.75f ? 3u
+                     : a <= 2.5f ? 4u : a < 3.5f ? 5u : a <= 5.0f ? 6u : 7u;
+    return m | (signbit(v) ? 8u : 0u);
+}
+
+// A sequence's part of a call: rows q0 .. q0+n-1 are its last n of len positions.
+// False (and ok cleared) where the device arrays hold values out of range.
+struct Kv4Seq {
+    int q0, n, len;
+};
+__device__ __forceinline__ bool kv4_seq(const Kv4AttnArgs& a, int s, Kv4Seq& r) {
+    r.q0 = a.cu[s];
+    const int q1 = a.cu[s + 1];
+    r.len = a.seq_len[s];
+    const bool good = r.q0 >= 0 && q1 >= r.q0 && q1 <= a.n_tokens && q1 - r.q0 <= a.max_new && r.len >= 0 &&
+                      (int64_t)r.len <= (int64_t)a.s.width * a.s.page;
+    r.n = good ? q1 - r.q0 : 0;
+    if (!good) r.len = 0;
+    return good;
+}
+
+}  // namespace qmoe

@@ -263,6 +263,24 @@ qmoe_status run_moe(qmoe_ctx* c, const float* x, const float* res, const float* 
 
 }  // namespace
 
+namespace qmoe {
+
+void create_error(const char* fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_create_err, sizeof(g_create_err), fmt, ap);
+    va_end(ap);
+    if (g_create_err[0]) fprintf(stderr, "qmoe_kv4_create: %s\n", g_create_err);
+}
+
+bool fail_next_alloc() {
+    if (g_fail_alloc <= 0) return false;
+    --g_fail_alloc;
+    return true;
+}
+
+}  // namespace qmoe
+
 extern "C" {
 
 size_t qmoe_workspace_bytes(const qmoe_config* cfg) {

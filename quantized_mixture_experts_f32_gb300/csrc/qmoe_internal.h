@@ -290,4 +290,9 @@ cudaError_t prefill_layer_prepare();
 cudaError_t launch_prefill_layer_attn(const PrefillLayerArgs& a, cudaStream_t st);
 float* prefill_layer_x2(void* scratch, int T, int H, int nq, int nkv, int hd);
 
+// Text that qmoe_last_error(NULL) gives on this thread (a failed qmoe_kv4_create;
+// "" clears it), and whether the allocation-failure hook takes the next allocation.
+void create_error(const char* fmt, ...);
+bool fail_next_alloc();
+
 }  // namespace qmoe
