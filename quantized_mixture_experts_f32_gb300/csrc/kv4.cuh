@@ -73,7 +73,15 @@ struct Kv4AttnArgs {
     float* lse;
     int* status;
 };
-cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, cudaStream_t st);
+// Workspace of the attention, zero between launches but for `parts`.
+struct Kv4Work {
+    float* parts;         // [kv4_part_floats] parts of items that several CTAs share
+    unsigned* arrive;     // [kv4_arrive_words] arrival counters of those items
+    int num_sms;
+};
+int kv4_arrive_words(int num_sms);
+size_t kv4_part_floats(int hd, int num_sms);
+cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st);
 
 __device__ __forceinline__ float kv4_load(const void* p, size_t i, int t) {
     return t == KV4_F32 ? static_cast<const float*>(p)[i]

@@ -19,22 +19,27 @@ struct qmoe_kv4 {
     void* ws;
     int* status;          // device status word
     unsigned* arrive;     // arrival counter of the plan kernel
+    qmoe::Kv4Work work;   // attention
 };
 
 namespace {
 
+constexpr int NOMINAL_SMS = 152;   // qmoe_kv4_workspace_bytes needs no device: a GB300's multiprocessors
+
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-    size_t status, arrive, total;
+    size_t status, arrive, items, parts, total;
 };
 
-Layout layout(const qmoe_kv4_config*) {
+Layout layout(const qmoe_kv4_config* c, int num_sms) {
     Layout L{};
     size_t off = 0;
     auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
     L.status = take(sizeof(int));
     L.arrive = take(sizeof(unsigned));
+    L.items = take(sizeof(unsigned) * qmoe::kv4_arrive_words(num_sms));
+    L.parts = take(sizeof(float) * qmoe::kv4_part_floats(c->head_dim, num_sms));
     L.total = off;
     return L;
 }
@@ -118,7 +123,7 @@ extern "C" {
 
 size_t qmoe_kv4_workspace_bytes(const qmoe_kv4_config* cfg) {
     char why[256];
-    return config_ok(cfg, why, sizeof(why)) ? layout(cfg).total : 0;
+    return config_ok(cfg, why, sizeof(why)) ? layout(cfg, NOMINAL_SMS).total : 0;
 }
 
 qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
@@ -140,7 +145,6 @@ qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
     }
     h->cfg = *cfg;
     h->stream = static_cast<cudaStream_t>(cfg->stream);
-    const Layout L = layout(cfg);
     cudaError_t e = cudaGetDevice(&h->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device);
     if (e != cudaSuccess) {
@@ -148,6 +152,7 @@ qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
         delete h;
         return QMOE_ERR_CUDA;
     }
+    const Layout L = layout(cfg, h->num_sms);
     e = qmoe::fail_next_alloc() ? cudaErrorMemoryAllocation : cudaMalloc(&h->ws, L.total);
     if (e != cudaSuccess) {
         cudaGetLastError();
@@ -158,7 +163,8 @@ qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
     char* b = static_cast<char*>(h->ws);
     h->status = reinterpret_cast<int*>(b + L.status);
     h->arrive = reinterpret_cast<unsigned*>(b + L.arrive);
-    e = cudaMemsetAsync(h->ws, 0, L.total, h->stream);
+    h->work = {reinterpret_cast<float*>(b + L.parts), reinterpret_cast<unsigned*>(b + L.items), h->num_sms};
+    e = cudaMemsetAsync(h->ws, 0, L.parts, h->stream);   // all but the attention's parts
     if (e == cudaSuccess) e = cudaStreamSynchronize(h->stream);
     if (e != cudaSuccess) {
         qmoe::create_error("workspace clear: %s", cudaGetErrorString(e));
@@ -288,7 +294,7 @@ qmoe_status qmoe_kv4_attention(qmoe_kv4* h, const qmoe_kv4_cache* cache, const v
     if (dev.e != cudaSuccess) return cuda_fail(h, dev.e, "device select");
     const qmoe::Kv4AttnArgs a{shape(h), cache_of(cache), q, (int)q_t, (int)out_t, q_stride, out_stride, n_seqs,
                               n_tokens, max_new, cu_tokens, seq_len, block_table, scale, out, lse, h->status};
-    const cudaError_t e = qmoe::launch_kv4_attention(a, h->stream);
+    const cudaError_t e = qmoe::launch_kv4_attention(a, h->work, h->stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "attention launch");
     h->err[0] = 0;
     return QMOE_OK;
