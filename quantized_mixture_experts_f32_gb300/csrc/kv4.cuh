@@ -73,12 +73,18 @@ struct Kv4AttnArgs {
     float* lse;
     int* status;
 };
+// Attention: sequences of at most few_rows rows (new tokens x heads of a group) by
+// launch_kv4_decode, the others by launch_kv4_extend.
 // Workspace of the attention, zero between launches but for `parts`.
 struct Kv4Work {
     float* parts;         // [kv4_part_floats] parts of items that several CTAs share
     unsigned* arrive;     // [kv4_arrive_words] arrival counters of those items
     int num_sms;
 };
+size_t kv4_decode_part_floats(int hd, int num_sms);
+size_t kv4_extend_part_floats(int hd, int num_sms);
+cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
+cudaError_t launch_kv4_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
 int kv4_arrive_words(int num_sms);
 size_t kv4_part_floats(int hd, int num_sms);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st);
@@ -87,12 +93,6 @@ __device__ __forceinline__ float kv4_load(const void* p, size_t i, int t) {
     return t == KV4_F32 ? static_cast<const float*>(p)[i]
          : t == KV4_F16 ? __half2float(static_cast<const __half*>(p)[i])
                         : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-__device__ __forceinline__ void kv4_store(void* p, size_t i, int t, float v) {
-    if (t == KV4_F32) static_cast<float*>(p)[i] = v;
-    else if (t == KV4_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
 }
 
 // nearest E2M1 code of v (ties to the even code), saturating at 6

@@ -22,6 +22,7 @@
 #include <math.h>
 
 #include "kv4.cuh"
+#include "kv4_row.cuh"
 #include "ptx_sync.cuh"
 
 namespace qmoe {
@@ -33,8 +34,6 @@ constexpr int DT = 32 * DW;
 constexpr int TP = 32;                   // positions a warp takes at a time
 constexpr int UNIT = TP * DW;            // positions a CTA takes at a time
 constexpr int STAGES = 2;                // stages per warp: one in use, one being copied
-constexpr float P_UP = 6.f;              // p is held as 2^(z - m + 6): its low part stays normal in fp16
-constexpr float P_SLACK = 8.f;           // m follows the maximum once it is 2^8 behind (p <= 2^14)
 
 template <int HD>
 struct DGeo {
@@ -59,40 +58,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
-__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
-
-// two E2M1 codes of byte b of w, times the scales s
-__device__ __forceinline__ uint32_t widen(uint32_t w, int b, __half2 s) {
-    const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(w >> (8 * b)), __NV_E2M1);
-    return h2u(__hmul2(__half2(r), s));
-}
-
-// E4M3 codes (one byte each) -> half2
-__device__ __forceinline__ __half2 scale2(uint32_t lo, uint32_t hi) {
-    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(lo | (hi << 8)), __NV_E4M3));
-}
-
-// two neighbouring elements of a row of type t, at element `at` (even)
-__device__ __forceinline__ float2 load2(const void* p, size_t at, int t) {
-    if (t == KV4_F32) return *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
-    const uint32_t b = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + at);
-    if (t == KV4_F16) return __half22float2(u2h(b));
-    return make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
-}
-
-__device__ __forceinline__ void store2(void* p, size_t at, int t, float x, float y) {
-    if (t == KV4_F32) *reinterpret_cast<float2*>(static_cast<float*>(p) + at) = make_float2(x, y);
-    else if (t == KV4_F16) *reinterpret_cast<__half2*>(static_cast<__half*>(p) + at) = __floats2half2_rn(x, y);
-    else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + at) = __floats2bfloat162_rn(x, y);
 }
 
 // column c of eight <-> position of eight: 0 4 1 5 2 6 3 7
@@ -133,7 +98,7 @@ __device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) { re
 
 template <int HD>
 __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
-    kv4_decode_kernel(const Kv4AttnArgs a, float* __restrict__ parts, unsigned* __restrict__ arrive) {
+    kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, float* __restrict__ parts, unsigned* __restrict__ arrive) {
     using G = DGeo<HD>;
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t* ring = sm;
@@ -156,7 +121,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             Kv4Seq q;
             if (!kv4_seq(a, s, q) && blockIdx.x == 0) atomicExch(a.status, ST_DEVICE_CHECK);
             pre[s] = run;
-            run += (long long)a.s.nkv * ((q.n * group + 7) / 8) * (q.len ? (q.len + UNIT - 1) / UNIT : 1);
+            if (q.n * group <= few_rows) run += (long long)a.s.nkv * ((q.n * group + 7) / 8) * (q.len ? (q.len + UNIT - 1) / UNIT : 1);
         }
         long long inc = run;
 #pragma unroll
@@ -238,25 +203,21 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             float big = 0.f;
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
-                v[i] = warp < rows ? load2(a.q, (size_t)(q.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
+                v[i] = warp < rows ? kv4_load2(a.q, (size_t)(q.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
                                    : make_float2(0.f, 0.f);
                 big = fmaxf(big, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-            const int e = big > 0.f && big < INFINITY ? ilogbf(big) : 0;
+            const int e = kv4_exponent(big);
             if (lane == 0) fac_s[warp] = ldexpf(a.scale * 1.4426950408889634f * kg, e);
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
-                const float x = ldexpf(v[i].x, -e), y = ldexpf(v[i].y, -e);
-                const __half2 hi = __floats2half2_rn(x, y);
-                const __half2 lo = __floats2half2_rn(x - __low2float(hi), y - __high2float(hi));
                 const int d = 2 * lane + 64 * i;
                 const int jj = HD == 256 ? (d >> 5) & 3 : d / (HD / 4);
                 const int wd = HD == 256 ? (d & 31) + 32 * (d >> 7) : d & (HD / 4 - 1);
                 uint32_t* f = qf + ((wd >> 2) * 32 + warp * 4 + jj) * 4 + (wd & 2);
-                f[0] = h2u(hi);
-                f[1] = h2u(lo);
+                kv4_split(ldexpf(v[i].x, -e), ldexpf(v[i].y, -e), f[0], f[1]);
             }
         }
         __syncthreads();
@@ -302,7 +263,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                             kw[n][0] = x.x;
                             kw[n][1] = x.y;
                             const uint32_t b = st[G::KS + p * G::SB + j];
-                            ks[n][0] = scale2(b, b);
+                            ks[n][0] = kv4_scale2(b, b);
                         } else {
                             const int ch = HD == 256 ? (j + 4 * hh) ^ (4 * (r & 1)) : j;
                             const uint4 x = *reinterpret_cast<const uint4*>(st + G::KC + row * G::ROWB + ch * 16);
@@ -311,8 +272,8 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                             kw[n][2] = x.z;
                             kw[n][3] = x.w;
                             const uint32_t b = *reinterpret_cast<const uint16_t*>(st + G::KS + p * G::SB + 8 * hh + 2 * j);
-                            ks[n][0] = scale2(b & 255u, b & 255u);
-                            ks[n][1] = scale2(b >> 8, b >> 8);
+                            ks[n][0] = kv4_scale2(b & 255u, b & 255u);
+                            ks[n][1] = kv4_scale2(b >> 8, b >> 8);
                         }
                     }
 #pragma unroll
@@ -323,7 +284,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                         for (int n = 0; n < 4; ++n) {
                             const uint32_t w = kw[n][k >> 1];
                             const __half2 sc = ks[n][k >> 2];
-                            mma_f16(z[n], af, widen(w, 2 * (k & 1), sc), widen(w, 2 * (k & 1) + 1, sc));
+                            mma_f16(z[n], af, kv4_widen(w, 2 * (k & 1), sc), kv4_widen(w, 2 * (k & 1) + 1, sc));
                         }
                     }
                 }
@@ -344,9 +305,9 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 }
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                if (__any_sync(0xffffffffu, mx > m + P_SLACK)) {
+                if (__any_sync(0xffffffffu, mx > m + KV4_P_SLACK)) {
                     const float mn = fmaxf(m, mx);
-                    const float c = m == -INFINITY ? 0.f : ex2(m - mn);
+                    const float c = m == -INFINITY ? 0.f : kv4_ex2(m - mn);
                     l *= c;
 #pragma unroll
                     for (int t2 = 0; t2 < HD / 8; ++t2)
@@ -354,16 +315,13 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                         for (int i = 0; i < 4; ++i) o[t2][i] *= c;
                     m = mn;
                 }
-                const float base = m == -INFINITY ? 0.f : m - P_UP;
+                const float base = m == -INFINITY ? 0.f : m - KV4_P_UP;
                 uint32_t pf[2][4];
 #pragma unroll
                 for (int n = 0; n < 4; ++n) {
-                    const float p0 = ex2(z[n][0] - base), p1 = ex2(z[n][1] - base);
+                    const float p0 = kv4_ex2(z[n][0] - base), p1 = kv4_ex2(z[n][1] - base);
                     l += p0 + p1;
-                    const __half2 hi = __floats2half2_rn(p0, p1);
-                    pf[n >> 1][2 * (n & 1)] = h2u(hi);
-                    pf[n >> 1][2 * (n & 1) + 1] =
-                        h2u(__floats2half2_rn(p0 - __low2float(hi), p1 - __high2float(hi)));
+                    kv4_split(p0, p1, pf[n >> 1][2 * (n & 1)], pf[n >> 1][2 * (n & 1) + 1]);
                 }
                 // o += p v, 16 positions at a time; column r holds the HD/8 elements from r * HD/8
 #pragma unroll
@@ -397,18 +355,15 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
                     for (int w = 0; w < VW; ++w) {
                         const int sh = HD == 256 ? 8 * (w >> 1) : 0;
-                        const __half2 sa = scale2((vs[0] >> sh) & 255u, (vs[1] >> sh) & 255u);
-                        const __half2 sb = scale2((vs[2] >> sh) & 255u, (vs[3] >> sh) & 255u);
-                        // bytes with one element of two positions: even elements, odd elements
-                        const uint32_t lo4 = 0x0f0f0f0fu;
-                        const uint32_t ea = (vw[0][w] & lo4) | ((vw[1][w] << 4) & ~lo4);
-                        const uint32_t eb = (vw[2][w] & lo4) | ((vw[3][w] << 4) & ~lo4);
-                        const uint32_t oa = ((vw[0][w] >> 4) & lo4) | (vw[1][w] & ~lo4);
-                        const uint32_t ob = ((vw[2][w] >> 4) & lo4) | (vw[3][w] & ~lo4);
+                        const __half2 sa = kv4_scale2((vs[0] >> sh) & 255u, (vs[1] >> sh) & 255u);
+                        const __half2 sb = kv4_scale2((vs[2] >> sh) & 255u, (vs[3] >> sh) & 255u);
+                        uint32_t ea, eb, oa, ob;
+                        kv4_pair(vw[0][w], vw[1][w], ea, oa);
+                        kv4_pair(vw[2][w], vw[3][w], eb, ob);
 #pragma unroll
                         for (int b = 0; b < 4; ++b) {
-                            mma_f16(o[8 * w + 2 * b], pf[sub], widen(ea, b, sa), widen(eb, b, sb));
-                            mma_f16(o[8 * w + 2 * b + 1], pf[sub], widen(oa, b, sa), widen(ob, b, sb));
+                            mma_f16(o[8 * w + 2 * b], pf[sub], kv4_widen(ea, b, sa), kv4_widen(eb, b, sb));
+                            mma_f16(o[8 * w + 2 * b + 1], pf[sub], kv4_widen(oa, b, sa), kv4_widen(ob, b, sb));
                         }
                     }
                 }
@@ -447,7 +402,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
         for (int i = 0; i < PT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
         auto add = [&](float mw, float lw, const float* x, bool shared) {
-            const float c = lw == 0.f ? 0.f : ex2(mw - mj);
+            const float c = lw == 0.f ? 0.f : kv4_ex2(mw - mj);
             lj += lw * c;
 #pragma unroll
             for (int i = 0; i < PT / 2; ++i) {
@@ -500,10 +455,10 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             const float inv = lj == 0.f ? 0.f : vg / lj;
             const size_t at = (size_t)(q.q0 + tok) * a.out_stride + (size_t)h * HD + d0;
 #pragma unroll
-            for (int i = 0; i < PT / 2; ++i) store2(a.out, at + 2 * i, a.out_t, acc[i].x * inv, acc[i].y * inv);
+            for (int i = 0; i < PT / 2; ++i) kv4_store2(a.out, at + 2 * i, a.out_t, acc[i].x * inv, acc[i].y * inv);
             if (a.lse && lane == 0)
                 a.lse[(size_t)(q.q0 + tok) * a.s.nq + h] =
-                    lj == 0.f ? -INFINITY : (mj - P_UP + log2f(lj)) * 0.6931471805599453f;
+                    lj == 0.f ? -INFINITY : (mj - KV4_P_UP + log2f(lj)) * 0.6931471805599453f;
         }
         __syncthreads();                               // the join buffer and q are free again
         u += t1 - t0;
@@ -511,26 +466,41 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 }
 
 template <int HD>
-cudaError_t launch_decode(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st) {
+cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)DGeo<HD>::smem(4096));
     if (e != cudaSuccess) return e;
     return launch_pdl(kv4_decode_kernel<HD>, dim3(w.num_sms * (HD == 256 ? 1 : 2)), dim3(DT), DGeo<HD>::smem(a.n_seqs),
-                      st, a, w.parts, w.arrive);
+                      st, a, few_rows, w.parts, w.arrive);
 }
 
 }  // namespace
 
 // a grid has two CTAs a multiprocessor at most, and each leaves two parts of eight rows at most
+size_t kv4_decode_part_floats(int hd, int num_sms) { return (size_t)4 * num_sms * (8 * hd + 16); }
+
+cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
+    switch (a.s.hd) {
+        case 64: return launch_decode<64>(a, few_rows, w, st);
+        case 128: return launch_decode<128>(a, few_rows, w, st);
+        default: return launch_decode<256>(a, few_rows, w, st);
+    }
+}
+
+// Rows (new tokens x heads of the group) up to which a sequence is the decode kernel's.
+constexpr int FEW_ROWS = 32;
+
 int kv4_arrive_words(int num_sms) { return 2 * num_sms; }
-size_t kv4_part_floats(int hd, int num_sms) { return (size_t)4 * num_sms * (8 * hd + 16); }
+
+size_t kv4_part_floats(int hd, int num_sms) {
+    const size_t x = kv4_decode_part_floats(hd, num_sms), y = kv4_extend_part_floats(hd, num_sms);
+    return x > y ? x : y;
+}
 
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st) {
-    switch (a.s.hd) {
-        case 64: return launch_decode<64>(a, w, st);
-        case 128: return launch_decode<128>(a, w, st);
-        default: return launch_decode<256>(a, w, st);
-    }
+    const cudaError_t e = launch_kv4_decode(a, FEW_ROWS, w, st);
+    if (e != cudaSuccess || (long long)a.max_new * (a.s.nq / a.s.nkv) <= FEW_ROWS) return e;
+    return launch_kv4_extend(a, FEW_ROWS, w, st);
 }
 
 }  // namespace qmoe

@@ -1,0 +1,106 @@
+// kv4_row.cuh -- arithmetic the cache's attention kernels share: widening codes,
+// splitting fp32 values into fp16 terms, rows of any type.
+#pragma once
+#include "kv4.cuh"
+
+namespace qmoe {
+
+// A row's weights are held as 2^(z - m + P_UP) and its m follows the running maximum
+// once that is P_SLACK ahead: at most 2^14 in fp16, and the low parts of all but
+// vanishing weights stay normal.
+constexpr float KV4_P_UP = 6.f;
+constexpr float KV4_P_SLACK = 8.f;
+
+__device__ __forceinline__ float kv4_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t kv4_u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ uint32_t kv4_pack(float x, float y) { return kv4_u(__floats2half2_rn(x, y)); }
+
+// x = hi + lo to 22 bits, as fp16 pairs
+__device__ __forceinline__ void kv4_split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    hi = kv4_u(h);
+    lo = kv4_pack(x - __low2float(h), y - __high2float(h));
+}
+
+// The exponent that brings a row of q whose largest magnitude is `big` to [1, 2).
+__device__ __forceinline__ int kv4_exponent(float big) { return big > 0.f && big < INFINITY ? ilogbf(big) : 0; }
+
+// two E2M1 codes of byte b of w, times the scales s: exact (2 x 4 significant bits)
+__device__ __forceinline__ uint32_t kv4_widen(uint32_t w, int b, __half2 s) {
+    const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(w >> (8 * b)), __NV_E2M1);
+    return kv4_u(__hmul2(__half2(r), s));
+}
+
+// two E4M3 codes -> half2
+__device__ __forceinline__ __half2 kv4_scale2(uint32_t lo, uint32_t hi) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(lo | (hi << 8)), __NV_E4M3));
+}
+
+// Eight elements each of two positions -> bytes that hold one element of both: the
+// even elements, the odd elements.
+__device__ __forceinline__ void kv4_pair(uint32_t a, uint32_t b, uint32_t& even, uint32_t& odd) {
+    constexpr uint32_t lo4 = 0x0f0f0f0fu;
+    even = (a & lo4) | ((b << 4) & ~lo4);
+    odd = ((a >> 4) & lo4) | (b & ~lo4);
+}
+
+// two neighbouring elements of a row of type t, at element `at` (even)
+__device__ __forceinline__ float2 kv4_load2(const void* p, size_t at, int t) {
+    if (t == KV4_F32) return *reinterpret_cast<const float2*>(static_cast<const float*>(p) + at);
+    uint32_t b = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + at);
+    if (t == KV4_F16) return __half22float2(*reinterpret_cast<__half2*>(&b));
+    return make_float2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
+}
+
+__device__ __forceinline__ void kv4_store2(void* p, size_t at, int t, float x, float y) {
+    if (t == KV4_F32) *reinterpret_cast<float2*>(static_cast<float*>(p) + at) = make_float2(x, y);
+    else if (t == KV4_F16) *reinterpret_cast<__half2*>(static_cast<__half*>(p) + at) = __floats2half2_rn(x, y);
+    else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + at) = __floats2bfloat162_rn(x, y);
+}
+
+// eight elements at a multiple of eight
+__device__ __forceinline__ void kv4_load8(const void* p, size_t at, int t, float (&v)[8]) {
+    if (t == KV4_F32) {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+        const float4 x = f[0], y = f[1];
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        return;
+    }
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = t == KV4_F16 ? __half22float2(*reinterpret_cast<__half2*>(&w[i]))
+                                      : make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ void kv4_store8(void* p, size_t at, int t, const float* v) {
+    if (t == KV4_F32) {
+        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+        f[0] = make_float4(v[0], v[1], v[2], v[3]);
+        f[1] = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (t == KV4_F16) {
+            w[i] = kv4_pack(v[2 * i], v[2 * i + 1]);
+        } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+    }
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace qmoe

@@ -308,7 +308,7 @@ def _check(kv, x, out, lse, cu, lens, table, scale=None, out_t=None):
         gl = lse[:t].double().cpu().numpy()
         empty = np.isneginf(wl)
         assert np.array_equal(np.isneginf(gl), empty)
-        assert (np.abs(gl - wl)[~empty] <= lb[~empty]).all()
+        assert (np.abs(gl[~empty] - wl[~empty]) <= lb[~empty]).all()
 
 
 LAYOUTS = [(8, 2, 128, 16), (4, 4, 64, 32), (14, 2, 64, 16), (32, 1, 128, 64), (6, 2, 256, 16), (10, 10, 128, 128),
