@@ -70,25 +70,27 @@ template <int HD>
 __device__ __forceinline__ void copy_stage(uint8_t* st, const Kv4Cache& c, const int64_t (&row)[2], int lane) {
     using G = DGeo<HD>;
     constexpr int CH = HD / 32;                        // 16-byte chunks of a position's codes
+    constexpr int PP = 32 / CH;                        // positions a warp's 32 chunks cover
 #pragma unroll
-    for (int it = 0; it < CH; ++it) {
-        const int x = it * 32 + lane, sub = x / (16 * CH), y = x % (16 * CH), p = y / CH, ch = y % CH;
-        const int64_t rw = sub ? row[1] : row[0];
-        if (rw < 0) continue;
-        const int kr = sub * 16 + (p & 8) + col_of_pos(p & 7), vr = sub * 16 + p;
-        const int kch = HD == 256 ? ch ^ (4 * (kr & 1)) : ch;
-        const int vch = HD == 256 ? ch ^ (2 * (p & 3)) : HD == 128 ? ch ^ (p & 2) : ch;
-        const size_t src = (size_t)rw * G::ROWB + (size_t)y * 16;
-        cp_async_cg16(st + G::KC + kr * G::ROWB + kch * 16, c.kc + src);
-        cp_async_cg16(st + G::VC + vr * G::ROWB + vch * 16, c.vc + src);
-    }
+    for (int sub = 0; sub < 2; ++sub) {
+        if (row[sub] < 0) continue;
+        const uint8_t* kc = c.kc + (size_t)row[sub] * G::ROWB + lane * 16;
+        const uint8_t* vc = c.vc + (size_t)row[sub] * G::ROWB + lane * 16;
 #pragma unroll
-    for (int it = 0; it < (4 * G::SB + 31) / 32; ++it) {       // 16 positions' scales are SB chunks
-        const int x = it * 32 + lane, v = x / (2 * G::SB), y = x % (2 * G::SB), sub = y / G::SB, ch = y % G::SB;
-        const int64_t rw = sub ? row[1] : row[0];
-        if (x >= 4 * G::SB || rw < 0) continue;
-        const size_t src = (size_t)rw * G::SB + (size_t)ch * 16;
-        cp_async_cg16(st + (v ? G::VS : G::KS) + (sub * G::SB + ch) * 16, (v ? c.vs : c.ks) + src);
+        for (int it = 0; it < 16 / PP; ++it) {
+            const int p = it * PP + lane / CH, ch = lane % CH;
+            const int kr = sub * 16 + (p & 8) + col_of_pos(p & 7), vr = sub * 16 + p;
+            const int kch = HD == 256 ? ch ^ (4 * (kr & 1)) : ch;
+            const int vch = HD == 256 ? ch ^ (2 * (p & 3)) : HD == 128 ? ch ^ (p & 2) : ch;
+            cp_async_cg16(st + G::KC + kr * G::ROWB + kch * 16, kc + it * 512);
+            cp_async_cg16(st + G::VC + vr * G::ROWB + vch * 16, vc + it * 512);
+        }
+        // 16 positions' scales are SB chunks: K's by the lanes from 0, V's by those behind
+        if (lane < 2 * G::SB) {
+            const int v = lane / G::SB, ch = lane % G::SB;
+            cp_async_cg16(st + (v ? G::VS : G::KS) + (sub * G::SB + ch) * 16,
+                          (v ? c.vs : c.ks) + (size_t)row[sub] * G::SB + (size_t)ch * 16);
+        }
     }
 }
 
@@ -254,7 +256,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 for (int hh = 0; hh < (HD == 256 ? 2 : 1); ++hh) {       // 256: the two halves of a row in turn
                     constexpr int KW = HD == 64 ? 2 : 4;                 // words of codes a lane has of a row
                     uint32_t kw[4][4];
-                    __half2 ks[4][2];
+                    __half2 ks[4];                                       // their one or two scales
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const int row = n * 8 + r, p = n * 8 + pos_of_col(r);
@@ -262,8 +264,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                             const uint2 x = *reinterpret_cast<const uint2*>(st + G::KC + row * G::ROWB + j * 8);
                             kw[n][0] = x.x;
                             kw[n][1] = x.y;
-                            const uint32_t b = st[G::KS + p * G::SB + j];
-                            ks[n][0] = kv4_scale2(b, b);
+                            ks[n] = kv4_scale2(st[G::KS + p * G::SB + j]);
                         } else {
                             const int ch = HD == 256 ? (j + 4 * hh) ^ (4 * (r & 1)) : j;
                             const uint4 x = *reinterpret_cast<const uint4*>(st + G::KC + row * G::ROWB + ch * 16);
@@ -271,20 +272,21 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                             kw[n][1] = x.y;
                             kw[n][2] = x.z;
                             kw[n][3] = x.w;
-                            const uint32_t b = *reinterpret_cast<const uint16_t*>(st + G::KS + p * G::SB + 8 * hh + 2 * j);
-                            ks[n][0] = kv4_scale2(b & 255u, b & 255u);
-                            ks[n][1] = kv4_scale2(b >> 8, b >> 8);
+                            ks[n] = kv4_scale2(*reinterpret_cast<const uint16_t*>(st + G::KS + p * G::SB + 8 * hh + 2 * j));
                         }
                     }
 #pragma unroll
-                    for (int k = 0; k < 2 * KW; ++k) {
-                        const uint4 qa = *reinterpret_cast<const uint4*>(qf + ((hh * 2 * KW + k) * 32 + lane) * 4);
-                        const uint32_t af[4] = {qa.x, qa.y, qa.z, qa.w};
+                    for (int w = 0; w < KW; ++w) {                       // a word is two steps of the product
+                        const uint4* qp = reinterpret_cast<const uint4*>(qf) + (hh * 2 * KW + 2 * w) * 32 + lane;
+                        const uint4 qa = qp[0], qb = qp[32];
+                        const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
-                            const uint32_t w = kw[n][k >> 1];
-                            const __half2 sc = ks[n][k >> 2];
-                            mma_f16(z[n], af, kv4_widen(w, 2 * (k & 1), sc), kv4_widen(w, 2 * (k & 1) + 1, sc));
+                            const __half2 sc = w & 2 ? __high2half2(ks[n]) : __low2half2(ks[n]);
+                            __half2 k[4];
+                            kv4_widen8(kw[n][w], k);
+                            mma_f16(z[n], fa, kv4_u(__hmul2(k[0], sc)), kv4_u(__hmul2(k[1], sc)));
+                            mma_f16(z[n], fb, kv4_u(__hmul2(k[2], sc)), kv4_u(__hmul2(k[3], sc)));
                         }
                     }
                 }
@@ -355,15 +357,19 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
                     for (int w = 0; w < VW; ++w) {
                         const int sh = HD == 256 ? 8 * (w >> 1) : 0;
-                        const __half2 sa = kv4_scale2((vs[0] >> sh) & 255u, (vs[1] >> sh) & 255u);
-                        const __half2 sb = kv4_scale2((vs[2] >> sh) & 255u, (vs[3] >> sh) & 255u);
-                        uint32_t ea, eb, oa, ob;
-                        kv4_pair(vw[0][w], vw[1][w], ea, oa);
-                        kv4_pair(vw[2][w], vw[3][w], eb, ob);
+                        const __half2 sa = kv4_scale2(kv4_bytes(vs[0] >> sh, vs[1] >> sh));
+                        const __half2 sb = kv4_scale2(kv4_bytes(vs[2] >> sh, vs[3] >> sh));
+                        uint32_t pa[2], pb[2];                           // even elements, odd elements
+                        kv4_pair(vw[0][w], vw[1][w], pa[0], pa[1]);
+                        kv4_pair(vw[2][w], vw[3][w], pb[0], pb[1]);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) {
-                            mma_f16(o[8 * w + 2 * b], pf[sub], kv4_widen(ea, b, sa), kv4_widen(eb, b, sb));
-                            mma_f16(o[8 * w + 2 * b + 1], pf[sub], kv4_widen(oa, b, sa), kv4_widen(ob, b, sb));
+                        for (int e = 0; e < 2; ++e) {
+                            __half2 va[4], vb[4];
+                            kv4_widen8(pa[e], va);
+                            kv4_widen8(pb[e], vb);
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                mma_f16(o[8 * w + 2 * b + e], pf[sub], kv4_u(__hmul2(va[b], sa)), kv4_u(__hmul2(vb[b], sb)));
                         }
                     }
                 }

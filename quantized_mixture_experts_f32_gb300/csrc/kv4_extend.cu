@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < G::KP; ++i) {
                 const int row = i * G::RPP + r0;
-                const __half2 s0 = kv4_scale2(sc[i] & 255u, sc[i] & 255u), s1 = kv4_scale2(sc[i] >> 8, sc[i] >> 8);
+                const __half2 both = kv4_scale2(sc[i]), s0 = __low2half2(both), s1 = __high2half2(both);
                 uint32_t x0 = w[i].x, x1 = w[i].y, x2 = w[i].z, x3 = w[i].w;
                 if (rot & 2) {
                     const uint32_t y0 = x0, y1 = x1;
@@ -492,8 +492,10 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 for (int k = 0; k < 4; ++k) {
                     const int kk = (k + rot) & 3;
                     const __half2 s = kk & 2 ? s1 : s0;
+                    __half2 e[4];
+                    kv4_widen8(xs[k], e);
                     *reinterpret_cast<uint4*>(tile + sw128_offset(row, ((jj & 1) * 4 + kk) * 8)) =
-                        make_uint4(kv4_widen(xs[k], 0, s), kv4_widen(xs[k], 1, s), kv4_widen(xs[k], 2, s), kv4_widen(xs[k], 3, s));
+                        make_uint4(kv4_u(__hmul2(e[0], s)), kv4_u(__hmul2(e[1], s)), kv4_u(__hmul2(e[2], s)), kv4_u(__hmul2(e[3], s)));
                 }
             }
             fence_proxy_async();
@@ -547,20 +549,23 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 uint8_t* tile = sm + G::V + b * G::KT + kb * (HD * 128);
                 __half2 s[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = kv4_scale2(sc[2 * i], sc[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) s[i] = kv4_scale2(kv4_bytes(sc[2 * i], sc[2 * i + 1]));
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    uint32_t ev[4], od[4];             // bytes of one element of two positions
+                    uint32_t pr[4][2];                 // bytes of one element of two positions: even, odd
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        kv4_pair(y ? w[2 * i].y : w[2 * i].x, y ? w[2 * i + 1].y : w[2 * i + 1].x, ev[i], od[i]);
+                        kv4_pair(y ? w[2 * i].y : w[2 * i].x, y ? w[2 * i + 1].y : w[2 * i + 1].x, pr[i][0], pr[i][1]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int d = dg * 16 + y * 8 + e;
-                        uint32_t o[4];
+                    for (int odd = 0; odd < 2; ++odd) {
+                        __half2 v[4][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = kv4_widen(e & 1 ? od[i] : ev[i], e >> 1, s[i]);
-                        *reinterpret_cast<uint4*>(tile + sw128_offset(d, pg8 * 8)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        for (int i = 0; i < 4; ++i) kv4_widen8(pr[i][odd], v[i]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4*>(tile + sw128_offset(dg * 16 + y * 8 + 2 * e + odd, pg8 * 8)) =
+                                make_uint4(kv4_u(__hmul2(v[0][e], s[0])), kv4_u(__hmul2(v[1][e], s[1])),
+                                           kv4_u(__hmul2(v[2][e], s[2])), kv4_u(__hmul2(v[3][e], s[3])));
                     }
                 }
             }

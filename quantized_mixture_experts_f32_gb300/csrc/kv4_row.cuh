@@ -30,16 +30,26 @@ __device__ __forceinline__ void kv4_split(float x, float y, uint32_t& hi, uint32
 // The exponent that brings a row of q whose largest magnitude is `big` to [1, 2).
 __device__ __forceinline__ int kv4_exponent(float big) { return big > 0.f && big < INFINITY ? ilogbf(big) : 0; }
 
-// two E2M1 codes of byte b of w, times the scales s: exact (2 x 4 significant bits)
-__device__ __forceinline__ uint32_t kv4_widen(uint32_t w, int b, __half2 s) {
-    const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(w >> (8 * b)), __NV_E2M1);
-    return kv4_u(__hmul2(__half2(r), s));
+// Eight E2M1 codes -> four half2, bytes in order.  One conversion a byte: naming the
+// bytes of w in PTX lets the conversion pick its byte, where extracting them first
+// cost an instruction more on the same (half-rate) pipe.
+__device__ __forceinline__ void kv4_widen8(uint32_t w, __half2 (&h)[4]) {
+    uint32_t r[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<__half2*>(&r[i]);
 }
 
-// two E4M3 codes -> half2
-__device__ __forceinline__ __half2 kv4_scale2(uint32_t lo, uint32_t hi) {
-    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(lo | (hi << 8)), __NV_E4M3));
+// two E4M3 codes (bytes 0 and 1 of x) -> half2
+__device__ __forceinline__ __half2 kv4_scale2(uint32_t x) {
+    return __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(x), __NV_E4M3));
 }
+// the low bytes of two words, as bytes 0 and 1
+__device__ __forceinline__ uint32_t kv4_bytes(uint32_t lo, uint32_t hi) { return __byte_perm(lo, hi, 0x0040); }
 
 // Eight elements each of two positions -> bytes that hold one element of both: the
 // even elements, the odd elements.
