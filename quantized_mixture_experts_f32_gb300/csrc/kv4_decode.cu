@@ -2,23 +2,23 @@
 // few tokens: decoding, draft tokens.  Bound by the cache's bytes (144 a position and
 // kv head at head_dim 128), then by the instructions that widen them.
 //
-// Row = (token, q head of the kv head's group), eight rows to an item.  With
+// Row = (token, q head of the kv head's group), 8 NR rows to an item.  With
 // z_p = q.k_p * scale * log2(e) the pass keeps a running maximum m, l = sum 2^(z-m)
 // and o = sum 2^(z-m) v_p; parts of an item's positions are joined by
 // m = max m_i, l = sum l_i 2^(m_i-m), o likewise.
 //
-// Both products are mma.sync m16n8k16 (fp16 in, fp32 out).  K and V are exact in
-// fp16 (2 x 4 significant bits), and the eight rows leave half of the 16-row operand
-// free: it takes the low parts, q = hi + lo and p = hi + lo (22 bits), so F32 rows
-// keep their precision for the price of 16-bit ones.  tcgen05 would want the widened
-// K and V in shared memory, 4x the bytes the cache has, for 128 rows of which eight
-// exist; here a thread widens what it has loaded straight into operand registers.
-// Each row of q is first scaled by the power of two of its largest element, so any
-// fp32 or bf16 range fits fp16.
+// Both products are mma.sync m16n8k16 (fp16 in, fp32 out) with the cache as the
+// 16-row operand and the rows as the eight columns: S^T = K Q^T, O^T += V^T P^T.  K and
+// V are exact in fp16 (2 x 4 significant bits).  F32 rows enter as hi + lo (TERMS = 2,
+// 22 bits), two products into one accumulator.  tcgen05 would want the widened K and V
+// in shared memory, 4x the bytes the cache has, for 128 rows of which eight exist;
+// here a thread widens what it has loaded straight into operand registers.  Each row
+// of q is first scaled by the power of two of its largest element, so any fp32 or
+// bf16 range fits fp16.
 //
 // The order of head elements in q.k and of positions in p.v is free: K and Q elements
-// are dealt to the four lanes of a column in contiguous runs (16-byte loads), and
-// columns to positions so that V's loads meet every bank once.
+// are dealt to the four lanes of a position in contiguous runs (16-byte loads), and
+// operand rows to positions so that V's loads meet every bank once.
 #include <math.h>
 
 #include "kv4.cuh"
@@ -35,15 +35,16 @@ constexpr int TP = 32;                   // positions a warp takes at a time
 constexpr int UNIT = TP * DW;            // positions a CTA takes at a time
 constexpr int STAGES = 2;                // stages per warp: one in use, one being copied
 
-template <int HD>
+template <int HD, int TERMS, int NR>
 struct DGeo {
+    static constexpr int ROWS = 8 * NR;
     static constexpr int ROWB = HD / 2, SB = HD / 16;          // bytes of codes and scales of a position
     static constexpr int KC = 0, VC = TP * ROWB, KS = 2 * TP * ROWB, VS = KS + TP * SB;
     static constexpr int STAGE = VS + TP * SB;
     static constexpr int RING = DW * STAGES * STAGE;
-    static constexpr int OLD = HD + 16;                        // row of the join buffer: 4 floats of padding a quarter
-    static constexpr int QF = HD * 32;                         // q fragments
-    static constexpr int PART = 8 * HD + 16;                   // floats of an item's part: o, m, l
+    static constexpr int OBLK = HD / 8 + 4, OLD = 8 * OBLK + 4;  // join buffer: eight runs of a row, padded apart
+    static constexpr int QF = HD * 16 * TERMS * NR;            // q fragments
+    static constexpr int PART = ROWS * (HD + 2);               // floats of an item's part: o, m, l
     static constexpr size_t smem(int n_seqs) { return (size_t)RING + QF + 8 * ((size_t)n_seqs + 1); }
     static_assert(DW * 8 * OLD * 4 <= RING, "the join buffer reuses the ring");
 };
@@ -60,15 +61,25 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// column c of eight <-> position of eight: 0 4 1 5 2 6 3 7
-__device__ __forceinline__ int pos_of_col(int c) { return (c >> 1) + 4 * (c & 1); }
-__device__ __forceinline__ int col_of_pos(int p) { return 2 * (p & 3) + (p >> 2); }
+// transposes an 8 x 8 matrix of halves held as (row lane/4, columns 2 (lane%4), +1)
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// keeps a rarely taken branch a branch, where selects would run every time
+__device__ __forceinline__ void apart() { asm volatile(""); }
+
+// operand row c of eight <-> position of eight: 0 4 1 5 2 6 3 7
+__device__ __forceinline__ int pos_of_row(int c) { return (c >> 1) + 4 * (c & 1); }
+__device__ __forceinline__ int row_of_pos(int p) { return 2 * (p & 3) + (p >> 2); }
 
 // One stage: 32 positions of one kv head, 16 at a time; row: index of the first of the
-// 16 positions in the cache (negative: not copied).  K rows lie in column order.
+// 16 positions in the cache (negative: not copied).  K lies in the order of operand rows.
 template <int HD>
 __device__ __forceinline__ void copy_stage(uint8_t* st, const Kv4Cache& c, const int64_t (&row)[2], int lane) {
-    using G = DGeo<HD>;
+    using G = DGeo<HD, 1, 1>;
     constexpr int CH = HD / 32;                        // 16-byte chunks of a position's codes
     constexpr int PP = 32 / CH;                        // positions a warp's 32 chunks cover
 #pragma unroll
@@ -79,7 +90,7 @@ __device__ __forceinline__ void copy_stage(uint8_t* st, const Kv4Cache& c, const
 #pragma unroll
         for (int it = 0; it < 16 / PP; ++it) {
             const int p = it * PP + lane / CH, ch = lane % CH;
-            const int kr = sub * 16 + (p & 8) + col_of_pos(p & 7), vr = sub * 16 + p;
+            const int kr = sub * 16 + (p & 8) + row_of_pos(p & 7), vr = sub * 16 + p;
             const int kch = HD == 256 ? ch ^ (4 * (kr & 1)) : ch;
             const int vch = HD == 256 ? ch ^ (2 * (p & 3)) : HD == 128 ? ch ^ (p & 2) : ch;
             cp_async_cg16(st + G::KC + kr * G::ROWB + kch * 16, kc + it * 512);
@@ -98,19 +109,19 @@ __device__ __forceinline__ void copy_stage(uint8_t* st, const Kv4Cache& c, const
 __device__ __forceinline__ long long unit_begin(long long w, int c, int g) { return w * c / g; }
 __device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) { return (int)(((x + 1) * g - 1) / w); }
 
-template <int HD>
+template <int HD, int TERMS, int NR>
 __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, float* __restrict__ parts, unsigned* __restrict__ arrive) {
-    using G = DGeo<HD>;
+    using G = DGeo<HD, TERMS, NR>;
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t* ring = sm;
-    uint32_t* qf = reinterpret_cast<uint32_t*>(sm + G::RING);                       // [HD/16][32 lanes][4]
+    uint32_t* qf = reinterpret_cast<uint32_t*>(sm + G::RING);                       // q fragments
     long long* pre = reinterpret_cast<long long*>(sm + G::RING + G::QF);            // [n_seqs+1]
     __shared__ long long wsum[DW];
-    __shared__ float fac_s[8], m_s[DW][8], l_s[DW][8];
+    __shared__ float fac_s[G::ROWS], m_s[DW][8], l_s[DW][8];
     __shared__ int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int r = lane >> 2, j = lane & 3;             // row (and K column), quarter of a row
+    const int r = lane >> 2, j = lane & 3;             // operand row (position, element run); a pair of q rows
     const int group = a.s.nq / a.s.nkv;
     pdl_wait();
     pdl_launch_dependents();
@@ -123,7 +134,8 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             Kv4Seq q;
             if (!kv4_seq(a, s, q) && blockIdx.x == 0) atomicExch(a.status, ST_DEVICE_CHECK);
             pre[s] = run;
-            if (q.n * group <= few_rows) run += (long long)a.s.nkv * ((q.n * group + 7) / 8) * (q.len ? (q.len + UNIT - 1) / UNIT : 1);
+            if (q.n * group <= few_rows)
+                run += (long long)a.s.nkv * ((q.n * group + G::ROWS - 1) / G::ROWS) * (q.len ? (q.len + UNIT - 1) / UNIT : 1);
         }
         long long inc = run;
 #pragma unroll
@@ -145,7 +157,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     const long long u_end = unit_begin(W, me + 1, Gn);
 
     for (long long u = unit_begin(W, me, Gn); u < u_end;) {
-        // the item that unit u belongs to: sequence, kv head, eight rows
+        // the item that unit u belongs to: sequence, kv head, rows
         int s = 0;
         for (int hi = a.n_seqs; hi - s > 1;) {
             const int mid = (s + hi) >> 1;
@@ -155,12 +167,12 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         Kv4Seq q;
         kv4_seq(a, s, q);
         const int tiles = q.len ? (q.len + UNIT - 1) / UNIT : 1;
-        const int rts = (q.n * group + 7) / 8;
+        const int rts = (q.n * group + G::ROWS - 1) / G::ROWS;
         const long long off = u - pre[s];
         const int item = (int)(off / tiles), t0 = (int)(off - (long long)item * tiles);
-        const int g = item / rts, row0 = (item - g * rts) * 8;
+        const int g = item / rts, row0 = (item - g * rts) * G::ROWS;
         const int t1 = (int)min((long long)tiles, t0 + (u_end - u));
-        const int rows = min(8, q.n * group - row0);
+        const int rows = min(G::ROWS, q.n * group - row0);
         const int32_t* table = a.table + (size_t)s * a.s.width;
         const float kg = a.c.kg[g], vg = a.c.vg[g];
 
@@ -198,41 +210,67 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         load_pages(t0);
         int use = issue(t0);
 
-        // q: warp w takes row w, scaled to [1, 2) by a power of two, as two fp16 terms
-        {
-            const int tok = (row0 + warp) / group, h = g * group + (row0 + warp) - tok * group;
+        // q: warp w takes the rows w, w + 8, scaled to [1, 2) by a power of two
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            const int row = nr * 8 + warp;
+            const int tok = (row0 + row) / group, h = g * group + (row0 + row) - tok * group;
             float2 v[HD / 64];
             float big = 0.f;
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
-                v[i] = warp < rows ? kv4_load2(a.q, (size_t)(q.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
-                                   : make_float2(0.f, 0.f);
+                v[i] = row < rows ? kv4_load2(a.q, (size_t)(q.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
+                                  : make_float2(0.f, 0.f);
                 big = fmaxf(big, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
             }
 #pragma unroll
             for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             const int e = kv4_exponent(big);
-            if (lane == 0) fac_s[warp] = ldexpf(a.scale * 1.4426950408889634f * kg, e);
+            const float fac = ldexpf(a.scale * 1.4426950408889634f * kg, e);
+            const float sign = fac < 0.f ? -1.f : 1.f;              // z's largest is q.k's largest then
+            if (lane == 0) fac_s[row] = fmaxf(fabsf(fac), 1e-38f);  // not 0: -inf stays -inf, and 1e-38 q.k is 0
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
+                uint32_t hi, lo;
+                kv4_split(ldexpf(v[i].x, -e) * sign, ldexpf(v[i].y, -e) * sign, hi, lo);
+                // element d -> lane jj's wd-th; fragment: step wd / 4, register (wd / 2) % 2.
+                // A lane's 16 bytes: TERMS = 1 two steps, TERMS = 2 the two terms of one.
                 const int d = 2 * lane + 64 * i;
                 const int jj = HD == 256 ? (d >> 5) & 3 : d / (HD / 4);
                 const int wd = HD == 256 ? (d & 31) + 32 * (d >> 7) : d & (HD / 4 - 1);
-                uint32_t* f = qf + ((wd >> 2) * 32 + warp * 4 + jj) * 4 + (wd & 2);
-                kv4_split(ldexpf(v[i].x, -e), ldexpf(v[i].y, -e), f[0], f[1]);
+                const int step = wd >> 2, b = (wd >> 1) & 1, at = warp * 4 + jj;
+                if (TERMS == 1) {
+                    qf[((nr * (HD / 32) + (step >> 1)) * 32 + at) * 4 + (step & 1) * 2 + b] = hi;
+                } else {
+                    qf[((nr * (HD / 16) + step) * 32 + at) * 4 + b] = hi;
+                    qf[((nr * (HD / 16) + step) * 32 + at) * 4 + 2 + b] = lo;
+                }
             }
         }
         __syncthreads();
 
-        const float fac = fac_s[r];
-        const int lim = r < rows ? q.len - q.n + (row0 + r) / group + 1 : 0;   // positions this row sees
+        // this lane's rows: 2 j and 2 j + 1 of each eight
+        float fac[NR][2], m[NR][2], l[NR][2], base[NR][2];
+        int lim[NR][2];                                // positions they see
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const int row = nr * 8 + 2 * j + y;
+                fac[nr][y] = fac_s[row];
+                lim[nr][y] = row < rows ? q.len - q.n + (row0 + row) / group + 1 : 0;
+                m[nr][y] = -INFINITY;
+                base[nr][y] = 0.f;
+                l[nr][y] = 0.f;
+            }
         const int lim_min = q.len - q.n + row0 / group + 1;
-        float m = -INFINITY, l = 0.f;
-        float o[HD / 8][4];
+        float o[NR][HD / 16][4];
 #pragma unroll
-        for (int t = 0; t < HD / 8; ++t)
+        for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+            for (int t = 0; t < HD / 16; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[nr][t][i] = 0.f;
 
         for (int t = t0; t < t1; ++t) {
             const int cur = use;
@@ -246,20 +284,22 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             if (cur) {
                 const uint8_t* st = myring + (t & 1) * G::STAGE;
                 const int pos = t * UNIT + warp * TP;
-                // S: columns = positions, four tiles of eight
-                float z[4][4];
+                // S^T: two tiles of 16 positions; lane: positions r, r + 8 of each, rows 2 j, 2 j + 1
+                float z[2][NR][4];
 #pragma unroll
-                for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z[n][i] = 0.f;
+                    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int hh = 0; hh < (HD == 256 ? 2 : 1); ++hh) {       // 256: the two halves of a row in turn
-                    constexpr int KW = HD == 64 ? 2 : 4;                 // words of codes a lane has of a row
+                        for (int i = 0; i < 4; ++i) z[n][nr][i] = 0.f;
+#pragma unroll
+                for (int hh = 0; hh < (HD == 256 ? 2 : 1); ++hh) {       // 256: the two halves of a position in turn
+                    constexpr int KW = HD == 64 ? 2 : 4;                 // words of codes a lane has of a position
                     uint32_t kw[4][4];
                     __half2 ks[4];                                       // their one or two scales
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
-                        const int row = n * 8 + r, p = n * 8 + pos_of_col(r);
+                        const int row = n * 8 + r, p = n * 8 + pos_of_row(r);
                         if (HD == 64) {
                             const uint2 x = *reinterpret_cast<const uint2*>(st + G::KC + row * G::ROWB + j * 8);
                             kw[n][0] = x.x;
@@ -277,55 +317,109 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                     }
 #pragma unroll
                     for (int w = 0; w < KW; ++w) {                       // a word is two steps of the product
-                        const uint4* qp = reinterpret_cast<const uint4*>(qf) + (hh * 2 * KW + 2 * w) * 32 + lane;
-                        const uint4 qa = qp[0], qb = qp[32];
-                        const uint32_t fa[4] = {qa.x, qa.y, qa.z, qa.w}, fb[4] = {qb.x, qb.y, qb.z, qb.w};
+                        uint32_t ka[2][2][4];                            // [tile][step]: operand registers
 #pragma unroll
                         for (int n = 0; n < 4; ++n) {
                             const __half2 sc = w & 2 ? __high2half2(ks[n]) : __low2half2(ks[n]);
                             __half2 k[4];
                             kv4_widen8(kw[n][w], k);
-                            mma_f16(z[n], fa, kv4_u(__hmul2(k[0], sc)), kv4_u(__hmul2(k[1], sc)));
-                            mma_f16(z[n], fb, kv4_u(__hmul2(k[2], sc)), kv4_u(__hmul2(k[3], sc)));
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) ka[n >> 1][b >> 1][2 * (b & 1) + (n & 1)] = kv4_u(__hmul2(k[b], sc));
+                        }
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) {
+                            const uint4* qp = reinterpret_cast<const uint4*>(qf) +
+                                              (nr * (HD / 32) * TERMS + (hh * KW + w) * TERMS) * 32 + lane;
+                            if (TERMS == 1) {
+                                const uint4 x = qp[0];
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    mma_f16(z[n][nr], ka[n][0], x.x, x.y);
+                                    mma_f16(z[n][nr], ka[n][1], x.z, x.w);
+                                }
+                            } else {
+                                const uint4 x = qp[0], y = qp[32];
+#pragma unroll
+                                for (int n = 0; n < 2; ++n) {
+                                    mma_f16(z[n][nr], ka[n][0], x.z, x.w);
+                                    mma_f16(z[n][nr], ka[n][0], x.x, x.y);
+                                    mma_f16(z[n][nr], ka[n][1], y.z, y.w);
+                                    mma_f16(z[n][nr], ka[n][1], y.x, y.y);
+                                }
+                            }
                         }
                     }
                 }
-                // z of this lane's row: hi + lo, columns 2 j and 2 j + 1 of each tile
                 const bool edge = cur != 3 || pos + TP > lim_min;
-                float mx = -INFINITY;
+                if (edge) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    z[n][0] = (z[n][0] + z[n][2]) * fac;
-                    z[n][1] = (z[n][1] + z[n][3]) * fac;
-                    if (edge) {
-                        const int p = pos + n * 8 + j;
-                        const bool in = (cur >> (n >> 1)) & 1;
-                        if (!in || p >= lim) z[n][0] = -INFINITY;
-                        if (!in || p + 4 >= lim) z[n][1] = -INFINITY;
+                    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                if (!((cur >> (n >> 1)) & 1) || pos + n * 8 + pos_of_row(r) >= lim[nr][y])
+                                    z[n >> 1][nr][2 * (n & 1) + y] = -INFINITY;
+                    apart();
+                }
+                // m follows a row's maximum only when some lane saw it 2^SLACK ahead
+                bool ahead = false;
+                float mx[NR][2];
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        float x = -INFINITY;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) {
+                            x = fmaxf(x, z[n >> 1][nr][2 * (n & 1) + y]);
+                        }
+                        mx[nr][y] = x * fac[nr][y];
+                        ahead |= mx[nr][y] > m[nr][y] + KV4_P_SLACK;
                     }
-                    mx = fmaxf(mx, fmaxf(z[n][0], z[n][1]));
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                if (__any_sync(0xffffffffu, mx > m + KV4_P_SLACK)) {
-                    const float mn = fmaxf(m, mx);
-                    const float c = m == -INFINITY ? 0.f : kv4_ex2(m - mn);
-                    l *= c;
+                if (__any_sync(0xffffffffu, ahead)) {
 #pragma unroll
-                    for (int t2 = 0; t2 < HD / 8; ++t2)
+                    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) o[t2][i] *= c;
-                    m = mn;
-                }
-                const float base = m == -INFINITY ? 0.f : m - KV4_P_UP;
-                uint32_t pf[2][4];
+                        for (int y = 0; y < 2; ++y) {
+                            float x = mx[nr][y];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float p0 = kv4_ex2(z[n][0] - base), p1 = kv4_ex2(z[n][1] - base);
-                    l += p0 + p1;
-                    kv4_split(p0, p1, pf[n >> 1][2 * (n & 1)], pf[n >> 1][2 * (n & 1) + 1]);
+                            for (int d = 4; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+                            const float mn = fmaxf(m[nr][y], x);
+                            const float c = m[nr][y] == -INFINITY ? 0.f : kv4_ex2(m[nr][y] - mn);
+                            m[nr][y] = mn;
+                            base[nr][y] = mn == -INFINITY ? 0.f : mn - KV4_P_UP;
+                            l[nr][y] *= c;
+#pragma unroll
+                            for (int t2 = 0; t2 < HD / 16; ++t2) {
+                                o[nr][t2][y] *= c;
+                                o[nr][t2][2 + y] *= c;
+                            }
+                        }
                 }
-                // o += p v, 16 positions at a time; column r holds the HD/8 elements from r * HD/8
+                // P^T as the eight-column operand: rows 2 j, 2 j + 1 of a position, transposed
+                uint32_t pf[2][NR][TERMS][2];
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        float p[2];
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const float zz = z[n >> 1][nr][2 * (n & 1) + y];
+                            p[y] = kv4_ex2(fmaf(zz, fac[nr][y], -base[nr][y]));
+                            l[nr][y] += p[y];
+                        }
+                        if (TERMS == 1) {
+                            pf[n >> 1][nr][0][n & 1] = transpose8(kv4_pack(p[0], p[1]));
+                        } else {
+                            uint32_t hi, lo;
+                            kv4_split(p[0], p[1], hi, lo);
+                            pf[n >> 1][nr][0][n & 1] = transpose8(hi);
+                            pf[n >> 1][nr][TERMS - 1][n & 1] = transpose8(lo);
+                        }
+                    }
+                // O^T += V^T P^T, 16 positions at a time; operand row r holds the HD/8 elements from r * HD/8
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub) {
                     constexpr int VW = HD / 64;                          // words of codes a lane has of a position
@@ -351,8 +445,13 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                             vw[i][3] = x.w;
                             vs[i] = *reinterpret_cast<const uint16_t*>(sr + 2 * r);
                         }
+                    }
+                    if (edge) {
                         // behind the last position the bytes may decode to NaN, which weight 0 would keep
-                        if (edge && (!((cur >> sub) & 1) || pos + sub * 16 + p >= q.len)) vs[i] = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!((cur >> sub) & 1) || pos + sub * 16 + 4 * i + j >= q.len) vs[i] = 0;
+                        apart();
                     }
 #pragma unroll
                     for (int w = 0; w < VW; ++w) {
@@ -362,14 +461,21 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                         uint32_t pa[2], pb[2];                           // even elements, odd elements
                         kv4_pair(vw[0][w], vw[1][w], pa[0], pa[1]);
                         kv4_pair(vw[2][w], vw[3][w], pb[0], pb[1]);
+                        __half2 va[2][4], vb[2][4];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            __half2 va[4], vb[4];
-                            kv4_widen8(pa[e], va);
-                            kv4_widen8(pb[e], vb);
+                            kv4_widen8(pa[e], va[e]);
+                            kv4_widen8(pb[e], vb[e]);
+                        }
 #pragma unroll
-                            for (int b = 0; b < 4; ++b)
-                                mma_f16(o[8 * w + 2 * b + e], pf[sub], kv4_u(__hmul2(va[b], sa)), kv4_u(__hmul2(vb[b], sb)));
+                        for (int b = 0; b < 4; ++b) {                    // elements 8 w + 2 b, 8 w + 2 b + 1
+                            const uint32_t av[4] = {kv4_u(__hmul2(va[0][b], sa)), kv4_u(__hmul2(va[1][b], sa)),
+                                                    kv4_u(__hmul2(vb[0][b], sb)), kv4_u(__hmul2(vb[1][b], sb))};
+#pragma unroll
+                            for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                                for (int tm = TERMS - 1; tm >= 0; --tm)
+                                    mma_f16(o[nr][4 * w + b], av, pf[sub][nr][tm][0], pf[sub][nr][tm][1]);
                         }
                     }
                 }
@@ -377,36 +483,21 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             __syncwarp();
         }
 
-        // join the warps
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        __syncthreads();                               // every warp is done with its ring and q
-        float* ob = reinterpret_cast<float*>(ring);    // [warp][row][OLD]
-        {
-            float* w = ob + (warp * 8 + r) * G::OLD + j * (HD / 4 + 4);
-#pragma unroll
-            for (int t = 0; t < HD / 8; t += 4) {
-                *reinterpret_cast<float4*>(w + t) = make_float4(o[t][0] + o[t][2], o[t + 1][0] + o[t + 1][2],
-                                                                o[t + 2][0] + o[t + 2][2], o[t + 3][0] + o[t + 3][2]);
-                *reinterpret_cast<float4*>(w + HD / 8 + t) =
-                    make_float4(o[t][1] + o[t][3], o[t + 1][1] + o[t + 1][3], o[t + 2][1] + o[t + 2][3],
-                                o[t + 3][1] + o[t + 3][3]);
-            }
-            if (j == 0) {
-                m_s[warp][r] = m;
-                l_s[warp][r] = l;
-            }
-        }
-        __syncthreads();
-        // warp -> row, lane -> HD/32 elements
-        constexpr int PT = HD / 32;
+        // join the warps, eight rows at a time
+        constexpr int PT = HD / 32;                    // elements of a lane then; warp -> row
         const int d0 = lane * PT;
+        const bool whole = t0 == 0 && t1 == tiles;
+        float* ob = reinterpret_cast<float*>(ring);    // [warp][row][OLD]
+        const long long i0 = u - t0;
+        const int c0 = cta_of_unit(W, i0, Gn), c1 = cta_of_unit(W, i0 + tiles - 1, Gn);
+        float* part = parts + (size_t)(2 * me + (me == c0)) * G::PART;
         float2 acc[PT / 2];
-        float mj = -INFINITY, lj = 0.f;
+        float mj, lj;
+        auto clear = [&]() {
+            lj = 0.f;
 #pragma unroll
-        for (int w = 0; w < DW; ++w) mj = fmaxf(mj, m_s[w][warp]);
-#pragma unroll
-        for (int i = 0; i < PT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+            for (int i = 0; i < PT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+        };
         auto add = [&](float mw, float lw, const float* x, bool shared) {
             const float c = lw == 0.f ? 0.f : kv4_ex2(mw - mj);
             lj += lw * c;
@@ -417,47 +508,9 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 acc[i].y += y.y * c;
             }
         };
-#pragma unroll
-        for (int w = 0; w < DW; ++w)
-            add(m_s[w][warp], l_s[w][warp], ob + (w * 8 + warp) * G::OLD + d0 + 4 * (d0 / (HD / 4)), true);
-        bool write = true;
-        if (t0 != 0 || t1 != tiles) {
-            // a part of the item: its CTAs leave their parts in the workspace, the last one joins them
-            const long long i0 = u - t0, i1 = i0 + tiles;
-            const int c0 = cta_of_unit(W, i0, Gn), c1 = cta_of_unit(W, i1 - 1, Gn);
-            float* part = parts + (size_t)(2 * me + (me == c0)) * G::PART;
-#pragma unroll
-            for (int i = 0; i < PT / 2; ++i) reinterpret_cast<float2*>(part + warp * HD + d0)[i] = acc[i];
-            if (lane == 0) {
-                part[8 * HD + warp] = mj;
-                part[8 * HD + 8 + warp] = lj;
-            }
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) last_s = atomicAdd(arrive + c0, 1u) == (unsigned)(c1 - c0);
-            __syncthreads();
-            write = last_s;
-            if (write) {
-                __threadfence();
-                if (tid == 0) arrive[c0] = 0u;
-                const int ns = c1 - c0 + 1;
-                auto part_of = [&](int i) { return parts + (size_t)(2 * (c0 + i) + (i == 0)) * G::PART; };
-                mj = -INFINITY;
-                for (int i = lane; i < ns; i += 32) mj = fmaxf(mj, __ldcg(part_of(i) + 8 * HD + warp));
-#pragma unroll
-                for (int x = 16; x; x >>= 1) mj = fmaxf(mj, __shfl_xor_sync(0xffffffffu, mj, x));
-                lj = 0.f;
-#pragma unroll
-                for (int i = 0; i < PT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-#pragma unroll 8
-                for (int i = 0; i < ns; ++i) {
-                    const float* p = part_of(i);
-                    add(__ldcg(p + 8 * HD + warp), __ldcg(p + 8 * HD + 8 + warp), p + warp * HD + d0, false);
-                }
-            }
-        }
-        if (write && warp < rows) {
-            const int tok = (row0 + warp) / group, h = g * group + (row0 + warp) - tok * group;
+        auto write = [&](int row) {
+            if (row >= rows) return;
+            const int tok = (row0 + row) / group, h = g * group + (row0 + row) - tok * group;
             const float inv = lj == 0.f ? 0.f : vg / lj;
             const size_t at = (size_t)(q.q0 + tok) * a.out_stride + (size_t)h * HD + d0;
 #pragma unroll
@@ -465,31 +518,102 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             if (a.lse && lane == 0)
                 a.lse[(size_t)(q.q0 + tok) * a.s.nq + h] =
                     lj == 0.f ? -INFINITY : (mj - KV4_P_UP + log2f(lj)) * 0.6931471805599453f;
+        };
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            __syncthreads();                           // the ring, q, or the last eight rows' join are done with
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[nr][y] += __shfl_xor_sync(0xffffffffu, l[nr][y], d);
+                float* w = ob + (warp * 8 + 2 * j + y) * G::OLD + r * G::OBLK;
+#pragma unroll
+                for (int t = 0; t < HD / 16; t += 2)
+                    *reinterpret_cast<float4*>(w + 2 * t) =
+                        make_float4(o[nr][t][y], o[nr][t][2 + y], o[nr][t + 1][y], o[nr][t + 1][2 + y]);
+                if (r == 0) {
+                    m_s[warp][2 * j + y] = m[nr][y];
+                    l_s[warp][2 * j + y] = l[nr][y];
+                }
+            }
+            __syncthreads();
+            mj = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < DW; ++w) mj = fmaxf(mj, m_s[w][warp]);
+            clear();
+#pragma unroll
+            for (int w = 0; w < DW; ++w)
+                add(m_s[w][warp], l_s[w][warp], ob + (w * 8 + warp) * G::OLD + (d0 / (HD / 8)) * G::OBLK + d0 % (HD / 8), true);
+            const int row = nr * 8 + warp;
+            if (whole) {
+                write(row);
+            } else {
+                // a part of the item: its CTAs leave their parts in the workspace, the last one joins them
+#pragma unroll
+                for (int i = 0; i < PT / 2; ++i) reinterpret_cast<float2*>(part + row * HD + d0)[i] = acc[i];
+                if (lane == 0) {
+                    part[G::ROWS * HD + row] = mj;
+                    part[G::ROWS * HD + G::ROWS + row] = lj;
+                }
+            }
+        }
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) last_s = atomicAdd(arrive + c0, 1u) == (unsigned)(c1 - c0);
+            __syncthreads();
+            if (last_s) {
+                __threadfence();
+                if (tid == 0) arrive[c0] = 0u;
+                const int ns = c1 - c0 + 1;
+                auto part_of = [&](int i) { return parts + (size_t)(2 * (c0 + i) + (i == 0)) * G::PART; };
+                for (int row = warp; row < rows; row += DW) {
+                    mj = -INFINITY;
+                    for (int i = lane; i < ns; i += 32) mj = fmaxf(mj, __ldcg(part_of(i) + G::ROWS * HD + row));
+#pragma unroll
+                    for (int x = 16; x; x >>= 1) mj = fmaxf(mj, __shfl_xor_sync(0xffffffffu, mj, x));
+                    clear();
+#pragma unroll 8
+                    for (int i = 0; i < ns; ++i) {
+                        const float* p = part_of(i);
+                        add(__ldcg(p + G::ROWS * HD + row), __ldcg(p + G::ROWS * HD + G::ROWS + row), p + row * HD + d0, false);
+                    }
+                    write(row);
+                }
+            }
         }
         __syncthreads();                               // the join buffer and q are free again
         u += t1 - t0;
     }
 }
 
-template <int HD>
+template <int HD, int TERMS, int NR>
 cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
-    const cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)DGeo<HD>::smem(4096));
+    using G = DGeo<HD, TERMS, NR>;
+    const cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<HD, TERMS, NR>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem(4096));
     if (e != cudaSuccess) return e;
-    return launch_pdl(kv4_decode_kernel<HD>, dim3(w.num_sms * (HD == 256 ? 1 : 2)), dim3(DT), DGeo<HD>::smem(a.n_seqs),
-                      st, a, few_rows, w.parts, w.arrive);
+    return launch_pdl(kv4_decode_kernel<HD, TERMS, NR>, dim3(w.num_sms * (HD == 256 ? 1 : 2)), dim3(DT),
+                      G::smem(a.n_seqs), st, a, few_rows, w.parts, w.arrive);
+}
+
+template <int HD, int TERMS>
+cudaError_t pick_rows(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
+    const bool two = (long long)a.max_new * (a.s.nq / a.s.nkv) > 8;
+    return two ? launch_decode<HD, TERMS, 2>(a, few_rows, w, st) : launch_decode<HD, TERMS, 1>(a, few_rows, w, st);
 }
 
 }  // namespace
 
-// a grid has two CTAs a multiprocessor at most, and each leaves two parts of eight rows at most
-size_t kv4_decode_part_floats(int hd, int num_sms) { return (size_t)4 * num_sms * (8 * hd + 16); }
+// a grid has two CTAs a multiprocessor at most, and each leaves two parts of 16 rows at most
+size_t kv4_decode_part_floats(int hd, int num_sms) { return (size_t)4 * num_sms * 16 * (hd + 2); }
 
 cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
+    const bool two = a.q_t == KV4_F32;
     switch (a.s.hd) {
-        case 64: return launch_decode<64>(a, few_rows, w, st);
-        case 128: return launch_decode<128>(a, few_rows, w, st);
-        default: return launch_decode<256>(a, few_rows, w, st);
+        case 64: return two ? pick_rows<64, 2>(a, few_rows, w, st) : pick_rows<64, 1>(a, few_rows, w, st);
+        case 128: return two ? pick_rows<128, 2>(a, few_rows, w, st) : pick_rows<128, 1>(a, few_rows, w, st);
+        default: return two ? pick_rows<256, 2>(a, few_rows, w, st) : pick_rows<256, 1>(a, few_rows, w, st);
     }
 }
 
