@@ -34,6 +34,7 @@ constexpr int DT = 32 * DW;
 constexpr int TP = 32;                   // positions a warp takes at a time
 constexpr int UNIT = TP * DW;            // positions a CTA takes at a time
 constexpr int STAGES = 2;                // stages per warp: one in use, one being copied
+constexpr int LEAD = 2;                  // what starting and joining an item costs, in units of positions
 
 template <int HD, int TERMS, int NR>
 struct DGeo {
@@ -105,7 +106,9 @@ __device__ __forceinline__ void copy_stage(uint8_t* st, const Kv4Cache& c, const
     }
 }
 
-// CTA c of g takes the units [w c / g, w (c+1) / g) of w; g <= w, so each has one at least
+// An item counts as LEAD units that hold no positions and then its positions' units, so
+// that a CTA with many short items has fewer positions.  CTA c of g takes the units
+// [w c / g, w (c+1) / g) of w; g <= w, so each has one at least.
 __device__ __forceinline__ long long unit_begin(long long w, int c, int g) { return w * c / g; }
 __device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) { return (int)(((x + 1) * g - 1) / w); }
 
@@ -135,7 +138,8 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             if (!kv4_seq(a, s, q) && blockIdx.x == 0) atomicExch(a.status, ST_DEVICE_CHECK);
             pre[s] = run;
             if (q.n * group <= few_rows)
-                run += (long long)a.s.nkv * ((q.n * group + G::ROWS - 1) / G::ROWS) * (q.len ? (q.len + UNIT - 1) / UNIT : 1);
+                run += (long long)a.s.nkv * ((q.n * group + G::ROWS - 1) / G::ROWS) *
+                       (LEAD + (q.len ? (q.len + UNIT - 1) / UNIT : 1));
         }
         long long inc = run;
 #pragma unroll
@@ -168,11 +172,25 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         kv4_seq(a, s, q);
         const int tiles = q.len ? (q.len + UNIT - 1) / UNIT : 1;
         const int rts = (q.n * group + G::ROWS - 1) / G::ROWS;
+        const int vu = LEAD + tiles;
         const long long off = u - pre[s];
-        const int item = (int)(off / tiles), t0 = (int)(off - (long long)item * tiles);
+        const int item = (int)(off / vu), v0 = (int)(off - (long long)item * vu);
         const int g = item / rts, row0 = (item - g * rts) * G::ROWS;
-        const int t1 = (int)min((long long)tiles, t0 + (u_end - u));
+        const int v1 = (int)min((long long)vu, v0 + (u_end - u));
+        const int t0 = max(v0 - LEAD, 0), t1 = v1 - LEAD;
+        const long long i0 = u - v0;                   // the item's first unit
+        u += v1 - v0;
+        if (t1 <= 0) break;                            // the lead alone: the next CTA starts the item
         const int rows = min(G::ROWS, q.n * group - row0);
+        if (q.len == 0) {                              // nothing to see
+            for (int i = tid; i < rows * (HD / 2); i += DT) {
+                const int row = i / (HD / 2), tok = (row0 + row) / group, h = g * group + (row0 + row) - tok * group;
+                kv4_store2(a.out, (size_t)(q.q0 + tok) * a.out_stride + (size_t)h * HD + 2 * (i - row * (HD / 2)), a.out_t,
+                           0.f, 0.f);
+                if (a.lse && i == row * (HD / 2)) a.lse[(size_t)(q.q0 + tok) * a.s.nq + h] = -INFINITY;
+            }
+            continue;
+        }
         const int32_t* table = a.table + (size_t)s * a.s.width;
         const float kg = a.c.kg[g], vg = a.c.vg[g];
 
@@ -488,8 +506,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         const int d0 = lane * PT;
         const bool whole = t0 == 0 && t1 == tiles;
         float* ob = reinterpret_cast<float*>(ring);    // [warp][row][OLD]
-        const long long i0 = u - t0;
-        const int c0 = cta_of_unit(W, i0, Gn), c1 = cta_of_unit(W, i0 + tiles - 1, Gn);
+        const int c0 = cta_of_unit(W, i0 + LEAD, Gn), c1 = cta_of_unit(W, i0 + vu - 1, Gn);
         float* part = parts + (size_t)(2 * me + (me == c0)) * G::PART;
         float2 acc[PT / 2];
         float mj, lj;
@@ -583,7 +600,6 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             }
         }
         __syncthreads();                               // the join buffer and q are free again
-        u += t1 - t0;
     }
 }
 
