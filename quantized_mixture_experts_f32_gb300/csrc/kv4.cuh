@@ -15,6 +15,7 @@ enum : int { KV4_F32 = 0, KV4_F16 = 1, KV4_BF16 = 2 };
 // Geometry of every layer's cache and the table that maps positions to pages.
 struct Kv4Shape {
     int nq, nkv, hd, page, n_pages, width;   // width: columns of the block table
+    int page_log2;
 };
 
 // One layer's cache.  codes [n_pages][nkv][page][hd/2], scales [n_pages][nkv][page][hd/16]

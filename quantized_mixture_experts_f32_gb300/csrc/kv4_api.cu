@@ -89,7 +89,9 @@ int dtype_bytes(int t) { return t == QMOE_F32 ? 4 : 2; }
 
 qmoe::Kv4Shape shape(const qmoe_kv4* h) {
     const qmoe_kv4_config& c = h->cfg;
-    return {c.n_heads, c.n_kv_heads, c.head_dim, c.page_size, c.n_pages, c.max_pages_per_seq};
+    int log2 = 0;
+    while ((1 << log2) < c.page_size) ++log2;
+    return {c.n_heads, c.n_kv_heads, c.head_dim, c.page_size, c.n_pages, c.max_pages_per_seq, log2};
 }
 
 qmoe_status check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c) {

@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         auto load_pages = [&](int t) {
             const int pos = (t + (lane >> 1)) * UNIT + warp * TP + 16 * (lane & 1);
             pid_t = t;
-            pid = t + (lane >> 1) < t1 && pos < q.len ? table[pos / a.s.page] : -1;
+            pid = t + (lane >> 1) < t1 && pos < q.len ? table[pos >> a.s.page_log2] : -1;
         };
         // starts the copies of turn t; returns which of its two halves hold positions
         auto issue = [&](int t) {

@@ -2,18 +2,20 @@
 // tokens (prompt chunks): bound by the two matrix products and the exponentials.
 //
 // An item is (sequence, kv head, 128 NT rows of (token, head of the group)); a CTA
-// walks its visible positions in chunks of KC.  Warps have roles:
-//   softmax  4 warps per 128 rows, a thread to a row (its TMEM lane): z from TMEM,
-//            running maximum m and sum l, p = 2^(z - m) back into TMEM as fp16
-//   K, V     4 warps each: codes from the cache, widened (exactly) to fp16 into
+// walks its visible positions in chunks of KC, and its softmax in steps of 64.  Its
+// warps have roles:
+//   softmax  4 warps per 128 rows, a thread to a row (its TMEM lane): z of a step from
+//            TMEM, running maximum m and sum l, p = 2^(z - m) back into TMEM as fp16
+//   K, V     3 and 4 warps: codes from the cache, widened (exactly) to fp16 into
 //            128B-swizzled K-major tiles, V transposed so that positions are K
 //   MMA      one thread: S = Q K^T and O += P V^T, tcgen05, P read from TMEM
-// With NT = 2 the two 128-row tiles share every widened K and V tile (the widening
-// costs as many issue slots as one tile's softmax) and their softmaxes alternate
-// with their products; with NT = 1 (F32 rows, head_dim 256: shared memory has no
-// room for two) the chunks of one tile alternate over two S buffers.  P overlays the
-// S it came from: the MMA thread issues the next S into it after the product that
-// reads P, and the tensor pipe runs them in that order.
+// With NT = 2 two 128-row tiles share every widened K and V tile (the widening costs
+// as many issue slots as one tile's softmax); with NT = 1 (F32 rows, head_dim 256)
+// shared memory has no room for two.
+// Every tile has two S slots of 64 columns, so the next step's S is there when a step's
+// softmax ends: with one slot a step waited for its own two products, which took
+// longer than its softmax.  P overlays the S it came from; the next S into the slot is
+// issued after the product that reads P and runs after it.
 // O is rescaled only when a row's maximum rose by 2^8 since the last time.
 // F32 rows: q = hi + lo and p = hi + lo, two products each (TERMS = 2).
 // Few items: the chunks of an item are split over CTAs, the last one joins the parts.
@@ -29,29 +31,57 @@ namespace qmoe {
 
 namespace {
 
+constexpr int SC = 64;                                               // positions of a softmax step
+
 template <int HD, int TERMS>
 struct EGeo {
     static constexpr int NT = HD <= 128 && TERMS == 1 ? 2 : 1;       // 128-row tiles
     static constexpr int KC = HD == 256 ? 64 : 128;                  // positions of a chunk
+    static constexpr int SPC = KC / SC;                              // steps of a chunk
     static constexpr int BUF = HD == 256 && TERMS == 2 ? 1 : 2;      // K and V tiles in shared memory
     static constexpr int ROWS = 128 * NT;
-    static constexpr int SOFT = 128 * NT;                            // softmax threads
-    static constexpr int THREADS = SOFT + 256 + 32;
+    static constexpr int SOFT = 128 * NT;                            // softmax threads, then K's, V's and MMA's
+    static constexpr int KTH = 96, VTH = 128, THREADS = SOFT + KTH + VTH + 32;
     static constexpr int QT = 128 * HD * 2, KT = KC * HD * 2;        // bytes of a tile
     static constexpr int Q = 0, K = NT * TERMS * QT, V = K + BUF * KT, BARS = V + BUF * KT;
     static constexpr size_t SMEM = 1024 + BARS + 256;
     static constexpr int LPR = HD / 32;                              // 16-byte runs of a position's codes
-    static constexpr int KP = KC * LPR / 128;                        // runs a K thread widens
-    static constexpr int RPP = 128 / LPR;                            // rows between them
+    static constexpr int RPP = KTH / LPR;                            // positions the K threads take at a time
+    static constexpr int KP = (KC + RPP - 1) / RPP;
     static constexpr int PART = ROWS * (HD + 2);                     // floats of a part
 };
 
-// D[tmem] (+)= A[tmem] * B^T, issued by one thread
-__device__ __forceinline__ void umma_f16_ta(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The MMA warp runs its loop as a whole, so that descriptors and addresses stay in
+// uniform registers; only the instructions themselves are one lane's (`one`).
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+
+// D[tmem] (+)= A[shared] * B^T
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B^T
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+
+// one arrival on the barrier at this shared address once the products issued so far are done
+__device__ __forceinline__ void mma_commit(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(one)
         : "memory");
 }
 
@@ -68,6 +98,30 @@ __device__ __forceinline__ void tmem_ld32(uint32_t t, uint32_t (&r)[32]) {
         : "memory");
 }
 
+// the same without the wait: the values are there after tmem_ld_wait
+__device__ __forceinline__ void tmem_ld32_start(uint32_t t, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
@@ -75,6 +129,32 @@ __device__ __forceinline__ void tmem_st16(uint32_t t, const uint32_t* r) {
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+
+// two fp32 values at a time
+__device__ __forceinline__ unsigned long long pair64(uint32_t x, uint32_t y) {
+    unsigned long long d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(x), "r"(y));
+    return d;
+}
+__device__ __forceinline__ void unpair64(unsigned long long d, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // a wait whose outcome the whole warp shares: what follows is collective
@@ -99,28 +179,16 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     extern __shared__ __align__(1024) uint8_t smraw[];
     uint8_t* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + G::BARS);
+    // by buffer: kfull .. vempty; by tile and slot: sfull .. odone
     uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6, *sfull = bars + 8,
-             *pfull = bars + 10, *odone = bars + 12, *qfull = bars + 14;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 15);
+             *pfull = bars + 12, *odone = bars + 16, *qfull = bars + 20;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
     __shared__ int wsum[G::THREADS / 32];
     __shared__ Piece piece_s;
     __shared__ int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.s.nq / a.s.nkv;
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(kfull + i, 128);
-            mbar_init(kempty + i, 1);
-            mbar_init(vfull + i, 128);
-            mbar_init(vempty + i, 1);
-            mbar_init(sfull + i, 1);
-            mbar_init(pfull + i, 128);
-            mbar_init(odone + i, 1);
-        }
-        mbar_init(qfull, G::SOFT);
-        fence_barrier_init();
-        piece_s.s = -1;
-    }
+    if (tid == 0) piece_s.s = -1;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -183,28 +251,46 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         }
         __syncthreads();
     }
-    const Piece p = piece_s;
+    const Piece& p = piece_s;                          // read where it is used: registers are scarce
     if (p.s < 0) return;
+    const int32_t* table = a.table + (size_t)p.s * a.s.width;
+    const int rows = min(G::ROWS, p.n * group - p.row0);
+    const int nact = (rows + 127) / 128;               // tiles with rows
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(kfull + i, G::KTH);
+            mbar_init(kempty + i, 1);
+            mbar_init(vfull + i, G::VTH);
+            mbar_init(vempty + i, 1);
+        }
+        for (int i = 0; i < 2 * NT; ++i) {
+            mbar_init(sfull + i, 1);
+            mbar_init(pfull + i, 128);
+            mbar_init(odone + i, 1);
+        }
+        mbar_init(qfull, G::SOFT);
+        fence_barrier_init();
+    }
     if (warp == 0) tmem_alloc(tslot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const int32_t* table = a.table + (size_t)p.s * a.s.width;
-    const int rows = min(G::ROWS, p.n * group - p.row0);
-    const int nact = (rows + 127) / 128;
     bool ok = true;
 
     if (warp < 4 * NT) {
         // ----------------------------------------------------------------- softmax
-        const int x = tid >> 7, t = tid & 127;
-        const int row = p.row0 + tid, tok = row / group, h = p.g * group + row - tok * group;
-        const bool live = tid < rows;
-        const int lim = live ? p.len - p.n + tok + 1 : 0;
-        const int lim_min = p.len - p.n + (p.row0 + (tid & ~31)) / group + 1;    // the warp's first row's
-        const size_t qat = (size_t)(p.q0 + tok) * a.q_stride + (size_t)h * HD;
+        const int x = tid >> 7, len = p.len;
+        // this row: token of the sequence, q head
+        auto row_tok = [&]() { return (p.row0 + tid) / group; };
+        auto row_head = [&](int tok) { return p.g * group + p.row0 + tid - tok * group; };
+        const int lim = tid < rows ? len - p.n + row_tok() + 1 : 0;
+        const int lim_min = len - p.n + (p.row0 + (tid & ~31)) / group + 1;      // the warp's first row's
         float fac;
         {
+            const int t = tid & 127, tok = row_tok();
+            const bool live = tid < rows;
+            const size_t qat = (size_t)(p.q0 + tok) * a.q_stride + (size_t)row_head(tok) * HD;
             float big = 0.f;
             if (live)
                 for (int d = 0; d < HD; d += 8) {
@@ -216,8 +302,9 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
             const int e = kv4_exponent(big);
             fac = ldexpf(a.scale * 1.4426950408889634f * a.c.kg[p.g], e);
             const float sign = fac < 0.f ? -1.f : 1.f;             // z's largest is s's largest then
-            fac = fabsf(fac);
+            fac = fmaxf(fabsf(fac), 1e-38f);                       // not 0: -inf stays -inf, and 1e-38 q.k is 0
             uint8_t* qs = sm + G::Q + x * TERMS * G::QT;
+#pragma unroll 1
             for (int d = 0; d < HD; d += 8) {
                 float v[8];
 #pragma unroll
@@ -237,112 +324,104 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         float m = -INFINITY, l = 0.f;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tO = tmem + lanes + 256 + x * HD;
-        // which 16-position runs of a chunk have a page: one bit each
-        auto pages_of = [&](int c) {
-            const int pos = c * KC + 16 * lane;
-            bool good = true;
-            if (lane < KC / 16 && pos < p.len) {
-                const int pg = table[pos / a.s.page];
-                good = pg >= 0 && pg < a.s.n_pages;
-                if (!good) atomicExch(a.status, ST_DEVICE_CHECK);
-            }
-            return __ballot_sync(0xffffffffu, good);
+        const int ns = (p.c1 - p.c0) * G::SPC, first = p.c0 * KC;        // steps, their first position
+        // which 16-position runs of a step have a page: one lane looks each up, a step ahead (at a
+        // position of the sequence in any case: a load without a condition waits for nothing)
+        auto run_page = [&](int step) {
+            return table[min(first + step * SC + 16 * (lane & 3), len - 1) >> a.s.page_log2];
         };
-        if (x < nact) {
-            uint32_t good = p.c0 < p.c1 ? pages_of(p.c0) : 0u;
-            for (int c = p.c0; c < p.c1; ++c) {
-                const int i = c - p.c0;
-                const int slot = NT == 2 ? x : i & 1;
-                const uint32_t par = NT == 2 ? i & 1 : (i >> 1) & 1;
-                const uint32_t tS = tmem + lanes + slot * 128;
-                const bool edge = (c + 1) * KC > lim_min || good != 0xffffffffu;
-                const uint32_t good_c = good;
-                if (c + 1 < p.c1) good = pages_of(c + 1);
-                if (!warp_wait(sfull + slot, par)) {
+        if (x < nact && ns) {
+            int pg = run_page(0);
+            for (int step = 0; step < ns; ++step) {
+                const int slot = step & 1, bar = 2 * x + slot, pos = first + step * SC;
+                const uint32_t tS = tmem + lanes + x * 128 + slot * 64;
+                const bool there = pg >= 0 && pg < a.s.n_pages;
+                const uint32_t good = __ballot_sync(0xffffffffu, there || pos + 16 * (lane & 3) >= len);
+                const bool edge = pos + SC > lim_min || good != 0xffffffffu;
+                if (good != 0xffffffffu && lane == 0) atomicExch(a.status, ST_DEVICE_CHECK);
+                pg = run_page(step + 1);
+                if (!warp_wait(sfull + bar, (step >> 1) & 1)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                auto largest = [&](auto masked) {
-                    float mx = -INFINITY;
+                uint32_t z[SC];
+                tmem_ld32_start(tS, z);
+                tmem_ld32_start(tS + 32, z + 32);
+                tmem_ld_wait();
+                if (edge) {
 #pragma unroll
-                    for (int b = 0; b < KC; b += 32) {
-                        uint32_t s[32];
-                        tmem_ld32(tS + b, s);
+                    for (int k = 0; k < SC; ++k)
+                        if (pos + k >= lim || !((good >> (k >> 4)) & 1)) z[k] = 0xff800000u;
+                    asm volatile("");                  // a branch, not selects that run every time
+                }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const bool see = !masked || (c * KC + b + k < lim && ((good_c >> ((b + k) >> 4)) & 1));
-                            if (see) mx = fmaxf(mx, __uint_as_float(s[k]));
-                        }
-                    }
-                    return mx > -INFINITY ? mx * fac : -INFINITY;
-                };
-                const float mx = edge ? largest(std::true_type{}) : largest(std::false_type{});
+                for (int k = 0; k < SC; k += 8)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        mx4[y] = max3(mx4[y], __uint_as_float(z[k + 2 * y]), __uint_as_float(z[k + 2 * y + 1]));
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
                 if (__any_sync(0xffffffffu, mx > m + KV4_P_SLACK)) {
                     const float mn = fmaxf(m, mx);
                     const float f = m == -INFINITY ? 0.f : kv4_ex2(m - mn);
                     l *= f;
                     m = mn;
-                    if (i) {
-                        if (NT == 1 && !warp_wait(odone + ((i - 1) & 1), ((i - 1) >> 1) & 1)) {
+                    if (step) {
+                        // S of this step came after the product before the last one
+                        if (!warp_wait(odone + (bar ^ 1), ((step - 1) >> 1) & 1)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
-                        for (int d = 0; d < HD; d += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(tO + d, o);
+#pragma unroll 1
+                        for (int d = 0; d < HD; d += 16) {         // small blocks: z stays in its registers
+                            float o[16];
+                            tmem_ld16(tO + d, o);
+                            uint32_t u[16];
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st16(tO + d, o);
-                            tmem_st16(tO + d + 16, o + 16);
+                            for (int k = 0; k < 16; ++k) u[k] = __float_as_uint(o[k] * f);
+                            tmem_st16(tO + d, u);
                         }
-                        tmem_st_wait();
                     }
                 }
                 const float base = m == -INFINITY ? 0.f : m - KV4_P_UP;
-                auto weights = [&](auto masked) {
-                    uint32_t lo_all[TERMS == 2 ? KC / 2 : 1];
+                // p over the z that made it
+                const unsigned long long fac2 = pair64(__float_as_uint(fac), __float_as_uint(fac));
+                const unsigned long long base2 = pair64(__float_as_uint(-base), __float_as_uint(-base));
+                unsigned long long l2[2] = {0ull, 0ull};
+                uint32_t hi[SC / 2], lo[TERMS == 2 ? SC / 2 : 1];
 #pragma unroll
-                    for (int b = 0; b < KC; b += 32) {
-                        uint32_t s[32], hi[16];
-                        tmem_ld32(tS + b, s);
-#pragma unroll
-                        for (int k = 0; k < 32; k += 2) {
-                            float p0 = kv4_ex2(fmaf(__uint_as_float(s[k]), fac, -base));
-                            float p1 = kv4_ex2(fmaf(__uint_as_float(s[k + 1]), fac, -base));
-                            if (masked) {
-                                const int at = c * KC + b + k;
-                                const bool run = (good_c >> ((b + k) >> 4)) & 1;
-                                if (!run || at >= lim) p0 = 0.f;
-                                if (!run || at + 1 >= lim) p1 = 0.f;
-                            }
-                            l += p0 + p1;
-                            if (TERMS == 2) kv4_split(p0, p1, hi[k / 2], lo_all[(b + k) / 2]);
-                            else hi[k / 2] = kv4_pack(p0, p1);
-                        }
-                        tmem_st16(tS + b / 2, hi);
-                    }
-                    if (TERMS == 2) {                  // over columns of S that are all read by now
-#pragma unroll
-                        for (int b = 0; b < KC / 2; b += 16) tmem_st16(tS + KC / 2 + b, lo_all + b);
-                    }
-                };
-                if (edge) weights(std::true_type{});
-                else weights(std::false_type{});
+                for (int k = 0; k < SC; k += 2) {
+                    float p0, p1;
+                    unpair64(fma2(pair64(z[k], z[k + 1]), fac2, base2), p0, p1);
+                    p0 = kv4_ex2(p0);
+                    p1 = kv4_ex2(p1);
+                    l2[(k >> 1) & 1] = add2(l2[(k >> 1) & 1], pair64(__float_as_uint(p0), __float_as_uint(p1)));
+                    if (TERMS == 2) kv4_split(p0, p1, hi[k / 2], lo[k / 2]);
+                    else hi[k / 2] = kv4_pack(p0, p1);
+                    if (k % 32 == 30) tmem_st16(tS + k / 32 * 16, hi + k / 32 * 16);
+                }
+                if (TERMS == 2) tmem_st32(tS + 32, lo);
+                {
+                    float x0, x1, x2, x3;
+                    unpair64(l2[0], x0, x1);
+                    unpair64(l2[1], x2, x3);
+                    l += (x0 + x1) + (x2 + x3);
+                }
                 tmem_st_wait();
                 tc_fence_before();
-                mbar_arrive(pfull + slot);
+                mbar_arrive(pfull + bar);
             }
         }
         // O, joined with the item's other parts where it was split
-        const int nc = p.c1 - p.c0;
-        // S of the last chunk came after the second but last product of its slot, so the phase waited for
+        // S of the last step came after the second but last product of its slot, so the phase waited for
         // here is that barrier's current one or the one just completed
-        const int lc = nc - 1;
-        if (ok && x < nact && nc && !warp_wait(odone + (NT == 2 ? x : lc & 1), (NT == 2 ? lc : lc >> 1) & 1)) ok = false;
+        const int nc = p.c1 - p.c0;
+        if (ok && x < nact && ns && !warp_wait(odone + 2 * x + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) ok = false;
         tc_fence_after();
-        bool write = ok && live;
+        const int tok = row_tok(), h = row_head(tok);
+        bool write = ok && tid < rows;
         const float vg = a.c.vg[p.g];
         const size_t oat = (size_t)(p.q0 + tok) * a.out_stride + (size_t)h * HD;
         if (p.splits == 1) {
@@ -427,52 +506,41 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         if (write && a.lse)
             a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] =
                 l == 0.f ? -INFINITY : (m - KV4_P_UP + log2f(l)) * 0.6931471805599453f;
-    } else if (warp < 4 * NT + 4) {
+    } else if (tid < G::SOFT + G::KTH) {
         // ----------------------------------------------------------------- K
-        const int kt = tid - G::SOFT, jj = kt % G::LPR, r0 = kt / G::LPR;
-        const int rot = G::LPR == 4 ? jj & 2 : G::LPR == 8 ? jj >> 1 : 0;   // quarter-warps store to eight banks groups
-        auto page_ids = [&](int c, int (&id)[G::KP]) {
+        const int wt = tid - G::SOFT;
+        // K: a thread widens KP runs of 32 elements
+        const int jj = wt % G::LPR, r0 = wt / G::LPR;
+        const int rot = G::LPR == 4 ? jj & 2 : G::LPR == 8 ? jj >> 1 : 0;   // a quarter-warp's stores meet every bank once
+        int id[G::KP];
+        uint4 kw[G::KP], kn[G::KP];
+        uint32_t kscale[G::KP], kscale_n[G::KP];
+        auto at_of = [&](int c, int i) { return c * KC + min(i * G::RPP + r0, KC - 1); };
+        auto pages = [&](int c) {
 #pragma unroll
-            for (int i = 0; i < G::KP; ++i) {
-                const int pos = c * KC + i * G::RPP + r0;
-                id[i] = c < p.c1 && pos < p.len ? table[pos / a.s.page] : -1;
-            }
+            for (int i = 0; i < G::KP; ++i) id[i] = table[min(at_of(c, i), p.len - 1) >> a.s.page_log2];
         };
-        auto load = [&](int c, const int (&id)[G::KP], uint4 (&w)[G::KP], uint32_t (&sc)[G::KP]) {
+        auto load = [&](int c) {
 #pragma unroll
             for (int i = 0; i < G::KP; ++i) {
-                w[i] = make_uint4(0, 0, 0, 0);
-                sc[i] = 0;
-                if (id[i] >= 0 && id[i] < a.s.n_pages) {
-                    const int pos = c * KC + i * G::RPP + r0;
+                kn[i] = make_uint4(0, 0, 0, 0);
+                kscale_n[i] = 0;
+                const int pos = at_of(c, i);
+                if (c < p.c1 && pos < p.len && id[i] >= 0 && id[i] < a.s.n_pages) {
                     const size_t at = ((size_t)id[i] * a.s.nkv + p.g) * a.s.page + (pos & (a.s.page - 1));
-                    w[i] = __ldg(reinterpret_cast<const uint4*>(a.c.kc + at * (HD / 2) + jj * 16));
-                    sc[i] = __ldg(reinterpret_cast<const uint16_t*>(a.c.ks + at * (HD / 16) + jj * 2));
+                    kn[i] = __ldg(reinterpret_cast<const uint4*>(a.c.kc + at * (HD / 2) + jj * 16));
+                    kscale_n[i] = __ldg(reinterpret_cast<const uint16_t*>(a.c.ks + at * (HD / 16) + jj * 2));
                 }
             }
         };
-        int id[G::KP];
-        uint4 w[G::KP];
-        uint32_t sc[G::KP];
-        page_ids(p.c0, id);
-        load(p.c0, id, w, sc);
-        page_ids(p.c0 + 1, id);
-        for (int c = p.c0; c < p.c1; ++c) {
-            uint4 wn[G::KP];
-            uint32_t sn[G::KP];
-            load(c + 1, id, wn, sn);
-            page_ids(c + 2, id);
-            const int i0 = c - p.c0, b = i0 % BUF, use = i0 / BUF;
-            if (use && !mbar_wait(kempty + b, (use - 1) & 1)) {
-                ok = false;
-                break;
-            }
+        auto k_store = [&](int b) {
             uint8_t* tile = sm + G::K + b * G::KT + (jj >> 1) * (KC * 128);
 #pragma unroll
             for (int i = 0; i < G::KP; ++i) {
                 const int row = i * G::RPP + r0;
-                const __half2 both = kv4_scale2(sc[i]), s0 = __low2half2(both), s1 = __high2half2(both);
-                uint32_t x0 = w[i].x, x1 = w[i].y, x2 = w[i].z, x3 = w[i].w;
+                if (KC % G::RPP && row >= KC) break;
+                const __half2 both = kv4_scale2(kscale[i]), s0 = __low2half2(both), s1 = __high2half2(both);
+                uint32_t x0 = kw[i].x, x1 = kw[i].y, x2 = kw[i].z, x3 = kw[i].w;
                 if (rot & 2) {
                     const uint32_t y0 = x0, y1 = x1;
                     x0 = x2;
@@ -498,157 +566,174 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                         make_uint4(kv4_u(__hmul2(e[0], s)), kv4_u(__hmul2(e[1], s)), kv4_u(__hmul2(e[2], s)), kv4_u(__hmul2(e[3], s)));
                 }
             }
-            fence_proxy_async();
-            mbar_arrive(kfull + b);
+        };
+        if (p.c0 < p.c1) {
+            pages(p.c0);
+            load(p.c0);
+            pages(p.c0 + 1);
+        }
+        for (int c = p.c0; c < p.c1; ++c) {
 #pragma unroll
             for (int i = 0; i < G::KP; ++i) {
-                w[i] = wn[i];
-                sc[i] = sn[i];
+                kw[i] = kn[i];
+                kscale[i] = kscale_n[i];
             }
+            load(c + 1);
+            pages(c + 2);
+            const int i0 = c - p.c0, b = i0 % BUF, use = i0 / BUF;
+            if (use && !mbar_wait(kempty + b, (use - 1) & 1)) {
+                ok = false;
+                break;
+            }
+            k_store(b);
+            fence_proxy_async();
+            mbar_arrive(kfull + b);
         }
-    } else if (warp < 4 * NT + 8) {
+    } else if (tid < G::SOFT + G::KTH + G::VTH) {
         // ----------------------------------------------------------------- V
-        const int vt = tid - G::SOFT - 128, pg8 = vt & 7, dg = (vt >> 3) % (HD / 16), kb = (vt >> 3) / (HD / 16);
-        const bool work = kb < KC / 64;
-        const int p0 = kb * 64 + pg8 * 8;              // eight positions, sixteen elements of each
-        auto page_id = [&](int c) {
-            const int pos = c * KC + p0;
-            return work && c < p.c1 && pos < p.len ? table[pos / a.s.page] : -1;
-        };
-        auto load = [&](int c, int id, uint2 (&w)[8], uint32_t (&sc)[8]) {
-            const bool there = id >= 0 && id < a.s.n_pages;
-            const int pos = c * KC + p0;
-            const size_t at = there ? ((size_t)id * a.s.nkv + p.g) * a.s.page + (pos & (a.s.page - 1)) : 0;
+        const int wt = tid - G::SOFT - G::KTH;         // eight positions of sixteen elements
+        const int pg8 = wt & 7, dg = (wt >> 3) % (HD / 16), kb = (wt >> 3) / (HD / 16);
+        const bool v_work = kb < KC / 64;
+        const int p0 = kb * 64 + pg8 * 8;
+        int id;
+        uint2 vw[8], vn[8];
+        uint32_t vscale[8], vscale_n[8];
+        auto page = [&](int c) { id = table[min(c * KC + p0, p.len - 1) >> a.s.page_log2]; };
+        auto load = [&](int c) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                vn[i] = make_uint2(0, 0);
+                vscale_n[i] = 0;
+            }
+            const int pos = c * KC + p0;
+            if (v_work && c < p.c1 && pos < p.len && id >= 0 && id < a.s.n_pages) {
+                const size_t at = ((size_t)id * a.s.nkv + p.g) * a.s.page + (pos & (a.s.page - 1));
+                const uint8_t* codes = a.c.vc + at * (HD / 2) + dg * 8;
+                const uint8_t* scales = a.c.vs + at * (HD / 16) + dg;
                 // behind the last position the bytes may decode to NaN, which weight 0 would keep
-                w[i] = make_uint2(0, 0);
-                sc[i] = 0;
-                if (there && pos + i < p.len) {
-                    w[i] = __ldg(reinterpret_cast<const uint2*>(a.c.vc + (at + i) * (HD / 2) + dg * 8));
-                    sc[i] = __ldg(a.c.vs + (at + i) * (HD / 16) + dg);
+                const int there = p.len - pos;
+                if (there >= 8) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        vn[i] = __ldg(reinterpret_cast<const uint2*>(codes + i * (HD / 2)));
+                        vscale_n[i] = __ldg(scales + i * (HD / 16));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (i < there) {
+                            vn[i] = __ldg(reinterpret_cast<const uint2*>(codes + i * (HD / 2)));
+                            vscale_n[i] = __ldg(scales + i * (HD / 16));
+                        }
                 }
             }
         };
-        uint2 w[8];
-        uint32_t sc[8];
-        int id = page_id(p.c0);
-        load(p.c0, id, w, sc);
-        id = page_id(p.c0 + 1);
+        auto v_store = [&](int b) {
+            uint8_t* tile = sm + G::V + b * G::KT + kb * (HD * 128);
+            __half2 s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = kv4_scale2(kv4_bytes(vscale[2 * i], vscale[2 * i + 1]));
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                uint32_t pr[4][2];                     // bytes of one element of two positions: even, odd
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    kv4_pair(y ? vw[2 * i].y : vw[2 * i].x, y ? vw[2 * i + 1].y : vw[2 * i + 1].x, pr[i][0], pr[i][1]);
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) {
+                    __half2 v[4][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kv4_widen8(pr[i][odd], v[i]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(tile + sw128_offset(dg * 16 + y * 8 + 2 * e + odd, pg8 * 8)) =
+                            make_uint4(kv4_u(__hmul2(v[0][e], s[0])), kv4_u(__hmul2(v[1][e], s[1])),
+                                       kv4_u(__hmul2(v[2][e], s[2])), kv4_u(__hmul2(v[3][e], s[3])));
+                }
+            }
+        };
+        if (p.c0 < p.c1) {
+            page(p.c0);
+            load(p.c0);
+            page(p.c0 + 1);
+        }
         for (int c = p.c0; c < p.c1; ++c) {
-            uint2 wn[8];
-            uint32_t sn[8];
-            load(c + 1, id, wn, sn);
-            id = page_id(c + 2);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                vw[i] = vn[i];
+                vscale[i] = vscale_n[i];
+            }
+            load(c + 1);
+            page(c + 2);
             const int i0 = c - p.c0, b = i0 % BUF, use = i0 / BUF;
             if (use && !mbar_wait(vempty + b, (use - 1) & 1)) {
                 ok = false;
                 break;
             }
-            if (work) {
-                uint8_t* tile = sm + G::V + b * G::KT + kb * (HD * 128);
-                __half2 s[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] = kv4_scale2(kv4_bytes(sc[2 * i], sc[2 * i + 1]));
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    uint32_t pr[4][2];                 // bytes of one element of two positions: even, odd
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        kv4_pair(y ? w[2 * i].y : w[2 * i].x, y ? w[2 * i + 1].y : w[2 * i + 1].x, pr[i][0], pr[i][1]);
-#pragma unroll
-                    for (int odd = 0; odd < 2; ++odd) {
-                        __half2 v[4][4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) kv4_widen8(pr[i][odd], v[i]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            *reinterpret_cast<uint4*>(tile + sw128_offset(dg * 16 + y * 8 + 2 * e + odd, pg8 * 8)) =
-                                make_uint4(kv4_u(__hmul2(v[0][e], s[0])), kv4_u(__hmul2(v[1][e], s[1])),
-                                           kv4_u(__hmul2(v[2][e], s[2])), kv4_u(__hmul2(v[3][e], s[3])));
-                    }
-                }
-            }
+            if (v_work) v_store(b);
             fence_proxy_async();
             mbar_arrive(vfull + b);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                w[i] = wn[i];
-                sc[i] = sn[i];
-            }
         }
-    } else if (lane == 0) {
+    } else {
         // ----------------------------------------------------------------- MMA
-        const int nc = p.c1 - p.c0;
-        const uint32_t idS = umma_idesc_f16(128, KC), idO = umma_idesc_f16(128, HD);
-        auto issue_s = [&](int x, int slot, int i) {   // S of tile x, chunk i, into the slot
-            const int b = i % BUF;
-#pragma unroll
-            for (int tm = 0; tm < TERMS; ++tm)
-#pragma unroll
-                for (int ks = 0; ks < HD / 16; ++ks) {
-                    const uint64_t ad = umma_sdesc(smem_u32(sm + G::Q + (x * TERMS + tm) * G::QT + (ks >> 2) * 16384)) + 2 * (ks & 3);
-                    const uint64_t bd = umma_sdesc(smem_u32(sm + G::K + b * G::KT + (ks >> 2) * (KC * 128))) + 2 * (ks & 3);
-                    umma_f16(tmem + slot * 128, ad, bd, idS, tm | ks);
-                }
-            umma_commit(sfull + slot);
-        };
-        auto issue_pv = [&](int x, int slot, int i) {
-            const int b = i % BUF;
-#pragma unroll
-            for (int tm = 0; tm < TERMS; ++tm)
-#pragma unroll
-                for (int ks = 0; ks < KC / 16; ++ks) {
-                    const uint64_t bd = umma_sdesc(smem_u32(sm + G::V + b * G::KT + (ks >> 2) * (HD * 128))) + 2 * (ks & 3);
-                    umma_f16_ta(tmem + 256 + x * HD, tmem + slot * 128 + tm * (KC / 2) + ks * 8, bd, idO, (uint32_t)(i | tm | ks));
-                }
-            umma_commit(odone + slot);
-        };
-        auto wait_k = [&](int i) { return mbar_wait(kfull + i % BUF, (i / BUF) & 1); };
-        ok = mbar_wait(qfull, 0);
-        tc_fence_after();
-        if (NT == 2) {
-            if (ok && nc) ok = wait_k(0);
+        const uint32_t one = elect_one();
+        auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };    // known to be uniform
+        const int ns = (int)same((p.c1 - p.c0) * G::SPC), tiles = (int)same(nact);
+        const uint32_t tm0 = same(tmem), smem0 = same(smem_u32(sm)), bar0 = smem0 + G::BARS;
+        const uint64_t qd = umma_sdesc(smem0 + G::Q), kd = umma_sdesc(smem0 + G::K), vd = umma_sdesc(smem0 + G::V);
+        const uint32_t idS = umma_idesc_f16(128, SC), idO = umma_idesc_f16(128, HD);
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity); };
+        auto k_there = [&](int step) {
+            const int i = step / G::SPC;
+            const bool there = wait(kfull + i % BUF, (i / BUF) & 1);
             tc_fence_after();
-            for (int x = 0; ok && nc && x < nact; ++x) issue_s(x, x, 0);
-            if (ok && nc) umma_commit(kempty);
-            for (int i = 0; ok && i < nc; ++i) {
-                ok = mbar_wait(vfull + i % BUF, (i / BUF) & 1);
-                for (int x = 0; ok && x < nact; ++x) {
-                    ok = mbar_wait(pfull + x, i & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(x, x, i);
-                    if (x == nact - 1) umma_commit(vempty + i % BUF);
-                    if (i + 1 < nc) {
-                        if (x == 0) ok = wait_k(i + 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        issue_s(x, x, i + 1);
-                        if (x == nact - 1) umma_commit(kempty + (i + 1) % BUF);
-                    }
-                }
-            }
-        } else {
-            for (int i = 0; ok && i < nc && i < 2; ++i) {
-                ok = wait_k(i);
+            return there;
+        };
+        // S of a step into its slot; the last one of a chunk frees the buffer.  Descriptors count in
+        // 16 bytes: a 64-wide block of a tile, then 32 bytes a product
+        auto s_of = [&](int x, int step) {
+            const int b = step / G::SPC % BUF, h = step % G::SPC;
+            const uint64_t ad = qd + (uint64_t)(x * TERMS * (G::QT / 16)), bd = kd + (uint64_t)(b * (G::KT / 16) + h * (SC * 8));
+            const uint32_t d = tm0 + x * 128 + (step & 1) * 64;
+#pragma unroll
+            for (int tm = TERMS - 1; tm >= 0; --tm)
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks)
+                    mma_ss(one, d, ad + (tm * (G::QT / 16) + (ks >> 2) * 1024 + 2 * (ks & 3)),
+                           bd + ((ks >> 2) * (KC * 8) + 2 * (ks & 3)), idS, (tm < TERMS - 1) | ks);
+            mma_commit(one, bar0 + 8 * (8 + 2 * x + (step & 1)));
+            if (x == tiles - 1 && h == G::SPC - 1) mma_commit(one, bar0 + 8 * (2 + b));
+        };
+        auto pv_of = [&](int x, int step) {
+            const int b = step / G::SPC % BUF, h = step % G::SPC;
+            const uint64_t bd = vd + (uint64_t)(b * (G::KT / 16) + h * (HD * 8));
+            const uint32_t d = tm0 + 256 + x * HD, ap = tm0 + x * 128 + (step & 1) * 64;
+#pragma unroll
+            for (int tm = TERMS - 1; tm >= 0; --tm)
+#pragma unroll
+                for (int ks = 0; ks < SC / 16; ++ks)
+                    mma_ts(one, d, ap + (tm * (SC / 2) + ks * 8), bd + 2 * ks, idO, (uint32_t)(step | (tm < TERMS - 1) | ks));
+            mma_commit(one, bar0 + 8 * (16 + 2 * x + (step & 1)));
+            if (x == tiles - 1 && h == G::SPC - 1) mma_commit(one, bar0 + 8 * (6 + b));
+        };
+        ok = wait(qfull, 0);
+        tc_fence_after();
+        for (int step = 0; ok && step < 2 && step < ns; ++step) {
+            ok = k_there(step);
+            for (int x = 0; ok && x < tiles; ++x) s_of(x, step);
+        }
+        for (int step = 0; ok && step < ns; ++step) {
+            const int i = step / G::SPC;
+            ok = wait(vfull + i % BUF, (i / BUF) & 1);
+            for (int x = 0; ok && x < tiles; ++x) {
+                ok = wait(pfull + 2 * x + (step & 1), (step >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                issue_s(0, i, i);
-                umma_commit(kempty + i % BUF);
-            }
-            for (int i = 0; ok && i < nc; ++i) {
-                ok = mbar_wait(vfull + i % BUF, (i / BUF) & 1) && mbar_wait(pfull + (i & 1), (i >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                issue_pv(0, i & 1, i);
-                umma_commit(vempty + i % BUF);
-                if (i + 2 < nc) {
-                    ok = wait_k(i + 2);
+                pv_of(x, step);
+                if (step + 2 < ns) {
+                    if (x == 0) ok = k_there(step + 2);
                     if (!ok) break;
-                    tc_fence_after();
-                    issue_s(0, i & 1, i + 2);
-                    umma_commit(kempty + (i + 2) % BUF);
+                    s_of(x, step + 2);
                 }
             }
         }
