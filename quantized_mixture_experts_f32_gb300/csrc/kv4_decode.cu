@@ -244,13 +244,14 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
             for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             const int e = kv4_exponent(big);
+            const Kv4Scale un = kv4_unscale(e);
             const float fac = ldexpf(a.scale * 1.4426950408889634f * kg, e);
-            const float sign = fac < 0.f ? -1.f : 1.f;              // z's largest is q.k's largest then
+            const float sign = fac < 0.f ? -un.b : un.b;            // z's largest is q.k's largest then
             if (lane == 0) fac_s[row] = fmaxf(fabsf(fac), 1e-38f);  // not 0: -inf stays -inf, and 1e-38 q.k is 0
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
                 uint32_t hi, lo;
-                kv4_split(ldexpf(v[i].x, -e) * sign, ldexpf(v[i].y, -e) * sign, hi, lo);
+                kv4_split(v[i].x * un.a * sign, v[i].y * un.a * sign, hi, lo);
                 // element d -> lane jj's wd-th; fragment: step wd / 4, register (wd / 2) % 2.
                 // A lane's 16 bytes: TERMS = 1 two steps, TERMS = 2 the two terms of one.
                 const int d = 2 * lane + 64 * i;
@@ -633,20 +634,25 @@ cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work&
     }
 }
 
-// Rows (new tokens x heads of the group) up to which a sequence is the decode kernel's.
-constexpr int FEW_ROWS = 32;
-
-int kv4_arrive_words(int num_sms) { return 2 * num_sms; }
+int kv4_arrive_words(int num_sms) { return 2 * num_sms; }   // a CTA of the one kernel, a part of the other
 
 size_t kv4_part_floats(int hd, int num_sms) {
     const size_t x = kv4_decode_part_floats(hd, num_sms), y = kv4_extend_part_floats(hd, num_sms);
     return x > y ? x : y;
 }
 
+// Which kernel a sequence's rows (new tokens x heads of the group) go to.  The decode kernel
+// reads and widens the cache once per 16 rows, the prompt kernel once per 256, with a dearer start
+// and end.  Measured, head_dim 128, 4 kv heads, bf16, us (decode / prompt kernel): 16 sequences of
+// 4096 positions, 16 rows 29.6 / 38.5, 24 rows 40.2 / 38.7, 64 rows 64 / 39; 64 of 1024, 16 rows
+// 33.8 / 42.3, 24 rows 49 / 42.  With few sequences the passes of the decode kernel run side by
+// side: 1 of 32768, 40 rows 36.0 / 40.2, 64 rows 39.4 / 40.4, 80 rows 45.6 / 50.2; 1 of 4096, 64
+// rows 19.4 / 26.8.
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st) {
-    const cudaError_t e = launch_kv4_decode(a, FEW_ROWS, w, st);
-    if (e != cudaSuccess || (long long)a.max_new * (a.s.nq / a.s.nkv) <= FEW_ROWS) return e;
-    return launch_kv4_extend(a, FEW_ROWS, w, st);
+    const int few = (long long)a.n_seqs * a.s.nkv * 8 <= w.num_sms ? 64 : 16;
+    const cudaError_t e = launch_kv4_decode(a, few, w, st);
+    if (e != cudaSuccess || (long long)a.max_new * (a.s.nq / a.s.nkv) <= few) return e;
+    return launch_kv4_extend(a, few, w, st);
 }
 
 }  // namespace qmoe

@@ -31,6 +31,7 @@ namespace qmoe {
 
 namespace {
 
+constexpr int EXTEND_PARTS = 2;                                      // parts of split items, a multiprocessor
 constexpr int SC = 64;                                               // positions of a softmax step
 
 template <int HD, int TERMS>
@@ -49,6 +50,7 @@ struct EGeo {
     static constexpr int RPP = KTH / LPR;                            // positions the K threads take at a time
     static constexpr int KP = (KC + RPP - 1) / RPP;
     static constexpr int PART = ROWS * (HD + 2);                     // floats of a part
+    static_assert(33 * ROWS * 4 <= 2 * BUF * KT, "the weights of a join take the buffers of K and V");
 };
 
 // The MMA warp runs its loop as a whole, so that descriptors and addresses stay in
@@ -167,13 +169,14 @@ struct Piece {
     int s, g, row0;          // sequence, kv head, first row
     int q0, n, len;
     int c0, c1;              // chunks
-    int split, splits, item;
+    int split, splits;
+    int part;                // the item's first part in the workspace; its arrival counter
 };
 
 template <int HD, int TERMS>
 __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     kv4_extend_kernel(const Kv4AttnArgs a, int few_rows, float* __restrict__ parts, unsigned* __restrict__ arrive,
-                      int num_sms) {
+                      int num_sms, int max_parts) {
     using G = EGeo<HD, TERMS>;
     constexpr int NT = G::NT, KC = G::KC, BUF = G::BUF;
     extern __shared__ __align__(1024) uint8_t smraw[];
@@ -192,61 +195,99 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    // the items of every sequence with more than few_rows rows; this CTA's piece of them
+    // the items of every sequence with more than few_rows rows, and this CTA's piece of them.  An item's
+    // chunks are split where it has more than the GPU's average share of a multiprocessor.
     {
         constexpr int T = G::THREADS;
         const int per = (a.n_seqs + T - 1) / T, s0 = min(tid * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
-        int run = 0;
-        for (int s = s0; s < s1; ++s) {
+        struct Seq {
             Kv4Seq q;
-            kv4_seq(a, s, q);                          // out of range: no rows (the other kernel reports it)
-            const int rows = q.n * group;
-            if (rows > few_rows) run += a.s.nkv * ((rows + G::ROWS - 1) / G::ROWS);
-        }
-        int inc = run;
+            int rows, qts, last;               // row tiles, chunks of the last of them
+        };
+        auto chunks = [&](const Kv4Seq& q, int row_end) {          // that rows up to row_end see
+            const int end = min(q.len, q.len - q.n + (row_end - 1) / group + 1);
+            return end > 0 ? (end + KC - 1) / KC : 0;
+        };
+        auto seq = [&](int s, Seq& r) {
+            kv4_seq(a, s, r.q);                        // out of range: no rows (the other kernel reports it)
+            r.rows = r.q.n * group;
+            r.qts = r.rows > few_rows ? (r.rows + G::ROWS - 1) / G::ROWS : 0;
+            r.last = r.qts ? chunks(r.q, r.rows) : 0;
+        };
+        auto block_sum = [&](int v, int& before) {     // sum over the CTA, and over the threads before
+            int inc = v;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, inc, d);
-            if (lane >= d) inc += o;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, inc, d);
+                if (lane >= d) inc += o;
+            }
+            __syncthreads();
+            if (lane == 31) wsum[warp] = inc;
+            __syncthreads();
+            int all = 0;
+            before = inc - v;
+            for (int w = 0; w < T / 32; ++w) {
+                if (w < warp) before += wsum[w];
+                all += wsum[w];
+            }
+            return all;
+        };
+        // total chunks, a sequence's tiles taken as evenly spread between its first and last
+        int work = 0, pieces = 0, parts_n = 0, base, part0, unused;
+        for (int s = s0; s < s1; ++s) {
+            Seq r;
+            seq(s, r);
+            if (r.qts) work += min(a.s.nkv * ((r.qts * (r.last + chunks(r.q, min(r.rows, (int)G::ROWS))) + 1) / 2), 1 << 20);
         }
-        if (lane == 31) wsum[warp] = inc;
-        __syncthreads();
-        int base = inc - run, items = 0;
-        for (int w = 0; w < T / 32; ++w) {
-            if (w < warp) base += wsum[w];
-            items += wsum[w];
+        work = block_sum(work, unused);
+        const int share = max(8, (int)(1.25f * (float)work / (float)num_sms) + 1);   // pieces fill one wave
+        auto splits_of = [&](const Seq& r) { return min(32, max(1, (r.last + share - 1) / share)); };
+        for (int s = s0; s < s1; ++s) {
+            Seq r;
+            seq(s, r);
+            const int k = splits_of(r), items = a.s.nkv * r.qts;
+            pieces += items * k;
+            if (k > 1) parts_n += items * k;
         }
-        const int splits = items ? max(1, min(num_sms / items, 32)) : 1;
-        const int item = (int)blockIdx.x / splits, split = (int)blockIdx.x - item * splits;
-        if (item >= base && item < base + run) {
+        const int all = block_sum(pieces, base), all_parts = block_sum(parts_n, part0);
+        // not more CTAs or parts than there are: every item whole then
+        const bool whole = all > (int)gridDim.x || all_parts > max_parts;
+        if (whole) {
+            pieces = 0;
             for (int s = s0; s < s1; ++s) {
-                Kv4Seq q;
-                kv4_seq(a, s, q);
-                const int rows = q.n * group;
-                if (rows <= few_rows) continue;
-                const int qts = (rows + G::ROWS - 1) / G::ROWS, mine = a.s.nkv * qts;
-                if (item < base + mine) {
+                Seq r;
+                seq(s, r);
+                pieces += a.s.nkv * r.qts;
+            }
+            block_sum(pieces, base);
+        }
+        const int me = blockIdx.x;
+        if (me >= base && me < base + pieces) {
+            for (int s = s0; s < s1; ++s) {
+                Seq r;
+                seq(s, r);
+                const int k = whole ? 1 : splits_of(r), mine = a.s.nkv * r.qts * k;
+                if (me < base + mine) {
                     // the last rows see the most positions: they start first
-                    const int x = item - base, qt = qts - 1 - x / a.s.nkv;
+                    const int at = me - base, split = at % k, item = at / k, qt = r.qts - 1 - item / a.s.nkv;
                     Piece p;
                     p.s = s;
-                    p.g = x % a.s.nkv;
+                    p.g = item % a.s.nkv;
                     p.row0 = qt * G::ROWS;
-                    p.q0 = q.q0;
-                    p.n = q.n;
-                    p.len = q.len;
-                    const int last_tok = min(p.row0 + G::ROWS, rows) - 1;
-                    const int end = min(q.len, q.len - q.n + last_tok / group + 1);
-                    const int nch = end > 0 ? (end + KC - 1) / KC : 0;
-                    p.splits = max(1, min(splits, nch / 4));       // four chunks to a split at least
+                    p.q0 = r.q.q0;
+                    p.n = r.q.n;
+                    p.len = r.q.len;
+                    const int nch = chunks(r.q, min(p.row0 + G::ROWS, r.rows));
+                    p.splits = max(1, min(k, nch / 4));            // four chunks to a split at least
                     p.split = split;
                     p.c0 = (int)((long long)nch * split / p.splits);
                     p.c1 = (int)((long long)nch * (split + 1) / p.splits);
-                    p.item = item;
+                    p.part = part0 + item * k;
                     if (split < p.splits) piece_s = p;
                     break;
                 }
                 base += mine;
+                if (k > 1) part0 += mine;
             }
         }
         __syncthreads();
@@ -281,43 +322,78 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     if (warp < 4 * NT) {
         // ----------------------------------------------------------------- softmax
         const int x = tid >> 7, len = p.len;
-        // this row: token of the sequence, q head
-        auto row_tok = [&]() { return (p.row0 + tid) / group; };
-        auto row_head = [&](int tok) { return p.g * group + p.row0 + tid - tok * group; };
-        const int lim = tid < rows ? len - p.n + row_tok() + 1 : 0;
-        const int lim_min = len - p.n + (p.row0 + (tid & ~31)) / group + 1;      // the warp's first row's
+        // token of the sequence and q head of a row of the item
+        auto tok_of = [&](int row) { return (p.row0 + row) / group; };
+        auto head_of = [&](int row, int tok) { return p.g * group + p.row0 + row - tok * group; };
+        const int lim = tid < rows ? len - p.n + tok_of(tid) + 1 : 0;
+        const int lim_min = len - p.n + tok_of(tid & ~31) + 1;                   // the warp's first row's
         float fac;
         {
-            const int t = tid & 127, tok = row_tok();
-            const bool live = tid < rows;
-            const size_t qat = (size_t)(p.q0 + tok) * a.q_stride + (size_t)row_head(tok) * HD;
-            float big = 0.f;
-            if (live)
+            // the warp's 32 rows of q, 16 bytes a lane, copied to where their fp16 terms belong (F32
+            // elements fill the places of both); then each thread scales its own row to [1, 2) by a
+            // power of two and splits it in place
+            constexpr int LR = HD / 8, RW = 32 / LR;   // lanes of a row, rows at a time
+            const float fac0 = a.scale * 1.4426950408889634f * a.c.kg[p.g];
+            uint8_t* qs = sm + G::Q + x * TERMS * G::QT;
+            {
+                const int d = (lane % LR) * 8, sub = lane / LR;
+                long long mine = -1;                   // where this thread's row starts
+                if (tid < rows) {
+                    const int tok = tok_of(tid), h = head_of(tid, tok);
+                    mine = ((long long)(p.q0 + tok) * a.q_stride + (long long)h * HD) * (TERMS == 2 ? 4 : 2);
+                }
+#pragma unroll 4
+                for (int r = 0; r < 32; r += RW) {
+                    const long long at = __shfl_sync(0xffffffffu, mine, r + sub);
+                    uint8_t* to = qs + (d >> 6) * 16384 + sw128_offset((tid & 96) + r + sub, d & 63);
+#pragma unroll
+                    for (int z = 0; z < TERMS; ++z) {
+                        if (at >= 0) cp_async_cg16(to + z * G::QT, static_cast<const uint8_t*>(a.q) + at + d * (TERMS == 2 ? 4 : 2) + 16 * z);
+                        else *reinterpret_cast<uint4*>(to + z * G::QT) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            cp_async_wait_all();
+            __syncwarp();
+            int exponent = 0;
+            auto load_q = [&](int d, float (&v)[8]) {
+                const uint8_t* at = qs + (d >> 6) * 16384 + sw128_offset(tid & 127, d & 63);
+                uint4 raw[TERMS];
+#pragma unroll
+                for (int z = 0; z < TERMS; ++z) raw[z] = *reinterpret_cast<const uint4*>(at + z * G::QT);
+                kv4_floats8(raw, a.q_t, v);
+            };
+            if (TERMS == 2 || a.q_t != KV4_F16) {      // fp16 rows are what they have to be
+                float big[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
                 for (int d = 0; d < HD; d += 8) {
                     float v[8];
-                    kv4_load8(a.q, qat + d, a.q_t, v);
+                    load_q(d, v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) big = fmaxf(big, fabsf(v[i]));
+                    for (int i = 0; i < 4; ++i) big[i] = max3(big[i], fabsf(v[i]), fabsf(v[4 + i]));
                 }
-            const int e = kv4_exponent(big);
-            fac = ldexpf(a.scale * 1.4426950408889634f * a.c.kg[p.g], e);
-            const float sign = fac < 0.f ? -1.f : 1.f;             // z's largest is s's largest then
-            fac = fmaxf(fabsf(fac), 1e-38f);                       // not 0: -inf stays -inf, and 1e-38 q.k is 0
-            uint8_t* qs = sm + G::Q + x * TERMS * G::QT;
-#pragma unroll 1
-            for (int d = 0; d < HD; d += 8) {
-                float v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                if (live) kv4_load8(a.q, qat + d, a.q_t, v);
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    kv4_split(ldexpf(v[2 * i], -e) * sign, ldexpf(v[2 * i + 1], -e) * sign, hi[i], lo[i]);
-                uint8_t* at = qs + (d >> 6) * 16384 + sw128_offset(t, d & 63);
-                *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if (TERMS == 2) *reinterpret_cast<uint4*>(at + G::QT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                exponent = kv4_exponent(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])));
             }
+            if (TERMS == 2 || a.q_t != KV4_F16 || fac0 < 0.f) {
+                const Kv4Scale un = kv4_unscale(exponent);
+                const float ub = fac0 < 0.f ? -un.b : un.b;        // z's largest is q.k's largest then
+#pragma unroll 2
+                for (int d = 0; d < HD; d += 8) {
+                    float v[8];
+                    load_q(d, v);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float v0 = v[2 * i] * un.a * ub, v1 = v[2 * i + 1] * un.a * ub;
+                        if (TERMS == 2) kv4_split(v0, v1, hi[i], lo[i]);
+                        else hi[i] = kv4_pack(v0, v1);
+                    }
+                    uint8_t* at = qs + (d >> 6) * 16384 + sw128_offset(tid & 127, d & 63);
+                    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if (TERMS == 2) *reinterpret_cast<uint4*>(at + G::QT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fac = fmaxf(ldexpf(fabsf(fac0), exponent), 1e-38f);    // not 0: -inf stays -inf, and 1e-38 q.k is 0
             fence_proxy_async();
             mbar_arrive(qfull);
         }
@@ -420,7 +496,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         const int nc = p.c1 - p.c0;
         if (ok && x < nact && ns && !warp_wait(odone + 2 * x + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) ok = false;
         tc_fence_after();
-        const int tok = row_tok(), h = row_head(tok);
+        const int tok = tok_of(tid), h = head_of(tid, tok);
         bool write = ok && tid < rows;
         const float vg = a.c.vg[p.g];
         const size_t oat = (size_t)(p.q0 + tok) * a.out_stride + (size_t)h * HD;
@@ -439,68 +515,94 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
             }
         } else {
             // part: O as float4 [HD/4][ROWS], then m, l [ROWS]
-            float* part = parts + (size_t)blockIdx.x * G::PART;
+            float* part = parts + (size_t)(p.part + p.split) * G::PART;
             for (int d = 0; d < HD && x < nact; d += 32) {
                 uint32_t o[32];
                 tmem_ld32(tO + d, o);
+                if (tid < rows) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                    reinterpret_cast<float4*>(part)[(size_t)((d + k) / 4) * G::ROWS + tid] =
-                        make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
-                                    __uint_as_float(o[k + 3]));
+                    for (int k = 0; k < 32; k += 4)
+                        reinterpret_cast<float4*>(part)[(size_t)((d + k) / 4) * G::ROWS + tid] =
+                            make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
+                                        __uint_as_float(o[k + 3]));
+                }
             }
             part[(size_t)HD * G::ROWS + tid] = m;
             part[(size_t)(HD + 1) * G::ROWS + tid] = l;
             __threadfence();
             named_bar(1, G::SOFT);
-            if (tid == 0) last_s = atomicAdd(arrive + p.item, 1u) == (unsigned)(p.splits - 1);
+            if (tid == 0) last_s = atomicAdd(arrive + p.part, 1u) == (unsigned)(p.splits - 1);
             named_bar(1, G::SOFT);
+            write = false;                             // below
             if (last_s) {
                 __threadfence();
-                if (tid == 0) arrive[p.item] = 0u;
-                const float* first = parts + (size_t)((int)blockIdx.x - p.split) * G::PART;
-                m = -INFINITY;
-                l = 0.f;
-                for (int i = 0; i < p.splits; ++i)
-                    m = fmaxf(m, __ldcg(first + (size_t)i * G::PART + (size_t)HD * G::ROWS + tid));
-                auto weight = [&](int i, float& li) {
-                    const float* pi = first + (size_t)i * G::PART + (size_t)HD * G::ROWS + tid;
-                    li = __ldcg(pi + G::ROWS);
-                    return li == 0.f ? 0.f : kv4_ex2(__ldcg(pi) - m);
-                };
-                for (int i = 0; i < p.splits; ++i) {
-                    float li;
-                    const float w = weight(i, li);
-                    l += li * w;
-                }
-                const float inv = l == 0.f ? 0.f : vg / l;
-                for (int d = 0; d < HD; d += 32) {
-                    float v[32];
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) v[y] = 0.f;
-                    for (int i = 0; i < p.splits; ++i) {
-                        float li;
-                        const float w = weight(i, li);
-                        if (li == 0.f) continue;
-                        const float4* pi = reinterpret_cast<const float4*>(first + (size_t)i * G::PART) +
-                                           (size_t)(d / 4) * G::ROWS + tid;
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) {
-                            const float4 u = __ldcg(pi + (size_t)y * G::ROWS);
-                            v[4 * y] += u.x * w;
-                            v[4 * y + 1] += u.y * w;
-                            v[4 * y + 2] += u.z * w;
-                            v[4 * y + 3] += u.w * w;
-                        }
+                if (tid == 0) arrive[p.part] = 0u;
+                const int splits = p.splits;
+                const float* first_part = parts + (size_t)p.part * G::PART;
+                // weights of the parts by row (the buffers of K and V are free: every product is done), then each
+                // thread four elements of a row at a time
+                float* wt = reinterpret_cast<float*>(sm + G::K);       // [splits][ROWS], 1 / sum at the end
+                if (tid < rows) {
+                    const float* ml = first_part + (size_t)HD * G::ROWS + tid;
+                    float mj = -INFINITY, lj = 0.f;
+#pragma unroll 8
+                    for (int y = 0; y < splits; ++y) mj = fmaxf(mj, __ldcg(ml + (size_t)y * G::PART));
+#pragma unroll 8
+                    for (int y = 0; y < splits; ++y) {
+                        const float li = __ldcg(ml + (size_t)y * G::PART + G::ROWS), mi = __ldcg(ml + (size_t)y * G::PART);
+                        const float w = li == 0.f ? 0.f : kv4_ex2(mi - mj);
+                        lj += li * w;
+                        wt[y * G::ROWS + tid] = w;
                     }
-#pragma unroll
-                    for (int y = 0; y < 32; ++y) v[y] *= inv;
-#pragma unroll
-                    for (int y = 0; y < 32; y += 8)
-                        if (write) kv4_store8(a.out, oat + d + y, a.out_t, v + y);
+                    wt[splits * G::ROWS + tid] = lj == 0.f ? 0.f : vg / lj;
+                    if (ok && a.lse)
+                        a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] =
+                            lj == 0.f ? -INFINITY : (mj - KV4_P_UP + log2f(lj)) * 0.6931471805599453f;
                 }
-            } else {
-                write = false;
+                named_bar(1, G::SOFT);
+                // eight elements of a row at a time, four of these in flight; neighbouring threads have
+                // neighbouring rows, as the parts do
+                const int total = rows * (HD / 8);
+#pragma unroll 1
+                for (int i0 = tid; i0 < total; i0 += 4 * G::SOFT) {
+                    float v[4][8];
+                    const float4* pi[4];
+                    int row[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = min(i0 + k * G::SOFT, total - 1), d8 = i / rows;
+                        row[k] = i - d8 * rows;
+                        pi[k] = reinterpret_cast<const float4*>(first_part) + (size_t)(2 * d8) * G::ROWS + row[k];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) v[k][y] = 0.f;
+                    }
+#pragma unroll 2
+                    for (int y = 0; y < splits; ++y)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float4 u0 = __ldcg(pi[k] + (size_t)y * (G::PART / 4));
+                            const float4 u1 = __ldcg(pi[k] + (size_t)y * (G::PART / 4) + G::ROWS);
+                            const float w = wt[y * G::ROWS + row[k]];
+                            v[k][0] += u0.x * w;
+                            v[k][1] += u0.y * w;
+                            v[k][2] += u0.z * w;
+                            v[k][3] += u0.w * w;
+                            v[k][4] += u1.x * w;
+                            v[k][5] += u1.y * w;
+                            v[k][6] += u1.z * w;
+                            v[k][7] += u1.w * w;
+                        }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = i0 + k * G::SOFT;
+                        if (i >= total || !ok) break;
+                        const float inv = wt[splits * G::ROWS + row[k]];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) v[k][y] *= inv;
+                        const int tk = tok_of(row[k]), hd = head_of(row[k], tk);
+                        kv4_store8(a.out, (size_t)(p.q0 + tk) * a.out_stride + (size_t)hd * HD + i / rows * 8, a.out_t, v[k]);
+                    }
+                }
             }
         }
         if (write && a.lse)
@@ -719,19 +821,19 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         ok = wait(qfull, 0);
         tc_fence_after();
         for (int step = 0; ok && step < 2 && step < ns; ++step) {
-            ok = k_there(step);
+            if (step % G::SPC == 0) ok = k_there(step);
             for (int x = 0; ok && x < tiles; ++x) s_of(x, step);
         }
         for (int step = 0; ok && step < ns; ++step) {
             const int i = step / G::SPC;
-            ok = wait(vfull + i % BUF, (i / BUF) & 1);
+            if (step % G::SPC == 0) ok = wait(vfull + i % BUF, (i / BUF) & 1);
             for (int x = 0; ok && x < tiles; ++x) {
                 ok = wait(pfull + 2 * x + (step & 1), (step >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 pv_of(x, step);
                 if (step + 2 < ns) {
-                    if (x == 0) ok = k_there(step + 2);
+                    if (x == 0 && (step + 2) % G::SPC == 0) ok = k_there(step + 2);
                     if (!ok) break;
                     s_of(x, step + 2);
                 }
@@ -751,21 +853,20 @@ cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, 
     const cudaError_t e = cudaFuncSetAttribute(kv4_extend_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)G::SMEM);
     if (e != cudaSuccess) return e;
-    // items: whole tiles of rows, and one that is not whole per sequence with enough rows
+    // items: whole tiles of rows, and one that is not whole per sequence with enough rows; splitting adds
+    // about two pieces a multiprocessor
     const long long rows = (long long)a.n_tokens * (a.s.nq / a.s.nkv);
     const long long ragged = rows / (few_rows + 1) < a.n_seqs ? rows / (few_rows + 1) : a.n_seqs;
-    long long grid = a.s.nkv * (rows / G::ROWS + ragged);
-    if (grid < w.num_sms) grid = w.num_sms;
+    const long long grid = a.s.nkv * (rows / G::ROWS + ragged) + 2 * w.num_sms;
     return launch_pdl(kv4_extend_kernel<HD, TERMS>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, a, few_rows,
-                      w.parts, w.arrive, w.num_sms);
+                      w.parts, w.arrive, w.num_sms, EXTEND_PARTS * w.num_sms);
 }
 
 }  // namespace
 
-// a split item's parts: at most one CTA a multiprocessor
 size_t kv4_extend_part_floats(int hd, int num_sms) {
     const size_t rows = hd <= 128 ? 256 : 128;
-    return (size_t)num_sms * rows * (hd + 2);
+    return (size_t)EXTEND_PARTS * num_sms * rows * (hd + 2);
 }
 
 cudaError_t launch_kv4_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {

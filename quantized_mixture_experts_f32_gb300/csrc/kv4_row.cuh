@@ -27,8 +27,22 @@ __device__ __forceinline__ void kv4_split(float x, float y, uint32_t& hi, uint32
     lo = kv4_pack(x - __low2float(h), y - __high2float(h));
 }
 
-// The exponent that brings a row of q whose largest magnitude is `big` to [1, 2).
-__device__ __forceinline__ int kv4_exponent(float big) { return big > 0.f && big < INFINITY ? ilogbf(big) : 0; }
+// The exponent e of a row's largest magnitude `big` (2^e <= big < 2^(e+1); 0 for zero,
+// infinity and NaN), and the factors that bring the row to [1, 2): two, as 2^-e alone
+// may be no fp32 number.
+__device__ __forceinline__ int kv4_exponent(float big) {
+    const uint32_t u = __float_as_uint(big);
+    if (u == 0u || u >= 0x7f800000u) return 0;
+    return u >= 0x00800000u ? (int)(u >> 23) - 127 : 31 - __clz(u) - 149;
+}
+__device__ __forceinline__ float kv4_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| < 127
+struct Kv4Scale {
+    float a, b;
+};
+__device__ __forceinline__ Kv4Scale kv4_unscale(int e) {
+    const int h = -e / 2;
+    return {kv4_pow2(h), kv4_pow2(-e - h)};
+}
 
 // Eight E2M1 codes -> four half2, bytes in order.  One conversion a byte: naming the
 // bytes of w in PTX lets the conversion pick its byte, where extracting them first
@@ -73,26 +87,29 @@ __device__ __forceinline__ void kv4_store2(void* p, size_t at, int t, float x, f
     else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + at) = __floats2bfloat162_rn(x, y);
 }
 
-// eight elements at a multiple of eight
-__device__ __forceinline__ void kv4_load8(const void* p, size_t at, int t, float (&v)[8]) {
-    if (t == KV4_F32) {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-        const float4 x = f[0], y = f[1];
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-        return;
-    }
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// eight elements as they were loaded: F32 from two words of 16 bytes, else one
+template <int N>
+__device__ __forceinline__ void kv4_floats8(const uint4 (&u)[N], int t, float (&v)[8]) {
+    const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w}, w2[4] = {u[N - 1].x, u[N - 1].y, u[N - 1].z, u[N - 1].w};
+    if constexpr (N == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = t == KV4_F16 ? __half22float2(*reinterpret_cast<__half2*>(&w[i]))
-                                      : make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        for (int i = 0; i < 4; ++i) {
+            v[i] = __uint_as_float(w[i]);
+            v[4 + i] = __uint_as_float(w2[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t x = w[i];
+            const float2 f = t == KV4_F16 ? __half22float2(*reinterpret_cast<__half2*>(&x))
+                                          : make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
     }
 }
 
+// eight elements at a multiple of eight
 __device__ __forceinline__ void kv4_store8(void* p, size_t at, int t, const float* v) {
     if (t == KV4_F32) {
         float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
