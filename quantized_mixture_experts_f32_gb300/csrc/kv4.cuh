@@ -43,6 +43,7 @@ struct Kv4PlanArgs {
     unsigned* arrive;     // zero between launches
     int* status;
 };
+cudaError_t kv4_plan_prepare();           // shared-memory limits, once a device
 cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, int num_sms, cudaStream_t st);
 
 struct Kv4AppendArgs {
@@ -84,25 +85,13 @@ struct Kv4Work {
 };
 size_t kv4_decode_part_floats(int hd, int num_sms);
 size_t kv4_extend_part_floats(int hd, int num_sms);
+cudaError_t kv4_decode_prepare();
+cudaError_t kv4_extend_prepare();
 cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
 cudaError_t launch_kv4_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
 int kv4_arrive_words(int num_sms);
 size_t kv4_part_floats(int hd, int num_sms);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st);
-
-__device__ __forceinline__ float kv4_load(const void* p, size_t i, int t) {
-    return t == KV4_F32 ? static_cast<const float*>(p)[i]
-         : t == KV4_F16 ? __half2float(static_cast<const __half*>(p)[i])
-                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-}
-
-// nearest E2M1 code of v (ties to the even code), saturating at 6
-__device__ __forceinline__ uint32_t kv4_e2m1_code(float v) {
-    const float a = fabsf(v);
-    const uint32_t m = a <= 0.25f ? 0u : a < 0.75f ? 1u : a <= 1.25f ? 2u : a < 1.75f ? 3u
-                     : a <= 2.5f ? 4u : a < 3.5f ? 5u : a <= 5.0f ? 6u : 7u;
-    return m | (signbit(v) ? 8u : 0u);
-}
 
 // A sequence's part of a call: rows q0 .. q0+n-1 are its last n of len positions.
 // False (and ok cleared) where the device arrays hold values out of range.

@@ -154,6 +154,14 @@ qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
         delete h;
         return QMOE_ERR_CUDA;
     }
+    e = qmoe::kv4_plan_prepare();
+    if (e == cudaSuccess) e = qmoe::kv4_decode_prepare();
+    if (e == cudaSuccess) e = qmoe::kv4_extend_prepare();
+    if (e != cudaSuccess) {
+        qmoe::create_error("kernel set-up: %s", cudaGetErrorString(e));
+        delete h;
+        return QMOE_ERR_CUDA;
+    }
     const Layout L = layout(cfg, h->num_sms);
     e = qmoe::fail_next_alloc() ? cudaErrorMemoryAllocation : cudaMalloc(&h->ws, L.total);
     if (e != cudaSuccess) {

@@ -607,9 +607,6 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 template <int HD, int TERMS, int NR>
 cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
     using G = DGeo<HD, TERMS, NR>;
-    const cudaError_t e = cudaFuncSetAttribute(kv4_decode_kernel<HD, TERMS, NR>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)G::smem(4096));
-    if (e != cudaSuccess) return e;
     return launch_pdl(kv4_decode_kernel<HD, TERMS, NR>, dim3(w.num_sms * (HD == 256 ? 1 : 2)), dim3(DT),
                       G::smem(a.n_seqs), st, a, few_rows, w.parts, w.arrive);
 }
@@ -621,6 +618,26 @@ cudaError_t pick_rows(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cuda
 }
 
 }  // namespace
+
+cudaError_t kv4_decode_prepare() {
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](auto kernel, size_t smem) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    };
+    allow(kv4_decode_kernel<64, 1, 1>, DGeo<64, 1, 1>::smem(4096));
+    allow(kv4_decode_kernel<64, 1, 2>, DGeo<64, 1, 2>::smem(4096));
+    allow(kv4_decode_kernel<64, 2, 1>, DGeo<64, 2, 1>::smem(4096));
+    allow(kv4_decode_kernel<64, 2, 2>, DGeo<64, 2, 2>::smem(4096));
+    allow(kv4_decode_kernel<128, 1, 1>, DGeo<128, 1, 1>::smem(4096));
+    allow(kv4_decode_kernel<128, 1, 2>, DGeo<128, 1, 2>::smem(4096));
+    allow(kv4_decode_kernel<128, 2, 1>, DGeo<128, 2, 1>::smem(4096));
+    allow(kv4_decode_kernel<128, 2, 2>, DGeo<128, 2, 2>::smem(4096));
+    allow(kv4_decode_kernel<256, 1, 1>, DGeo<256, 1, 1>::smem(4096));
+    allow(kv4_decode_kernel<256, 1, 2>, DGeo<256, 1, 2>::smem(4096));
+    allow(kv4_decode_kernel<256, 2, 1>, DGeo<256, 2, 1>::smem(4096));
+    allow(kv4_decode_kernel<256, 2, 2>, DGeo<256, 2, 2>::smem(4096));
+    return e;
+}
 
 // a grid has two CTAs a multiprocessor at most, and each leaves two parts of 16 rows at most
 size_t kv4_decode_part_floats(int hd, int num_sms) { return (size_t)4 * num_sms * 16 * (hd + 2); }

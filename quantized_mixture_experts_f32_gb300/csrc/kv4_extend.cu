@@ -850,9 +850,6 @@ template <int HD, int TERMS>
 cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
     using G = EGeo<HD, TERMS>;
     static_assert(G::SMEM <= 227 * 1024, "one CTA's shared memory");
-    const cudaError_t e = cudaFuncSetAttribute(kv4_extend_kernel<HD, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)G::SMEM);
-    if (e != cudaSuccess) return e;
     // items: whole tiles of rows, and one that is not whole per sequence with enough rows; splitting adds
     // about two pieces a multiprocessor
     const long long rows = (long long)a.n_tokens * (a.s.nq / a.s.nkv);
@@ -863,6 +860,20 @@ cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, 
 }
 
 }  // namespace
+
+cudaError_t kv4_extend_prepare() {
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](auto kernel, size_t smem) {
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    };
+    allow(kv4_extend_kernel<64, 1>, EGeo<64, 1>::SMEM);
+    allow(kv4_extend_kernel<64, 2>, EGeo<64, 2>::SMEM);
+    allow(kv4_extend_kernel<128, 1>, EGeo<128, 1>::SMEM);
+    allow(kv4_extend_kernel<128, 2>, EGeo<128, 2>::SMEM);
+    allow(kv4_extend_kernel<256, 1>, EGeo<256, 1>::SMEM);
+    allow(kv4_extend_kernel<256, 2>, EGeo<256, 2>::SMEM);
+    return e;
+}
 
 size_t kv4_extend_part_floats(int hd, int num_sms) {
     const size_t rows = hd <= 128 ? 256 : 128;

@@ -175,15 +175,17 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
 
 }  // namespace
 
+cudaError_t kv4_plan_prepare() {
+    static_assert(sizeof(int) * 4 * PL_MAX <= 64 * 1024, "the scan's shared memory");
+    return cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)(sizeof(int) * 4 * PL_MAX));
+}
+
 cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, int num_sms, cudaStream_t st) {
     const int items = a.cap > a.n ? a.cap : a.n;
     int grid = (items + PL_THREADS - 1) / PL_THREADS;
     if (grid > num_sms) grid = num_sms;
     const size_t smem = sizeof(int) * 4 * (size_t)a.n;
-    static_assert(sizeof(int) * 4 * PL_MAX <= 64 * 1024, "the scan's shared memory");
-    cudaError_t e = cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(sizeof(int) * 4 * PL_MAX));
-    if (e != cudaSuccess) return e;
     return launch_pdl(kv4_plan_kernel, dim3(grid), dim3(PL_THREADS), smem, st, a);
 }
 
