@@ -255,6 +255,44 @@ def test_append_zero_global_and_slots_past_the_cache(q):
         kv.close()
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -60, 2.0 ** -100, 2.0 ** 60, 2.0 ** 100])
+def test_append_at_and_beside_every_border(q, scale):
+    """Quotients on a border between two codes, one step of x above and below it, and random ones, for
+    small, ordinary and large global scales."""
+    rng = np.random.default_rng(4)
+    t, nkv, hd, page = 256, 2, 128, 64
+    kv = Kv(q, nkv, nkv, hd, page, 5, 1, t, 5)
+    try:
+        f = np.float32
+        kv.g = (rng.uniform(0.7, 1.4, (2, nkv)) * scale).astype(f)
+        kv.kg.copy_(cuda(kv.g[0]))
+        kv.vg.copy_(cuda(kv.g[1]))
+        borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], f)
+        rows = []
+        for g in kv.g:
+            sv = R.e4m3_values()[rng.integers(1, 127, (t, nkv, hd // 16))].astype(f)
+            d = (sv * g[:, None]).astype(f)[..., None]
+            x = (borders[rng.integers(0, 7, (t, nkv, hd // 16, 16))] * d).astype(f)
+            x = np.where(rng.uniform(size=x.shape) < 0.33, np.nextafter(x, f(0)),
+                         np.where(rng.uniform(size=x.shape) < 0.5, np.nextafter(x, f(np.inf)), x)).astype(f)
+            x[..., 8:12] = (rng.uniform(0, 6, x[..., 8:12].shape) * d).astype(f)
+            x[..., 15] = (f(6) * d[..., 0]).astype(f)              # the largest: the block's scale is sv
+            x *= rng.choice([-1, 1], x.shape).astype(f)
+            rows.append(x.reshape(t, nkv, hd))
+        x = [cuda(r.reshape(t, -1)) for r in rows]
+        hat = torch.empty(2, t, nkv * hd, device="cuda")
+        kv.append(x[0], x[1], cuda(np.arange(t)), "F32", hat[0], hat[1])
+        assert kv.status() == 0
+        p, o = np.arange(t) // page, np.arange(t) % page
+        for i, n in enumerate("kv"):
+            c, s, val = R.quantise(rows[i], kv.g[i])
+            assert np.array_equal(kv.t[n + "_codes"].cpu().numpy()[p, :, o], c)
+            assert np.array_equal(kv.t[n + "_scales"].cpu().numpy()[p, :, o], s)
+            assert np.array_equal(hat[i].cpu().numpy(), val.reshape(t, -1).astype(f))
+    finally:
+        kv.close()
+
+
 def test_append_of_what_is_not_finite_keeps_scales_finite(q):
     kv = Kv(q, 1, 1, 64, 16, 1, 1, 8, 1)
     try:
