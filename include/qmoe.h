@@ -420,6 +420,28 @@ qmoe_status qmoe_kv4_attention(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const 
                                const int32_t* block_table, float scale, void* out,
                                qmoe_dtype out_t, int64_t out_stride, float* lse);
 
+/* One serving step of a ragged batch through n_layers qwen3moe decoder layers over
+ * paged 4-bit caches, in place on hidden (F32 [n_tokens][H], device): the layer of
+ * qmoe_prefill for n_tokens tokens of n_seqs sequences, each at its own position,
+ * with its K and V rows appended (qmoe_kv4_append) and attended to
+ * (qmoe_kv4_attention, q rows and output as fp16) in caches[l] instead of the
+ * layers' own fp16 caches (k_cache and v_cache of the layers are not used and may
+ * be NULL).  Decoding, draft tokens and prompt chunks may share a call.
+ *  kv        : handle with the context's n_heads, n_kv_heads and head_dim, on its
+ *              device and stream.
+ *  cu_tokens, seq_len, block_table, positions, slots : of the step, as
+ *              qmoe_kv4_plan gives them; max_new as for qmoe_kv4_attention.
+ *  ids_out   : nullable, int32 [n_layers][n_tokens][k] selected experts.
+ * Rows behind cu_tokens[n_seqs] (a padded batch) are left as they were, their ids
+ * unspecified.  Requires the attention geometry in the config and the shapes of
+ * qmoe_prefill; max_ctx does not bound the positions.  Device-side findings are in
+ * the status words of both the context and the handle. */
+qmoe_status qmoe_step_kv4(qmoe_ctx* ctx, qmoe_kv4* kv, const qmoe_layer_weights* layers,
+                          const qmoe_kv4_cache* caches, int n_layers, int n_seqs, int n_tokens,
+                          int max_new, const int32_t* cu_tokens, const int32_t* seq_len,
+                          const int32_t* block_table, const int32_t* positions,
+                          const int64_t* slots, float* hidden, int32_t* ids_out);
+
 /* Allocation-free variant of qmoe_forward for decode-sized calls.  The pages
  * have no counterpart to this entry point; it exists for callers that cannot
  * allocate device memory: processes whose device memory is owned by their own

@@ -69,7 +69,7 @@ EXPORTED = ["qmoe_create", "qmoe_destroy", "qmoe_set_stream", "qmoe_forward", "q
             "qmoe_debug_stall_next", "qmoe_debug_fail_alloc",
             "qmoe_kv4_create", "qmoe_kv4_destroy", "qmoe_kv4_set_stream", "qmoe_kv4_workspace_bytes",
             "qmoe_kv4_get_status", "qmoe_kv4_last_error", "qmoe_kv4_plan", "qmoe_kv4_append",
-            "qmoe_kv4_attention"]
+            "qmoe_kv4_attention", "qmoe_step_kv4"]
 
 
 class qmoe_config(C.Structure):
@@ -174,6 +174,9 @@ def _load():
     L.qmoe_kv4_attention.argtypes = [vp, C.POINTER(qmoe_kv4_cache), vp, i, i64, i, i, i, ip, ip, ip,
                                      C.c_float, vp, i, i64, fp]
     L.qmoe_kv4_attention.restype = i
+    L.qmoe_step_kv4.argtypes = [vp, vp, C.POINTER(qmoe_layer_weights), C.POINTER(qmoe_kv4_cache), i, i, i,
+                                i, ip, ip, ip, ip, vp, fp, ip]
+    L.qmoe_step_kv4.restype = i
     return L
 
 
@@ -182,11 +185,7 @@ lib = _load()
 
 def _ptr(t):
     """Device (or host) address of a tensor-like object, or None."""
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _check(ctx, status):
@@ -366,6 +365,13 @@ def qmoe_kv4_attention(kv, cache, q, q_t, q_stride, n_seqs, n_tokens, max_new, c
                                           n_tokens, max_new, _ptr(cu_tokens), _ptr(seq_len),
                                           _ptr(block_table), scale, _ptr(out), out_t, out_stride,
                                           _ptr(lse)))
+
+
+def qmoe_step_kv4(ctx, kv, layers, caches, n_layers, n_seqs, n_tokens, max_new, cu_tokens, seq_len,
+                  block_table, positions, slots, hidden, ids_out=None):
+    _check(ctx, lib.qmoe_step_kv4(ctx, kv, layers, caches, n_layers, n_seqs, n_tokens, max_new,
+                                  _ptr(cu_tokens), _ptr(seq_len), _ptr(block_table), _ptr(positions),
+                                  _ptr(slots), _ptr(hidden), _ptr(ids_out)))
 
 
 def make_kv4_config(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_seqs, max_tokens,

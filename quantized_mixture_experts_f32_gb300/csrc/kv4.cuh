@@ -93,6 +93,15 @@ int kv4_arrive_words(int num_sms);
 size_t kv4_part_floats(int hd, int num_sms);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st);
 
+// What qmoe_step_kv4 needs of a handle.
+struct Kv4View {
+    Kv4Shape s;
+    Kv4Work w;
+    int* status;
+    cudaStream_t stream;
+    int device, max_seqs, max_tokens;
+};
+
 // A sequence's part of a call: rows q0 .. q0+n-1 are its last n of len positions.
 // False (and ok cleared) where the device arrays hold values out of range.
 struct Kv4Seq {

@@ -121,6 +121,18 @@ qmoe_status check_rows(qmoe_kv4* h, const char* name, const void* p, int dtype, 
 
 }  // namespace
 
+namespace qmoe {
+
+Kv4View kv4_view(const qmoe_kv4* h) {
+    return {shape(h), h->work, h->status, h->stream, h->device, h->cfg.max_seqs, h->cfg.max_tokens};
+}
+
+qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c) { return check_cache(h, c); }
+
+Kv4Cache kv4_cache(const qmoe_kv4_cache* c) { return cache_of(c); }
+
+}  // namespace qmoe
+
 extern "C" {
 
 size_t qmoe_kv4_workspace_bytes(const qmoe_kv4_config* cfg) {

@@ -111,6 +111,69 @@ __global__ void rope_table_rows(const double* __restrict__ inv_freq, int half, i
     cs[i] = rope_cs(inv_freq, j, pos0 + t);
 }
 
+// the same for tokens at positions of their own (negative: a row that is no token, position 0)
+__global__ void rope_table_at(const double* __restrict__ inv_freq, int half, const int32_t* __restrict__ positions,
+                              int T, float2* __restrict__ cs) {
+    pdl_wait();
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i >= T * half) return;
+    const int t = i / half, j = i - t * half;
+    cs[i] = rope_cs(inv_freq, j, max(positions[t], 0));
+}
+
+// one warp per (token, head): per-head RMSNorm and NEOX RoPE; q as fp16 rows
+// [token][head][hd], k in place (fp32; the cache's append quantises it with v)
+__global__ void __launch_bounds__(128) qk_norm_rope_rows(float* __restrict__ qkv, int nq, int nkv, int hd,
+                                                         const float* __restrict__ q_norm,
+                                                         const float* __restrict__ k_norm, float eps,
+                                                         const float2* __restrict__ rcs, __half* __restrict__ qh, int T) {
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int t = blockIdx.x, hh = blockIdx.y * 4 + warp;
+    if (t >= T || hh >= nq + nkv) return;
+    const int n = hd / 32;
+    const bool isq = hh < nq;
+    float* src = qkv + (size_t)t * (nq + 2 * nkv) * hd + (size_t)hh * hd;
+    const float* nw = isq ? q_norm : k_norm;
+    float v[8];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        v[i] = i < n ? src[lane + 32 * i] : 0.f;
+        ss = fmaf(v[i], v[i], ss);
+    }
+    ss = warp_sum(ss);
+    const float r = rsqrtf(ss / (float)hd + eps);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < n) v[i] = v[i] * r * nw[lane + 32 * i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (i < n / 2) {
+            const float2 cs = rcs[(size_t)t * (hd / 2) + lane + 32 * i];
+            const float a = v[i], b = v[i + n / 2];
+            v[i] = a * cs.x - b * cs.y;
+            v[i + n / 2] = b * cs.x + a * cs.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i < n) {
+            if (isq) qh[((size_t)t * nq + hh) * hd + lane + 32 * i] = __float2half_rn(v[i]);
+            else src[lane + 32 * i] = v[i];
+        }
+    }
+}
+
+// rows behind the last token (*n_tokens of them are tokens): src -> dst
+__global__ void __launch_bounds__(NR_THREADS) copy_rows_behind(const float* __restrict__ src, float* __restrict__ dst,
+                                                               const int32_t* __restrict__ n_tokens, int H) {
+    pdl_wait();
+    if ((int)blockIdx.x < *n_tokens) return;
+    const size_t base = (size_t)blockIdx.x * H;
+    for (int i = threadIdx.x; i < H; i += NR_THREADS) dst[base + i] = src[base + i];
+}
+
 // one warp per (token, head): heads 0..nq-1 are q heads (RMSNorm q_norm, RoPE,
 // fp32 out), heads nq..nq+nkv-1 are kv heads (k: RMSNorm k_norm, RoPE, fp16 into
 // cache slot pos0 + t; v: fp16 into the same slot).  Lane owns dims lane + 32 i,
@@ -581,39 +644,83 @@ cudaError_t prefill_layer_prepare() {
     return e;
 }
 
-cudaError_t launch_prefill_layer_attn(const PrefillLayerArgs& a, cudaStream_t st) {
-    const int qd = a.nq * a.hd, kvd = a.nkv * a.hd, T = a.T;
-    const size_t xin_cols = a.H > qd ? a.H : qd;
+namespace {
+
+// where a layer's rows lie in the scratch
+struct LayerScratch {
+    float* qkv;       // [T][qd + 2 kvd]
+    float* qr;        // [T][qd] q rows, fp32 or fp16
+    __half* x16;      // [T][max(H, qd)]
+    __half* att16;    // [T][qd]
+    float* x2;        // [T][H] MoE input, then two planes [T][H] of the O projection
+    float2* rcs;      // [T][hd/2] RoPE cos / sin
+};
+
+LayerScratch layer_scratch(const PrefillLayerArgs& a) {
+    const size_t qd = (size_t)a.nq * a.hd, kvd = (size_t)a.nkv * a.hd, T = a.T;
+    const size_t xin_cols = (size_t)a.H > qd ? (size_t)a.H : qd;
     auto al = [](size_t v) { return (v + 255) / 256 * 256; };
     unsigned char* b = static_cast<unsigned char*>(a.scratch);
-    float* qkv = reinterpret_cast<float*>(b);
-    b += al(4 * (size_t)T * (qd + 2 * kvd));
-    float* qr = reinterpret_cast<float*>(b);
-    b += al(4 * (size_t)T * qd);
-    __half* x16 = reinterpret_cast<__half*>(b);
-    b += al(2 * (size_t)T * xin_cols);
-    __half* att16 = reinterpret_cast<__half*>(b);
-    b += al(2 * (size_t)T * qd);
-    float* x2 = reinterpret_cast<float*>(b);
-    // B1: x = RMSNorm(h) * attn_norm, fp16 rows
-    cudaError_t e = launch_pdl(rmsnorm_rows<1>, dim3(T), dim3(NR_THREADS), 0, st, a.hidden, a.attn_norm,
-                               a.eps, a.H, x16);
+    LayerScratch s;
+    s.qkv = reinterpret_cast<float*>(b);
+    b += al(4 * T * (qd + 2 * kvd));
+    s.qr = reinterpret_cast<float*>(b);
+    b += al(4 * T * qd);
+    s.x16 = reinterpret_cast<__half*>(b);
+    b += al(2 * T * xin_cols);
+    s.att16 = reinterpret_cast<__half*>(b);
+    b += al(2 * T * qd);
+    s.x2 = reinterpret_cast<float*>(b);
+    b += al(4 * T * a.H) + al(8 * T * a.H);
+    s.rcs = reinterpret_cast<float2*>(b);
+    return s;
+}
+
+// B1 + B2: x = RMSNorm(h) * attn_norm as fp16 rows; q, k, v rows of every token,
+// side by side in one [T][qd + 2 kvd] buffer, the three projections in one launch
+cudaError_t launch_qkv(const PrefillLayerArgs& a, const LayerScratch& s, cudaStream_t st) {
+    const int qd = a.nq * a.hd, kvd = a.nkv * a.hd;
+    const cudaError_t e = launch_pdl(rmsnorm_rows<1>, dim3(a.T), dim3(NR_THREADS), 0, st, a.hidden, a.attn_norm,
+                                     a.eps, a.H, s.x16);
     if (e != cudaSuccess) return e;
-    // B2: q, k, v rows of every token, side by side in one [T][qd + 2 kvd]
-    // buffer, the three projections in one launch
-    const int ld = qd + 2 * kvd;
-    {
-        const DenseSeg segs[3] = {{a.wq, qd, 0}, {a.wk, kvd, qd}, {a.wv, kvd, qd + kvd}};
-        e = launch_dense_q4k_gemm_multi(segs, 3, a.H, x16, T, qkv, ld, nullptr, 1, 0, st);
+    const DenseSeg segs[3] = {{a.wq, qd, 0}, {a.wk, kvd, qd}, {a.wv, kvd, qd + kvd}};
+    return launch_dense_q4k_gemm_multi(segs, 3, a.H, s.x16, a.T, s.qkv, qd + 2 * kvd, nullptr, 1, 0, st);
+}
+
+// B7 + B8: h = h + Wo att, x2 = RMSNorm(h) * ffn_norm (the MoE input; h stays the
+// residual).  With too few row x token tiles to fill the GPU the O projection is
+// split over K into two planes that the norm kernel adds.
+cudaError_t launch_out(const PrefillLayerArgs& a, const LayerScratch& s, cudaStream_t st) {
+    const int qd = a.nq * a.hd, T = a.T;
+    const DenseSeg so{a.wo, a.H, 0};
+    if (2 * dense_q4k_items(a.H, T) <= device_sm_count() && (qd / QK) % 2 == 0) {
+        float* part = s.x2 + (size_t)T * a.H;              // two [T][H] planes after x2
+        const cudaError_t e = launch_dense_q4k_gemm_multi(&so, 1, qd, s.att16, T, part, a.H, nullptr, 2, (size_t)T * a.H, st);
         if (e != cudaSuccess) return e;
+        return launch_pdl(residual_rmsnorm_rows, dim3(T), dim3(NR_THREADS), 0, st, a.hidden, part,
+                          part + (size_t)T * a.H, a.ffn_norm, a.eps, a.H, s.x2);
     }
+    // in place: every element of h is read and written by one thread
+    const cudaError_t e = launch_dense_q4k_gemm_multi(&so, 1, qd, s.att16, T, a.hidden, a.H, a.hidden, 1, 0, st);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(rmsnorm_rows<0>, dim3(T), dim3(NR_THREADS), 0, st, a.hidden, a.ffn_norm, a.eps, a.H, s.x2);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_layer_attn(const PrefillLayerArgs& a, cudaStream_t st) {
+    const int qd = a.nq * a.hd, T = a.T;
+    const LayerScratch s = layer_scratch(a);
+    float *qkv = s.qkv, *qr = s.qr;
+    __half* att16 = s.att16;
+    cudaError_t e = launch_qkv(a, s, st);
+    if (e != cudaSuccess) return e;
     // B3-B5: per-head Q/K RMSNorm, NEOX RoPE, fp16 KV append at pos0 + t (q as
     // fp16 rows grouped by kv head for the tensor-core attention, else fp32)
     const int group = a.nq / a.nkv;
     const bool tc = pt_supported(group, a.hd);
     __half* qh = tc ? reinterpret_cast<__half*>(qr) : nullptr;
-    float2* rcs = reinterpret_cast<float2*>(reinterpret_cast<unsigned char*>(x2) + al(4 * (size_t)T * a.H) +
-                                            al(8 * (size_t)T * a.H));
+    float2* rcs = s.rcs;
     e = launch_pdl(rope_table_rows, dim3((T * (a.hd / 2) + 255) / 256), dim3(256), 0, st, a.inv_freq,
                    a.hd / 2, a.pos0, T, rcs);
     if (e != cudaSuccess) return e;
@@ -639,23 +746,32 @@ cudaError_t launch_prefill_layer_attn(const PrefillLayerArgs& a, cudaStream_t st
                        a.pos0, a.max_ctx, T, att16);
     }
     if (e != cudaSuccess) return e;
-    // B7 + B8: h = h + Wo att, x2 = RMSNorm(h) * ffn_norm (the MoE input; h
-    // stays the residual).  With too few row x token tiles to fill the GPU the
-    // O projection is split over K into two planes that the norm kernel adds.
-    const DenseSeg so{a.wo, a.H, 0};
-    if (2 * dense_q4k_items(a.H, T) <= device_sm_count() && (qd / QK) % 2 == 0) {
-        float* part = x2 + (size_t)T * a.H;                // two [T][H] planes after x2
-        e = launch_dense_q4k_gemm_multi(&so, 1, qd, att16, T, part, a.H, nullptr, 2, (size_t)T * a.H, st);
+    return launch_out(a, s, st);
+}
+
+cudaError_t launch_step_layer_qkv(const PrefillLayerArgs& a, const int32_t* positions, bool table, StepRows* rows,
+                                  cudaStream_t st) {
+    const LayerScratch s = layer_scratch(a);
+    cudaError_t e = launch_qkv(a, s, st);
+    if (e != cudaSuccess) return e;
+    if (table) {
+        e = launch_pdl(rope_table_at, dim3((a.T * (a.hd / 2) + 255) / 256), dim3(256), 0, st, a.inv_freq, a.hd / 2,
+                       positions, a.T, s.rcs);
         if (e != cudaSuccess) return e;
-        return launch_pdl(residual_rmsnorm_rows, dim3(T), dim3(NR_THREADS), 0, st, a.hidden, part,
-                          part + (size_t)T * a.H, a.ffn_norm, a.eps, a.H, x2);
-    } else {
-        // in place: every element of h is read and written by one thread
-        e = launch_dense_q4k_gemm_multi(&so, 1, qd, att16, T, a.hidden, a.H, a.hidden, 1, 0, st);
-        if (e != cudaSuccess) return e;
-        return launch_pdl(rmsnorm_rows<0>, dim3(T), dim3(NR_THREADS), 0, st, a.hidden, a.ffn_norm, a.eps, a.H,
-                          x2);
     }
+    __half* qh = reinterpret_cast<__half*>(s.qr);
+    const int qd = a.nq * a.hd, kvd = a.nkv * a.hd;
+    *rows = {qh, s.qkv + qd, s.qkv + qd + kvd, s.att16, qd + 2 * kvd};
+    return launch_pdl(qk_norm_rope_rows, dim3(a.T, (a.nq + a.nkv + 3) / 4), dim3(128), 0, st, s.qkv, a.nq, a.nkv, a.hd,
+                      a.q_norm, a.k_norm, a.eps, s.rcs, qh, a.T);
+}
+
+cudaError_t launch_step_layer_out(const PrefillLayerArgs& a, cudaStream_t st) {
+    return launch_out(a, layer_scratch(a), st);
+}
+
+cudaError_t launch_copy_rows_behind(const float* src, float* dst, const int32_t* n_tokens, int T, int H, cudaStream_t st) {
+    return launch_pdl(copy_rows_behind, dim3(T), dim3(NR_THREADS), 0, st, src, dst, n_tokens, H);
 }
 
 float* prefill_layer_x2(void* scratch, int T, int H, int nq, int nkv, int hd) {

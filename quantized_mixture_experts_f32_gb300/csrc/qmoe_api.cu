@@ -9,6 +9,7 @@
 #include <new>
 
 #include "../../include/qmoe.h"
+#include "kv4.cuh"
 #include "qmoe_internal.h"
 
 struct qmoe_ctx {
@@ -181,16 +182,17 @@ qmoe_status check_forward(qmoe_ctx* c, const float* in, const float* router_w, c
     return QMOE_OK;
 }
 
-qmoe_status check_layers(qmoe_ctx* c, const qmoe_layer_weights* layers, int n_layers) {
+// own_cache: the layers' own fp16 caches are used
+qmoe_status check_layers(qmoe_ctx* c, const qmoe_layer_weights* layers, int n_layers, bool own_cache = true) {
     for (int l = 0; l < n_layers; ++l) {
         const qmoe_layer_weights& w = layers[l];
         if (!w.attn_norm || !w.wq || !w.wk || !w.wv || !w.wo || !w.q_norm || !w.k_norm ||
             !w.ffn_norm || !w.router_w || !w.gate_exps || !w.up_exps || !w.down_exps ||
-            !w.k_cache || !w.v_cache)
+            (own_cache && (!w.k_cache || !w.v_cache)))
             return fail(c, QMOE_ERR_INVALID_ARG, "layer %d: null pointer", l);
         if (!aligned16(w.wq) || !aligned16(w.wk) || !aligned16(w.wv) || !aligned16(w.wo) ||
             !aligned16(w.router_w) || !aligned16(w.gate_exps) || !aligned16(w.up_exps) ||
-            !aligned16(w.down_exps) || !aligned16(w.k_cache) || !aligned16(w.v_cache) ||
+            !aligned16(w.down_exps) || (own_cache && (!aligned16(w.k_cache) || !aligned16(w.v_cache))) ||
             !aligned16(w.attn_norm) || !aligned16(w.ffn_norm))
             return fail(c, QMOE_ERR_MISALIGNED, "layer %d: a base pointer is not 16-byte aligned", l);
         if (!valid_qtype(w.down_t))
@@ -264,6 +266,11 @@ qmoe_status run_moe(qmoe_ctx* c, const float* x, const float* res, const float* 
 }  // namespace
 
 namespace qmoe {
+
+// kv4_api.cu
+Kv4View kv4_view(const qmoe_kv4* h);
+qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c);
+Kv4Cache kv4_cache(const qmoe_kv4_cache* c);
 
 void create_error(const char* fmt, ...) {
     va_list ap;
@@ -801,6 +808,85 @@ qmoe_status qmoe_prefill(qmoe_ctx* c, const qmoe_layer_weights* layers, int n_la
                                  nullptr);
         if (st != QMOE_OK) return st;
     }
+    c->err[0] = 0;
+    return QMOE_OK;
+}
+
+qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* layers,
+                          const qmoe_kv4_cache* caches, int n_layers, int n_seqs, int n_tokens,
+                          int max_new, const int32_t* cu_tokens, const int32_t* seq_len,
+                          const int32_t* block_table, const int32_t* positions,
+                          const int64_t* slots, float* hidden, int32_t* ids_out) {
+    if (!c) return QMOE_ERR_INVALID_ARG;
+    const qmoe_config& k = c->cfg;
+    if (k.n_heads < 1)
+        return fail(c, QMOE_ERR_INVALID_ARG, "context was created without attention geometry");
+    if (!c->pl_scratch)
+        return fail(c, QMOE_ERR_SHAPE, "the batched layer does not serve n_heads=%d n_kv_heads=%d head_dim=%d "
+                    "(needs at most 8 q heads per kv head and 128-row multiples)", k.n_heads, k.n_kv_heads, k.head_dim);
+    if (!kv || !layers || !caches || n_layers < 1 || !cu_tokens || !seq_len || !block_table || !positions || !slots ||
+        !hidden)
+        return fail(c, QMOE_ERR_INVALID_ARG, "null pointer or n_layers < 1");
+    const qmoe::Kv4View v = qmoe::kv4_view(kv);
+    if (v.s.nq != k.n_heads || v.s.nkv != k.n_kv_heads || v.s.hd != k.head_dim)
+        return fail(c, QMOE_ERR_SHAPE, "the cache handle has %d/%d heads of %d, the context %d/%d of %d", v.s.nq, v.s.nkv,
+                    v.s.hd, k.n_heads, k.n_kv_heads, k.head_dim);
+    if (v.stream != c->stream || v.device != c->device)
+        return fail(c, QMOE_ERR_INVALID_ARG, "context and cache handle must have the same device and stream");
+    if (n_seqs < 1 || n_seqs > v.max_seqs)
+        return fail(c, QMOE_ERR_SHAPE, "n_seqs=%d outside 1..max_seqs=%d", n_seqs, v.max_seqs);
+    if (n_tokens < 1 || n_tokens > k.max_tokens || n_tokens > v.max_tokens)
+        return fail(c, QMOE_ERR_SHAPE, "n_tokens=%d outside 1..max_tokens=%d (context), %d (cache handle)", n_tokens,
+                    k.max_tokens, v.max_tokens);
+    if (max_new < 1 || max_new > n_tokens)
+        return fail(c, QMOE_ERR_SHAPE, "max_new=%d outside 1..n_tokens=%d", max_new, n_tokens);
+    if (!aligned16(hidden)) return fail(c, QMOE_ERR_MISALIGNED, "hidden must be 16-byte aligned");
+    if (((reinterpret_cast<uintptr_t>(cu_tokens) | reinterpret_cast<uintptr_t>(seq_len) |
+          reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(positions)) & 3u) ||
+        (reinterpret_cast<uintptr_t>(slots) & 7u))
+        return fail(c, QMOE_ERR_MISALIGNED, "int32 arrays must be 4-byte aligned, slots 8-byte");
+    {
+        qmoe_status ls = check_layers(c, layers, n_layers, false);
+        if (ls != QMOE_OK) return ls;
+        for (int l = 0; l < n_layers; ++l)
+            if ((ls = qmoe::kv4_check_cache(kv, caches + l)) != QMOE_OK)
+                return fail(c, ls, "layer %d: %s", l, qmoe_kv4_last_error(kv));
+    }
+    // rows behind the last token are left as they were: the layers run over them, so they are kept aside
+    cudaError_t e = qmoe::launch_copy_rows_behind(hidden, c->hout, cu_tokens + n_seqs, n_tokens, k.hidden, c->stream);
+    if (e != cudaSuccess) return cuda_fail(c, e, "row copy launch");
+    float* x2 = qmoe::prefill_layer_x2(c->pl_scratch, n_tokens, k.hidden, k.n_heads, k.n_kv_heads, k.head_dim);
+    for (int l = 0; l < n_layers; ++l) {
+        const qmoe_layer_weights& w = layers[l];
+        const qmoe::PrefillLayerArgs a{n_tokens, k.hidden, k.n_heads, k.n_kv_heads, k.head_dim, 0, 0, k.rms_eps,
+                                       c->inv_freq, w.attn_norm, static_cast<const uint8_t*>(w.wq),
+                                       static_cast<const uint8_t*>(w.wk), static_cast<const uint8_t*>(w.wv),
+                                       static_cast<const uint8_t*>(w.wo), w.q_norm, w.k_norm, w.ffn_norm, nullptr,
+                                       nullptr, hidden, c->pl_scratch, c->status};
+        qmoe::StepRows r;
+        e = qmoe::launch_step_layer_qkv(a, positions, l == 0, &r, c->stream);
+        if (e != cudaSuccess) return cuda_fail(c, e, "Q/K/V launch");
+        const qmoe::Kv4Cache cache = qmoe::kv4_cache(caches + l);
+        const qmoe::Kv4AppendArgs ap{v.s, cache, r.k, r.v, qmoe::KV4_F32, n_tokens, r.kv_stride, r.kv_stride, slots,
+                                     nullptr, nullptr, v.status};
+        e = qmoe::launch_kv4_append(ap, c->stream);
+        if (e != cudaSuccess) return cuda_fail(c, e, "append launch");
+        const int64_t qd = (int64_t)k.n_heads * k.head_dim;
+        const qmoe::Kv4AttnArgs at{v.s, cache, r.q, qmoe::KV4_F16, qmoe::KV4_F16, qd, qd, n_seqs, n_tokens, max_new,
+                                   cu_tokens, seq_len, block_table, 1.0f / sqrtf((float)k.head_dim), r.att, nullptr,
+                                   v.status};
+        e = qmoe::launch_kv4_attention(at, v.w, c->stream);
+        if (e != cudaSuccess) return cuda_fail(c, e, "attention launch");
+        e = qmoe::launch_step_layer_out(a, c->stream);
+        if (e != cudaSuccess) return cuda_fail(c, e, "O projection launch");
+        // h = h + MoE(x2), the residual in place as in qmoe_prefill
+        int32_t* ids_l = ids_out ? ids_out + (size_t)l * n_tokens * k.top_k : nullptr;
+        const qmoe_status st = run_moe(c, x2, hidden, nullptr, w.router_w, w.gate_exps, w.up_exps, w.down_exps, QMOE_Q4_K,
+                                       QMOE_Q4_K, w.down_t, n_tokens, hidden, ids_l, nullptr);
+        if (st != QMOE_OK) return st;
+    }
+    e = qmoe::launch_copy_rows_behind(c->hout, hidden, cu_tokens + n_seqs, n_tokens, k.hidden, c->stream);
+    if (e != cudaSuccess) return cuda_fail(c, e, "row copy launch");
     c->err[0] = 0;
     return QMOE_OK;
 }

@@ -288,6 +288,22 @@ size_t prefill_layer_scratch_bytes(int T, int H, int nq, int nkv, int hd);
 bool prefill_layer_supported(int H, int nq, int nkv, int hd);
 cudaError_t prefill_layer_prepare();
 cudaError_t launch_prefill_layer_attn(const PrefillLayerArgs& a, cudaStream_t st);
+// The same layer around attention over another cache (qmoe_step_kv4), for tokens at
+// positions of their own: its part before (norm, Q/K/V, per-head norms, RoPE; `table`
+// makes the positions' RoPE table first) leaves q, k and v rows, the attention fills
+// `att`, its part behind adds the O projection and normalises.
+struct StepRows {
+    __half* q;                // [T][nq*hd]
+    float* k;                 // rows kv_stride apart
+    float* v;
+    __half* att;              // [T][nq*hd]
+    int kv_stride;
+};
+cudaError_t launch_step_layer_qkv(const PrefillLayerArgs& a, const int32_t* positions, bool table, StepRows* rows,
+                                  cudaStream_t st);
+cudaError_t launch_step_layer_out(const PrefillLayerArgs& a, cudaStream_t st);
+// rows *n_tokens .. T-1 of src to dst
+cudaError_t launch_copy_rows_behind(const float* src, float* dst, const int32_t* n_tokens, int T, int H, cudaStream_t st);
 float* prefill_layer_x2(void* scratch, int T, int H, int nq, int nkv, int hd);
 
 // Text that qmoe_last_error(NULL) gives on this thread (a failed qmoe_kv4_create;
