@@ -23,8 +23,7 @@ namespace qmoe {
 namespace {
 
 constexpr int PL_THREADS = 512;
-constexpr int PL_PER = 8;                       // requests a thread scans
-constexpr int PL_MAX = PL_THREADS * PL_PER;
+constexpr int PL_MAX = 8 * PL_THREADS;          // requests
 
 struct Sum3 {
     long long tok, need, back;
@@ -50,6 +49,10 @@ __device__ __forceinline__ int find_owner(const int* pre, int n, int x) {
     return lo;
 }
 
+// PER: requests a thread scans, no more than there have to be: a small step is latency
+// alone, and the code of eight takes longer to fetch than to run (8 requests, 5.6 us with
+// PER 8 and 3.3 with 1).
+template <int PER>
 __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs a) {
     extern __shared__ int sm[];
     int* s_len = sm;                            // [n]
@@ -61,17 +64,19 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) why = 0;
     pdl_wait();
+    pdl_launch_dependents();
+    const int f = *a.n_free;
     __syncthreads();
 
-    Sum3 mine[PL_PER], run{0, 0, 0};
+    Sum3 mine[PER], run{0, 0, 0};
     int bad = 0;
 #pragma unroll
-    for (int i = 0; i < PL_PER; ++i) {
-        const int s = tid * PL_PER + i;
+    for (int i = 0; i < PER; ++i) {
+        const int s = tid * PER + i;
         mine[i] = run;
         if (s < a.n) {
             const int L = a.seq_len[s], N = a.new_len[s];
-            s_len[s] = L;
+            s_len[s] = N < 0 ? ~L : L;                 // the sign tells finished requests apart
             if (L < 0 || (long long)L > (long long)a.width * a.page) {
                 bad = max(bad, ST_DEVICE_CHECK);
             } else {
@@ -100,7 +105,6 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
     const Sum3 base = {before.tok + inc.tok - run.tok, before.need + inc.need - run.need,
                        before.back + inc.back - run.back};
     // the step is served as a whole or not at all
-    const int f = *a.n_free;
     int st = why;
     if (st == 0 || st == 4) {
         const long long left = (long long)f + total.back - total.need;
@@ -111,8 +115,8 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
     const bool ok = st == 0;
     const int n_tok = ok ? (int)total.tok : 0, n_need = ok ? (int)total.need : 0, n_back = ok ? (int)total.back : 0;
 #pragma unroll
-    for (int i = 0; i < PL_PER; ++i) {
-        const int s = tid * PL_PER + i;
+    for (int i = 0; i < PER; ++i) {
+        const int s = tid * PER + i;
         if (s < a.n) {
             const Sum3 p = base + mine[i];
             p_tok[s] = ok ? (int)p.tok : 0;
@@ -129,14 +133,15 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
         return a.table[(size_t)s * a.width + (i - p_back[s])];
     };
     auto taken = [&](int k) { return k < n_back ? returned(n_back - 1 - k) : a.free_pages[f - 1 - (k - n_back)]; };
-    auto have_of = [&](int s) { return (s_len[s] + a.page - 1) / a.page; };
+    auto len_of = [&](int s) { return s_len[s] < 0 ? ~s_len[s] : s_len[s]; };
+    auto have_of = [&](int s) { return (len_of(s) + a.page - 1) / a.page; };
 
     for (int t = gtid; t < a.cap; t += gn) {
         int pos = -1;
         int64_t slot = -1;
         if (t < n_tok) {
             const int s = find_owner(p_tok, a.n, t);
-            pos = s_len[s] + (t - p_tok[s]);
+            pos = len_of(s) + (t - p_tok[s]);
             const int c = pos / a.page, h = have_of(s);
             const int pg = c < h ? a.table[(size_t)s * a.width + c] : taken(p_need[s] + c - h);
             slot = (int64_t)pg * a.page + (pos - c * a.page);
@@ -152,23 +157,25 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
     for (int s = gtid; s <= a.n; s += gn) a.cu[s] = s < a.n ? p_tok[s] : n_tok;
 
     // last CTA out: every CTA has read the lengths and n_free
-    __shared__ int last;
-    __syncthreads();
-    if (tid == 0) {
-        __threadfence();
-        last = atomicAdd(a.arrive, 1u) == gridDim.x - 1;
+    if (gridDim.x > 1) {
+        __shared__ int last;
+        __syncthreads();
+        if (tid == 0) {
+            __threadfence();
+            last = atomicAdd(a.arrive, 1u) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!last) return;
+        if (tid == 0) *a.arrive = 0u;
+    } else {
+        __syncthreads();
     }
-    __syncthreads();
-    if (!last) return;
     for (int s = tid; s < a.n; s += PL_THREADS) {
-        // recomputed from this CTA's copy: a finished request is one that returns
-        // pages or has none, so its arriving count says which
         const int add = (s + 1 < a.n ? p_tok[s + 1] : n_tok) - p_tok[s];
-        a.seq_len_out[s] = ok && a.new_len[s] < 0 ? 0 : s_len[s] + add;
+        a.seq_len_out[s] = !ok ? a.seq_len[s] : s_len[s] < 0 ? 0 : s_len[s] + add;
     }
     if (tid == 0) {
         *a.n_free_out = f + n_back - n_need;
-        *a.arrive = 0u;
         if (!ok) atomicExch(a.status, st);
     }
 }
@@ -177,7 +184,7 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
 
 cudaError_t kv4_plan_prepare() {
     static_assert(sizeof(int) * 4 * PL_MAX <= 64 * 1024, "the scan's shared memory");
-    return cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kv4_plan_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)(sizeof(int) * 4 * PL_MAX));
 }
 
@@ -186,7 +193,10 @@ cudaError_t launch_kv4_plan(const Kv4PlanArgs& a, int num_sms, cudaStream_t st) 
     int grid = (items + PL_THREADS - 1) / PL_THREADS;
     if (grid > num_sms) grid = num_sms;
     const size_t smem = sizeof(int) * 4 * (size_t)a.n;
-    return launch_pdl(kv4_plan_kernel, dim3(grid), dim3(PL_THREADS), smem, st, a);
+    const int per = (a.n + PL_THREADS - 1) / PL_THREADS;
+    return launch_pdl(per <= 1 ? kv4_plan_kernel<1> : per <= 2 ? kv4_plan_kernel<2> : per <= 4 ? kv4_plan_kernel<4>
+                                                                                       : kv4_plan_kernel<8>,
+                      dim3(grid), dim3(PL_THREADS), smem, st, a);
 }
 
 }  // namespace qmoe
