@@ -43,11 +43,10 @@ struct DGeo {
     static constexpr int KC = 0, VC = TP * ROWB, KS = 2 * TP * ROWB, VS = KS + TP * SB;
     static constexpr int STAGE = VS + TP * SB;
     static constexpr int RING = DW * STAGES * STAGE;
-    static constexpr int OBLK = HD / 8 + 4, OLD = 8 * OBLK + 4;  // join buffer: eight runs of a row, padded apart
-    static constexpr int QF = HD * 16 * TERMS * NR;            // q fragments
+    static constexpr int QF = HD * 16 * TERMS * NR;            // q fragments of an item
     static constexpr int PART = ROWS * (HD + 2);               // floats of an item's part: o, m, l
-    static constexpr size_t smem(int n_seqs) { return (size_t)RING + QF + 8 * ((size_t)n_seqs + 1); }
-    static_assert(DW * 8 * OLD * 4 <= RING, "the join buffer reuses the ring");
+    static constexpr size_t smem(int n_seqs) { return (size_t)RING + 2 * QF + 8 * ((size_t)n_seqs + 1); }
+    static_assert(8 * HD * 4 <= STAGE, "a warp's eight rows of o take a stage of its ring");
 };
 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -75,6 +74,23 @@ __device__ __forceinline__ void apart() { asm volatile(""); }
 // operand row c of eight <-> position of eight: 0 4 1 5 2 6 3 7
 __device__ __forceinline__ int pos_of_row(int c) { return (c >> 1) + 4 * (c & 1); }
 __device__ __forceinline__ int row_of_pos(int p) { return 2 * (p & 3) + (p >> 2); }
+
+// where the float4 idx of a row of o lies in the join buffer, so that writing (lanes: a run of the
+// elements of rows 2 j, 2 j + 1) meets every bank once
+template <int HD>
+__device__ __forceinline__ int join_at(int idx, int row) {
+    const int j = (row >> 1) & 3;
+    return idx ^ (HD == 64 ? (j & 1) | ((j & 2) << 1) : HD == 128 ? j : j | (((idx >> 3) & 1) << 2));
+}
+
+// What a CTA does next: a part of an item, all of it where t0 = 0 and t1 = tiles.
+struct Segment {
+    long long next;          // first unit behind it
+    int s, g, row0, rows;    // sequence, kv head, first row, rows
+    int q0, n, len;
+    int t0, t1, tiles;       // its units of positions
+    int c0, c1;              // CTAs that share the item
+};
 
 // One stage: 32 positions of one kv head, 16 at a time; row: index of the first of the
 // 16 positions in the cache (negative: not copied).  K lies in the order of operand rows.
@@ -118,10 +134,11 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     using G = DGeo<HD, TERMS, NR>;
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t* ring = sm;
-    uint32_t* qf = reinterpret_cast<uint32_t*>(sm + G::RING);                       // q fragments
-    long long* pre = reinterpret_cast<long long*>(sm + G::RING + G::QF);            // [n_seqs+1]
+    uint32_t* qf2 = reinterpret_cast<uint32_t*>(sm + G::RING);                      // q fragments, two items
+    long long* pre = reinterpret_cast<long long*>(sm + G::RING + 2 * G::QF);        // [n_seqs+1]
     __shared__ long long wsum[DW];
-    __shared__ float fac_s[G::ROWS], m_s[DW][8], l_s[DW][8];
+    __shared__ float fac_s[2][G::ROWS], m_s[DW][8], l_s[DW][8];
+    __shared__ Segment seg_s[2];
     __shared__ int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, j = lane & 3;             // operand row (position, element run); a pair of q rows
@@ -160,8 +177,10 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     if (me >= Gn) return;
     const long long u_end = unit_begin(W, me + 1, Gn);
 
-    for (long long u = unit_begin(W, me, Gn); u < u_end;) {
-        // the item that unit u belongs to: sequence, kv head, rows
+    // the segment that starts with unit u (one thread); tiles = 0: none
+    auto describe = [&](long long u, Segment& r) {
+        r.tiles = 0;
+        if (u >= u_end) return;
         int s = 0;
         for (int hi = a.n_seqs; hi - s > 1;) {
             const int mid = (s + hi) >> 1;
@@ -170,75 +189,72 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         }
         Kv4Seq q;
         kv4_seq(a, s, q);
-        const int tiles = q.len ? (q.len + UNIT - 1) / UNIT : 1;
+        const int tiles = q.len ? (q.len + UNIT - 1) / UNIT : 1, vu = LEAD + tiles;
         const int rts = (q.n * group + G::ROWS - 1) / G::ROWS;
-        const int vu = LEAD + tiles;
         const long long off = u - pre[s];
         const int item = (int)(off / vu), v0 = (int)(off - (long long)item * vu);
-        const int g = item / rts, row0 = (item - g * rts) * G::ROWS;
         const int v1 = (int)min((long long)vu, v0 + (u_end - u));
-        const int t0 = max(v0 - LEAD, 0), t1 = v1 - LEAD;
+        if (v1 <= LEAD) return;                        // the lead alone: the next CTA starts the item
+        r.next = u + (v1 - v0);
+        r.s = s;
+        r.g = item / rts;
+        r.row0 = (item - r.g * rts) * G::ROWS;
+        r.rows = min(G::ROWS, q.n * group - r.row0);
+        r.q0 = q.q0;
+        r.n = q.n;
+        r.len = q.len;
+        r.t0 = max(v0 - LEAD, 0);
+        r.t1 = v1 - LEAD;
+        r.tiles = tiles;
         const long long i0 = u - v0;                   // the item's first unit
-        u += v1 - v0;
-        if (t1 <= 0) break;                            // the lead alone: the next CTA starts the item
-        const int rows = min(G::ROWS, q.n * group - row0);
-        if (q.len == 0) {                              // nothing to see
-            for (int i = tid; i < rows * (HD / 2); i += DT) {
-                const int row = i / (HD / 2), tok = (row0 + row) / group, h = g * group + (row0 + row) - tok * group;
-                kv4_store2(a.out, (size_t)(q.q0 + tok) * a.out_stride + (size_t)h * HD + 2 * (i - row * (HD / 2)), a.out_t,
-                           0.f, 0.f);
-                if (a.lse && i == row * (HD / 2)) a.lse[(size_t)(q.q0 + tok) * a.s.nq + h] = -INFINITY;
-            }
-            continue;
-        }
-        const int32_t* table = a.table + (size_t)s * a.s.width;
-        const float kg = a.c.kg[g], vg = a.c.vg[g];
+        r.c0 = cta_of_unit(W, i0 + LEAD, Gn);
+        r.c1 = cta_of_unit(W, i0 + vu - 1, Gn);
+    };
 
-        // page ids of 16 of the warp's turns: lane 2 i + half
-        uint8_t* myring = ring + warp * STAGES * G::STAGE;
-        int pid, pid_t;
-        auto load_pages = [&](int t) {
+    uint8_t* myring = ring + warp * STAGES * G::STAGE;
+    int stage = 0;                                     // where the copies of the next turn go
+    int use = 0;                                       // which halves of that turn hold positions
+    int pid = -1, pid_t = 0;                           // page ids of 16 of the warp's turns: lane 2 i + half
+    // starts the copies of turn t of a segment
+    auto issue = [&](const Segment& r, int t, bool fresh) {
+        if (fresh || t - pid_t >= 16) {
             const int pos = (t + (lane >> 1)) * UNIT + warp * TP + 16 * (lane & 1);
             pid_t = t;
-            pid = t + (lane >> 1) < t1 && pos < q.len ? table[pos >> a.s.page_log2] : -1;
-        };
-        // starts the copies of turn t; returns which of its two halves hold positions
-        auto issue = [&](int t) {
-            if (t - pid_t >= 16) load_pages(t);
-            const int pos = t * UNIT + warp * TP;
-            int64_t row[2];
-            int use = 0;
+            pid = t + (lane >> 1) < r.t1 && pos < r.len ? a.table[(size_t)r.s * a.s.width + (pos >> a.s.page_log2)] : -1;
+        }
+        const int pos = t * UNIT + warp * TP;
+        int64_t row[2];
+        use = 0;
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
-                const int pg = __shfl_sync(0xffffffffu, pid, 2 * (t - pid_t) + sub);
-                row[sub] = -1;
-                if (pos + 16 * sub < q.len) {
-                    if (pg >= 0 && pg < a.s.n_pages) {
-                        row[sub] = ((int64_t)pg * a.s.nkv + g) * a.s.page + ((pos + 16 * sub) & (a.s.page - 1));
-                        use |= 1 << sub;
-                    } else if (lane == 0) {
-                        atomicExch(a.status, ST_DEVICE_CHECK);
-                    }
+        for (int sub = 0; sub < 2; ++sub) {
+            const int pg = __shfl_sync(0xffffffffu, pid, 2 * (t - pid_t) + sub);
+            row[sub] = -1;
+            if (pos + 16 * sub < r.len) {
+                if (pg >= 0 && pg < a.s.n_pages) {
+                    row[sub] = ((int64_t)pg * a.s.nkv + r.g) * a.s.page + ((pos + 16 * sub) & (a.s.page - 1));
+                    use |= 1 << sub;
+                } else if (lane == 0) {
+                    atomicExch(a.status, ST_DEVICE_CHECK);
                 }
             }
-            copy_stage<HD>(myring + (t & 1) * G::STAGE, a.c, row, lane);
-            cp_commit();
-            return use;
-        };
-        load_pages(t0);
-        int use = issue(t0);
-
-        // q: warp w takes the rows w, w + 8, scaled to [1, 2) by a power of two
+        }
+        copy_stage<HD>(myring + stage * G::STAGE, a.c, row, lane);
+        cp_commit();
+    };
+    // q: warp w takes the rows w, w + 8, scaled to [1, 2) by a power of two
+    auto take_q = [&](const Segment& r, int buf) {
+        uint32_t* qf = qf2 + buf * (G::QF / 4);
+        const float kg = a.c.kg[r.g];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             const int row = nr * 8 + warp;
-            const int tok = (row0 + row) / group, h = g * group + (row0 + row) - tok * group;
+            const int tok = (r.row0 + row) / group, h = r.g * group + (r.row0 + row) - tok * group;
             float2 v[HD / 64];
             float big = 0.f;
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
-                v[i] = row < rows ? kv4_load2(a.q, (size_t)(q.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
-                                  : make_float2(0.f, 0.f);
+                v[i] = row < r.rows ? kv4_load2(a.q, (size_t)(r.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
+                                    : make_float2(0.f, 0.f);
                 big = fmaxf(big, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
             }
 #pragma unroll
@@ -247,7 +263,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             const Kv4Scale un = kv4_unscale(e);
             const float fac = ldexpf(a.scale * 1.4426950408889634f * kg, e);
             const float sign = fac < 0.f ? -un.b : un.b;            // z's largest is q.k's largest then
-            if (lane == 0) fac_s[row] = fmaxf(fabsf(fac), 1e-38f);  // not 0: -inf stays -inf, and 1e-38 q.k is 0
+            if (lane == 0) fac_s[buf][row] = fmaxf(fabsf(fac), 1e-38f);  // not 0: -inf stays -inf, and 1e-38 q.k is 0
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
                 uint32_t hi, lo;
@@ -266,7 +282,19 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 }
             }
         }
-        __syncthreads();
+    };
+
+    if (tid == 0) describe(unit_begin(W, me, Gn), seg_s[0]);
+    __syncthreads();
+    if (seg_s[0].tiles == 0) return;
+    issue(seg_s[0], seg_s[0].t0, true);
+    take_q(seg_s[0], 0);
+    __syncthreads();
+    for (int cur = 0;; cur ^= 1) {
+        const Segment& S = seg_s[cur];
+        const uint32_t* qf = qf2 + cur * (G::QF / 4);
+        const int len = S.len, rows = S.rows, row0 = S.row0, t0 = S.t0, t1 = S.t1;
+        if (tid == DT - 32) describe(S.next, seg_s[cur ^ 1]);      // while the others start
 
         // this lane's rows: 2 j and 2 j + 1 of each eight
         float fac[NR][2], m[NR][2], l[NR][2], base[NR][2];
@@ -276,13 +304,13 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
                 const int row = nr * 8 + 2 * j + y;
-                fac[nr][y] = fac_s[row];
-                lim[nr][y] = row < rows ? q.len - q.n + (row0 + row) / group + 1 : 0;
+                fac[nr][y] = fac_s[cur][row];
+                lim[nr][y] = row < rows ? len - S.n + (row0 + row) / group + 1 : 0;
                 m[nr][y] = -INFINITY;
                 base[nr][y] = 0.f;
                 l[nr][y] = 0.f;
             }
-        const int lim_min = q.len - q.n + row0 / group + 1;
+        const int lim_min = len - S.n + row0 / group + 1;
         float o[NR][HD / 16][4];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
@@ -292,16 +320,17 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 for (int i = 0; i < 4; ++i) o[nr][t][i] = 0.f;
 
         for (int t = t0; t < t1; ++t) {
-            const int cur = use;
+            const int halves = use;
+            const uint8_t* st = myring + stage * G::STAGE;
+            stage ^= 1;
             if (t + 1 < t1) {
-                use = issue(t + 1);
+                issue(S, t + 1, false);
                 cp_wait<1>();
             } else {
                 cp_wait<0>();
             }
             __syncwarp();
-            if (cur) {
-                const uint8_t* st = myring + (t & 1) * G::STAGE;
+            if (halves) {
                 const int pos = t * UNIT + warp * TP;
                 // S^T: two tiles of 16 positions; lane: positions r, r + 8 of each, rows 2 j, 2 j + 1
                 float z[2][NR][4];
@@ -369,7 +398,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                         }
                     }
                 }
-                const bool edge = cur != 3 || pos + TP > lim_min;
+                const bool edge = halves != 3 || pos + TP > lim_min;
                 if (edge) {
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr)
@@ -377,7 +406,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                         for (int n = 0; n < 4; ++n)
 #pragma unroll
                             for (int y = 0; y < 2; ++y)
-                                if (!((cur >> (n >> 1)) & 1) || pos + n * 8 + pos_of_row(r) >= lim[nr][y])
+                                if (!((halves >> (n >> 1)) & 1) || pos + n * 8 + pos_of_row(r) >= lim[nr][y])
                                     z[n >> 1][nr][2 * (n & 1) + y] = -INFINITY;
                     apart();
                 }
@@ -469,7 +498,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                         // behind the last position the bytes may decode to NaN, which weight 0 would keep
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            if (!((cur >> sub) & 1) || pos + sub * 16 + 4 * i + j >= q.len) vs[i] = 0;
+                            if (!((halves >> sub) & 1) || pos + sub * 16 + 4 * i + j >= len) vs[i] = 0;
                         apart();
                     }
 #pragma unroll
@@ -502,13 +531,13 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             __syncwarp();
         }
 
-        // join the warps, eight rows at a time
+        // join the warps, eight rows at a time, each warp's in the stage it used last (the other one
+        // takes the next segment's first copies)
         constexpr int PT = HD / 32;                    // elements of a lane then; warp -> row
-        const int d0 = lane * PT;
-        const bool whole = t0 == 0 && t1 == tiles;
-        float* ob = reinterpret_cast<float*>(ring);    // [warp][row][OLD]
-        const int c0 = cta_of_unit(W, i0 + LEAD, Gn), c1 = cta_of_unit(W, i0 + vu - 1, Gn);
-        float* part = parts + (size_t)(2 * me + (me == c0)) * G::PART;
+        const int d0 = lane * PT, last_stage = stage ^ 1;
+        const bool whole = t0 == 0 && t1 == S.tiles;
+        float* part = parts + (size_t)(2 * me + (me == S.c0)) * G::PART;
+        const float vg = a.c.vg[S.g];
         float2 acc[PT / 2];
         float mj, lj;
         auto clear = [&]() {
@@ -516,52 +545,54 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
             for (int i = 0; i < PT / 2; ++i) acc[i] = make_float2(0.f, 0.f);
         };
-        auto add = [&](float mw, float lw, const float* x, bool shared) {
-            const float c = lw == 0.f ? 0.f : kv4_ex2(mw - mj);
-            lj += lw * c;
-#pragma unroll
-            for (int i = 0; i < PT / 2; ++i) {
-                const float2 y = shared ? reinterpret_cast<const float2*>(x)[i] : __ldcg(reinterpret_cast<const float2*>(x) + i);
-                acc[i].x += y.x * c;
-                acc[i].y += y.y * c;
-            }
-        };
         auto write = [&](int row) {
             if (row >= rows) return;
-            const int tok = (row0 + row) / group, h = g * group + (row0 + row) - tok * group;
+            const int tok = (row0 + row) / group, h = S.g * group + (row0 + row) - tok * group;
             const float inv = lj == 0.f ? 0.f : vg / lj;
-            const size_t at = (size_t)(q.q0 + tok) * a.out_stride + (size_t)h * HD + d0;
+            const size_t at = (size_t)(S.q0 + tok) * a.out_stride + (size_t)h * HD + d0;
 #pragma unroll
             for (int i = 0; i < PT / 2; ++i) kv4_store2(a.out, at + 2 * i, a.out_t, acc[i].x * inv, acc[i].y * inv);
             if (a.lse && lane == 0)
-                a.lse[(size_t)(q.q0 + tok) * a.s.nq + h] =
+                a.lse[(size_t)(S.q0 + tok) * a.s.nq + h] =
                     lj == 0.f ? -INFINITY : (mj - KV4_P_UP + log2f(lj)) * 0.6931471805599453f;
         };
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            __syncthreads();                           // the ring, q, or the last eight rows' join are done with
+            if (nr) __syncthreads();                   // the first eight rows are read
+            float4* mine = reinterpret_cast<float4*>(myring + last_stage * G::STAGE);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l[nr][y] += __shfl_xor_sync(0xffffffffu, l[nr][y], d);
-                float* w = ob + (warp * 8 + 2 * j + y) * G::OLD + r * G::OBLK;
+                const int row = 2 * j + y;
 #pragma unroll
                 for (int t = 0; t < HD / 16; t += 2)
-                    *reinterpret_cast<float4*>(w + 2 * t) =
+                    mine[row * (HD / 4) + join_at<HD>(r * (HD / 32) + t / 2, row)] =
                         make_float4(o[nr][t][y], o[nr][t][2 + y], o[nr][t + 1][y], o[nr][t + 1][2 + y]);
                 if (r == 0) {
-                    m_s[warp][2 * j + y] = m[nr][y];
-                    l_s[warp][2 * j + y] = l[nr][y];
+                    m_s[warp][row] = m[nr][y];
+                    l_s[warp][row] = l[nr][y];
                 }
             }
             __syncthreads();
+            if (nr == 0 && seg_s[cur ^ 1].tiles) issue(seg_s[cur ^ 1], seg_s[cur ^ 1].t0, true);
             mj = -INFINITY;
 #pragma unroll
             for (int w = 0; w < DW; ++w) mj = fmaxf(mj, m_s[w][warp]);
             clear();
 #pragma unroll
-            for (int w = 0; w < DW; ++w)
-                add(m_s[w][warp], l_s[w][warp], ob + (w * 8 + warp) * G::OLD + (d0 / (HD / 8)) * G::OBLK + d0 % (HD / 8), true);
+            for (int w = 0; w < DW; ++w) {
+                const float* ob = reinterpret_cast<const float*>(ring + (w * STAGES + last_stage) * G::STAGE) + warp * HD;
+                const float c = l_s[w][warp] == 0.f ? 0.f : kv4_ex2(m_s[w][warp] - mj);
+                lj += l_s[w][warp] * c;
+#pragma unroll
+                for (int i = 0; i < PT / 2; ++i) {
+                    const int d = d0 + 2 * i;
+                    const float2 y = *reinterpret_cast<const float2*>(ob + 4 * join_at<HD>(d >> 2, warp) + (d & 3));
+                    acc[i].x += y.x * c;
+                    acc[i].y += y.y * c;
+                }
+            }
             const int row = nr * 8 + warp;
             if (whole) {
                 write(row);
@@ -575,7 +606,9 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 }
             }
         }
+        if (seg_s[cur ^ 1].tiles) take_q(seg_s[cur ^ 1], cur ^ 1);
         if (!whole) {
+            const int c0 = S.c0, c1 = S.c1;
             __threadfence();
             __syncthreads();
             if (tid == 0) last_s = atomicAdd(arrive + c0, 1u) == (unsigned)(c1 - c0);
@@ -594,13 +627,22 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll 8
                     for (int i = 0; i < ns; ++i) {
                         const float* p = part_of(i);
-                        add(__ldcg(p + G::ROWS * HD + row), __ldcg(p + G::ROWS * HD + G::ROWS + row), p + row * HD + d0, false);
+                        const float lw = __ldcg(p + G::ROWS * HD + G::ROWS + row), mw = __ldcg(p + G::ROWS * HD + row);
+                        const float c = lw == 0.f ? 0.f : kv4_ex2(mw - mj);
+                        lj += lw * c;
+#pragma unroll
+                        for (int k = 0; k < PT / 2; ++k) {
+                            const float2 y = __ldcg(reinterpret_cast<const float2*>(p + row * HD + d0) + k);
+                            acc[k].x += y.x * c;
+                            acc[k].y += y.y * c;
+                        }
                     }
                     write(row);
                 }
             }
         }
-        __syncthreads();                               // the join buffer and q are free again
+        if (seg_s[cur ^ 1].tiles == 0) return;
+        __syncthreads();                               // the next segment's q is there, the join is read
     }
 }
 
