@@ -54,28 +54,31 @@ struct EGeo {
 };
 
 // The MMA warp runs its loop as a whole, so that descriptors and addresses stay in
-// uniform registers; only the instructions themselves are one lane's (`one`).
+// uniform registers; only the instructions themselves are one lane's (`one`; a branch
+// around them took the operands through lane registers, twice the time a product).
+// Descriptors change in their low words alone (addresses in units of 16 bytes).
 __device__ __forceinline__ uint32_t elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p;
 }
 
-// D[tmem] (+)= A[shared] * B^T
-__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] = A[shared] * B^T, or += it
+template <int ADD>
+__device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "n"(ADD), "r"(one)
         : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B^T
-__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(one)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "r"(add), "r"(one)
         : "memory");
 }
 
@@ -782,7 +785,9 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         auto same = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };    // known to be uniform
         const int ns = (int)same((p.c1 - p.c0) * G::SPC), tiles = (int)same(nact);
         const uint32_t tm0 = same(tmem), smem0 = same(smem_u32(sm)), bar0 = smem0 + G::BARS;
-        const uint64_t qd = umma_sdesc(smem0 + G::Q), kd = umma_sdesc(smem0 + G::K), vd = umma_sdesc(smem0 + G::V);
+        const uint32_t high = (uint32_t)(umma_sdesc(0) >> 32);                    // of every descriptor
+        const uint32_t qd = (uint32_t)umma_sdesc(smem0 + G::Q), kd = (uint32_t)umma_sdesc(smem0 + G::K),
+                       vd = (uint32_t)umma_sdesc(smem0 + G::V);
         const uint32_t idS = umma_idesc_f16(128, SC), idO = umma_idesc_f16(128, HD);
         auto wait = [&](uint64_t* bar, uint32_t parity) { return warp_wait(bar, parity); };
         auto k_there = [&](int step) {
@@ -791,32 +796,39 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
             tc_fence_after();
             return there;
         };
-        // S of a step into its slot; the last one of a chunk frees the buffer.  Descriptors count in
-        // 16 bytes: a 64-wide block of a tile, then 32 bytes a product
+        // S of a step into its slot; the last one of a chunk frees the buffer.  A product takes 32 bytes of
+        // a tile's 64-wide block
         auto s_of = [&](int x, int step) {
             const int b = step / G::SPC % BUF, h = step % G::SPC;
-            const uint64_t ad = qd + (uint64_t)(x * TERMS * (G::QT / 16)), bd = kd + (uint64_t)(b * (G::KT / 16) + h * (SC * 8));
+            const uint32_t ad = qd + x * TERMS * (G::QT / 16), bd = kd + b * (G::KT / 16) + h * (SC * 8);
             const uint32_t d = tm0 + x * 128 + (step & 1) * 64;
+            const uint32_t full = bar0 + 8 * (8 + 2 * x + (step & 1)), empty = bar0 + 8 * (2 + b);
+            const bool last = x == tiles - 1 && h == G::SPC - 1;
 #pragma unroll
             for (int tm = TERMS - 1; tm >= 0; --tm)
 #pragma unroll
-                for (int ks = 0; ks < HD / 16; ++ks)
-                    mma_ss(one, d, ad + (tm * (G::QT / 16) + (ks >> 2) * 1024 + 2 * (ks & 3)),
-                           bd + ((ks >> 2) * (KC * 8) + 2 * (ks & 3)), idS, (tm < TERMS - 1) | ks);
-            mma_commit(one, bar0 + 8 * (8 + 2 * x + (step & 1)));
-            if (x == tiles - 1 && h == G::SPC - 1) mma_commit(one, bar0 + 8 * (2 + b));
+                for (int ks = 0; ks < HD / 16; ++ks) {
+                    const uint32_t ak = ad + (tm * (G::QT / 16) + (ks >> 2) * 1024 + 2 * (ks & 3));
+                    const uint32_t bk = bd + ((ks >> 2) * (KC * 8) + 2 * (ks & 3));
+                    if (tm == TERMS - 1 && ks == 0) mma_ss<0>(one, d, ak, bk, high, idS);
+                    else mma_ss<1>(one, d, ak, bk, high, idS);
+                }
+            mma_commit(one, full);
+            if (last) mma_commit(one, empty);
         };
         auto pv_of = [&](int x, int step) {
             const int b = step / G::SPC % BUF, h = step % G::SPC;
-            const uint64_t bd = vd + (uint64_t)(b * (G::KT / 16) + h * (HD * 8));
+            const uint32_t bd = vd + b * (G::KT / 16) + h * (HD * 8);
             const uint32_t d = tm0 + 256 + x * HD, ap = tm0 + x * 128 + (step & 1) * 64;
+            const uint32_t done = bar0 + 8 * (16 + 2 * x + (step & 1)), empty = bar0 + 8 * (6 + b);
+            const bool last = x == tiles - 1 && h == G::SPC - 1;
 #pragma unroll
             for (int tm = TERMS - 1; tm >= 0; --tm)
 #pragma unroll
                 for (int ks = 0; ks < SC / 16; ++ks)
-                    mma_ts(one, d, ap + (tm * (SC / 2) + ks * 8), bd + 2 * ks, idO, (uint32_t)(step | (tm < TERMS - 1) | ks));
-            mma_commit(one, bar0 + 8 * (16 + 2 * x + (step & 1)));
-            if (x == tiles - 1 && h == G::SPC - 1) mma_commit(one, bar0 + 8 * (6 + b));
+                    mma_ts(one, d, ap + (tm * (SC / 2) + ks * 8), bd + 2 * ks, high, idO, (uint32_t)(step | (tm < TERMS - 1) | ks));
+            mma_commit(one, done);
+            if (last) mma_commit(one, empty);
         };
         ok = wait(qfull, 0);
         tc_fence_after();
