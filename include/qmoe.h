@@ -331,8 +331,10 @@ typedef struct {
     const float* v_global;  /* [n_kv_heads] */
 } qmoe_kv4_cache;
 
-/* Create a handle on the current device and allocate its workspace.  On failure
- * qmoe_last_error(NULL) tells why. */
+/* Create a handle on the current device and allocate its workspace (parts of
+ * attention items that several CTAs share: about 5 MB for decoding, 40 MB where a
+ * sequence may bring more than 16 rows of q, tokens times n_heads/n_kv_heads).  On
+ * failure qmoe_last_error(NULL) tells why. */
 qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out);
 void qmoe_kv4_destroy(qmoe_kv4* kv);
 qmoe_status qmoe_kv4_set_stream(qmoe_kv4* kv, void* stream);
@@ -410,9 +412,9 @@ qmoe_status qmoe_kv4_append(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const voi
  * have fp32 accumulators and the running maximum and sum are fp32; F32 rows enter
  * the tensor cores as two fp16 terms each, F16 and BF16 rows as one (K and V are
  * exact in fp16).  A sequence whose offsets, length or new tokens are out of range
- * (negative, past the table row, n_tokens or max_new) is skipped, and a position
- * whose page id is out of range counts as not visible; both set
- * QMOE_ERR_DEVICE_CHECK.  Row addresses, strides in bytes and out 16-byte aligned;
+ * (negative, past the table row, n_tokens or max_new) is skipped, a position whose
+ * page id is out of range counts as not visible, and offsets that descend anywhere
+ * leave all rows as they were; each sets QMOE_ERR_DEVICE_CHECK.  Row addresses, strides in bytes and out 16-byte aligned;
  * out must not overlap q. */
 qmoe_status qmoe_kv4_attention(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const void* q,
                                qmoe_dtype q_t, int64_t q_stride, int n_seqs, int n_tokens,

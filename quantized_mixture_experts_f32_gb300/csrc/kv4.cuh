@@ -90,7 +90,7 @@ cudaError_t kv4_extend_prepare();
 cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
 cudaError_t launch_kv4_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
 int kv4_arrive_words(int num_sms);
-size_t kv4_part_floats(int hd, int num_sms);
+size_t kv4_part_floats(int hd, int num_sms, long long max_rows);   // rows: tokens x heads of a group
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st);
 
 // What qmoe_step_kv4 needs of a handle.

@@ -39,7 +39,8 @@ Layout layout(const qmoe_kv4_config* c, int num_sms) {
     L.status = take(sizeof(int));
     L.arrive = take(sizeof(unsigned));
     L.items = take(sizeof(unsigned) * qmoe::kv4_arrive_words(num_sms));
-    L.parts = take(sizeof(float) * qmoe::kv4_part_floats(c->head_dim, num_sms));
+    L.parts = take(sizeof(float) * qmoe::kv4_part_floats(c->head_dim, num_sms, (long long)c->max_tokens *
+                                                                                 (c->n_heads / c->n_kv_heads)));
     L.total = off;
     return L;
 }

@@ -150,9 +150,11 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     {
         const int per = (a.n_seqs + DT - 1) / DT, s0 = min(tid * per, a.n_seqs), s1 = min(s0 + per, a.n_seqs);
         long long run = 0;
+        bool descends = false;
         for (int s = s0; s < s1; ++s) {
             Kv4Seq q;
             if (!kv4_seq(a, s, q) && blockIdx.x == 0) atomicExch(a.status, ST_DEVICE_CHECK);
+            descends |= a.cu[s + 1] < a.cu[s];
             pre[s] = run;
             if (q.n * group <= few_rows)
                 run += (long long)a.s.nkv * ((q.n * group + G::ROWS - 1) / G::ROWS) *
@@ -165,7 +167,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             if (lane >= d) inc += o;
         }
         if (lane == 31) wsum[warp] = inc;
-        __syncthreads();
+        if (__syncthreads_or(descends)) return;        // rows of several sequences; the status says so
         long long base = inc - run;
         for (int w = 0; w < warp; ++w) base += wsum[w];
         for (int s = s0; s < s1; ++s) pre[s] += base;
@@ -695,8 +697,11 @@ cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work&
 
 int kv4_arrive_words(int num_sms) { return 2 * num_sms; }   // a CTA of the one kernel, a part of the other
 
-size_t kv4_part_floats(int hd, int num_sms) {
-    const size_t x = kv4_decode_part_floats(hd, num_sms), y = kv4_extend_part_floats(hd, num_sms);
+constexpr int FEW_ROWS = 16, FEW_ROWS_FEW_SEQS = 64;
+
+size_t kv4_part_floats(int hd, int num_sms, long long max_rows) {
+    const size_t x = kv4_decode_part_floats(hd, num_sms);
+    const size_t y = max_rows > FEW_ROWS ? kv4_extend_part_floats(hd, num_sms) : 0;
     return x > y ? x : y;
 }
 
@@ -708,7 +713,7 @@ size_t kv4_part_floats(int hd, int num_sms) {
 // side: 1 of 32768, 40 rows 36.0 / 40.2, 64 rows 39.4 / 40.4, 80 rows 45.6 / 50.2; 1 of 4096, 64
 // rows 19.4 / 26.8.
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st) {
-    const int few = (long long)a.n_seqs * a.s.nkv * 8 <= w.num_sms ? 64 : 16;
+    const int few = (long long)a.n_seqs * a.s.nkv * 8 <= w.num_sms ? FEW_ROWS_FEW_SEQS : FEW_ROWS;
     const cudaError_t e = launch_kv4_decode(a, few, w, st);
     if (e != cudaSuccess || (long long)a.max_new * (a.s.nq / a.s.nkv) <= few) return e;
     return launch_kv4_extend(a, few, w, st);

@@ -21,8 +21,6 @@
 // Few items: the chunks of an item are split over CTAs, the last one joins the parts.
 #include <math.h>
 
-#include <type_traits>
-
 #include "kv4.cuh"
 #include "kv4_row.cuh"
 #include "umma.cuh"
@@ -116,6 +114,7 @@ __device__ __forceinline__ void tmem_ld32_start(uint32_t t, uint32_t* r) {
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
 __device__ __forceinline__ void tmem_st32(uint32_t t, const uint32_t* r) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -236,12 +235,17 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
             return all;
         };
         // total chunks, a sequence's tiles taken as evenly spread between its first and last
+        // (as far as 2^18 a sequence: it only sets the share)
         int work = 0, pieces = 0, parts_n = 0, base, part0, unused;
+        bool descends = false;
         for (int s = s0; s < s1; ++s) {
             Seq r;
             seq(s, r);
-            if (r.qts) work += min(a.s.nkv * ((r.qts * (r.last + chunks(r.q, min(r.rows, (int)G::ROWS))) + 1) / 2), 1 << 20);
+            descends |= a.cu[s + 1] < a.cu[s];
+            const float both = (float)r.last + (float)chunks(r.q, min(r.rows, (int)G::ROWS));
+            if (r.qts) work += (int)fminf(0.5f * (float)a.s.nkv * (float)r.qts * both, 262144.f);
         }
+        if (__syncthreads_or(descends)) return;        // rows of several sequences (the other kernel reports it)
         work = block_sum(work, unused);
         const int share = max(8, (int)(1.25f * (float)work / (float)num_sms) + 1);   // pieces fill one wave
         auto splits_of = [&](const Seq& r) { return min(32, max(1, (r.last + share - 1) / share)); };
@@ -493,7 +497,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 mbar_arrive(pfull + bar);
             }
         }
-        // O, joined with the item's other parts where it was split
+        // O, joined with the item's other parts where it was split.
         // S of the last step came after the second but last product of its slot, so the phase waited for
         // here is that barrier's current one or the one just completed
         const int nc = p.c1 - p.c0;
@@ -542,8 +546,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 if (tid == 0) arrive[p.part] = 0u;
                 const int splits = p.splits;
                 const float* first_part = parts + (size_t)p.part * G::PART;
-                // weights of the parts by row (the buffers of K and V are free: every product is done), then each
-                // thread four elements of a row at a time
+                // weights of the parts by row (the buffers of K and V are free: every product is done)
                 float* wt = reinterpret_cast<float*>(sm + G::K);       // [splits][ROWS], 1 / sum at the end
                 if (tid < rows) {
                     const float* ml = first_part + (size_t)HD * G::ROWS + tid;
@@ -614,7 +617,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     } else if (tid < G::SOFT + G::KTH) {
         // ----------------------------------------------------------------- K
         const int wt = tid - G::SOFT;
-        // K: a thread widens KP runs of 32 elements
+        // a thread widens KP runs of 32 elements
         const int jj = wt % G::LPR, r0 = wt / G::LPR;
         const int rot = G::LPR == 4 ? jj & 2 : G::LPR == 8 ? jj >> 1 : 0;   // a quarter-warp's stores meet every bank once
         int id[G::KP];
@@ -887,6 +890,7 @@ cudaError_t kv4_extend_prepare() {
     return e;
 }
 
+// none for calls whose every row is the decode kernel's
 size_t kv4_extend_part_floats(int hd, int num_sms) {
     const size_t rows = hd <= 128 ? 256 : 128;
     return (size_t)EXTEND_PARTS * num_sms * rows * (hd + 2);

@@ -530,6 +530,60 @@ def test_sequences_out_of_range_are_skipped(q, news):
         kv.close()
 
 
+@pytest.mark.parametrize("news", [[1, 1, 1, 1], [20, 30, 3, 40]])
+def test_descending_offsets_compute_nothing(q, news):
+    lens = [40, 70, 9, 50]
+    kv, x, cu, table = _filled(q, lens, news, 8, 2, 64, 16, "F32", 8)
+    try:
+        for bad in ([0, cu[2], cu[1], cu[3], cu[4]], [cu[4], 0, cu[4], 0, cu[4]], [0, -3, cu[2], cu[3], cu[4]]):
+            out, lse = kv.attention(x, np.array(bad, np.int32), lens, table, "F32", max_new=x.shape[0])
+            assert kv.status() == 8
+            assert (out == 77.0).all() and (lse == 77.0).all()
+        out, lse = kv.attention(x, cu, lens, table, "F32")
+        assert kv.status() == 0
+        _check(kv, x, out, lse, cu, lens, table)
+    finally:
+        kv.close()
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_device_arrays_of_any_content_are_safe(q, seed):
+    """Offsets, lengths, tables and slots of any bits: nothing out of range is followed, rows of the
+    sequences that are in order are right, and the handle serves the next call."""
+    rng = np.random.default_rng(seed)
+    lens, news = [40, 70, 9, 50, 33], [1, 30, 3, 1, 17]
+    kv, x, cu, table = _filled(q, lens, news, 8, 2, 64, 16, "F32", 8)
+    try:
+        want, wl = kv.attention(x, cu, lens, table, "F32")
+        wild = lambda n: rng.integers(-2 ** 31, 2 ** 31, n).astype(np.int32)  # noqa: E731
+        kv.attention(x, wild(6), wild(5), wild(table.size).reshape(table.shape), "F32", max_new=x.shape[0])
+        kv.attention(x, np.sort(wild(6)), wild(5), wild(table.size).reshape(table.shape), "F32", max_new=x.shape[0])
+        kv.attention(x, cu, wild(5), wild(table.size).reshape(table.shape), "F32")
+        kv.status()
+        good = rng.permutation(5)[:2]
+        ln, tb = wild(5), wild(table.size).reshape(table.shape)
+        ln = np.where(ln > 0, -ln, ln)
+        ln[good], tb[good] = np.array(lens)[good], table[good]
+        out, lse = kv.attention(x, cu, ln, tb, "F32")
+        assert kv.status() == 8
+        for s in range(5):
+            rows = slice(int(cu[s]), int(cu[s + 1]))
+            if s in good:
+                assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], wl[rows])
+            else:
+                assert (out[rows] == 77.0).all()
+        before = {n: t.clone() for n, t in kv.t.items()}
+        kv.append(x[:, :128], x[:, 128:256], cuda(rng.integers(2 ** 40, 2 ** 62, x.shape[0])), ks=512, vs=512)
+        assert kv.status() == 8
+        assert all(torch.equal(kv.t[n], before[n]) for n in before)
+        kv.plan(wild(5), wild(5), wild(table.size).reshape(table.shape), wild(kv.n_pages), int(wild(1)[0]), 50)
+        kv.status()
+        again, _ = kv.attention(x, cu, lens, table, "F32")
+        assert kv.status() == 0 and torch.equal(again, want)
+    finally:
+        kv.close()
+
+
 # --------------------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", ["F32", "BF16"])
