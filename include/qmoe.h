@@ -414,8 +414,8 @@ qmoe_status qmoe_kv4_append(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const voi
  * exact in fp16).  A sequence whose offsets, length or new tokens are out of range
  * (negative, past the table row, n_tokens or max_new) is skipped, a position whose
  * page id is out of range counts as not visible, and offsets that descend anywhere
- * leave all rows as they were; each sets QMOE_ERR_DEVICE_CHECK.  Row addresses, strides in bytes and out 16-byte aligned;
- * out must not overlap q. */
+ * leave all rows as they were; each sets QMOE_ERR_DEVICE_CHECK.  Row addresses,
+ * strides in bytes and out 16-byte aligned; out must not overlap q. */
 qmoe_status qmoe_kv4_attention(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const void* q,
                                qmoe_dtype q_t, int64_t q_stride, int n_seqs, int n_tokens,
                                int max_new, const int32_t* cu_tokens, const int32_t* seq_len,

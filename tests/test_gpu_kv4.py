@@ -584,6 +584,140 @@ def test_device_arrays_of_any_content_are_safe(q, seed):
         kv.close()
 
 
+@pytest.mark.parametrize("dtype", ["F32", "BF16"])
+@pytest.mark.parametrize("nq,nkv,hd,page,lens,news", [
+    (8, 1, 128, 64, [6000], [24]), (4, 2, 64, 16, [5000, 90], [70, 40]), (2, 2, 256, 32, [2900], [130]),
+    (32, 1, 64, 16, [4100, 7, 2000], [5, 1, 9])])
+def test_chunks_of_a_long_context_split_over_the_gpu(q, nq, nkv, hd, page, lens, news, dtype):
+    kv, x, cu, table = _filled(q, lens, news, nq, nkv, hd, page, dtype, 77)
+    try:
+        out, lse = kv.attention(x, cu, lens, table, dtype)
+        assert kv.status() == 0
+        _check(kv, x, out, lse, cu, lens, table)
+        last = (lens[0] - 1) // page
+        table[0, 3], table[0, last // 2], table[0, last] = -1, kv.n_pages, -2 ** 31
+        out, lse = kv.attention(x, cu, lens, table, dtype)
+        assert kv.status() == 8
+        _check(kv, x, out, lse, cu, lens, table)
+    finally:
+        kv.close()
+
+
+def test_the_most_sequences(q):
+    rng = np.random.default_rng(3)
+    n = 4096
+    lens = rng.integers(0, 40, n)
+    news = np.where(rng.uniform(size=n) < 0.9, 1, rng.integers(0, 20, n))
+    kv, x, cu, table = _filled(q, lens, news, 4, 1, 64, 16, "BF16", 6)
+    try:
+        out, lse = kv.attention(x, cu, lens, table, "BF16")
+        assert kv.status() == 0
+        _check(kv, x, out, lse, cu, lens, table)
+    finally:
+        kv.close()
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [20, 30, 3]])
+def test_caches_past_32_bits(q, news):
+    """5.2e9 bytes of codes each for K and V: the same rows as from a small cache, bit for bit."""
+    lens, nq, nkv, hd, page, n_pages = [40, 170, 9], 16, 2, 128, 64, 640_000
+    kv, x, cu, table = _filled(q, lens, news, nq, nkv, hd, page, "F16", 8)
+    big = Kv(q, nq, nkv, hd, page, n_pages, 3, 300, kv.width, 0, 8)
+    try:
+        assert big.t["k_codes"].numel() > 2 ** 32
+        far = np.where(table >= 0, n_pages - 1 - 70_000 * table, -1).astype(np.int32)
+        slots = lambda t: np.array([int(t[s, p // page]) * page + p % page  # noqa: E731
+                                    for s in range(3) for p in range(lens[s])], np.int64)
+        rows = torch.randn(2, sum(lens), nkv * hd, device="cuda")
+        kv.append(rows[0], rows[1], cuda(slots(table)))
+        big.append(rows[0], rows[1], cuda(slots(far)))
+        want, wl = kv.attention(x, cu, lens, table, "F16")
+        out, lse = big.attention(x, cu, lens, far, "F16")
+        assert kv.status() == 0 and big.status() == 0
+        assert torch.equal(out, want) and torch.equal(lse, wl)
+        st, r = big.plan(np.array([60, 0, 0], np.int32), np.array([10, 70, 1], np.int32),
+                         np.where(np.arange(kv.width) == 0, far[0, 0], -1) * np.ones((3, 1), np.int32),
+                         np.array([5, n_pages - 2, 6, n_pages - 1] + [-9] * (n_pages - 4), np.int32), 4, 81)
+        assert st == 0 and r["slots"][[4, 10, 80]].tolist() == [(n_pages - 1) * 64, 6 * 64, 5 * 64]
+    finally:
+        kv.close()
+        big.close()
+
+
+@pytest.mark.parametrize("nq,new", [(8, 1), (64, 2)])
+def test_rows_past_32_bits_apart(q, nq, new):
+    lens, nkv, hd, far = [40, 70], 1, 64, 2 ** 31 + 8
+    kv, x, cu, table = _filled(q, lens, [new, new], nq, nkv, hd, 16, "F16", 5)
+    try:
+        want, _ = kv.attention(x, cu, lens, table, "F16")
+        t, row = x.shape
+        wide = torch.empty((t - 1) * far + row, dtype=x.dtype, device="cuda")
+        view = wide.as_strided((t, row), (far, 1))
+        view.copy_(x)
+        out = torch.empty_like(wide)
+        kv.attention(view, cu, lens, table, "F16", qs=far, os=far, out=out, lse=False)
+        assert kv.status() == 0 and torch.equal(out.as_strided((t, row), (far, 1)), want)
+        rows = torch.randn(2, t, hd, device="cuda").to(x.dtype)
+        hat = torch.empty(4, t, hd, device="cuda")
+        slots = cuda(np.arange(t))
+        kv.append(rows[0], rows[1], slots, "F16", hat[0], hat[1])
+        a, b = wide.as_strided((t, hd), (far, 1)), out.as_strided((t, hd), (far, 1))
+        a.copy_(rows[0])
+        b.copy_(rows[1])
+        kv.append(a, b, slots, "F16", hat[2], hat[3], ks=far, vs=far)
+        assert kv.status() == 0 and torch.equal(hat[:2], hat[2:])
+    finally:
+        kv.close()
+
+
+def test_two_handles_on_two_streams(q):
+    lens, news = [2000, 70, 900], [1, 30, 5]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    sets = [_filled(q, lens, news, 8, 2, 64, 16, "BF16", 8 + i, stream=s.cuda_stream) for i, s in enumerate(streams)]
+    try:
+        want = []
+        for kv, x, cu, table in sets:
+            torch.cuda.synchronize()
+            want.append(kv.attention(x, cu, lens, table, "BF16"))
+            assert kv.status() == 0
+        dev = [(cuda(cu), cuda(np.array(lens, np.int32)), cuda(table)) for _, _, cu, table in sets]
+        outs = [[(torch.empty_like(w[0]), torch.empty_like(w[1])) for _ in range(40)] for w in want]
+        torch.cuda.synchronize()
+        for i in range(40):
+            for (kv, x, _, _), d, o in zip(sets, dev, outs):
+                q.qmoe_kv4_attention(kv.h, kv.cache, x, q.DTYPE["BF16"], 0, 3, x.shape[0], 30, *d, kv.hd ** -0.5,
+                                     o[i][0], q.DTYPE["BF16"], 0, o[i][1])
+        for (kv, *_), w, o in zip(sets, want, outs):
+            assert kv.status() == 0
+            assert all(torch.equal(a, w[0]) and torch.equal(b, w[1]) for a, b in o)
+    finally:
+        for kv, *_ in sets:
+            kv.close()
+
+
+def test_a_handle_that_only_decodes(q):
+    """max_tokens of few rows: no room for parts of prompt chunks, and none is needed."""
+    nq, nkv, hd, page = 8, 2, 128, 16
+    lens = [3000 + 16 * i for i in range(20)]
+    kv, x, cu, table = _filled(q, lens, [1] * 4 + [0] * 16, nq, nkv, hd, page, "F32", 8)
+    small = Kv(q, nq, nkv, hd, page, kv.n_pages, 20, 4, kv.width)
+    assert q.qmoe_kv4_workspace_bytes(q.make_kv4_config(nq, nkv, hd, page, 9, 20, 4, 9)) < 8 << 20
+    try:
+        for n in (20, 2):
+            c, ln = cu[:n + 1].copy(), lens[:n]
+            c[-1] = 4
+            if n == 2:
+                c[1] = 1                                           # one and three new tokens
+            want, wl = kv.attention(x, c, ln, table, "F32")
+            q.qmoe_kv4_attention(small.h, kv.cache, x, 0, 0, n, 4, 4, cuda(c), cuda(np.array(ln, np.int32)),
+                                 cuda(table), hd ** -0.5, want2 := torch.empty_like(want), 0, 0, None)
+            assert kv.status() == 0 and small.status() == 0 and torch.equal(want2, want)
+            _check(kv, x, want, wl, c, ln, table)
+    finally:
+        kv.close()
+        small.close()
+
+
 # --------------------------------------------------------------------------- together
 
 @pytest.mark.parametrize("dtype", ["F32", "BF16"])
