@@ -76,21 +76,22 @@ struct Kv4AttnArgs {
     int* status;
 };
 // Attention: sequences of at most few_rows rows (new tokens x heads of a group) by
-// launch_kv4_decode, the others by launch_kv4_extend.
-// Workspace of the attention, zero between launches but for `parts`.
+// launch_kv4_decode, the others by launch_kv4_extend.  The two may run side by side, so
+// each has its own workspace, zero between launches but for the parts.
 struct Kv4Work {
-    float* parts;         // [kv4_part_floats] parts of items that several CTAs share
-    unsigned* arrive;     // [kv4_arrive_words] arrival counters of those items
+    float *parts, *ext_parts;          // parts of items that several CTAs share
+    unsigned *arrive, *ext_arrive;     // [kv4_arrive_words] each: arrival counters of those items
     int num_sms;
 };
+constexpr int KV4_FEW_ROWS = 16;       // few_rows at least
 size_t kv4_decode_part_floats(int hd, int num_sms);
-size_t kv4_extend_part_floats(int hd, int num_sms);
+size_t kv4_extend_part_floats(int hd, int num_sms, long long max_rows);   // rows: tokens x heads of a group
 cudaError_t kv4_decode_prepare();
 cudaError_t kv4_extend_prepare();
-cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
+// behind: launched right after launch_kv4_extend on the stream
+cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st);
 cudaError_t launch_kv4_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
 int kv4_arrive_words(int num_sms);
-size_t kv4_part_floats(int hd, int num_sms, long long max_rows);   // rows: tokens x heads of a group
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st);
 
 // What qmoe_step_kv4 needs of a handle.

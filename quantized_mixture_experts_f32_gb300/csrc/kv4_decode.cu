@@ -130,7 +130,8 @@ __device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) { re
 
 template <int HD, int TERMS, int NR>
 __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
-    kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, float* __restrict__ parts, unsigned* __restrict__ arrive) {
+    kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, int behind_extend, float* __restrict__ parts,
+                      unsigned* __restrict__ arrive) {
     using G = DGeo<HD, TERMS, NR>;
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t* ring = sm;
@@ -143,8 +144,15 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, j = lane & 3;             // operand row (position, element run); a pair of q rows
     const int group = a.s.nq / a.s.nkv;
-    pdl_wait();
+    // Behind the prompt kernel nothing is waited for: it started its dependents after its own wait, so what it
+    // waited for is complete, and it writes nothing that is read here.  The last CTA waits for it before it
+    // ends, for the sake of what comes next; the others make room for each other.
+    if (!behind_extend) pdl_wait();
+    else __threadfence();
     pdl_launch_dependents();
+    auto leave = [&] {
+        if (behind_extend && blockIdx.x == gridDim.x - 1) pdl_wait();
+    };
 
     // units of every sequence, as prefix sums
     {
@@ -167,7 +175,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
             if (lane >= d) inc += o;
         }
         if (lane == 31) wsum[warp] = inc;
-        if (__syncthreads_or(descends)) return;        // rows of several sequences; the status says so
+        if (__syncthreads_or(descends)) return leave();            // rows of several sequences; the status says so
         long long base = inc - run;
         for (int w = 0; w < warp; ++w) base += wsum[w];
         for (int s = s0; s < s1; ++s) pre[s] += base;
@@ -176,7 +184,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     __syncthreads();
     const long long W = pre[a.n_seqs];
     const int Gn = (int)min((long long)gridDim.x, W), me = blockIdx.x;
-    if (me >= Gn) return;
+    if (me >= Gn) return leave();
     const long long u_end = unit_begin(W, me + 1, Gn);
 
     // the segment that starts with unit u (one thread); tiles = 0: none
@@ -262,14 +270,13 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
             for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             const int e = kv4_exponent(big);
-            const Kv4Scale un = kv4_unscale(e);
-            const float fac = ldexpf(a.scale * 1.4426950408889634f * kg, e);
-            const float sign = fac < 0.f ? -un.b : un.b;            // z's largest is q.k's largest then
+            const float fac = kv4_factor(a.scale, kg, e);
+            const float un = fac < 0.f ? -kv4_pow2(-e) : kv4_pow2(-e);            // z's largest is q.k's largest then
             if (lane == 0) fac_s[buf][row] = fmaxf(fabsf(fac), 1e-38f);  // not 0: -inf stays -inf, and 1e-38 q.k is 0
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
                 uint32_t hi, lo;
-                kv4_split(v[i].x * un.a * sign, v[i].y * un.a * sign, hi, lo);
+                kv4_split(v[i].x * un, v[i].y * un, hi, lo);
                 // element d -> lane jj's wd-th; fragment: step wd / 4, register (wd / 2) % 2.
                 // A lane's 16 bytes: TERMS = 1 two steps, TERMS = 2 the two terms of one.
                 const int d = 2 * lane + 64 * i;
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 
     if (tid == 0) describe(unit_begin(W, me, Gn), seg_s[0]);
     __syncthreads();
-    if (seg_s[0].tiles == 0) return;
+    if (seg_s[0].tiles == 0) return leave();
     issue(seg_s[0], seg_s[0].t0, true);
     take_q(seg_s[0], 0);
     __syncthreads();
@@ -643,22 +650,22 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 }
             }
         }
-        if (seg_s[cur ^ 1].tiles == 0) return;
+        if (seg_s[cur ^ 1].tiles == 0) return leave();
         __syncthreads();                               // the next segment's q is there, the join is read
     }
 }
 
 template <int HD, int TERMS, int NR>
-cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
+cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st) {
     using G = DGeo<HD, TERMS, NR>;
     return launch_pdl(kv4_decode_kernel<HD, TERMS, NR>, dim3(w.num_sms * (HD == 256 ? 1 : 2)), dim3(DT),
-                      G::smem(a.n_seqs), st, a, few_rows, w.parts, w.arrive);
+                      G::smem(a.n_seqs), st, a, few_rows, (int)behind, w.parts, w.arrive);
 }
 
 template <int HD, int TERMS>
-cudaError_t pick_rows(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
+cudaError_t pick_rows(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st) {
     const bool two = (long long)a.max_new * (a.s.nq / a.s.nkv) > 8;
-    return two ? launch_decode<HD, TERMS, 2>(a, few_rows, w, st) : launch_decode<HD, TERMS, 1>(a, few_rows, w, st);
+    return two ? launch_decode<HD, TERMS, 2>(a, few_rows, behind, w, st) : launch_decode<HD, TERMS, 1>(a, few_rows, behind, w, st);
 }
 
 }  // namespace
@@ -686,24 +693,16 @@ cudaError_t kv4_decode_prepare() {
 // a grid has two CTAs a multiprocessor at most, and each leaves two parts of 16 rows at most
 size_t kv4_decode_part_floats(int hd, int num_sms) { return (size_t)4 * num_sms * 16 * (hd + 2); }
 
-cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
+cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st) {
     const bool two = a.q_t == KV4_F32;
     switch (a.s.hd) {
-        case 64: return two ? pick_rows<64, 2>(a, few_rows, w, st) : pick_rows<64, 1>(a, few_rows, w, st);
-        case 128: return two ? pick_rows<128, 2>(a, few_rows, w, st) : pick_rows<128, 1>(a, few_rows, w, st);
-        default: return two ? pick_rows<256, 2>(a, few_rows, w, st) : pick_rows<256, 1>(a, few_rows, w, st);
+        case 64: return two ? pick_rows<64, 2>(a, few_rows, behind, w, st) : pick_rows<64, 1>(a, few_rows, behind, w, st);
+        case 128: return two ? pick_rows<128, 2>(a, few_rows, behind, w, st) : pick_rows<128, 1>(a, few_rows, behind, w, st);
+        default: return two ? pick_rows<256, 2>(a, few_rows, behind, w, st) : pick_rows<256, 1>(a, few_rows, behind, w, st);
     }
 }
 
 int kv4_arrive_words(int num_sms) { return 2 * num_sms; }   // a CTA of the one kernel, a part of the other
-
-constexpr int FEW_ROWS = 16, FEW_ROWS_FEW_SEQS = 64;
-
-size_t kv4_part_floats(int hd, int num_sms, long long max_rows) {
-    const size_t x = kv4_decode_part_floats(hd, num_sms);
-    const size_t y = max_rows > FEW_ROWS ? kv4_extend_part_floats(hd, num_sms) : 0;
-    return x > y ? x : y;
-}
 
 // Which kernel a sequence's rows (new tokens x heads of the group) go to.  The decode kernel
 // reads and widens the cache once per 16 rows, the prompt kernel once per 256, with a dearer start
@@ -712,11 +711,19 @@ size_t kv4_part_floats(int hd, int num_sms, long long max_rows) {
 // 33.8 / 42.3, 24 rows 49 / 42.  With few sequences the passes of the decode kernel run side by
 // side: 1 of 32768, 40 rows 36.0 / 40.2, 64 rows 39.4 / 40.4, 80 rows 45.6 / 50.2; 1 of 4096, 64
 // rows 19.4 / 26.8.
+//
+// The prompt kernel goes first: its CTAs do not end together, and the decode kernel's, smaller and
+// more, run where it has ended (24 requests of 300-6000 positions, 7 of them with up to 500 new
+// tokens: NEW us; the decode kernel first, OLD us).
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st) {
-    const int few = (long long)a.n_seqs * a.s.nkv * 8 <= w.num_sms ? FEW_ROWS_FEW_SEQS : FEW_ROWS;
-    const cudaError_t e = launch_kv4_decode(a, few, w, st);
-    if (e != cudaSuccess || (long long)a.max_new * (a.s.nq / a.s.nkv) <= few) return e;
-    return launch_kv4_extend(a, few, w, st);
+    constexpr int few_alone = 64;
+    const int few = (long long)a.n_seqs * a.s.nkv * 8 <= w.num_sms ? few_alone : KV4_FEW_ROWS;
+    const bool prompts = (long long)a.max_new * (a.s.nq / a.s.nkv) > few;
+    if (prompts) {
+        const cudaError_t e = launch_kv4_extend(a, few, w, st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kv4_decode(a, few, prompts, w, st);
 }
 
 }  // namespace qmoe

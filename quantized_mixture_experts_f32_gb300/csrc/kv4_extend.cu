@@ -48,7 +48,9 @@ struct EGeo {
     static constexpr int RPP = KTH / LPR;                            // positions the K threads take at a time
     static constexpr int KP = (KC + RPP - 1) / RPP;
     static constexpr int PART = ROWS * (HD + 2);                     // floats of a part
-    static_assert(33 * ROWS * 4 <= 2 * BUF * KT, "the weights of a join take the buffers of K and V");
+    static constexpr int SPLITS = 31;                                // of an item at most
+    static_assert(ROWS * HD * 4 <= V, "O passes through the tiles of Q and K on its way out");
+    static_assert((SPLITS + 1) * ROWS * 4 <= BUF * KT, "the weights of a join take the buffers of V");
 };
 
 // The MMA warp runs its loop as a whole, so that descriptors and addresses stay in
@@ -189,11 +191,28 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
              *pfull = bars + 12, *odone = bars + 16, *qfull = bars + 20;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
     __shared__ int wsum[G::THREADS / 32];
+    __shared__ int3 wsum3[G::THREADS / 32];
     __shared__ Piece piece_s;
-    __shared__ int last_s;
+    __shared__ int last_s, joined_s;
+    __shared__ long long row_at[G::SOFT];              // bytes to where a row of the item is stored
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int group = a.s.nq / a.s.nkv;
-    if (tid == 0) piece_s.s = -1;
+    if (tid == 0) {
+        piece_s.s = -1;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(kfull + i, G::KTH);
+            mbar_init(kempty + i, 1);
+            mbar_init(vfull + i, G::VTH);
+            mbar_init(vempty + i, 1);
+        }
+        for (int i = 0; i < 2 * NT; ++i) {
+            mbar_init(sfull + i, 1);
+            mbar_init(pfull + i, 128);
+            mbar_init(odone + i, 1);
+        }
+        mbar_init(qfull, G::SOFT);
+        fence_barrier_init();
+    }
     pdl_wait();
     pdl_launch_dependents();
 
@@ -216,79 +235,85 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
             r.qts = r.rows > few_rows ? (r.rows + G::ROWS - 1) / G::ROWS : 0;
             r.last = r.qts ? chunks(r.q, r.rows) : 0;
         };
-        auto block_sum = [&](int v, int& before) {     // sum over the CTA, and over the threads before
-            int inc = v;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, inc, d);
-                if (lane >= d) inc += o;
-            }
-            __syncthreads();
-            if (lane == 31) wsum[warp] = inc;
-            __syncthreads();
-            int all = 0;
-            before = inc - v;
-            for (int w = 0; w < T / 32; ++w) {
-                if (w < warp) before += wsum[w];
-                all += wsum[w];
-            }
-            return all;
-        };
+        // with no more sequences than threads a thread's only one is looked up once
+        const bool single = per == 1;
+        Seq one;
+        one.qts = 0;
+        bool descends = false;
         // total chunks, a sequence's tiles taken as evenly spread between its first and last
         // (as far as 2^18 a sequence: it only sets the share)
-        int work = 0, pieces = 0, parts_n = 0, base, part0, unused;
-        bool descends = false;
+        int work = 0;
         for (int s = s0; s < s1; ++s) {
-            Seq r;
-            seq(s, r);
+            seq(s, one);
             descends |= a.cu[s + 1] < a.cu[s];
-            const float both = (float)r.last + (float)chunks(r.q, min(r.rows, (int)G::ROWS));
-            if (r.qts) work += (int)fminf(0.5f * (float)a.s.nkv * (float)r.qts * both, 262144.f);
+            const float both = (float)one.last + (float)chunks(one.q, min(one.rows, (int)G::ROWS));
+            if (one.qts) work += (int)fminf(0.5f * (float)a.s.nkv * (float)one.qts * both, 262144.f);
         }
+        work = __reduce_add_sync(0xffffffffu, work);
+        if (lane == 0) wsum[warp] = work;
         if (__syncthreads_or(descends)) return;        // rows of several sequences (the other kernel reports it)
-        work = block_sum(work, unused);
+        work = 0;
+#pragma unroll
+        for (int w = 0; w < T / 32; ++w) work += wsum[w];
         const int share = max(8, (int)(1.25f * (float)work / (float)num_sms) + 1);   // pieces fill one wave
-        auto splits_of = [&](const Seq& r) { return min(32, max(1, (r.last + share - 1) / share)); };
+        auto splits_of = [&](const Seq& r) { return min(G::SPLITS, max(1, (r.last + share - 1) / share)); };
+        int items = 0, pieces = 0, parts_n = 0;
         for (int s = s0; s < s1; ++s) {
-            Seq r;
-            seq(s, r);
-            const int k = splits_of(r), items = a.s.nkv * r.qts;
-            pieces += items * k;
-            if (k > 1) parts_n += items * k;
+            if (!single) seq(s, one);
+            const int k = splits_of(one), it = a.s.nkv * one.qts;
+            items += it;
+            pieces += it * k;
+            if (k > 1) parts_n += it * k;
         }
-        const int all = block_sum(pieces, base), all_parts = block_sum(parts_n, part0);
+        // sums over the CTA, and over the threads before
+        int inc_i = items, inc_p = pieces, inc_n = parts_n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int oi = __shfl_up_sync(0xffffffffu, inc_i, d), op = __shfl_up_sync(0xffffffffu, inc_p, d),
+                      on = __shfl_up_sync(0xffffffffu, inc_n, d);
+            if (lane >= d) {
+                inc_i += oi;
+                inc_p += op;
+                inc_n += on;
+            }
+        }
+        if (lane == 31) wsum3[warp] = make_int3(inc_i, inc_p, inc_n);
+        __syncthreads();
+        int all = 0, all_parts = 0, base_i = inc_i - items, base_p = inc_p - pieces, part0 = inc_n - parts_n;
+#pragma unroll
+        for (int w = 0; w < T / 32; ++w) {
+            const int3 o = wsum3[w];
+            all += o.y;
+            all_parts += o.z;
+            if (w < warp) {
+                base_i += o.x;
+                base_p += o.y;
+                part0 += o.z;
+            }
+        }
         // not more CTAs or parts than there are: every item whole then
         const bool whole = all > (int)gridDim.x || all_parts > max_parts;
-        if (whole) {
-            pieces = 0;
-            for (int s = s0; s < s1; ++s) {
-                Seq r;
-                seq(s, r);
-                pieces += a.s.nkv * r.qts;
-            }
-            block_sum(pieces, base);
-        }
         const int me = blockIdx.x;
-        if (me >= base && me < base + pieces) {
+        int base = whole ? base_i : base_p;
+        if (me >= base && me < base + (whole ? items : pieces)) {
             for (int s = s0; s < s1; ++s) {
-                Seq r;
-                seq(s, r);
-                const int k = whole ? 1 : splits_of(r), mine = a.s.nkv * r.qts * k;
+                if (!single) seq(s, one);
+                const int k = whole ? 1 : splits_of(one), mine = a.s.nkv * one.qts * k;
                 if (me < base + mine) {
                     // the last rows see the most positions: they start first
-                    const int at = me - base, split = at % k, item = at / k, qt = r.qts - 1 - item / a.s.nkv;
+                    const int at = me - base, split = at % k, item = at / k, qt = one.qts - 1 - item / a.s.nkv;
                     Piece p;
                     p.s = s;
                     p.g = item % a.s.nkv;
                     p.row0 = qt * G::ROWS;
-                    p.q0 = r.q.q0;
-                    p.n = r.q.n;
-                    p.len = r.q.len;
-                    const int nch = chunks(r.q, min(p.row0 + G::ROWS, r.rows));
+                    p.q0 = one.q.q0;
+                    p.n = one.q.n;
+                    p.len = one.q.len;
+                    const int nch = chunks(one.q, min(p.row0 + G::ROWS, one.rows));
                     p.splits = max(1, min(k, nch / 4));            // four chunks to a split at least
                     p.split = split;
-                    p.c0 = (int)((long long)nch * split / p.splits);
-                    p.c1 = (int)((long long)nch * (split + 1) / p.splits);
+                    p.c0 = nch * split / p.splits;
+                    p.c1 = nch * (split + 1) / p.splits;
                     p.part = part0 + item * k;
                     if (split < p.splits) piece_s = p;
                     break;
@@ -304,21 +329,6 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     const int32_t* table = a.table + (size_t)p.s * a.s.width;
     const int rows = min(G::ROWS, p.n * group - p.row0);
     const int nact = (rows + 127) / 128;               // tiles with rows
-    if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(kfull + i, G::KTH);
-            mbar_init(kempty + i, 1);
-            mbar_init(vfull + i, G::VTH);
-            mbar_init(vempty + i, 1);
-        }
-        for (int i = 0; i < 2 * NT; ++i) {
-            mbar_init(sfull + i, 1);
-            mbar_init(pfull + i, 128);
-            mbar_init(odone + i, 1);
-        }
-        mbar_init(qfull, G::SOFT);
-        fence_barrier_init();
-    }
     if (warp == 0) tmem_alloc(tslot, 512);
     tc_fence_before();
     __syncthreads();
@@ -334,76 +344,74 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         auto head_of = [&](int row, int tok) { return p.g * group + p.row0 + row - tok * group; };
         const int lim = tid < rows ? len - p.n + tok_of(tid) + 1 : 0;
         const int lim_min = len - p.n + tok_of(tid & ~31) + 1;                   // the warp's first row's
-        float fac;
-        {
-            // the warp's 32 rows of q, 16 bytes a lane, copied to where their fp16 terms belong (F32
-            // elements fill the places of both); then each thread scales its own row to [1, 2) by a
-            // power of two and splits it in place
+        // where the thread's row starts: in q, and in out
+        const int tok = tok_of(tid), h = head_of(tid, tok);
+        float fac = 0.f;
+        if (x < nact) {
+            // Eight elements of a row a lane, first as they are to where their fp16 terms belong (F32 elements
+            // fill the places of both), all at once; then the row's largest by shuffles, and the row scaled to
+            // [1, 2) by a power of two (to what is exact below 2^-126) and split in place.
             constexpr int LR = HD / 8, RW = 32 / LR;   // lanes of a row, rows at a time
-            const float fac0 = a.scale * 1.4426950408889634f * a.c.kg[p.g];
-            uint8_t* qs = sm + G::Q + x * TERMS * G::QT;
-            {
-                const int d = (lane % LR) * 8, sub = lane / LR;
-                long long mine = -1;                   // where this thread's row starts
-                if (tid < rows) {
-                    const int tok = tok_of(tid), h = head_of(tid, tok);
-                    mine = ((long long)(p.q0 + tok) * a.q_stride + (long long)h * HD) * (TERMS == 2 ? 4 : 2);
-                }
+            const float kg = a.c.kg[p.g];
+            // of scale * kg: z's largest is q.k's largest then
+            const uint32_t sign = (int)(__float_as_uint(a.scale) ^ __float_as_uint(kg)) < 0 ? 0x80008000u : 0u;
+            const int d = (lane % LR) * 8, sub = lane / LR;
+            const long long mine = tid < rows ? ((long long)(p.q0 + tok) * a.q_stride + (long long)h * HD) * (TERMS == 2 ? 4 : 2) : -1;
+            uint8_t* qs = sm + G::Q + x * TERMS * G::QT + (d >> 6) * 16384;
+            auto word = [&](int r) { return qs + sw128_offset((tid & 96) + r + sub, d & 63); };
 #pragma unroll 4
-                for (int r = 0; r < 32; r += RW) {
-                    const long long at = __shfl_sync(0xffffffffu, mine, r + sub);
-                    uint8_t* to = qs + (d >> 6) * 16384 + sw128_offset((tid & 96) + r + sub, d & 63);
+            for (int r = 0; r < 32; r += RW) {
+                const long long at = __shfl_sync(0xffffffffu, mine, r + sub);
 #pragma unroll
-                    for (int z = 0; z < TERMS; ++z) {
-                        if (at >= 0) cp_async_cg16(to + z * G::QT, static_cast<const uint8_t*>(a.q) + at + d * (TERMS == 2 ? 4 : 2) + 16 * z);
-                        else *reinterpret_cast<uint4*>(to + z * G::QT) = make_uint4(0, 0, 0, 0);
-                    }
+                for (int z = 0; z < TERMS; ++z) {
+                    if (at >= 0) cp_async_cg16(word(r) + z * G::QT, static_cast<const uint8_t*>(a.q) + at + d * (TERMS == 2 ? 4 : 2) + 16 * z);
+                    else *reinterpret_cast<uint4*>(word(r) + z * G::QT) = make_uint4(0, 0, 0, 0);
                 }
             }
             cp_async_wait_all();
-            __syncwarp();
             int exponent = 0;
-            auto load_q = [&](int d, float (&v)[8]) {
-                const uint8_t* at = qs + (d >> 6) * 16384 + sw128_offset(tid & 127, d & 63);
-                uint4 raw[TERMS];
+            if (TERMS == 2 || a.q_t != KV4_F16 || sign) {          // fp16 rows are what they have to be
+                constexpr int RB = 32 / RW < 8 ? 32 / RW : 8;      // in flight
+#pragma unroll 1
+                for (int r0 = 0; r0 < 32; r0 += RB * RW) {
+                    float v[RB][8], big[RB];
 #pragma unroll
-                for (int z = 0; z < TERMS; ++z) raw[z] = *reinterpret_cast<const uint4*>(at + z * G::QT);
-                kv4_floats8(raw, a.q_t, v);
-            };
-            if (TERMS == 2 || a.q_t != KV4_F16) {      // fp16 rows are what they have to be
-                float big[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-                for (int d = 0; d < HD; d += 8) {
-                    float v[8];
-                    load_q(d, v);
+                    for (int i = 0; i < RB; ++i) {
+                        uint4 raw[TERMS];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) big[i] = max3(big[i], fabsf(v[i]), fabsf(v[4 + i]));
-                }
-                exponent = kv4_exponent(fmaxf(fmaxf(big[0], big[1]), fmaxf(big[2], big[3])));
-            }
-            if (TERMS == 2 || a.q_t != KV4_F16 || fac0 < 0.f) {
-                const Kv4Scale un = kv4_unscale(exponent);
-                const float ub = fac0 < 0.f ? -un.b : un.b;        // z's largest is q.k's largest then
-#pragma unroll 2
-                for (int d = 0; d < HD; d += 8) {
-                    float v[8];
-                    load_q(d, v);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float v0 = v[2 * i] * un.a * ub, v1 = v[2 * i + 1] * un.a * ub;
-                        if (TERMS == 2) kv4_split(v0, v1, hi[i], lo[i]);
-                        else hi[i] = kv4_pack(v0, v1);
+                        for (int z = 0; z < TERMS; ++z) raw[z] = *reinterpret_cast<const uint4*>(word(r0 + i * RW) + z * G::QT);
+                        kv4_floats8(raw, a.q_t, v[i]);
+                        big[i] = max3(max3(fabsf(v[i][0]), fabsf(v[i][1]), fabsf(v[i][2])),
+                                      max3(fabsf(v[i][3]), fabsf(v[i][4]), fabsf(v[i][5])), fmaxf(fabsf(v[i][6]), fabsf(v[i][7])));
                     }
-                    uint8_t* at = qs + (d >> 6) * 16384 + sw128_offset(tid & 127, d & 63);
-                    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (TERMS == 2) *reinterpret_cast<uint4*>(at + G::QT) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int o = LR / 2; o > 0; o >>= 1)
+#pragma unroll
+                        for (int i = 0; i < RB; ++i) big[i] = fmaxf(big[i], __shfl_xor_sync(0xffffffffu, big[i], o));
+#pragma unroll
+                    for (int i = 0; i < RB; ++i) {
+                        const int e = kv4_exponent(big[i]);
+                        const float un = kv4_pow2(-e);
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float v0 = v[i][2 * k] * un, v1 = v[i][2 * k + 1] * un;
+                            if (TERMS == 2) kv4_split(v0, v1, hi[k], lo[k]);
+                            else hi[k] = kv4_pack(v0, v1);
+                        }
+                        uint8_t* at = word(r0 + i * RW);
+                        *reinterpret_cast<uint4*>(at) = make_uint4(hi[0] ^ sign, hi[1] ^ sign, hi[2] ^ sign, hi[3] ^ sign);
+                        if (TERMS == 2) *reinterpret_cast<uint4*>(at + G::QT) = make_uint4(lo[0] ^ sign, lo[1] ^ sign, lo[2] ^ sign, lo[3] ^ sign);
+                        // the thread whose row it is keeps the exponent
+                        const int back = lane - r0 - i * RW, er = __shfl_sync(0xffffffffu, e, (back * LR) & 31);
+                        if (back >= 0 && back < RW) exponent = er;
+                    }
                 }
             }
-            fac = fmaxf(ldexpf(fabsf(fac0), exponent), 1e-38f);    // not 0: -inf stays -inf, and 1e-38 q.k is 0
+            fac = fmaxf(fabsf(kv4_factor(a.scale, kg, exponent)), 1e-38f);   // not 0: -inf stays -inf, and 1e-38 q.k is 0
             fence_proxy_async();
-            mbar_arrive(qfull);
         }
+        mbar_arrive(qfull);
         float m = -INFINITY, l = 0.f;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t tO = tmem + lanes + 256 + x * HD;
@@ -500,120 +508,168 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         // O, joined with the item's other parts where it was split.
         // S of the last step came after the second but last product of its slot, so the phase waited for
         // here is that barrier's current one or the one just completed
-        const int nc = p.c1 - p.c0;
         if (ok && x < nact && ns && !warp_wait(odone + 2 * x + ((ns - 1) & 1), ((ns - 1) >> 1) & 1)) ok = false;
         tc_fence_after();
-        const int tok = tok_of(tid), h = head_of(tid, tok);
-        bool write = ok && tid < rows;
+        if (!ns) named_bar(1, G::SOFT);                // q is no longer stored where O goes
+        const int split = p.split, splits = p.splits;
         const float vg = a.c.vg[p.g];
-        const size_t oat = (size_t)(p.q0 + tok) * a.out_stride + (size_t)h * HD;
-        if (p.splits == 1) {
-            const float inv = l == 0.f ? 0.f : vg / l;
-            for (int d = 0; d < HD && x < nact; d += 32) {
-                uint32_t o[32];
-                if (nc) tmem_ld32(tO + d, o);
-#pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    float v[8];
-#pragma unroll
-                    for (int y = 0; y < 8; ++y) v[y] = nc && l != 0.f ? __uint_as_float(o[k + y]) * inv : 0.f;
-                    if (write) kv4_store8(a.out, oat + d + k, a.out_t, v);
-                }
-            }
-        } else {
-            // part: O as float4 [HD/4][ROWS], then m, l [ROWS]
-            float* part = parts + (size_t)(p.part + p.split) * G::PART;
-            for (int d = 0; d < HD && x < nact; d += 32) {
+        // the CTA that comes last to the end of an item keeps its part; the others leave theirs to it
+        bool keeps = false;
+        if (splits > 1) {
+            named_bar(1, G::SOFT);
+            if (tid == 0) last_s = atomicAdd(arrive + p.part, 1u) == (unsigned)(splits - 1);
+            named_bar(1, G::SOFT);
+            keeps = last_s;
+        }
+        float* part = parts + (size_t)(p.part + split) * G::PART;            // O [ROWS][HD], then m, l [ROWS]
+        const bool to_part = splits > 1 && !keeps;
+        // A warp's rows of O in shared memory (every S is done: the tiles of Q and K are free), as they will
+        // be stored, rows in order with their 16-byte words permuted; then neighbouring lanes store
+        // neighbouring words (a thread storing its own row took twice as long).
+        uint8_t* mine = sm + (size_t)warp * 32 * HD * 4;
+        row_at[tid] = tid >= rows || !ok ? -1
+                      : to_part ? (long long)tid * HD * 4
+                                : ((long long)(p.q0 + tok) * a.out_stride + (long long)h * HD) * (a.out_t == KV4_F32 ? 4 : 2);
+        const int to_t = splits > 1 ? KV4_F32 : a.out_t, words = HD / (to_t == KV4_F32 ? 4 : 8);
+        if (x < nact) {
+            const float inv = splits > 1 ? 1.f : l == 0.f ? 0.f : vg / l;
+            const bool some = ns && (splits > 1 || l != 0.f);
+            uint8_t* row = mine + lane * words * 16;
+#pragma unroll 1
+            for (int d = 0; d < HD; d += 32) {
                 uint32_t o[32];
                 tmem_ld32(tO + d, o);
-                if (tid < rows) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4)
-                        reinterpret_cast<float4*>(part)[(size_t)((d + k) / 4) * G::ROWS + tid] =
-                            make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
-                                        __uint_as_float(o[k + 3]));
+                for (int k = 0; k < 32; ++k) o[k] = some ? __float_as_uint(__uint_as_float(o[k]) * inv) : 0u;
+                if (to_t == KV4_F32) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4*>(row + ((d / 4 + k) ^ (lane & 7)) * 16) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t u[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) u[y] = kv4_pack16(__uint_as_float(o[8 * k + 2 * y]), __uint_as_float(o[8 * k + 2 * y + 1]), to_t);
+                        *reinterpret_cast<uint4*>(row + ((d / 8 + k) ^ (lane & 7)) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
+                    }
                 }
             }
-            part[(size_t)HD * G::ROWS + tid] = m;
-            part[(size_t)(HD + 1) * G::ROWS + tid] = l;
-            __threadfence();
-            named_bar(1, G::SOFT);
-            if (tid == 0) last_s = atomicAdd(arrive + p.part, 1u) == (unsigned)(p.splits - 1);
-            named_bar(1, G::SOFT);
-            write = false;                             // below
-            if (last_s) {
-                __threadfence();
-                if (tid == 0) arrive[p.part] = 0u;
-                const int splits = p.splits;
-                const float* first_part = parts + (size_t)p.part * G::PART;
-                // weights of the parts by row (the buffers of K and V are free: every product is done)
-                float* wt = reinterpret_cast<float*>(sm + G::K);       // [splits][ROWS], 1 / sum at the end
-                if (tid < rows) {
-                    const float* ml = first_part + (size_t)HD * G::ROWS + tid;
-                    float mj = -INFINITY, lj = 0.f;
-#pragma unroll 8
-                    for (int y = 0; y < splits; ++y) mj = fmaxf(mj, __ldcg(ml + (size_t)y * G::PART));
-#pragma unroll 8
-                    for (int y = 0; y < splits; ++y) {
-                        const float li = __ldcg(ml + (size_t)y * G::PART + G::ROWS), mi = __ldcg(ml + (size_t)y * G::PART);
-                        const float w = li == 0.f ? 0.f : kv4_ex2(mi - mj);
-                        lj += li * w;
-                        wt[y * G::ROWS + tid] = w;
-                    }
-                    wt[splits * G::ROWS + tid] = lj == 0.f ? 0.f : vg / lj;
-                    if (ok && a.lse)
-                        a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] =
-                            lj == 0.f ? -INFINITY : (mj - KV4_P_UP + log2f(lj)) * 0.6931471805599453f;
-                }
-                named_bar(1, G::SOFT);
-                // eight elements of a row at a time, four of these in flight; neighbouring threads have
-                // neighbouring rows, as the parts do
-                const int total = rows * (HD / 8);
+            __syncwarp();
+            if (!keeps) {
+                uint8_t* base = to_part ? reinterpret_cast<uint8_t*>(part) : static_cast<uint8_t*>(a.out);
+                const int shift = __ffs(words) - 1;
 #pragma unroll 1
-                for (int i0 = tid; i0 < total; i0 += 4 * G::SOFT) {
-                    float v[4][8];
-                    const float4* pi[4];
-                    int row[4];
+                for (int i0 = lane; i0 < 32 * words; i0 += 8 * 32) {
+                    uint4 u[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int i = min(i0 + k * G::SOFT, total - 1), d8 = i / rows;
-                        row[k] = i - d8 * rows;
-                        pi[k] = reinterpret_cast<const float4*>(first_part) + (size_t)(2 * d8) * G::ROWS + row[k];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) v[k][y] = 0.f;
+                    for (int k = 0; k < 8; ++k) {
+                        const int i = i0 + 32 * k;
+                        u[k] = *reinterpret_cast<const uint4*>(mine + (i ^ ((i >> shift) & 7)) * 16);
                     }
-#pragma unroll 2
-                    for (int y = 0; y < splits; ++y)
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float4 u0 = __ldcg(pi[k] + (size_t)y * (G::PART / 4));
-                            const float4 u1 = __ldcg(pi[k] + (size_t)y * (G::PART / 4) + G::ROWS);
-                            const float w = wt[y * G::ROWS + row[k]];
-                            v[k][0] += u0.x * w;
-                            v[k][1] += u0.y * w;
-                            v[k][2] += u0.z * w;
-                            v[k][3] += u0.w * w;
-                            v[k][4] += u1.x * w;
-                            v[k][5] += u1.y * w;
-                            v[k][6] += u1.z * w;
-                            v[k][7] += u1.w * w;
-                        }
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int i = i0 + k * G::SOFT;
-                        if (i >= total || !ok) break;
-                        const float inv = wt[splits * G::ROWS + row[k]];
-#pragma unroll
-                        for (int y = 0; y < 8; ++y) v[k][y] *= inv;
-                        const int tk = tok_of(row[k]), hd = head_of(row[k], tk);
-                        kv4_store8(a.out, (size_t)(p.q0 + tk) * a.out_stride + (size_t)hd * HD + i / rows * 8, a.out_t, v[k]);
+                    for (int k = 0; k < 8; ++k) {
+                        const int i = i0 + 32 * k;
+                        const long long at = row_at[warp * 32 + (i >> shift)];
+                        if (at >= 0) *reinterpret_cast<uint4*>(base + at + 16 * (i & (words - 1))) = u[k];
                     }
                 }
             }
         }
-        if (write && a.lse)
-            a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] =
-                l == 0.f ? -INFINITY : (m - KV4_P_UP + log2f(l)) * 0.6931471805599453f;
+        auto log_sum = [&](float mr, float lr) { return lr == 0.f ? -INFINITY : (mr - KV4_P_UP + log2f(lr)) * 0.6931471805599453f; };
+        if (splits > 1) {
+            part[(size_t)HD * G::ROWS + tid] = m;
+            part[(size_t)(HD + 1) * G::ROWS + tid] = l;
+        }
+        if (splits == 1) {
+            if (ok && tid < rows && a.lse) a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] = log_sum(m, l);
+        } else if (to_part) {
+            __threadfence();
+            named_bar(1, G::SOFT);
+            if (tid == 0) atomicAdd(arrive + p.part + 1, 1u);
+        } else {
+            // The others are past their products: their parts are there in no more time than it takes to
+            // store one.
+            if (tid == 0) {
+                ok = grid_wait(arrive + p.part + 1, (unsigned)(splits - 1)) && ok;
+                arrive[p.part] = 0u;
+                arrive[p.part + 1] = 0u;
+                joined_s = ok;
+            }
+            named_bar(1, G::SOFT);
+            ok = joined_s && ok;
+            __threadfence();
+            const float* first_part = parts + (size_t)p.part * G::PART;
+            // weights of the parts by row
+            float* wt = reinterpret_cast<float*>(sm + G::V);           // [splits][ROWS], vg / sum at the end
+            if (tid < rows) {
+                const float* ml = first_part + (size_t)HD * G::ROWS + tid;
+                float mj = -INFINITY, lj = 0.f;
+#pragma unroll 8
+                for (int y = 0; y < splits; ++y) mj = fmaxf(mj, __ldcg(ml + (size_t)y * G::PART));
+#pragma unroll 8
+                for (int y = 0; y < splits; ++y) {
+                    const float li = __ldcg(ml + (size_t)y * G::PART + G::ROWS), mi = __ldcg(ml + (size_t)y * G::PART);
+                    const float w = li == 0.f ? 0.f : kv4_ex2(mi - mj);
+                    lj += li * w;
+                    wt[y * G::ROWS + tid] = w;
+                }
+                wt[splits * G::ROWS + tid] = lj == 0.f ? 0.f : vg / lj;
+                if (ok && a.lse) a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] = log_sum(mj, lj);
+            }
+            named_bar(1, G::SOFT);
+            // eight elements of a row at a time, four of these in flight
+            const int total = ok ? rows * (HD / 8) : 0;
+#pragma unroll 1
+            for (int i0 = tid; i0 < total; i0 += 4 * G::SOFT) {
+                float v[4][8];
+                const float4* pi[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = min(i0 + k * G::SOFT, total - 1), r = i / (HD / 8), w = i % (HD / 8) * 2;
+                    pi[k] = reinterpret_cast<const float4*>(first_part) + 2 * i;
+                    const float f = wt[split * G::ROWS + r];
+                    const uint8_t* row = sm + (size_t)r * HD * 4;
+                    const float4 u0 = *reinterpret_cast<const float4*>(row + (w ^ (r & 7)) * 16);
+                    const float4 u1 = *reinterpret_cast<const float4*>(row + ((w + 1) ^ (r & 7)) * 16);
+                    v[k][0] = u0.x * f;
+                    v[k][1] = u0.y * f;
+                    v[k][2] = u0.z * f;
+                    v[k][3] = u0.w * f;
+                    v[k][4] = u1.x * f;
+                    v[k][5] = u1.y * f;
+                    v[k][6] = u1.z * f;
+                    v[k][7] = u1.w * f;
+                }
+#pragma unroll 2
+                for (int z = 0; z < splits - 1; ++z) {
+                    const int y = z + (z >= split);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 u0 = __ldcg(pi[k] + (size_t)y * (G::PART / 4));
+                        const float4 u1 = __ldcg(pi[k] + (size_t)y * (G::PART / 4) + 1);
+                        const float f = wt[y * G::ROWS + min(i0 + k * G::SOFT, total - 1) / (HD / 8)];
+                        v[k][0] += u0.x * f;
+                        v[k][1] += u0.y * f;
+                        v[k][2] += u0.z * f;
+                        v[k][3] += u0.w * f;
+                        v[k][4] += u1.x * f;
+                        v[k][5] += u1.y * f;
+                        v[k][6] += u1.z * f;
+                        v[k][7] += u1.w * f;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k * G::SOFT, r = i / (HD / 8);
+                    if (i >= total) break;
+                    const float inv = wt[splits * G::ROWS + r];
+#pragma unroll
+                    for (int y = 0; y < 8; ++y) v[k][y] *= inv;
+                    kv4_store8(static_cast<uint8_t*>(a.out) + row_at[r], i % (HD / 8) * 8, a.out_t, v[k]);
+                }
+            }
+        }
     } else if (tid < G::SOFT + G::KTH) {
         // ----------------------------------------------------------------- K
         const int wt = tid - G::SOFT;
@@ -871,7 +927,7 @@ cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, 
     const long long ragged = rows / (few_rows + 1) < a.n_seqs ? rows / (few_rows + 1) : a.n_seqs;
     const long long grid = a.s.nkv * (rows / G::ROWS + ragged) + 2 * w.num_sms;
     return launch_pdl(kv4_extend_kernel<HD, TERMS>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, a, few_rows,
-                      w.parts, w.arrive, w.num_sms, EXTEND_PARTS * w.num_sms);
+                      w.ext_parts, w.ext_arrive, w.num_sms, EXTEND_PARTS * w.num_sms);
 }
 
 }  // namespace
@@ -890,8 +946,9 @@ cudaError_t kv4_extend_prepare() {
     return e;
 }
 
-// none for calls whose every row is the decode kernel's
-size_t kv4_extend_part_floats(int hd, int num_sms) {
+// none where every row is the decode kernel's
+size_t kv4_extend_part_floats(int hd, int num_sms, long long max_rows) {
+    if (max_rows <= KV4_FEW_ROWS) return 0;
     const size_t rows = hd <= 128 ? 256 : 128;
     return (size_t)EXTEND_PARTS * num_sms * rows * (hd + 2);
 }

@@ -27,21 +27,20 @@ __device__ __forceinline__ void kv4_split(float x, float y, uint32_t& hi, uint32
     lo = kv4_pack(x - __low2float(h), y - __high2float(h));
 }
 
-// The exponent e of a row's largest magnitude `big` (2^e <= big < 2^(e+1); 0 for zero,
-// infinity and NaN), and the factors that bring the row to [1, 2): two, as 2^-e alone
-// may be no fp32 number.
+// For a row whose largest magnitude is `big`, the e for which 2^-e brings it to [1, 2):
+// -126 .. 126, so that 2^-e is a normal number (a row below 2^-126 is a multiple of
+// 2^-149, and 2^126 of it exact in two fp16 terms; a 16-bit row's in one); 0 for zero,
+// infinity and NaN.
 __device__ __forceinline__ int kv4_exponent(float big) {
-    const uint32_t u = __float_as_uint(big);
-    if (u == 0u || u >= 0x7f800000u) return 0;
-    return u >= 0x00800000u ? (int)(u >> 23) - 127 : 31 - __clz(u) - 149;
+    const int e = (int)(__float_as_uint(big) >> 23) - 127;
+    return e == -127 && big == 0.f || e > 127 ? 0 : min(max(e, -126), 126);
 }
 __device__ __forceinline__ float kv4_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| < 127
-struct Kv4Scale {
-    float a, b;
-};
-__device__ __forceinline__ Kv4Scale kv4_unscale(int e) {
-    const int h = -e / 2;
-    return {kv4_pow2(h), kv4_pow2(-e - h)};
+
+// z of a row scaled by 2^-e, in powers of two, from its product with K's codes; the scale
+// meets 2^e first, so that neither a tiny scale nor a large row leaves fp32's range on the way
+__device__ __forceinline__ float kv4_factor(float scale, float global, int e) {
+    return ldexpf(scale, e) * (1.4426950408889634f * global);
 }
 
 // Eight E2M1 codes -> four half2, bytes in order.  One conversion a byte: naming the
@@ -109,6 +108,13 @@ __device__ __forceinline__ void kv4_floats8(const uint4 (&u)[N], int t, float (&
     }
 }
 
+// two values as F16 or BF16
+__device__ __forceinline__ uint32_t kv4_pack16(float x, float y, int t) {
+    if (t == KV4_F16) return kv4_pack(x, y);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
 // eight elements at a multiple of eight
 __device__ __forceinline__ void kv4_store8(void* p, size_t at, int t, const float* v) {
     if (t == KV4_F32) {
@@ -119,14 +125,7 @@ __device__ __forceinline__ void kv4_store8(void* p, size_t at, int t, const floa
     }
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (t == KV4_F16) {
-            w[i] = kv4_pack(v[2 * i], v[2 * i + 1]);
-        } else {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-    }
+    for (int i = 0; i < 4; ++i) w[i] = kv4_pack16(v[2 * i], v[2 * i + 1], t);
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -472,6 +472,38 @@ def test_rows_of_any_size(q, mag, news):
         kv.close()
 
 
+@pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
+@pytest.mark.parametrize("news", [[1, 1], [33, 20]])
+def test_rows_at_the_ends_of_their_type(q, news, dtype):
+    """Rows of subnormals and rows with the type's largest values: scaled before they are products' operands.
+    (The sums of products stay below fp32's largest number: few elements of the largest rows are not zero.)"""
+    lens = [40, 70]
+    kv, x, cu, table = _filled(q, lens, news, 8, 2, 64, 16, "F32", 23)
+    try:
+        info = torch.finfo(TORCH[dtype])
+        x = x.reshape(-1, 8, 64)
+        x[:, :4] *= info.smallest_normal / 2                       # heads 0 .. 3: some multiples of the smallest step
+        x[:, 4:, 2:] = 0
+        x[:, 4:, :2] = x[:, 4:, :2].sign() * info.max
+        x = x.reshape(-1, 512).to(TORCH[dtype])
+        assert torch.isfinite(x).all() and (x != 0).any(1).all()
+        for scale in (2.0 / float(x.abs().max()), min(1.0 / float(info.smallest_normal), 3e38)):
+            out, lse = kv.attention(x, cu, lens, table, dtype, scale=scale)
+            assert kv.status() == 0
+            heads = range(8) if scale < 1 else range(4)            # the largest rows' z overflow with the second
+            xq = x.double().cpu().numpy().reshape(-1, 8, 64)
+            if scale > 1:
+                xq[:, 4:] = 0
+            want, wl, vmax, zabs, seen = R.attention(xq, kv.values(), cu, lens, table, scale, kv.page)
+            ob, lb = R.attention_bound(want, vmax, zabs, seen, 64, dtype != "F32", info.eps / 2)
+            got, gl = out.double().cpu().numpy().reshape(-1, 8, 64), lse.double().cpu().numpy()
+            for h in heads:
+                assert (np.abs(got[:, h] - want[:, h]) <= ob[:, h] + float(info.smallest_normal)).all(), (h, scale)
+                assert (np.abs(gl[:, h] - wl[:, h]) <= lb[:, h]).all(), (h, scale)
+    finally:
+        kv.close()
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [20, 30, 3]])
 def test_one_row_that_is_not_finite_harms_no_other(q, news):
     lens = [40, 70, 9]
