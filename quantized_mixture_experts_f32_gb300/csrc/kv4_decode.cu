@@ -664,7 +664,8 @@ cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const
 
 template <int HD, int TERMS>
 cudaError_t pick_rows(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st) {
-    const bool two = (long long)a.max_new * (a.s.nq / a.s.nkv) > 8;
+    const int group = a.s.nq / a.s.nkv;
+    const bool two = behind ? group > 8 : (long long)a.max_new * group > 8;
     return two ? launch_decode<HD, TERMS, 2>(a, few_rows, behind, w, st) : launch_decode<HD, TERMS, 1>(a, few_rows, behind, w, st);
 }
 

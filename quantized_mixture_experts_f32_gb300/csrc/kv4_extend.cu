@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     uint64_t *kfull = bars, *kempty = bars + 2, *vfull = bars + 4, *vempty = bars + 6, *sfull = bars + 8,
              *pfull = bars + 12, *odone = bars + 16, *qfull = bars + 20;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(bars + 21);
-    __shared__ int wsum[G::THREADS / 32];
+    __shared__ int2 wsum[G::THREADS / 32];
     __shared__ int3 wsum3[G::THREADS / 32];
     __shared__ Piece piece_s;
     __shared__ int last_s, joined_s;
@@ -240,22 +240,30 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         Seq one;
         one.qts = 0;
         bool descends = false;
-        // total chunks, a sequence's tiles taken as evenly spread between its first and last
-        // (as far as 2^18 a sequence: it only sets the share)
-        int work = 0;
+        // total chunks, a sequence's tiles taken as evenly spread between its first and last, and as if all were
+        // its last (as far as 2^18 a sequence: they only set the share)
+        int work = 0, most = 0;
         for (int s = s0; s < s1; ++s) {
             seq(s, one);
             descends |= a.cu[s + 1] < a.cu[s];
             const float both = (float)one.last + (float)chunks(one.q, min(one.rows, (int)G::ROWS));
-            if (one.qts) work += (int)fminf(0.5f * (float)a.s.nkv * (float)one.qts * both, 262144.f);
+            if (one.qts) {
+                work += (int)fminf(0.5f * (float)a.s.nkv * (float)one.qts * both, 262144.f);
+                most += (int)fminf((float)a.s.nkv * (float)one.qts * (float)one.last, 262144.f);
+            }
         }
         work = __reduce_add_sync(0xffffffffu, work);
-        if (lane == 0) wsum[warp] = work;
+        most = __reduce_add_sync(0xffffffffu, most);
+        if (lane == 0) wsum[warp] = make_int2(work, most);
         if (__syncthreads_or(descends)) return;        // rows of several sequences (the other kernel reports it)
-        work = 0;
+        work = most = 0;
 #pragma unroll
-        for (int w = 0; w < T / 32; ++w) work += wsum[w];
-        const int share = max(8, (int)(1.25f * (float)work / (float)num_sms) + 1);   // pieces fill one wave
+        for (int w = 0; w < T / 32; ++w) {
+            work += wsum[w].x;
+            most += wsum[w].y;
+        }
+        // pieces that fill one wave, and no more of them than items and multiprocessors
+        const int share = max(8, (int)(fmaxf(1.25f * (float)work, (float)most) / (float)num_sms) + 1);
         auto splits_of = [&](const Seq& r) { return min(G::SPLITS, max(1, (r.last + share - 1) / share)); };
         int items = 0, pieces = 0, parts_n = 0;
         for (int s = s0; s < s1; ++s) {
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 part0 += o.z;
             }
         }
-        // not more CTAs or parts than there are: every item whole then
+        // not more CTAs or parts than there are (past the sums' limit): every item whole then
         const bool whole = all > (int)gridDim.x || all_parts > max_parts;
         const int me = blockIdx.x;
         int base = whole ? base_i : base_p;
@@ -921,11 +929,11 @@ template <int HD, int TERMS>
 cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st) {
     using G = EGeo<HD, TERMS>;
     static_assert(G::SMEM <= 227 * 1024, "one CTA's shared memory");
-    // items: whole tiles of rows, and one that is not whole per sequence with enough rows; splitting adds
-    // about two pieces a multiprocessor
+    // items: whole tiles of rows, and one that is not whole per sequence with enough rows; splitting adds a
+    // piece a multiprocessor at most
     const long long rows = (long long)a.n_tokens * (a.s.nq / a.s.nkv);
     const long long ragged = rows / (few_rows + 1) < a.n_seqs ? rows / (few_rows + 1) : a.n_seqs;
-    const long long grid = a.s.nkv * (rows / G::ROWS + ragged) + 2 * w.num_sms;
+    const long long grid = a.s.nkv * (rows / G::ROWS + ragged) + w.num_sms;
     return launch_pdl(kv4_extend_kernel<HD, TERMS>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, a, few_rows,
                       w.ext_parts, w.ext_arrive, w.num_sms, EXTEND_PARTS * w.num_sms);
 }
