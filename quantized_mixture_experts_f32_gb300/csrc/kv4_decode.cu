@@ -125,8 +125,13 @@ __device__ __forceinline__ void copy_stage(uint8_t* st, const Kv4Cache& c, const
 // An item counts as LEAD units that hold no positions and then its positions' units, so
 // that a CTA with many short items has fewer positions.  CTA c of g takes the units
 // [w c / g, w (c+1) / g) of w; g <= w, so each has one at least.
-__device__ __forceinline__ long long unit_begin(long long w, int c, int g) { return w * c / g; }
-__device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) { return (int)(((x + 1) * g - 1) / w); }
+// (Divisions of 64 bits take five times as long: only where 32 do not hold w g.)
+__device__ __forceinline__ long long unit_begin(long long w, int c, int g) {
+    return w * g < 1ll << 32 ? (uint32_t)w * (uint32_t)c / (uint32_t)g : w * c / g;
+}
+__device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) {
+    return w * g < 1ll << 32 ? (int)((((uint32_t)x + 1) * (uint32_t)g - 1) / (uint32_t)w) : (int)(((x + 1) * g - 1) / w);
+}
 
 template <int HD, int TERMS, int NR>
 __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
@@ -202,7 +207,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         const int tiles = q.len ? (q.len + UNIT - 1) / UNIT : 1, vu = LEAD + tiles;
         const int rts = (q.n * group + G::ROWS - 1) / G::ROWS;
         const long long off = u - pre[s];
-        const int item = (int)(off / vu), v0 = (int)(off - (long long)item * vu);
+        const int item = off < (1ll << 31) ? (int)((uint32_t)off / (uint32_t)vu) : (int)(off / vu), v0 = (int)(off - (long long)item * vu);
         const int v1 = (int)min((long long)vu, v0 + (u_end - u));
         if (v1 <= LEAD) return;                        // the lead alone: the next CTA starts the item
         r.next = u + (v1 - v0);
@@ -252,21 +257,30 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         cp_commit();
     };
     // q: warp w takes the rows w, w + 8, scaled to [1, 2) by a power of two
-    auto take_q = [&](const Segment& r, int buf) {
+    struct Rows {
+        float2 v[NR][HD / 64];
+    };
+    auto load_q = [&](const Segment& r, Rows& x) {
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            const int row = nr * 8 + warp;
+            const int tok = (r.row0 + row) / group, h = r.g * group + (r.row0 + row) - tok * group;
+#pragma unroll
+            for (int i = 0; i < HD / 64; ++i)
+                x.v[nr][i] = row < r.rows ? kv4_load2(a.q, (size_t)(r.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
+                                          : make_float2(0.f, 0.f);
+        }
+    };
+    auto put_q = [&](const Segment& r, int buf, const Rows& x) {
         uint32_t* qf = qf2 + buf * (G::QF / 4);
         const float kg = a.c.kg[r.g];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             const int row = nr * 8 + warp;
-            const int tok = (r.row0 + row) / group, h = r.g * group + (r.row0 + row) - tok * group;
-            float2 v[HD / 64];
+            const float2(&v)[HD / 64] = x.v[nr];
             float big = 0.f;
 #pragma unroll
-            for (int i = 0; i < HD / 64; ++i) {
-                v[i] = row < r.rows ? kv4_load2(a.q, (size_t)(r.q0 + tok) * a.q_stride + (size_t)h * HD + 2 * lane + 64 * i, a.q_t)
-                                    : make_float2(0.f, 0.f);
-                big = fmaxf(big, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
-            }
+            for (int i = 0; i < HD / 64; ++i) big = fmaxf(big, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
 #pragma unroll
             for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             const int e = kv4_exponent(big);
@@ -296,8 +310,12 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     if (tid == 0) describe(unit_begin(W, me, Gn), seg_s[0]);
     __syncthreads();
     if (seg_s[0].tiles == 0) return leave();
-    issue(seg_s[0], seg_s[0].t0, true);
-    take_q(seg_s[0], 0);
+    {
+        Rows x;
+        load_q(seg_s[0], x);                           // on its way while the first page ids are
+        issue(seg_s[0], seg_s[0].t0, true);
+        put_q(seg_s[0], 0, x);
+    }
     __syncthreads();
     for (int cur = 0;; cur ^= 1) {
         const Segment& S = seg_s[cur];
@@ -615,36 +633,71 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 }
             }
         }
-        if (seg_s[cur ^ 1].tiles) take_q(seg_s[cur ^ 1], cur ^ 1);
+        if (seg_s[cur ^ 1].tiles) {
+            Rows x;
+            load_q(seg_s[cur ^ 1], x);
+            put_q(seg_s[cur ^ 1], cur ^ 1, x);
+        }
         if (!whole) {
             const int c0 = S.c0, c1 = S.c1;
-            __threadfence();
             __syncthreads();
-            if (tid == 0) last_s = atomicAdd(arrive + c0, 1u) == (unsigned)(c1 - c0);
+            if (tid == 0) {
+                __threadfence();
+                last_s = atomicAdd(arrive + c0, 1u) == (unsigned)(c1 - c0);
+                if (last_s) {
+                    arrive[c0] = 0u;
+                    __threadfence();
+                }
+            }
             __syncthreads();
             if (last_s) {
-                __threadfence();
-                if (tid == 0) arrive[c0] = 0u;
                 const int ns = c1 - c0 + 1;
                 auto part_of = [&](int i) { return parts + (size_t)(2 * (c0 + i) + (i == 0)) * G::PART; };
+                constexpr int AT = 8;                  // parts in flight
                 for (int row = warp; row < rows; row += DW) {
-                    mj = -INFINITY;
-                    for (int i = lane; i < ns; i += 32) mj = fmaxf(mj, __ldcg(part_of(i) + G::ROWS * HD + row));
+                    float2 v[AT][PT / 2];
+                    auto load = [&](int i0) {
+#pragma unroll
+                        for (int y = 0; y < AT; ++y) {
+                            const float2* p = reinterpret_cast<const float2*>(part_of(min(i0 + y, ns - 1)) + row * HD + d0);
+#pragma unroll
+                            for (int k = 0; k < PT / 2; ++k) v[y][k] = __ldcg(p + k);
+                        }
+                    };
+                    // m and l of 32 parts a lane each, and the first parts behind them
+                    auto m_of = [&](int i) { return i < ns ? __ldcg(part_of(i) + G::ROWS * HD + row) : -INFINITY; };
+                    auto l_of = [&](int i) { return i < ns ? __ldcg(part_of(i) + G::ROWS * HD + G::ROWS + row) : 0.f; };
+                    float mw = m_of(lane), lw = l_of(lane);
+                    load(0);
+                    mj = mw;
+                    for (int i = lane + 32; i < ns; i += 32) mj = fmaxf(mj, m_of(i));
 #pragma unroll
                     for (int x = 16; x; x >>= 1) mj = fmaxf(mj, __shfl_xor_sync(0xffffffffu, mj, x));
                     clear();
-#pragma unroll 8
-                    for (int i = 0; i < ns; ++i) {
-                        const float* p = part_of(i);
-                        const float lw = __ldcg(p + G::ROWS * HD + G::ROWS + row), mw = __ldcg(p + G::ROWS * HD + row);
-                        const float c = lw == 0.f ? 0.f : kv4_ex2(mw - mj);
-                        lj += lw * c;
-#pragma unroll
-                        for (int k = 0; k < PT / 2; ++k) {
-                            const float2 y = __ldcg(reinterpret_cast<const float2*>(p + row * HD + d0) + k);
-                            acc[k].x += y.x * c;
-                            acc[k].y += y.y * c;
+#pragma unroll 1
+                    for (int i0 = 0; i0 < ns; i0 += AT) {
+                        if (i0 && i0 % 32 == 0) {
+                            mw = m_of(i0 + lane);
+                            lw = l_of(i0 + lane);
                         }
+                        const float c = lw == 0.f ? 0.f : kv4_ex2(mw - mj);          // of part i0 / 32 * 32 + lane
+                        if (i0 % 32 == 0) {
+                            float sum = lw * c;
+#pragma unroll
+                            for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                            lj += sum;
+                        }
+#pragma unroll
+                        for (int y = 0; y < AT; ++y) {
+                            const float cy = __shfl_sync(0xffffffffu, c, (i0 + y) & 31);
+#pragma unroll
+                            for (int k = 0; k < PT / 2; ++k) {
+                                // a part past the last one counts nothing (its c is 0, v the last one's)
+                                acc[k].x += i0 + y < ns ? v[y][k].x * cy : 0.f;
+                                acc[k].y += i0 + y < ns ? v[y][k].y * cy : 0.f;
+                            }
+                        }
+                        if (i0 + AT < ns) load(i0 + AT);
                     }
                     write(row);
                 }
@@ -664,8 +717,16 @@ cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const
 
 template <int HD, int TERMS>
 cudaError_t pick_rows(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st) {
+    // Items of 16 rows read and widen the cache once where items of 8 do twice, which costs less than it seems:
+    // their two items run side by side, or one finds the other's bytes in L2, in shorter code.  bf16, 4 kv heads,
+    // 16 rows, us (items of 16 / 8): 1 sequence of 1000 positions 15.2 / 10.3, 65536 39 / 28, 262144 70 / 68 (head_dim
+    // 256: 95 / 114); 2 of 4096 17.2 / 11.5, of 131072 65 / 65; 4 of 131072 101 / 118 (head_dim 64: 62 / 83, 256:
+    // 154 / 217).  So with few sequences 8.  Beside prompts too: requests bring one token there as a rule, and
+    // what is smaller fills the multiprocessors that come free more evenly (24 requests of 300-6000 positions,
+    // four with up to 500 new tokens, the others with one, 82.9 / 75.1; 23 with two and one with 500, 90.4 / 83.8).
     const int group = a.s.nq / a.s.nkv;
-    const bool two = behind ? group > 8 : (long long)a.max_new * group > 8;
+    const bool two = (long long)a.max_new * group > 8 &&
+                     (behind ? group > 8 : (long long)a.n_seqs * a.s.nkv * 16 > w.num_sms);
     return two ? launch_decode<HD, TERMS, 2>(a, few_rows, behind, w, st) : launch_decode<HD, TERMS, 1>(a, few_rows, behind, w, st);
 }
 
@@ -714,8 +775,9 @@ int kv4_arrive_words(int num_sms) { return 2 * num_sms; }   // a CTA of the one 
 // rows 19.4 / 26.8.
 //
 // The prompt kernel goes first: its CTAs do not end together, and the decode kernel's, smaller and
-// more, run where it has ended (24 requests of 300-6000 positions, 7 of them with up to 500 new
-// tokens: NEW us; the decode kernel first, OLD us).
+// more, run where it has ended (bf16, 24 requests of 300-6000 positions, four of them with up to 500
+// new tokens: 75.1 us, the decode kernel first 82.1; 64 that decode and one with 500: 80.9, 85.8; 8
+// that decode and 8 with 200: 83.9, 97.7).
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st) {
     constexpr int few_alone = 64;
     const int few = (long long)a.n_seqs * a.s.nkv * 8 <= w.num_sms ? few_alone : KV4_FEW_ROWS;

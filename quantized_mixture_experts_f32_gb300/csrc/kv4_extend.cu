@@ -592,21 +592,23 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         if (splits == 1) {
             if (ok && tid < rows && a.lse) a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] = log_sum(m, l);
         } else if (to_part) {
-            __threadfence();
             named_bar(1, G::SOFT);
-            if (tid == 0) atomicAdd(arrive + p.part + 1, 1u);
+            if (tid == 0) {
+                __threadfence();
+                atomicAdd(arrive + p.part + 1, 1u);
+            }
         } else {
             // The others are past their products: their parts are there in no more time than it takes to
             // store one.
             if (tid == 0) {
                 ok = grid_wait(arrive + p.part + 1, (unsigned)(splits - 1)) && ok;
+                __threadfence();
                 arrive[p.part] = 0u;
                 arrive[p.part + 1] = 0u;
                 joined_s = ok;
             }
             named_bar(1, G::SOFT);
             ok = joined_s && ok;
-            __threadfence();
             const float* first_part = parts + (size_t)p.part * G::PART;
             // weights of the parts by row
             float* wt = reinterpret_cast<float*>(sm + G::V);           // [splits][ROWS], vg / sum at the end

@@ -370,6 +370,22 @@ def test_decode_rows(q, nq, nkv, hd, page, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("nq,nkv,new", [(32, 2, [1]), (26, 2, [1]), (8, 2, [3, 1, 4]), (32, 2, [1, 0, 40])])
+def test_many_sequences_of_more_than_eight_rows(q, nq, nkv, new, hd, dtype):
+    """Items of 16 rows, some short of them, alone and beside prompts."""
+    lens = ([1, 33, 0, 700, 16, 257, 5, 1500, 64, 90] * 3)[:24]
+    news = [min(x, max(n, 1)) for x, n in zip(new * 24, lens)]
+    kv, x, cu, table = _filled(q, lens, news, nq, nkv, hd, 32, dtype, hd + nq)
+    try:
+        out, lse = kv.attention(x, cu, lens, table, dtype)
+        assert kv.status() == 0
+        _check(kv, x, out, lse, cu, lens, table)
+    finally:
+        kv.close()
+
+
+@pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
 @pytest.mark.parametrize("nq,nkv,hd,page", LAYOUTS)
 def test_several_new_tokens(q, nq, nkv, hd, page, dtype):
     lens = [5, 70, 0, 33, 129, 40, 3]
