@@ -19,6 +19,13 @@
 // The order of head elements in q.k and of positions in p.v is free: K and Q elements
 // are dealt to the four lanes of a position in contiguous runs (16-byte loads), and
 // operand rows to positions so that V's loads meet every bank once.
+//
+// All positions of all items are dealt out evenly to two CTAs a multiprocessor, whatever
+// sequence they belong to.  Measured (32 q heads, 4 kv heads of 128, one token each): 4
+// sequences of 131072 positions, F16, 66 us, 4.6 TB/s, bound by issue (61% of the slots;
+// widening keeps the ALU at 50%, the tensor pipe at 23%); 64 of 100-8192, BF16, 28.6 us,
+// 2.5 TB/s, with a start and an end of about 9 us; 1 of 4096, F32, 11.2 us, of which the
+// positions are 2: lengths and shares take 1.8, the first bytes 1.8, the join 3.5.
 #include <math.h>
 
 #include "kv4.cuh"

@@ -8,7 +8,8 @@
 //            TMEM, running maximum m and sum l, p = 2^(z - m) back into TMEM as fp16
 //   K, V     3 and 4 warps: codes from the cache, widened (exactly) to fp16 into
 //            128B-swizzled K-major tiles, V transposed so that positions are K
-//   MMA      one thread: S = Q K^T and O += P V^T, tcgen05, P read from TMEM
+//   MMA      one warp, one lane of which issues: S = Q K^T and O += P V^T, tcgen05, P
+//            read from TMEM
 // With NT = 2 two 128-row tiles share every widened K and V tile (the widening costs
 // as many issue slots as one tile's softmax); with NT = 1 (F32 rows, head_dim 256)
 // shared memory has no room for two.
@@ -18,7 +19,16 @@
 // issued after the product that reads P and runs after it.
 // O is rescaled only when a row's maximum rose by 2^8 since the last time.
 // F32 rows: q = hi + lo and p = hi + lo, two products each (TERMS = 2).
-// Few items: the chunks of an item are split over CTAs, the last one joins the parts.
+// Few items: the chunks of an item are split over CTAs; the one that comes last keeps its
+// part and joins the others' to it.
+//
+// Measured (32 q heads, 4 kv heads of 128): 4 sequences of 8192-16384 positions that bring
+// 2048 BF16 tokens each, 1180 us, 1370 TFLOP/s of visible products; the issue slots are
+// 61% taken (widening, exponentials, moves from and to TMEM) and the tensor pipe 58%: the
+// softmax of a step, its two products and the widening of its positions each take most of
+// the step's 900 ns.  777 F32 tokens from their first, 29.8 us: an item's start (lengths, q)
+// and end take 10 of its 20 us, and 196 items are 1.3 waves.  Pieces taken in turn by CTAs
+// that stay were no faster (1173 us; the short calls 2 us slower).
 #include <math.h>
 
 #include "kv4.cuh"
