@@ -55,8 +55,8 @@ struct EGeo {
     static constexpr int Q = 0, K = NT * TERMS * QT, V = K + BUF * KT, BARS = V + BUF * KT;
     static constexpr size_t SMEM = 1024 + BARS + 256;
     static constexpr int LPR = HD / 32;                              // 16-byte runs of a position's codes
-    static constexpr int RPP = KTH / LPR;                            // positions the K threads take at a time
-    static constexpr int KP = (KC + RPP - 1) / RPP;
+    static constexpr int GPR = KTH / LPR / (KC / 16);                // positions of a run of 16 at a time
+    static constexpr int KP = (16 + GPR - 1) / GPR;                  // times
     static constexpr int PART = ROWS * (HD + 2);                     // floats of a part
     static constexpr int SPLITS = 31;                                // of an item at most
     static_assert(ROWS * HD * 4 <= V, "O passes through the tiles of Q and K on its way out");
@@ -693,36 +693,43 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     } else if (tid < G::SOFT + G::KTH) {
         // ----------------------------------------------------------------- K
         const int wt = tid - G::SOFT;
-        // a thread widens KP runs of 32 elements
-        const int jj = wt % G::LPR, r0 = wt / G::LPR;
-        const int rot = G::LPR == 4 ? jj & 2 : G::LPR == 8 ? jj >> 1 : 0;   // a quarter-warp's stores meet every bank once
-        int id[G::KP];
+        // A thread widens 32 elements of every GPR-th position of a run of 16, which one page holds: one page id
+        // and one address, the rest are constants.  Positions behind the last one are masked, whatever they hold.
+        const int jj = wt % G::LPR, run = wt / G::LPR / G::GPR, sub = wt / G::LPR % G::GPR;
+        const int rot = G::LPR == 4 ? jj & 2 : G::LPR == 8 ? jj >> 1 : 0;
+        // (`flip`: positions of every other run change places, so that with `rot` a quarter-warp's stores meet every
+        // bank once)
+        const int flip = run & 1 ? G::LPR == 4 ? 1 : G::LPR == 2 ? 2 : 0 : 0;
+        auto in_run = [&](int i) { return (sub + i * G::GPR) ^ flip; };
+        auto there = [&](int i) { return 16 % G::GPR == 0 || i < G::KP - 1 || sub < 16 % G::GPR; };
+        int id;
         uint4 kw[G::KP], kn[G::KP];
         uint32_t kscale[G::KP], kscale_n[G::KP];
-        auto at_of = [&](int c, int i) { return c * KC + min(i * G::RPP + r0, KC - 1); };
-        auto pages = [&](int c) {
-#pragma unroll
-            for (int i = 0; i < G::KP; ++i) id[i] = table[min(at_of(c, i), p.len - 1) >> a.s.page_log2];
-        };
+        auto page = [&](int c) { id = table[min(c * KC + run * 16, p.len - 1) >> a.s.page_log2]; };
         auto load = [&](int c) {
 #pragma unroll
             for (int i = 0; i < G::KP; ++i) {
                 kn[i] = make_uint4(0, 0, 0, 0);
                 kscale_n[i] = 0;
-                const int pos = at_of(c, i);
-                if (c < p.c1 && pos < p.len && id[i] >= 0 && id[i] < a.s.n_pages) {
-                    const size_t at = ((size_t)id[i] * a.s.nkv + p.g) * a.s.page + (pos & (a.s.page - 1));
-                    kn[i] = __ldg(reinterpret_cast<const uint4*>(a.c.kc + at * (HD / 2) + jj * 16));
-                    kscale_n[i] = __ldg(reinterpret_cast<const uint16_t*>(a.c.ks + at * (HD / 16) + jj * 2));
-                }
+            }
+            if (c < p.c1 && c * KC + run * 16 < p.len && id >= 0 && id < a.s.n_pages) {
+                const size_t at = ((size_t)id * a.s.nkv + p.g) * a.s.page + ((c * KC + run * 16) & (a.s.page - 1));
+                const uint8_t* codes = a.c.kc + at * (HD / 2) + jj * 16;
+                const uint8_t* scales = a.c.ks + at * (HD / 16) + jj * 2;
+#pragma unroll
+                for (int i = 0; i < G::KP; ++i)
+                    if (there(i)) {
+                        kn[i] = __ldg(reinterpret_cast<const uint4*>(codes + in_run(i) * (HD / 2)));
+                        kscale_n[i] = __ldg(reinterpret_cast<const uint16_t*>(scales + in_run(i) * (HD / 16)));
+                    }
             }
         };
         auto k_store = [&](int b) {
             uint8_t* tile = sm + G::K + b * G::KT + (jj >> 1) * (KC * 128);
 #pragma unroll
             for (int i = 0; i < G::KP; ++i) {
-                const int row = i * G::RPP + r0;
-                if (KC % G::RPP && row >= KC) break;
+                const int row = run * 16 + in_run(i);
+                if (!there(i)) break;
                 const __half2 both = kv4_scale2(kscale[i]), s0 = __low2half2(both), s1 = __high2half2(both);
                 uint32_t x0 = kw[i].x, x1 = kw[i].y, x2 = kw[i].z, x3 = kw[i].w;
                 if (rot & 2) {
@@ -752,9 +759,9 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
             }
         };
         if (p.c0 < p.c1) {
-            pages(p.c0);
+            page(p.c0);
             load(p.c0);
-            pages(p.c0 + 1);
+            page(p.c0 + 1);
         }
         for (int c = p.c0; c < p.c1; ++c) {
 #pragma unroll
@@ -763,7 +770,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 kscale[i] = kscale_n[i];
             }
             load(c + 1);
-            pages(c + 2);
+            page(c + 2);
             const int i0 = c - p.c0, b = i0 % BUF, use = i0 / BUF;
             if (use && !mbar_wait(kempty + b, (use - 1) & 1)) {
                 ok = false;
