@@ -81,7 +81,7 @@ struct Kv4AttnArgs {
 struct Kv4Work {
     float *parts, *ext_parts;          // parts of items that several CTAs share
     unsigned *arrive, *ext_arrive;     // [kv4_arrive_words] each: arrival counters of those items
-    unsigned* ext_queue;               // [2] pieces taken, CTAs that found none left
+    unsigned* ext_total;               // pieces the prompt kernel works on, while it does
     int num_sms;
 };
 constexpr int KV4_FEW_ROWS = 16;       // few_rows at least

@@ -142,7 +142,7 @@ __device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) {
 
 template <int HD, int TERMS, int NR>
 __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
-    kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, int behind_extend, float* __restrict__ parts,
+    kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, unsigned* __restrict__ ext_total, float* __restrict__ parts,
                       unsigned* __restrict__ arrive) {
     using G = DGeo<HD, TERMS, NR>;
     extern __shared__ __align__(16) uint8_t sm[];
@@ -156,14 +156,17 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, j = lane & 3;             // operand row (position, element run); a pair of q rows
     const int group = a.s.nq / a.s.nkv;
-    // Behind the prompt kernel nothing is waited for: it started its dependents after its own wait, so what it
-    // waited for is complete, and it writes nothing that is read here.  The last CTA waits for it before it
-    // ends, for the sake of what comes next; the others make room for each other.
-    if (!behind_extend) pdl_wait();
+    // Behind the prompt kernel (ext_total) nothing is waited for: it started its dependents after its own wait,
+    // so what it waited for is complete, and it writes nothing that is read here.  The last CTA waits for it
+    // before it ends, for the sake of what comes next; the others make room for each other.
+    if (!ext_total) pdl_wait();
     else __threadfence();
     pdl_launch_dependents();
     auto leave = [&] {
-        if (behind_extend && blockIdx.x == gridDim.x - 1) pdl_wait();
+        if (ext_total && blockIdx.x == gridDim.x - 1) {
+            pdl_wait();
+            if (tid == 0) *ext_total = 0u;
+        }
     };
 
     // units of every sequence, as prefix sums
@@ -719,7 +722,7 @@ template <int HD, int TERMS, int NR>
 cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st) {
     using G = DGeo<HD, TERMS, NR>;
     return launch_pdl(kv4_decode_kernel<HD, TERMS, NR>, dim3(w.num_sms * (HD == 256 ? 1 : 2)), dim3(DT),
-                      G::smem(a.n_seqs), st, a, few_rows, (int)behind, w.parts, w.arrive);
+                      G::smem(a.n_seqs), st, a, few_rows, behind ? w.ext_total : nullptr, w.parts, w.arrive);
 }
 
 template <int HD, int TERMS>
@@ -793,7 +796,9 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStr
         const cudaError_t e = launch_kv4_extend(a, few, w, st);
         if (e != cudaSuccess) return e;
     }
-    return launch_kv4_decode(a, few, prompts, w, st);
+    const cudaError_t e = launch_kv4_decode(a, few, prompts, w, st);
+    if (e != cudaSuccess && prompts) cudaMemsetAsync(w.ext_total, 0, sizeof(unsigned), st);   // which the kernel would have
+    return e;
 }
 
 }  // namespace qmoe

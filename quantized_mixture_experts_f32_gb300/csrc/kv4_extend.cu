@@ -23,10 +23,10 @@
 // part and joins the others' to it.
 //
 // Measured (32 q heads, 4 kv heads of 128): 4 sequences of 8192-16384 positions that bring
-// 2048 BF16 tokens each, 1180 us, 1370 TFLOP/s of visible products; the issue slots are
+// 2048 BF16 tokens each, 1190 us, 1361 TFLOP/s of visible products; the issue slots are
 // 61% taken (widening, exponentials, moves from and to TMEM) and the tensor pipe 58%: the
 // softmax of a step, its two products and the widening of its positions each take most of
-// the step's 900 ns.  777 F32 tokens from their first, 29.8 us: an item's start (lengths, q)
+// the step's 900 ns.  777 F32 tokens from their first, 30 us: an item's start (lengths, q)
 // and end take 10 of its 20 us, and 196 items are 1.3 waves.  Pieces taken in turn by CTAs
 // that stay were no faster (1173 us; the short calls 2 us slower).
 #include <math.h>
@@ -190,7 +190,7 @@ struct Piece {
 template <int HD, int TERMS>
 __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     kv4_extend_kernel(const Kv4AttnArgs a, int few_rows, float* __restrict__ parts, unsigned* __restrict__ arrive,
-                      int num_sms, int max_parts) {
+                      unsigned* __restrict__ total, int num_sms, int max_parts) {
     using G = EGeo<HD, TERMS>;
     constexpr int NT = G::NT, KC = G::KC, BUF = G::BUF;
     extern __shared__ __align__(1024) uint8_t smraw[];
@@ -225,6 +225,13 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     }
     pdl_wait();
     pdl_launch_dependents();
+    // The grid is as large as the host has to fear; a CTA behind the last piece need not scan to learn that if
+    // the first one has told (total: pieces + 1, or 0; the decode kernel behind this one clears it).  500 new
+    // tokens beside 512 requests of one: 131 us, all scanning 151; beside 2000, 264 and 346.
+    if ((int)blockIdx.x >= num_sms) {
+        const unsigned t = tid == 0 ? ld_acquire_gpu(total) : 0u;
+        if (__syncthreads_or(t && blockIdx.x + 1 >= t)) return;
+    }
 
     // the items of every sequence with more than few_rows rows, and this CTA's piece of them.  An item's
     // chunks are split where it has more than the GPU's average share of a multiprocessor.
@@ -313,6 +320,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         const bool whole = all > (int)gridDim.x || all_parts > max_parts;
         const int me = blockIdx.x;
         int base = whole ? base_i : base_p;
+        if (me == 0 && tid == 0 && !whole) atomicExch(total, (unsigned)all + 1u);
         if (me >= base && me < base + (whole ? items : pieces)) {
             for (int s = s0; s < s1; ++s) {
                 if (!single) seq(s, one);
@@ -954,7 +962,7 @@ cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, 
     const long long ragged = rows / (few_rows + 1) < a.n_seqs ? rows / (few_rows + 1) : a.n_seqs;
     const long long grid = a.s.nkv * (rows / G::ROWS + ragged) + w.num_sms;
     return launch_pdl(kv4_extend_kernel<HD, TERMS>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, a, few_rows,
-                      w.ext_parts, w.ext_arrive, w.num_sms, EXTEND_PARTS * w.num_sms);
+                      w.ext_parts, w.ext_arrive, w.ext_total, w.num_sms, EXTEND_PARTS * w.num_sms);
 }
 
 }  // namespace

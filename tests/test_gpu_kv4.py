@@ -806,6 +806,72 @@ def test_steps_of_a_serving_loop(q, dtype):
         kv.close()
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_what_follows_prompts_beside_decoding_sees_every_row(q, captured):
+    """The attention's two kernels overlap: an append of its output right behind it, and the next attention into
+    the same rows, find them complete, call after call and replay after replay."""
+    s = torch.cuda.Stream()
+    lens, news = [3000, 900, 40, 2500, 300, 17] * 4, [200, 1, 40, 1, 1, 17] * 4
+    kv, x, cu, table = _filled(q, lens, news, 8, 2, 64, 16, "F32", 31, stream=s.cuda_stream)
+    t = x.shape[0]
+    to = Kv(q, 8, 8, 64, 16, t // 16 + 1, 1, t, 1, s.cuda_stream)
+    try:
+        want, _ = kv.attention(x, cu, lens, table, "F32")
+        slots = cuda(np.arange(t))
+        hat = torch.empty(2, t, 512, device="cuda")
+        to.append(want, want, slots, "F32", hat[0], hat[1])
+        assert kv.status() == 0 and to.status() == 0
+        dev = cuda(cu), cuda(np.array(lens, np.int32)), cuda(table)
+        n = 6
+        out = torch.empty(t, 512, device="cuda")
+        hats = torch.empty(n, 2, t, 512, device="cuda")
+
+        def run():
+            for i in range(n):
+                out.fill_(float("nan"))
+                q.qmoe_kv4_attention(kv.h, kv.cache, x, 0, 0, len(lens), t, 200, *dev, 0.125, out, 0, 0, None)
+                to.append(out, out, slots, "F32", hats[i][0], hats[i][1])
+
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            if captured:
+                g = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(g, stream=s):
+                    run()
+            for _ in range(5):
+                g.replay() if captured else run()
+        torch.cuda.synchronize()
+        assert kv.status() == 0 and to.status() == 0
+        assert torch.equal(out, want) and all(torch.equal(h, hat) for h in hats)
+    finally:
+        kv.close()
+        to.close()
+
+
+def test_prompts_among_many_that_decode(q):
+    """Far fewer pieces than the host has to fear, as lengths change from call to call."""
+    rng = np.random.default_rng(9)
+    n = 600
+    for big in (1, 40, 0, 3):
+        news = np.ones(n, int)
+        news[rng.permutation(n)[:big]] = rng.integers(9, 150, big)
+        lens = news + rng.integers(0, 60, n)
+        kv, x, cu, table = _filled(q, lens, news, 4, 1, 64, 16, "F16", big)
+        try:
+            for k in range(3):
+                out, lse = kv.attention(x, cu, lens, table, "F16", max_new=150)
+                assert kv.status() == 0
+                if k in (0, 2):
+                    _check(kv, x, out, lse, cu, lens, table)
+                else:                                              # the same handle, every second request idle
+                    half = np.where(np.arange(n) % 2, 0, lens)
+                    out, lse = kv.attention(x, cu, half, table, "F16", max_new=150)
+                    assert kv.status() == 0
+                    _check(kv, x, out, lse, cu, half, table)
+        finally:
+            kv.close()
+
+
 def test_a_captured_step_replayed_while_lengths_grow(q):
     nq, nkv, hd, page, n, width, n_pages, cap = 8, 2, 64, 16, 4, 6, 24, 4
     s = torch.cuda.Stream()
