@@ -332,9 +332,9 @@ typedef struct {
 } qmoe_kv4_cache;
 
 /* Create a handle on the current device and allocate its workspace (parts of
- * attention items that several CTAs share: about 5 MB for decoding, 40 MB where a
- * sequence may bring more than 16 rows of q, tokens times n_heads/n_kv_heads).  On
- * failure qmoe_last_error(NULL) tells why. */
+ * attention items that several CTAs share: 3 to 10 MB for decoding, 20 to 40 MB more
+ * where a call may bring more than 16 rows of q, tokens times n_heads/n_kv_heads).
+ * On failure qmoe_last_error(NULL) tells why. */
 qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out);
 void qmoe_kv4_destroy(qmoe_kv4* kv);
 qmoe_status qmoe_kv4_set_stream(qmoe_kv4* kv, void* stream);
