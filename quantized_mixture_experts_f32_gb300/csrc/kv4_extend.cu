@@ -646,47 +646,49 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 if (ok && a.lse) a.lse[(size_t)(p.q0 + tok) * a.s.nq + h] = log_sum(mj, lj);
             }
             named_bar(1, G::SOFT);
-            // eight elements of a row at a time, four of these in flight
+            // Eight elements of a row at a time, four of these in flight; the parts in their order, whichever of
+            // them was kept, so that results do not depend on who came last.
             const int total = ok ? rows * (HD / 8) : 0;
 #pragma unroll 1
             for (int i0 = tid; i0 < total; i0 += 4 * G::SOFT) {
                 float v[4][8];
                 const float4* pi[4];
+                int row[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const int i = min(i0 + k * G::SOFT, total - 1), r = i / (HD / 8), w = i % (HD / 8) * 2;
+                    const int i = min(i0 + k * G::SOFT, total - 1);
+                    row[k] = i / (HD / 8);
                     pi[k] = reinterpret_cast<const float4*>(first_part) + 2 * i;
-                    const float f = wt[split * G::ROWS + r];
-                    const uint8_t* row = sm + (size_t)r * HD * 4;
-                    const float4 u0 = *reinterpret_cast<const float4*>(row + (w ^ (r & 7)) * 16);
-                    const float4 u1 = *reinterpret_cast<const float4*>(row + ((w + 1) ^ (r & 7)) * 16);
-                    v[k][0] = u0.x * f;
-                    v[k][1] = u0.y * f;
-                    v[k][2] = u0.z * f;
-                    v[k][3] = u0.w * f;
-                    v[k][4] = u1.x * f;
-                    v[k][5] = u1.y * f;
-                    v[k][6] = u1.z * f;
-                    v[k][7] = u1.w * f;
-                }
-#pragma unroll 2
-                for (int z = 0; z < splits - 1; ++z) {
-                    const int y = z + (z >= split);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 u0 = __ldcg(pi[k] + (size_t)y * (G::PART / 4));
-                        const float4 u1 = __ldcg(pi[k] + (size_t)y * (G::PART / 4) + 1);
-                        const float f = wt[y * G::ROWS + min(i0 + k * G::SOFT, total - 1) / (HD / 8)];
-                        v[k][0] += u0.x * f;
-                        v[k][1] += u0.y * f;
-                        v[k][2] += u0.z * f;
-                        v[k][3] += u0.w * f;
-                        v[k][4] += u1.x * f;
-                        v[k][5] += u1.y * f;
-                        v[k][6] += u1.z * f;
-                        v[k][7] += u1.w * f;
-                    }
+                    for (int y = 0; y < 8; ++y) v[k][y] = 0.f;
                 }
+                auto add = [&](int k, int y, const float4& u0, const float4& u1) {
+                    const float f = wt[y * G::ROWS + row[k]];
+                    v[k][0] += u0.x * f;
+                    v[k][1] += u0.y * f;
+                    v[k][2] += u0.z * f;
+                    v[k][3] += u0.w * f;
+                    v[k][4] += u1.x * f;
+                    v[k][5] += u1.y * f;
+                    v[k][6] += u1.z * f;
+                    v[k][7] += u1.w * f;
+                };
+                auto add_parts = [&](int y0, int y1) {
+#pragma unroll 2
+                    for (int y = y0; y < y1; ++y)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            add(k, y, __ldcg(pi[k] + (size_t)y * (G::PART / 4)), __ldcg(pi[k] + (size_t)y * (G::PART / 4) + 1));
+                };
+                add_parts(0, split);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int w = min(i0 + k * G::SOFT, total - 1) % (HD / 8) * 2, r = row[k];
+                    const uint8_t* own = sm + (size_t)r * HD * 4;
+                    add(k, split, *reinterpret_cast<const float4*>(own + (w ^ (r & 7)) * 16),
+                        *reinterpret_cast<const float4*>(own + ((w + 1) ^ (r & 7)) * 16));
+                }
+                add_parts(split + 1, splits);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     const int i = i0 + k * G::SOFT, r = i / (HD / 8);

@@ -33,7 +33,7 @@ class Kv:
     def __init__(self, q, nq=8, nkv=2, hd=128, page=16, n_pages=40, seqs=8, tokens=256, width=12, stream=0,
                  seed=0):
         self.q, self.nq, self.nkv, self.hd, self.page, self.n_pages, self.width = q, nq, nkv, hd, page, n_pages, width
-        self.tokens = tokens
+        self.tokens, self.stream = tokens, stream
         self.h = q.qmoe_kv4_create(q.make_kv4_config(nq, nkv, hd, page, n_pages, seqs, tokens, width, stream))
         self.t = {}
         for n in ("k", "v"):
@@ -47,6 +47,11 @@ class Kv:
 
     def close(self):
         self.q.qmoe_kv4_destroy(self.h)
+
+    def ready(self):
+        """What the current stream made is there for a handle on another one."""
+        if self.stream:
+            torch.cuda.current_stream().synchronize()
 
     def status(self):
         return self.q.qmoe_kv4_get_status(self.h)
@@ -80,10 +85,11 @@ class Kv:
             out = torch.full((t, self.nq * self.hd), 77.0, dtype=TORCH[out_t], device="cuda")
         ls = torch.full((t, self.nq), 77.0, dtype=torch.float32, device="cuda") if lse else None
         scale = self.hd ** -0.5 if scale is None else scale
+        dev = [cuda(np.asarray(v, np.int32)) for v in (cu, seq_len, table)]
+        self.ready()
         self.q.qmoe_kv4_attention(self.h, self.cache, x, self.q.DTYPE[dtype], qs, len(seq_len), t,
-                                  max_new or max(1, int(np.diff(cu).max())), cuda(np.asarray(cu, np.int32)),
-                                  cuda(np.asarray(seq_len, np.int32)), cuda(np.asarray(table, np.int32)), scale, out,
-                                  self.q.DTYPE[out_t], os, ls)
+                                  max_new or max(1, int(np.diff(cu).max())), *dev, scale, out, self.q.DTYPE[out_t], os,
+                                  ls)
         return out, ls
 
     def values(self):
@@ -324,7 +330,9 @@ def _filled(q, lens, news, nq, nkv, hd, page, dtype, seed, width=None, extra=3, 
     if len(slots):
         rows = torch.from_numpy(rng.normal(size=(2, len(slots), nkv * hd)).astype(np.float32)).cuda()
         rows[0] *= torch.from_numpy(np.exp(0.4 * rng.normal(size=nkv * hd)).astype(np.float32)).cuda()
-        kv.append(rows[0], rows[1], cuda(slots))
+        slots = cuda(slots)
+        kv.ready()
+        kv.append(rows[0], rows[1], slots)
         assert kv.status() == 0
     x = torch.from_numpy(rng.normal(size=(t, nq * hd)).astype(np.float32) * 1.5).cuda().to(TORCH[dtype])
     cu = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
@@ -642,6 +650,9 @@ def test_chunks_of_a_long_context_split_over_the_gpu(q, nq, nkv, hd, page, lens,
         out, lse = kv.attention(x, cu, lens, table, dtype)
         assert kv.status() == 0
         _check(kv, x, out, lse, cu, lens, table)
+        for _ in range(10):                                        # whichever CTA comes last
+            again, lse2 = kv.attention(x, cu, lens, table, dtype)
+            assert torch.equal(out, again) and torch.equal(lse, lse2)
         last = (lens[0] - 1) // page
         table[0, 3], table[0, last // 2], table[0, last] = -1, kv.n_pages, -2 ** 31
         out, lse = kv.attention(x, cu, lens, table, dtype)
@@ -816,15 +827,15 @@ def test_what_follows_prompts_beside_decoding_sees_every_row(q, captured):
     t = x.shape[0]
     to = Kv(q, 8, 8, 64, 16, t // 16 + 1, 1, t, 1, s.cuda_stream)
     try:
-        want, _ = kv.attention(x, cu, lens, table, "F32")
-        slots = cuda(np.arange(t))
-        hat = torch.empty(2, t, 512, device="cuda")
+        slots, dev = cuda(np.arange(t)), (cuda(cu), cuda(np.array(lens, np.int32)), cuda(table))
+        hat, n = torch.empty(2, t, 512, device="cuda"), 6
+        want, out = torch.empty(t, 512, device="cuda"), torch.empty(t, 512, device="cuda")
+        hats = torch.empty(n, 2, t, 512, device="cuda")
+        torch.cuda.synchronize()                                   # what the default stream made is there
+        q.qmoe_kv4_attention(kv.h, kv.cache, x, 0, 0, len(lens), t, 200, *dev, 0.125, want, 0, 0, None)
+        torch.cuda.synchronize()
         to.append(want, want, slots, "F32", hat[0], hat[1])
         assert kv.status() == 0 and to.status() == 0
-        dev = cuda(cu), cuda(np.array(lens, np.int32)), cuda(table)
-        n = 6
-        out = torch.empty(t, 512, device="cuda")
-        hats = torch.empty(n, 2, t, 512, device="cuda")
 
         def run():
             for i in range(n):
