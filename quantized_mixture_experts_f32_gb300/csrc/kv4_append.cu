@@ -86,7 +86,7 @@ __device__ __forceinline__ void append_lane(const Kv4AppendArgs& a, int t, int c
 
 // blockIdx.y: 0 = K, 1 = V.  A CTA takes rows_cta whole rows where they fit its
 // threads, else one row in turns, so that indices stay 32 bits wide.  16384 F32 rows of
-// four heads of 128 take 24.5 us, 5.9 TB/s of rows, codes and values (75% of the issue
+// four heads of 128 take 24.7 us, 5.8 TB/s of rows, codes and values (75% of the issue
 // slots, 61% of the warps); four elements a lane and the compiler's division took 37 us,
 // bound by instructions.  64 BF16 rows take 1.8 us, latency alone.
 template <int F32>

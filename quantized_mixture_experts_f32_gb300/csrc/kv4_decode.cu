@@ -22,9 +22,9 @@
 //
 // All positions of all items are dealt out evenly to two CTAs a multiprocessor, whatever
 // sequence they belong to.  Measured (32 q heads, 4 kv heads of 128, one token each): 4
-// sequences of 131072 positions, F16, 66 us, 4.6 TB/s, bound by issue (61% of the slots;
-// widening keeps the ALU at 50%, the tensor pipe at 23%); 64 of 100-8192, BF16, 28.6 us,
-// 2.5 TB/s, with a start and an end of about 9 us; 1 of 4096, F32, 11.2 us, of which the
+// sequences of 131072 positions, F16, 66.6 us, 4.5 TB/s, bound by issue (61% of the slots;
+// widening keeps the ALU at 50%, the tensor pipe at 23%); 64 of 100-8192, BF16, 28.7 us,
+// 2.5 TB/s, with a start and an end of about 9 us; 1 of 4096, F32, 11.3 us, of which the
 // positions are 2: lengths and shares take 1.8, the first bytes 1.8, the join 3.5.
 #include <math.h>
 

@@ -23,10 +23,10 @@
 // part and joins the others' to it.
 //
 // Measured (32 q heads, 4 kv heads of 128): 4 sequences of 8192-16384 positions that bring
-// 2048 BF16 tokens each, 1190 us, 1361 TFLOP/s of visible products; the issue slots are
+// 2048 BF16 tokens each, 1174 us, 1380 TFLOP/s of visible products; the issue slots are
 // 61% taken (widening, exponentials, moves from and to TMEM) and the tensor pipe 58%: the
 // softmax of a step, its two products and the widening of its positions each take most of
-// the step's 900 ns.  777 F32 tokens from their first, 30 us: an item's start (lengths, q)
+// the step's 900 ns.  777 F32 tokens from their first, 29.6 us: an item's start (lengths, q)
 // and end take 10 of its 20 us, and 196 items are 1.3 waves.  Pieces taken in turn by CTAs
 // that stay were no faster (1173 us; the short calls 2 us slower).
 #include <math.h>

@@ -17,8 +17,8 @@
 // so the last CTA to arrive writes them, after every CTA has read them.
 //
 // Bound by latency: the lengths' load, the scan, the search, the free page, the store,
-// each waiting for the one before.  8 requests of one token 3.4 us (one CTA, which needs
-// no arrival), 2048 requests with up to 200 tokens each 9.8 us, of which 2.2 MB take 0.3.
+// each waiting for the one before.  8 requests of one token 3.2 us (one CTA, which needs
+// no arrival), 2048 requests with up to 200 tokens each 9.5 us, of which 2.2 MB take 0.3.
 // Two and three CTAs a multiprocessor took 11.4 and 14.9 us there, more scanning than they
 // saved.
 #include "kv4.cuh"

@@ -37,10 +37,12 @@ __device__ __forceinline__ int kv4_exponent(float big) {
 }
 __device__ __forceinline__ float kv4_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| < 127
 
-// z of a row scaled by 2^-e, in powers of two, from its product with K's codes; the scale
-// meets 2^e first, so that neither a tiny scale nor a large row leaves fp32's range on the way
+// z of a row scaled by 2^-e, in powers of two, from its product with K's codes; 2^e in
+// halves, so that neither a tiny scale or global nor a large row leaves fp32's range on
+// the way where the result is in it
 __device__ __forceinline__ float kv4_factor(float scale, float global, int e) {
-    return ldexpf(scale, e) * (1.4426950408889634f * global);
+    const int h = e / 2;
+    return scale * kv4_pow2(h) * (1.4426950408889634f * global) * kv4_pow2(e - h);
 }
 
 // Eight E2M1 codes -> four half2, bytes in order.  One conversion a byte: naming the
