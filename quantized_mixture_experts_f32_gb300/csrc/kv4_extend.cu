@@ -77,7 +77,8 @@ __device__ __forceinline__ uint32_t elect_one() {
 template <int ADD>
 __device__ __forceinline__ void mma_ss(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
         "r"(a), "r"(b), "r"(high), "r"(idesc), "n"(ADD), "r"(one)
         : "memory");
@@ -570,13 +571,15 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 if (to_t == KV4_F32) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        *reinterpret_cast<uint4*>(row + ((d / 4 + k) ^ (lane & 7)) * 16) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        *reinterpret_cast<uint4*>(row + ((d / 4 + k) ^ (lane & 7)) * 16) =
+                            make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 } else {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         uint32_t u[4];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) u[y] = kv4_pack16(__uint_as_float(o[8 * k + 2 * y]), __uint_as_float(o[8 * k + 2 * y + 1]), to_t);
+                        for (int y = 0; y < 4; ++y)
+                            u[y] = kv4_pack16(__uint_as_float(o[8 * k + 2 * y]), __uint_as_float(o[8 * k + 2 * y + 1]), to_t);
                         *reinterpret_cast<uint4*>(row + ((d / 8 + k) ^ (lane & 7)) * 16) = make_uint4(u[0], u[1], u[2], u[3]);
                     }
                 }
@@ -602,7 +605,9 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 }
             }
         }
-        auto log_sum = [&](float mr, float lr) { return lr == 0.f ? -INFINITY : (mr - KV4_P_UP + log2f(lr)) * 0.6931471805599453f; };
+        auto log_sum = [&](float mr, float lr) {
+            return lr == 0.f ? -INFINITY : (mr - KV4_P_UP + log2f(lr)) * 0.6931471805599453f;
+        };
         if (splits > 1) {
             part[(size_t)HD * G::ROWS + tid] = m;
             part[(size_t)(HD + 1) * G::ROWS + tid] = l;
