@@ -430,7 +430,7 @@ qmoe_status qmoe_kv4_attention(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const 
  * layers' own fp16 caches (k_cache and v_cache of the layers are not used and may
  * be NULL).  Decoding, draft tokens and prompt chunks may share a call.
  *  kv        : handle with the context's n_heads, n_kv_heads and head_dim, on its
- *              device and stream.
+ *              device (where the call runs, whichever is current) and stream.
  *  cu_tokens, seq_len, block_table, positions, slots : of the step, as
  *              qmoe_kv4_plan gives them; max_new as for qmoe_kv4_attention.
  *  ids_out   : nullable, int32 [n_layers][n_tokens][k] selected experts.

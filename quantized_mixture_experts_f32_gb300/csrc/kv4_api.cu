@@ -74,20 +74,6 @@ qmoe_status cuda_fail(qmoe_kv4* h, cudaError_t e, const char* what) {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// makes the handle's device current for the call
-struct OnDevice {
-    int before = -1;
-    cudaError_t e;
-    explicit OnDevice(int device) {
-        e = cudaGetDevice(&before);
-        if (e == cudaSuccess && before != device) e = cudaSetDevice(device);
-        else before = -1;
-    }
-    ~OnDevice() {
-        if (before >= 0) cudaSetDevice(before);
-    }
-};
-
 bool valid_dtype(int t) { return t == QMOE_F32 || t == QMOE_F16 || t == QMOE_BF16; }
 int dtype_bytes(int t) { return t == QMOE_F32 ? 4 : 2; }
 
@@ -207,7 +193,7 @@ qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
 void qmoe_kv4_destroy(qmoe_kv4* h) {
     if (!h) return;
     {
-        OnDevice dev(h->device);
+        qmoe::OnDevice dev(h->device);
         cudaStreamSynchronize(h->stream);
         cudaFree(h->ws);
     }
@@ -225,7 +211,7 @@ const char* qmoe_kv4_last_error(qmoe_kv4* h) { return h ? h->err : qmoe_last_err
 
 qmoe_status qmoe_kv4_get_status(qmoe_kv4* h) {
     if (!h) return QMOE_ERR_INVALID_ARG;
-    OnDevice dev(h->device);
+    qmoe::OnDevice dev(h->device);
     if (dev.e != cudaSuccess) return cuda_fail(h, dev.e, "device select");
     int st = 0;
     cudaError_t e = cudaMemcpyAsync(&st, h->status, sizeof(int), cudaMemcpyDeviceToHost, h->stream);
@@ -256,7 +242,7 @@ qmoe_status qmoe_kv4_plan(qmoe_kv4* h, int n_seqs, const int32_t* seq_len, const
         return fail(h, QMOE_ERR_MISALIGNED, "int32 arrays must be 4-byte aligned, slots 8-byte");
     if (seq_len_out == new_len || cu_tokens == seq_len || cu_tokens == new_len || cu_tokens == seq_len_out)
         return fail(h, QMOE_ERR_INVALID_ARG, "only seq_len_out = seq_len and n_free_out = n_free may alias");
-    OnDevice dev(h->device);
+    qmoe::OnDevice dev(h->device);
     if (dev.e != cudaSuccess) return cuda_fail(h, dev.e, "device select");
     const qmoe::Kv4PlanArgs a{n_seqs, c.page_size, c.n_pages, c.max_pages_per_seq, cap_tokens, seq_len, new_len,
                               block_table, free_pages, n_free, seq_len_out, n_free_out, cu_tokens, positions,
@@ -283,7 +269,7 @@ qmoe_status qmoe_kv4_append(qmoe_kv4* h, const qmoe_kv4_cache* cache, const void
     if (s != QMOE_OK) return s;
     if (!aligned(slots, 8) || !aligned(k_hat, 16) || !aligned(v_hat, 16))
         return fail(h, QMOE_ERR_MISALIGNED, "slots must be 8-byte, k_hat and v_hat 16-byte aligned");
-    OnDevice dev(h->device);
+    qmoe::OnDevice dev(h->device);
     if (dev.e != cudaSuccess) return cuda_fail(h, dev.e, "device select");
     const qmoe::Kv4AppendArgs a{shape(h), cache_of(cache), k, v, (int)dtype, n_tokens, k_stride, v_stride, slots,
                                 k_hat, v_hat, h->status};
@@ -318,7 +304,7 @@ qmoe_status qmoe_kv4_attention(qmoe_kv4* h, const qmoe_kv4_cache* cache, const v
     if (!aligned(cu_tokens, 4) || !aligned(seq_len, 4) || !aligned(block_table, 4) || !aligned(lse, 4))
         return fail(h, QMOE_ERR_MISALIGNED, "cu_tokens, seq_len, block_table and lse must be 4-byte aligned");
     if (out == q) return fail(h, QMOE_ERR_INVALID_ARG, "out must not overlap q");
-    OnDevice dev(h->device);
+    qmoe::OnDevice dev(h->device);
     if (dev.e != cudaSuccess) return cuda_fail(h, dev.e, "device select");
     const qmoe::Kv4AttnArgs a{shape(h), cache_of(cache), q, (int)q_t, (int)out_t, q_stride, out_stride, n_seqs,
                               n_tokens, max_new, cu_tokens, seq_len, block_table, scale, out, lse, h->status};

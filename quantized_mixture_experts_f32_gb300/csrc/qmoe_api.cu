@@ -852,6 +852,8 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* l
             if ((ls = qmoe::kv4_check_cache(kv, caches + l)) != QMOE_OK)
                 return fail(c, ls, "layer %d: %s", l, qmoe_kv4_last_error(kv));
     }
+    qmoe::OnDevice dev(c->device);
+    if (dev.e != cudaSuccess) return cuda_fail(c, dev.e, "device select");
     // rows behind the last token are left as they were: the layers run over them, so they are kept aside
     cudaError_t e = qmoe::launch_copy_rows_behind(hidden, c->hout, cu_tokens + n_seqs, n_tokens, k.hidden, c->stream);
     if (e != cudaSuccess) return cuda_fail(c, e, "row copy launch");

@@ -306,6 +306,20 @@ cudaError_t launch_step_layer_out(const PrefillLayerArgs& a, cudaStream_t st);
 cudaError_t launch_copy_rows_behind(const float* src, float* dst, const int32_t* n_tokens, int T, int H, cudaStream_t st);
 float* prefill_layer_x2(void* scratch, int T, int H, int nq, int nkv, int hd);
 
+// makes a handle's device current for a call (e: whether that went well), the one before it afterwards
+struct OnDevice {
+    int before = -1;
+    cudaError_t e;
+    explicit OnDevice(int device) {
+        e = cudaGetDevice(&before);
+        if (e == cudaSuccess && before != device) e = cudaSetDevice(device);
+        else before = -1;
+    }
+    ~OnDevice() {
+        if (before >= 0) cudaSetDevice(before);
+    }
+};
+
 // Text that qmoe_last_error(NULL) gives on this thread (a failed qmoe_kv4_create;
 // "" clears it), and whether the allocation-failure hook takes the next allocation.
 void create_error(const char* fmt, ...);

@@ -75,3 +75,26 @@ def test_product_path_does_not_import_the_oracle():
             if f.endswith((".py", ".cu", ".cuh", ".h", ".cpp")):
                 txt = open(os.path.join(dp, f)).read()
                 assert not re.search(r"(import\s+oracle|from\s+oracle|qmoe_oracle)", txt), f
+
+
+def _bodies(src):
+    """Name -> body of the functions a C++ source defines with the qmoe_ prefix."""
+    out = {}
+    for m in re.finditer(r"^[\w ]+?[ *](qmoe_\w+)\([^;{]*?\) \{\n(.*?)^\}", src, flags=re.S | re.M):
+        out[m.group(1)] = m.group(2)
+    return out
+
+
+def test_calls_on_a_cache_handle_select_its_device():
+    """They run on the handle's device, whichever is current: whatever reaches the device stands behind the
+    guard that selects it and puts the current one back."""
+    csrc = os.path.join(ROOT, "quantized_mixture_experts_f32_gb300", "csrc")
+    bodies = {}
+    for f in ("kv4_api.cu", "qmoe_api.cu"):
+        bodies.update(_bodies(open(os.path.join(csrc, f)).read()))
+    for name in ("qmoe_kv4_destroy", "qmoe_kv4_get_status", "qmoe_kv4_plan", "qmoe_kv4_append", "qmoe_kv4_attention",
+                 "qmoe_step_kv4"):
+        body = bodies[name]
+        device = re.search(r"\blaunch_\w+\(|\bcuda[A-Z]\w+\((?!\w*, dev\.e)|\brun_moe\(", body)
+        guard = re.search(r"\bOnDevice dev\(\w+->device\);", body)
+        assert device and guard and guard.start() < device.start(), name
