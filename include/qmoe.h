@@ -303,7 +303,9 @@ qmoe_status qmoe_prefill(qmoe_ctx* ctx, const qmoe_layer_weights* layers, int n_
  * whichever device is current.  Calls that share a handle share its workspace:
  * they must be ordered (graphs captured from one handle must not run at the same
  * time).  Contents of device arrays are checked on the device: an index outside
- * its range is never followed, and sets the status word (QMOE_ERR_DEVICE_CHECK). */
+ * its range is never followed, and sets the status word (QMOE_ERR_DEVICE_CHECK).
+ * Waits between CTAs are bounded: one that runs out sets QMOE_ERR_TIMEOUT, the rows
+ * it was for are not written, and the handle serves the next call. */
 typedef enum { QMOE_F32 = 0, QMOE_F16 = 1, QMOE_BF16 = 2 } qmoe_dtype;
 
 typedef struct qmoe_kv4 qmoe_kv4;
@@ -508,9 +510,15 @@ const char* qmoe_last_error(qmoe_ctx* ctx);
  *   wait_ns, records QMOE_ERR_TIMEOUT in the status word and exits without
  *   computing (its outputs are left unwritten).  Later launches are normal:
  *   this is how a test shows that a timed-out launch leaves the context usable.
- * qmoe_debug_fail_alloc: the next n workspace allocations of qmoe_create, in
- *   any thread, fail as if the device were out of memory (QMOE_ERR_NO_MEMORY). */
+ * qmoe_kv4_debug_stall_next: in the next qmoe_kv4_attention or qmoe_step_kv4 (its
+ *   first layer) on this handle the CTAs that share an item of a prompt chunk hand
+ *   their parts over wait_ns late (1..10^9); past 200 ms the CTA that joins them
+ *   gives up: QMOE_ERR_TIMEOUT, the item's rows left unwritten.
+ * qmoe_debug_fail_alloc: the next n workspace allocations of qmoe_create and
+ *   qmoe_kv4_create, in any thread, fail as if the device were out of memory
+ *   (QMOE_ERR_NO_MEMORY). */
 qmoe_status qmoe_debug_stall_next(qmoe_ctx* ctx, uint64_t wait_ns);
+qmoe_status qmoe_kv4_debug_stall_next(qmoe_kv4* kv, uint64_t wait_ns);
 void qmoe_debug_fail_alloc(int n);
 
 /* Bytes of workspace a context with this config allocates (0 on bad config). */

@@ -69,7 +69,7 @@ EXPORTED = ["qmoe_create", "qmoe_destroy", "qmoe_set_stream", "qmoe_forward", "q
             "qmoe_debug_stall_next", "qmoe_debug_fail_alloc",
             "qmoe_kv4_create", "qmoe_kv4_destroy", "qmoe_kv4_set_stream", "qmoe_kv4_workspace_bytes",
             "qmoe_kv4_get_status", "qmoe_kv4_last_error", "qmoe_kv4_plan", "qmoe_kv4_append",
-            "qmoe_kv4_attention", "qmoe_step_kv4"]
+            "qmoe_kv4_attention", "qmoe_step_kv4", "qmoe_kv4_debug_stall_next"]
 
 
 class qmoe_config(C.Structure):
@@ -177,6 +177,8 @@ def _load():
     L.qmoe_step_kv4.argtypes = [vp, vp, C.POINTER(qmoe_layer_weights), C.POINTER(qmoe_kv4_cache), i, i, i,
                                 i, ip, ip, ip, ip, vp, fp, ip]
     L.qmoe_step_kv4.restype = i
+    L.qmoe_kv4_debug_stall_next.argtypes = [vp, C.c_uint64]
+    L.qmoe_kv4_debug_stall_next.restype = i
     return L
 
 
@@ -372,6 +374,10 @@ def qmoe_step_kv4(ctx, kv, layers, caches, n_layers, n_seqs, n_tokens, max_new, 
     _check(ctx, lib.qmoe_step_kv4(ctx, kv, layers, caches, n_layers, n_seqs, n_tokens, max_new,
                                   _ptr(cu_tokens), _ptr(seq_len), _ptr(block_table), _ptr(positions),
                                   _ptr(slots), _ptr(hidden), _ptr(ids_out)))
+
+
+def qmoe_kv4_debug_stall_next(kv, wait_ns: int):
+    _check_kv4(kv, lib.qmoe_kv4_debug_stall_next(kv, wait_ns))
 
 
 def make_kv4_config(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_seqs, max_tokens,

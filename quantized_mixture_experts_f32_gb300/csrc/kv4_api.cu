@@ -20,6 +20,7 @@ struct qmoe_kv4 {
     int* status;          // device status word
     unsigned* arrive;     // arrival counter of the plan kernel
     qmoe::Kv4Work work;   // attention
+    unsigned long long stall_ns;   // test hook: work.stall_ns of the next attention
 };
 
 namespace {
@@ -29,7 +30,7 @@ constexpr int NOMINAL_SMS = 152;   // qmoe_kv4_workspace_bytes needs no device: 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-    size_t status, arrive, items, ext_items, ext_total, parts, ext_parts, total;
+    size_t status, arrive, items, ext_items, parts, ext_parts, total;
 };
 
 Layout layout(const qmoe_kv4_config* c, int num_sms) {
@@ -39,8 +40,7 @@ Layout layout(const qmoe_kv4_config* c, int num_sms) {
     L.status = take(sizeof(int));
     L.arrive = take(sizeof(unsigned));
     L.items = take(sizeof(unsigned) * qmoe::kv4_arrive_words(num_sms));
-    L.ext_items = take(sizeof(unsigned) * qmoe::kv4_arrive_words(num_sms));
-    L.ext_total = take(sizeof(unsigned));
+    L.ext_items = take(sizeof(unsigned) * qmoe::kv4_ext_words(num_sms));
     L.parts = take(sizeof(float) * qmoe::kv4_decode_part_floats(c->head_dim, num_sms));
     L.ext_parts = take(sizeof(float) * qmoe::kv4_extend_part_floats(c->head_dim, num_sms,
                                                                     (long long)c->max_tokens * (c->n_heads / c->n_kv_heads)));
@@ -113,8 +113,8 @@ qmoe_status check_rows(qmoe_kv4* h, const char* name, const void* p, int dtype, 
 
 namespace qmoe {
 
-Kv4View kv4_view(const qmoe_kv4* h) {
-    return {shape(h), h->work, h->status, h->stream, h->device, h->cfg.max_seqs, h->cfg.max_tokens};
+Kv4View kv4_view(qmoe_kv4* h) {
+    return {shape(h), h->work, h->status, &h->stall_ns, h->stream, h->device, h->cfg.max_seqs, h->cfg.max_tokens};
 }
 
 qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c) { return check_cache(h, c); }
@@ -176,8 +176,7 @@ qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
     h->status = reinterpret_cast<int*>(b + L.status);
     h->arrive = reinterpret_cast<unsigned*>(b + L.arrive);
     h->work = {reinterpret_cast<float*>(b + L.parts), reinterpret_cast<float*>(b + L.ext_parts),
-               reinterpret_cast<unsigned*>(b + L.items), reinterpret_cast<unsigned*>(b + L.ext_items),
-               reinterpret_cast<unsigned*>(b + L.ext_total), h->num_sms};
+               reinterpret_cast<unsigned*>(b + L.items), reinterpret_cast<unsigned*>(b + L.ext_items), h->num_sms, 0};
     e = cudaMemsetAsync(h->ws, 0, L.parts, h->stream);   // all but the attention's parts
     if (e == cudaSuccess) e = cudaStreamSynchronize(h->stream);
     if (e != cudaSuccess) {
@@ -308,9 +307,18 @@ qmoe_status qmoe_kv4_attention(qmoe_kv4* h, const qmoe_kv4_cache* cache, const v
     if (dev.e != cudaSuccess) return cuda_fail(h, dev.e, "device select");
     const qmoe::Kv4AttnArgs a{shape(h), cache_of(cache), q, (int)q_t, (int)out_t, q_stride, out_stride, n_seqs,
                               n_tokens, max_new, cu_tokens, seq_len, block_table, scale, out, lse, h->status};
-    const cudaError_t e = qmoe::launch_kv4_attention(a, h->work, h->stream);
+    qmoe::Kv4Work w = h->work;
+    w.stall_ns = h->stall_ns;
+    h->stall_ns = 0;
+    const cudaError_t e = qmoe::launch_kv4_attention(a, w, h->stream);
     if (e != cudaSuccess) return cuda_fail(h, e, "attention launch");
     h->err[0] = 0;
+    return QMOE_OK;
+}
+
+qmoe_status qmoe_kv4_debug_stall_next(qmoe_kv4* h, uint64_t wait_ns) {
+    if (!h || wait_ns == 0 || wait_ns > 1000000000ull) return QMOE_ERR_INVALID_ARG;
+    h->stall_ns = wait_ns;
     return QMOE_OK;
 }
 

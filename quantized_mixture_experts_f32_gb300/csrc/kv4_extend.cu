@@ -191,7 +191,7 @@ struct Piece {
 template <int HD, int TERMS>
 __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
     kv4_extend_kernel(const Kv4AttnArgs a, int few_rows, float* __restrict__ parts, unsigned* __restrict__ arrive,
-                      unsigned* __restrict__ total, int num_sms, int max_parts) {
+                      unsigned* __restrict__ total, int num_sms, int max_parts, unsigned long long stall_ns) {
     using G = EGeo<HD, TERMS>;
     constexpr int NT = G::NT, KC = G::KC, BUF = G::BUF;
     extern __shared__ __align__(1024) uint8_t smraw[];
@@ -617,17 +617,18 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         } else if (to_part) {
             named_bar(1, G::SOFT);
             if (tid == 0) {
+                if (stall_ns)                          // test hook, one second at most
+                    for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < stall_ns;) __nanosleep(1000);
                 __threadfence();
                 atomicAdd(arrive + p.part + 1, 1u);
             }
         } else {
             // The others are past their products: their parts are there in no more time than it takes to
-            // store one.
+            // store one.  The counters are cleared behind this kernel, not here: a part that comes after the
+            // wait gave up still counts.
             if (tid == 0) {
                 ok = grid_wait(arrive + p.part + 1, (unsigned)(splits - 1)) && ok;
                 __threadfence();
-                arrive[p.part] = 0u;
-                arrive[p.part + 1] = 0u;
                 joined_s = ok;
             }
             named_bar(1, G::SOFT);
@@ -969,7 +970,8 @@ cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, 
     const long long ragged = rows / (few_rows + 1) < a.n_seqs ? rows / (few_rows + 1) : a.n_seqs;
     const long long grid = a.s.nkv * (rows / G::ROWS + ragged) + w.num_sms;
     return launch_pdl(kv4_extend_kernel<HD, TERMS>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, a, few_rows,
-                      w.ext_parts, w.ext_arrive, w.ext_total, w.num_sms, EXTEND_PARTS * w.num_sms);
+                      w.ext_parts, w.ext_arrive, w.ext_arrive + kv4_arrive_words(w.num_sms), w.num_sms,
+                      EXTEND_PARTS * w.num_sms, w.stall_ns);
 }
 
 }  // namespace

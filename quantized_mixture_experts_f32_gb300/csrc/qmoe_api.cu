@@ -268,7 +268,7 @@ qmoe_status run_moe(qmoe_ctx* c, const float* x, const float* res, const float* 
 namespace qmoe {
 
 // kv4_api.cu
-Kv4View kv4_view(const qmoe_kv4* h);
+Kv4View kv4_view(qmoe_kv4* h);
 qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c);
 Kv4Cache kv4_cache(const qmoe_kv4_cache* c);
 
@@ -827,7 +827,7 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* l
     if (!kv || !layers || !caches || n_layers < 1 || !cu_tokens || !seq_len || !block_table || !positions || !slots ||
         !hidden)
         return fail(c, QMOE_ERR_INVALID_ARG, "null pointer or n_layers < 1");
-    const qmoe::Kv4View v = qmoe::kv4_view(kv);
+    qmoe::Kv4View v = qmoe::kv4_view(kv);
     if (v.s.nq != k.n_heads || v.s.nkv != k.n_kv_heads || v.s.hd != k.head_dim)
         return fail(c, QMOE_ERR_SHAPE, "the cache handle has %d/%d heads of %d, the context %d/%d of %d", v.s.nq, v.s.nkv,
                     v.s.hd, k.n_heads, k.n_kv_heads, k.head_dim);
@@ -854,6 +854,8 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* l
     }
     qmoe::OnDevice dev(c->device);
     if (dev.e != cudaSuccess) return cuda_fail(c, dev.e, "device select");
+    v.w.stall_ns = *v.stall_ns;
+    *v.stall_ns = 0;
     // rows behind the last token are left as they were: the layers run over them, so they are kept aside
     cudaError_t e = qmoe::launch_copy_rows_behind(hidden, c->hout, cu_tokens + n_seqs, n_tokens, k.hidden, c->stream);
     if (e != cudaSuccess) return cuda_fail(c, e, "row copy launch");
@@ -878,6 +880,7 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* l
                                    cu_tokens, seq_len, block_table, 1.0f / sqrtf((float)k.head_dim), r.att, nullptr,
                                    v.status};
         e = qmoe::launch_kv4_attention(at, v.w, c->stream);
+        v.w.stall_ns = 0;
         if (e != cudaSuccess) return cuda_fail(c, e, "attention launch");
         e = qmoe::launch_step_layer_out(a, c->stream);
         if (e != cudaSuccess) return cuda_fail(c, e, "O projection launch");

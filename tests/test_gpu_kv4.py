@@ -662,6 +662,32 @@ def test_chunks_of_a_long_context_split_over_the_gpu(q, nq, nkv, hd, page, lens,
         kv.close()
 
 
+def test_parts_that_come_late_are_reported_and_forgotten(q):
+    """The CTA that joins a split item gives up on parts that come too late; what they count afterwards is not
+    taken for the next call's parts, whose own come late, but in time."""
+    lens, news, nq, nkv, hd = [6000], [24], 8, 1, 128
+    kv, x, cu, table = _filled(q, lens, news, nq, nkv, hd, 64, "BF16", 5)
+    try:
+        y = x.flip(0).contiguous()
+        want, wl = kv.attention(y, cu, lens, table, "BF16")
+        assert kv.status() == 0
+        for _ in range(2):
+            q.qmoe_kv4_debug_stall_next(kv.h, 400_000_000)
+            out, lse = kv.attention(x, cu, lens, table, "BF16")
+            assert kv.status() == 7                                # QMOE_ERR_TIMEOUT, and no row of it
+            assert (out == 77.0).all() and (lse == 77.0).all()
+            for wait in (20_000_000, 0, 1_000_000):
+                if wait:
+                    q.qmoe_kv4_debug_stall_next(kv.h, wait)
+                out, lse = kv.attention(y, cu, lens, table, "BF16")
+                assert kv.status() == 0
+                assert torch.equal(out, want) and torch.equal(lse, wl)
+        assert q.lib.qmoe_kv4_debug_stall_next(kv.h, 0) == 1 and q.lib.qmoe_kv4_debug_stall_next(None, 5) == 1
+        assert q.lib.qmoe_kv4_debug_stall_next(kv.h, 2_000_000_000) == 1
+    finally:
+        kv.close()
+
+
 def test_the_most_sequences(q):
     rng = np.random.default_rng(3)
     n = 4096
