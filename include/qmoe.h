@@ -372,7 +372,10 @@ const char* qmoe_kv4_last_error(qmoe_kv4* kv);
  * and slots are -1, lengths, tables and the free list stay, and the status word
  * says why: QMOE_ERR_DEVICE_CHECK (a length or n_free out of range, more pages
  * free than exist), QMOE_ERR_SHAPE (more than cap_tokens new tokens, or a request
- * longer than its table row), QMOE_ERR_NO_MEMORY (too few free pages). */
+ * longer than its table row), QMOE_ERR_NO_MEMORY (too few free pages).
+ * Page ids are not what a step is refused for: one outside 0..n_pages-1 that the step
+ * pushes, pops or gives a token a slot in stays as it is in table and stack, its
+ * tokens have slot -1, and the status is QMOE_ERR_DEVICE_CHECK. */
 qmoe_status qmoe_kv4_plan(qmoe_kv4* kv, int n_seqs, const int32_t* seq_len, const int32_t* new_len,
                           int32_t* block_table, int32_t* free_pages, const int32_t* n_free,
                           int cap_tokens, int32_t* seq_len_out, int32_t* n_free_out,

@@ -141,6 +141,13 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
     auto taken = [&](int k) { return k < n_back ? returned(n_back - 1 - k) : a.free_pages[f - 1 - (k - n_back)]; };
     auto len_of = [&](int s) { return s_len[s] < 0 ? ~s_len[s] : s_len[s]; };
     auto have_of = [&](int s) { return (len_of(s) + a.page - 1) / a.page; };
+    // Page ids are handed on as they are; one that is no page's is reported, and its tokens go nowhere.  Every
+    // page that is taken has a token.
+    auto is_page = [&](int pg) {
+        const bool good = (unsigned)pg < (unsigned)a.n_pages;
+        if (!good) atomicExch(a.status, ST_DEVICE_CHECK);
+        return good;
+    };
 
     for (int t = gtid; t < a.cap; t += gn) {
         int pos = -1;
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
             pos = len_of(s) + (t - p_tok[s]);
             const int c = pos / a.page, h = have_of(s);
             const int pg = c < h ? a.table[(size_t)s * a.width + c] : taken(p_need[s] + c - h);
-            slot = (int64_t)pg * a.page + (pos - c * a.page);
+            if (is_page(pg)) slot = (int64_t)pg * a.page + (pos - c * a.page);
         }
         a.positions[t] = pos;
         a.slots[t] = slot;
@@ -159,7 +166,11 @@ __global__ void __launch_bounds__(PL_THREADS) kv4_plan_kernel(const Kv4PlanArgs 
         const int s = find_owner(p_need, a.n, k);
         a.table[(size_t)s * a.width + have_of(s) + (k - p_need[s])] = taken(k);
     }
-    for (int i = gtid; i < n_back - n_need; i += gn) a.free_pages[f + i] = returned(i);
+    for (int i = gtid; i < n_back - n_need; i += gn) {
+        const int pg = returned(i);
+        is_page(pg);
+        a.free_pages[f + i] = pg;
+    }
     for (int s = gtid; s <= a.n; s += gn) a.cu[s] = s < a.n ? p_tok[s] : n_tok;
 
     // last CTA out: every CTA has read the lengths and n_free

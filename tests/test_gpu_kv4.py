@@ -198,6 +198,48 @@ def test_plan_refuses_a_step_as_a_whole(q, what, status):
         kv.close()
 
 
+@pytest.mark.parametrize("n", [3, 700])
+@pytest.mark.parametrize("where", ["free", "returned", "returned and taken", "cached"])
+@pytest.mark.parametrize("bad", [-1, "n_pages", -2 ** 31, 2 ** 31 - 1])
+def test_plan_reports_pages_out_of_range(q, bad, where, n):
+    """In the free stack, among a finished request's pages, or where a request's next token goes: the id is
+    handed on as it is, its tokens have no slot, and the status word says so; all else as ever."""
+    rng = np.random.default_rng(n)
+    page, width, cap = 16, 4, 40 + 8 * n
+    seq_len = rng.integers(1, 32, n).astype(np.int32)
+    new_len = rng.integers(0, 9, n).astype(np.int32)
+    seq_len[:3], new_len[:3] = [20, 33, 16], [3, -1, 17 if where == "returned and taken" else 1]
+    if where == "returned":
+        new_len[0], new_len[2:] = 0, 0
+    elif where == "free":
+        new_len[1] = 1
+    n_pages = 3 * n + 9
+    table, free, n_free = _tables(rng, seq_len, width, page, n_pages)
+    bad = n_pages if bad == "n_pages" else bad
+    if where == "free":
+        free[:n_free] = bad
+    elif where == "cached":
+        table[0, 1] = bad
+    else:
+        table[1, 2 if where == "returned and taken" else 0] = bad
+    want = R.plan(seq_len, new_len, table, free, n_free, page, n_pages, cap)
+    out = (want["slots"] // page < 0) | (want["slots"] // page >= n_pages)
+    assert where == "returned" or (out & (want["pos"] >= 0)).any()
+    want["slots"][out] = -1
+    kv = Kv(q, 1, 1, 64, page, n_pages, n, cap, width)
+    try:
+        st, got = kv.plan(seq_len, new_len, table, free, n_free, cap)
+        assert st == 8
+        _same_plan(got, want, table)
+        assert kv.status() == 0
+        table[0, 3] = table[1, 3] = bad                            # columns that nothing looks up
+        table[0, 1], table[1, :3], free[:n_free] = 0, [1, 2, 3], np.arange(n_free)
+        st, got = kv.plan(seq_len, new_len, table, free, n_free, cap)
+        assert st == 0
+    finally:
+        kv.close()
+
+
 # --------------------------------------------------------------------------- append
 
 @pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
