@@ -80,8 +80,8 @@ struct Kv4AttnArgs {
 // each has its own workspace, zero between launches but for the parts.
 struct Kv4Work {
     float *parts, *ext_parts;          // parts of items that several CTAs share
-    unsigned *arrive, *ext_arrive;     // [kv4_arrive_words] and [kv4_ext_words]: arrival counters of those items,
-                                       // and behind the prompt kernel's the pieces it works on, while it does
+    unsigned *arrive, *ext_arrive;     // [kv4_arrive_words] each: arrival counters of those items
+    unsigned* ext_total;               // pieces the prompt kernel works on, while it does
     int num_sms;
     unsigned long long stall_ns;       // test hook: parts of split items are handed over this much later
 };
@@ -94,7 +94,6 @@ cudaError_t kv4_extend_prepare();
 cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st);
 cudaError_t launch_kv4_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, cudaStream_t st);
 int kv4_arrive_words(int num_sms);
-int kv4_ext_words(int num_sms);
 cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStream_t st);
 
 // What qmoe_step_kv4 needs of a handle.

@@ -30,7 +30,7 @@ constexpr int NOMINAL_SMS = 152;   // qmoe_kv4_workspace_bytes needs no device: 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 struct Layout {
-    size_t status, arrive, items, ext_items, parts, ext_parts, total;
+    size_t status, arrive, items, ext_items, ext_total, parts, ext_parts, total;
 };
 
 Layout layout(const qmoe_kv4_config* c, int num_sms) {
@@ -40,7 +40,8 @@ Layout layout(const qmoe_kv4_config* c, int num_sms) {
     L.status = take(sizeof(int));
     L.arrive = take(sizeof(unsigned));
     L.items = take(sizeof(unsigned) * qmoe::kv4_arrive_words(num_sms));
-    L.ext_items = take(sizeof(unsigned) * qmoe::kv4_ext_words(num_sms));
+    L.ext_items = take(sizeof(unsigned) * qmoe::kv4_arrive_words(num_sms));
+    L.ext_total = take(sizeof(unsigned));
     L.parts = take(sizeof(float) * qmoe::kv4_decode_part_floats(c->head_dim, num_sms));
     L.ext_parts = take(sizeof(float) * qmoe::kv4_extend_part_floats(c->head_dim, num_sms,
                                                                     (long long)c->max_tokens * (c->n_heads / c->n_kv_heads)));
@@ -176,7 +177,8 @@ qmoe_status qmoe_kv4_create(const qmoe_kv4_config* cfg, qmoe_kv4** out) {
     h->status = reinterpret_cast<int*>(b + L.status);
     h->arrive = reinterpret_cast<unsigned*>(b + L.arrive);
     h->work = {reinterpret_cast<float*>(b + L.parts), reinterpret_cast<float*>(b + L.ext_parts),
-               reinterpret_cast<unsigned*>(b + L.items), reinterpret_cast<unsigned*>(b + L.ext_items), h->num_sms, 0};
+               reinterpret_cast<unsigned*>(b + L.items), reinterpret_cast<unsigned*>(b + L.ext_items),
+               reinterpret_cast<unsigned*>(b + L.ext_total), h->num_sms, 0};
     e = cudaMemsetAsync(h->ws, 0, L.parts, h->stream);   // all but the attention's parts
     if (e == cudaSuccess) e = cudaStreamSynchronize(h->stream);
     if (e != cudaSuccess) {

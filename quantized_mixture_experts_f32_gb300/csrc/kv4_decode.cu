@@ -142,8 +142,8 @@ __device__ __forceinline__ int cta_of_unit(long long w, long long x, int g) {
 
 template <int HD, int TERMS, int NR>
 __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
-    kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, unsigned* __restrict__ ext_arrive, int ext_words,
-                      float* __restrict__ parts, unsigned* __restrict__ arrive) {
+    kv4_decode_kernel(const Kv4AttnArgs a, int few_rows, unsigned* __restrict__ ext_total, float* __restrict__ parts,
+                      unsigned* __restrict__ arrive) {
     using G = DGeo<HD, TERMS, NR>;
     extern __shared__ __align__(16) uint8_t sm[];
     uint8_t* ring = sm;
@@ -156,17 +156,16 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int r = lane >> 2, j = lane & 3;             // operand row (position, element run); a pair of q rows
     const int group = a.s.nq / a.s.nkv;
-    // Behind the prompt kernel (ext_words) nothing is waited for: it started its dependents after its own wait,
+    // Behind the prompt kernel (ext_total) nothing is waited for: it started its dependents after its own wait,
     // so what it waited for is complete, and it writes nothing that is read here.  The last CTA waits for it
-    // before it ends, for the sake of what comes next, and clears its counters, which it no longer touches then
-    // even where one of its waits gave up; the others make room for each other.
-    if (!ext_words) pdl_wait();
+    // before it ends, for the sake of what comes next; the others make room for each other.
+    if (!ext_total) pdl_wait();
     else __threadfence();
     pdl_launch_dependents();
     auto leave = [&] {
-        if (ext_words && blockIdx.x == gridDim.x - 1) {
+        if (ext_total && blockIdx.x == gridDim.x - 1) {
             pdl_wait();
-            for (int i = tid; i < ext_words; i += DT) ext_arrive[i] = 0u;
+            if (tid == 0) *ext_total = 0u;
         }
     };
 
@@ -723,8 +722,7 @@ template <int HD, int TERMS, int NR>
 cudaError_t launch_decode(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4Work& w, cudaStream_t st) {
     using G = DGeo<HD, TERMS, NR>;
     return launch_pdl(kv4_decode_kernel<HD, TERMS, NR>, dim3(w.num_sms * (HD == 256 ? 1 : 2)), dim3(DT),
-                      G::smem(a.n_seqs), st, a, few_rows, w.ext_arrive, behind ? kv4_ext_words(w.num_sms) : 0, w.parts,
-                      w.arrive);
+                      G::smem(a.n_seqs), st, a, few_rows, behind ? w.ext_total : nullptr, w.parts, w.arrive);
 }
 
 template <int HD, int TERMS>
@@ -777,7 +775,6 @@ cudaError_t launch_kv4_decode(const Kv4AttnArgs& a, int few_rows, bool behind, c
 }
 
 int kv4_arrive_words(int num_sms) { return 2 * num_sms; }   // a CTA of the one kernel, a part of the other
-int kv4_ext_words(int num_sms) { return kv4_arrive_words(num_sms) + 1; }
 
 // Which kernel a sequence's rows (new tokens x heads of the group) go to.  The decode kernel
 // reads and widens the cache once per 16 rows, the prompt kernel once per 256, with a dearer start
@@ -800,8 +797,7 @@ cudaError_t launch_kv4_attention(const Kv4AttnArgs& a, const Kv4Work& w, cudaStr
         if (e != cudaSuccess) return e;
     }
     const cudaError_t e = launch_kv4_decode(a, few, prompts, w, st);
-    if (e != cudaSuccess && prompts)                                       // which the kernel would have cleared
-        cudaMemsetAsync(w.ext_arrive, 0, sizeof(unsigned) * kv4_ext_words(w.num_sms), st);
+    if (e != cudaSuccess && prompts) cudaMemsetAsync(w.ext_total, 0, sizeof(unsigned), st);   // which the kernel would have
     return e;
 }
 

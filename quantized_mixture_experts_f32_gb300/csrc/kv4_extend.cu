@@ -620,16 +620,17 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 if (stall_ns)                          // test hook, one second at most
                     for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < stall_ns;) __nanosleep(1000);
                 __threadfence();
-                atomicAdd(arrive + p.part + 1, 1u);
+                if (atomicAdd(arrive + p.part + 1, 1u) == (unsigned)(splits - 1)) arrive[p.part] = arrive[p.part + 1] = 0u;
             }
         } else {
             // The others are past their products: their parts are there in no more time than it takes to
-            // store one.  The counters are cleared behind this kernel, not here: a part that comes after the
-            // wait gave up still counts.
+            // store one.  Where the wait gave up all the same, the parts that come later still count, and this
+            // CTA as one of them: whoever is last clears the counters.
             if (tid == 0) {
-                ok = grid_wait(arrive + p.part + 1, (unsigned)(splits - 1)) && ok;
+                const bool all = grid_wait(arrive + p.part + 1, (unsigned)(splits - 1));
                 __threadfence();
-                joined_s = ok;
+                if (all || atomicAdd(arrive + p.part + 1, 1u) == (unsigned)(splits - 1)) arrive[p.part] = arrive[p.part + 1] = 0u;
+                joined_s = all && ok;
             }
             named_bar(1, G::SOFT);
             ok = joined_s && ok;
@@ -970,8 +971,7 @@ cudaError_t launch_extend(const Kv4AttnArgs& a, int few_rows, const Kv4Work& w, 
     const long long ragged = rows / (few_rows + 1) < a.n_seqs ? rows / (few_rows + 1) : a.n_seqs;
     const long long grid = a.s.nkv * (rows / G::ROWS + ragged) + w.num_sms;
     return launch_pdl(kv4_extend_kernel<HD, TERMS>, dim3((unsigned)grid), dim3(G::THREADS), G::SMEM, st, a, few_rows,
-                      w.ext_parts, w.ext_arrive, w.ext_arrive + kv4_arrive_words(w.num_sms), w.num_sms,
-                      EXTEND_PARTS * w.num_sms, w.stall_ns);
+                      w.ext_parts, w.ext_arrive, w.ext_total, w.num_sms, EXTEND_PARTS * w.num_sms, w.stall_ns);
 }
 
 }  // namespace
