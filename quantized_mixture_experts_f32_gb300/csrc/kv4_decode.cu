@@ -284,6 +284,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     auto put_q = [&](const Segment& r, int buf, const Rows& x) {
         uint32_t* qf = qf2 + buf * (G::QF / 4);
         const float kg = a.c.kg[r.g];
+        const Kv4Factor factor = kv4_factor(a.scale, kg);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
             const int row = nr * 8 + warp;
@@ -294,9 +295,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
 #pragma unroll
             for (int o = 16; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
             const int e = kv4_exponent(big);
-            const float fac = kv4_factor(a.scale, kg, e);
-            const float un = fac < 0.f ? -kv4_pow2(-e) : kv4_pow2(-e);            // z's largest is q.k's largest then
-            if (lane == 0) fac_s[buf][row] = fmaxf(fabsf(fac), 1e-38f);  // not 0: -inf stays -inf, and 1e-38 q.k is 0
+            const float un = kv4_negative(a.scale, kg) ? -kv4_pow2(-e) : kv4_pow2(-e);   // z's largest is q.k's largest then
 #pragma unroll
             for (int i = 0; i < HD / 64; ++i) {
                 uint32_t hi, lo;
@@ -314,6 +313,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                     qf[((nr * (HD / 16) + step) * 32 + at) * 4 + 2 + b] = lo;
                 }
             }
+            if (lane == 0) fac_s[buf][row] = kv4_factor_of(factor, e);
         }
     };
 

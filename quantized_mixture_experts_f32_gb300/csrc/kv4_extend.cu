@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
             constexpr int LR = HD / 8, RW = 32 / LR;   // lanes of a row, rows at a time
             const float kg = a.c.kg[p.g];
             // of scale * kg: z's largest is q.k's largest then
-            const uint32_t sign = (int)(__float_as_uint(a.scale) ^ __float_as_uint(kg)) < 0 ? 0x80008000u : 0u;
+            const uint32_t sign = kv4_negative(a.scale, kg) ? 0x80008000u : 0u;
             const int d = (lane % LR) * 8, sub = lane / LR;
             const long long mine = tid < rows ? ((long long)(p.q0 + tok) * a.q_stride + (long long)h * HD) * (TERMS == 2 ? 4 : 2) : -1;
             uint8_t* qs = sm + G::Q + x * TERMS * G::QT + (d >> 6) * 16384;
@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                     }
                 }
             }
-            fac = fmaxf(fabsf(kv4_factor(a.scale, kg, exponent)), 1e-38f);   // not 0: -inf stays -inf, and 1e-38 q.k is 0
+            fac = kv4_factor_of(kv4_factor(a.scale, kg), exponent);
             fence_proxy_async();
         }
         mbar_arrive(qfull);

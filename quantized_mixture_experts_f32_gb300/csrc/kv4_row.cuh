@@ -37,12 +37,30 @@ __device__ __forceinline__ int kv4_exponent(float big) {
 }
 __device__ __forceinline__ float kv4_pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }   // |e| < 127
 
-// z of a row scaled by 2^-e, in powers of two, from its product with K's codes; 2^e in
-// halves, so that neither a tiny scale or global nor a large row leaves fp32's range on
-// the way where the result is in it
-__device__ __forceinline__ float kv4_factor(float scale, float global, int e) {
-    const int h = e / 2;
-    return scale * kv4_pow2(h) * (1.4426950408889634f * global) * kv4_pow2(e - h);
+// What brings a row's product with K's codes to its scores in powers of two, in size:
+// scale * log2(e) * global * 2^e for a row that was scaled by 2^-e.  The factors' own
+// powers of two are set apart (f in 2^-46 .. 2^5, or 0) and put in with the row's as one
+// exponent, so that nothing leaves fp32's range on the way where the result is in it.
+struct Kv4Factor {
+    float f;
+    int e;
+};
+__device__ __forceinline__ Kv4Factor kv4_factor(float scale, float global) {
+    scale = fabsf(scale);
+    global = fabsf(global);
+    const int es = kv4_exponent(scale), eg = kv4_exponent(global);
+    const float f = scale * kv4_pow2(-es) * (1.4426950408889634f * (global * kv4_pow2(-eg)));
+    return {f, f == 0.f ? -1024 : es + eg};
+}
+// Not 0, so that a masked -inf stays -inf (1e-38 q.k is 0 to any other score), and finite,
+// so that a q.k of 0 stays 0.
+__device__ __forceinline__ float kv4_factor_of(const Kv4Factor& x, int e) {
+    const int bits = (int)__float_as_uint(x.f), all = x.e + e, to = (bits >> 23) + all;
+    return to < 1 ? 1e-38f : to > 254 ? 3.4e38f : __uint_as_float((uint32_t)(bits + all * (1 << 23)));
+}
+// whether that product is negative
+__device__ __forceinline__ bool kv4_negative(float scale, float global) {
+    return (int)(__float_as_uint(scale) ^ __float_as_uint(global)) < 0;
 }
 
 // Eight E2M1 codes -> four half2, bytes in order.  One conversion a byte: naming the

@@ -524,6 +524,44 @@ def test_any_finite_scale(q, scale, news):
         kv.close()
 
 
+@pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
+@pytest.mark.parametrize("kg,mag", [(3e38, 1.0), (1e-42, 1.0), (2.0 ** -100, 2.0 ** -14), (2.0 ** 126, 2.0 ** -14), (2.0 ** -149, 2.0 ** 10)])
+@pytest.mark.parametrize("news", [[1, 1], [33, 20]])
+def test_scale_and_global_at_opposite_ends(q, news, kg, mag, dtype):
+    """Scores of ordinary size from a scale and a global of which either leaves fp32's range together with a
+    constant or with the row's size."""
+    lens = [40, 70]
+    kv, x, cu, table = _filled(q, lens, news, 8, 2, 64, 16, dtype, 2)
+    try:
+        kv.g[0][:] = kg
+        kv.kg.copy_(cuda(kv.g[0]))
+        x = x * mag
+        scale = float(np.float32(0.125 * (5 / 2688) / np.float64(np.float32(kg)) / mag))
+        assert 0 < scale < 3.4e38
+        out, lse = kv.attention(x, cu, lens, table, dtype, scale=scale)
+        assert kv.status() == 0
+        _check(kv, x, out, lse, cu, lens, table, scale=scale)
+    finally:
+        kv.close()
+
+
+def test_scores_of_zero_under_a_factor_past_the_range(q):
+    """q.k is 0 whatever scale * global is."""
+    lens = [40, 70]
+    for news in ([1, 1], [33, 20]):
+        kv, x, cu, table = _filled(q, lens, news, 8, 2, 64, 16, "F32", 2)
+        try:
+            kv.kg.fill_(1e30)
+            kv.t["k_codes"].zero_()
+            kv.t["k_scales"].fill_(0x38)
+            out, lse = kv.attention(x, cu, lens, table, "F32", scale=1e30)
+            kv.t["k_codes"].fill_(0x11)
+            want, wl = kv.attention(x, cu, lens, table, "F32", scale=0.0)
+            assert kv.status() == 0 and torch.equal(out, want) and torch.equal(lse, wl)
+        finally:
+            kv.close()
+
+
 @pytest.mark.parametrize("mag", [1e-6, 1e4, 1e18])
 @pytest.mark.parametrize("news", [[1, 1], [33, 20]])
 def test_rows_of_any_size(q, mag, news):
