@@ -26,6 +26,7 @@
 // widening keeps the ALU at 50%, the tensor pipe at 23%); 64 of 100-8192, BF16, 28.7 us,
 // 2.5 TB/s, with a start and an end of about 9 us; 1 of 4096, F32, 11.3 us, of which the
 // positions are 2: lengths and shares take 1.8, the first bytes 1.8, the join 3.5.
+#include <limits.h>
 #include <math.h>
 
 #include "kv4.cuh"
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
     uint32_t* qf2 = reinterpret_cast<uint32_t*>(sm + G::RING);                      // q fragments, two items
     long long* pre = reinterpret_cast<long long*>(sm + G::RING + 2 * G::QF);        // [n_seqs+1]
     __shared__ long long wsum[DW];
-    __shared__ float fac_s[2][G::ROWS], m_s[DW][8], l_s[DW][8];
+    __shared__ __align__(8) float fac_s[2][G::ROWS], m_s[DW][8], l_s[DW][8];
     __shared__ Segment seg_s[2];
     __shared__ int last_s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -347,6 +348,13 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                 base[nr][y] = 0.f;
                 l[nr][y] = 0.f;
             }
+        bool far = false;
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) far |= kv4_far<HD>(fac[nr][0]) | kv4_far<HD>(fac[nr][1]);
+        far = __any_sync(0xffffffffu, far);            // z takes its factor in the branch of masks then
+        if (far)
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) fac[nr][0] = fac[nr][1] = 1.f;
         const int lim_min = len - S.n + row0 / group + 1;
         float o[NR][HD / 16][4];
 #pragma unroll
@@ -435,7 +443,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                         }
                     }
                 }
-                const bool edge = halves != 3 || pos + TP > lim_min;
+                const bool edge = halves != 3 || pos + TP > lim_min || far;
                 if (edge) {
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr)
@@ -445,6 +453,17 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
                             for (int y = 0; y < 2; ++y)
                                 if (!((halves >> (n >> 1)) & 1) || pos + n * 8 + pos_of_row(r) >= lim[nr][y])
                                     z[n >> 1][nr][2 * (n & 1) + y] = -INFINITY;
+                    if (far) {
+#pragma unroll
+                        for (int nr = 0; nr < NR; ++nr) {
+                            const float2 f = *reinterpret_cast<const float2*>(fac_s[cur] + nr * 8 + 2 * j);
+#pragma unroll
+                            for (int n = 0; n < 4; ++n) {
+                                z[n >> 1][nr][2 * (n & 1)] = __fmul_rn(z[n >> 1][nr][2 * (n & 1)], f.x);
+                                z[n >> 1][nr][2 * (n & 1) + 1] = __fmul_rn(z[n >> 1][nr][2 * (n & 1) + 1], f.y);
+                            }
+                        }
+                    }
                     apart();
                 }
                 // m follows a row's maximum only when some lane saw it 2^SLACK ahead

@@ -29,6 +29,7 @@
 // the step's 900 ns.  777 F32 tokens from their first, 29.6 us: an item's start (lengths, q)
 // and end take 10 of its 20 us, and 196 items are 1.3 waves.  Pieces taken in turn by CTAs
 // that stay were no faster (1173 us; the short calls 2 us slower).
+#include <limits.h>
 #include <math.h>
 
 #include "kv4.cuh"
@@ -370,7 +371,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
         auto tok_of = [&](int row) { return (p.row0 + row) / group; };
         auto head_of = [&](int row, int tok) { return p.g * group + p.row0 + row - tok * group; };
         const int lim = tid < rows ? len - p.n + tok_of(tid) + 1 : 0;
-        const int lim_min = len - p.n + tok_of(tid & ~31) + 1;                   // the warp's first row's
+        int lim_min = len - p.n + tok_of(tid & ~31) + 1;                         // the warp's first row's
         // where the thread's row starts: in q, and in out
         const int tok = tok_of(tid), h = head_of(tid, tok);
         float fac = 0.f;
@@ -436,6 +437,19 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 }
             }
             fac = kv4_factor_of(kv4_factor(a.scale, kg), exponent);
+            float largest = fac;                       // for rows in [1, 2)
+            if (TERMS == 1 && a.q_t == KV4_F16 && !sign) {
+                __half2 big = __float2half2_rn(0.f);   // of what this lane has of any of the warp's rows
+#pragma unroll
+                for (int r = 0; r < 32; r += RW) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(word(r));
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) big = __hmax2(big, __habs2(*reinterpret_cast<const __half2*>(&w[k])));
+                }
+                largest *= kv4_pow2(kv4_exponent(fminf(fmaxf(__low2float(big), __high2float(big)), 65504.f)));
+            }
+            if (__any_sync(0xffffffffu, kv4_far<HD>(largest))) lim_min = INT_MIN;   // z takes fac in the branch of masks
             fence_proxy_async();
         }
         mbar_arrive(qfull);
@@ -471,6 +485,9 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
 #pragma unroll
                     for (int k = 0; k < SC; ++k)
                         if (pos + k >= lim || !((good >> (k >> 4)) & 1)) z[k] = 0xff800000u;
+                    if (lim_min == INT_MIN)
+#pragma unroll
+                        for (int k = 0; k < SC; ++k) z[k] = __float_as_uint(__fmul_rn(__uint_as_float(z[k]), fac));
                     asm volatile("");                  // a branch, not selects that run every time
                 }
                 float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -479,7 +496,8 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
 #pragma unroll
                     for (int y = 0; y < 4; ++y)
                         mx4[y] = max3(mx4[y], __uint_as_float(z[k + 2 * y]), __uint_as_float(z[k + 2 * y + 1]));
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fac;
+                const float f1 = lim_min == INT_MIN ? 1.f : fac;   // what z still wants
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * f1;
                 if (__any_sync(0xffffffffu, mx > m + KV4_P_SLACK)) {
                     const float mn = fmaxf(m, mx);
                     const float f = m == -INFINITY ? 0.f : kv4_ex2(m - mn);
@@ -505,7 +523,7 @@ __global__ void __launch_bounds__(EGeo<HD, TERMS>::THREADS, 1)
                 }
                 const float base = m == -INFINITY ? 0.f : m - KV4_P_UP;
                 // p over the z that made it
-                const unsigned long long fac2 = pair64(__float_as_uint(fac), __float_as_uint(fac));
+                const unsigned long long fac2 = pair64(__float_as_uint(f1), __float_as_uint(f1));
                 const unsigned long long base2 = pair64(__float_as_uint(-base), __float_as_uint(-base));
                 unsigned long long l2[2] = {0ull, 0ull};
                 uint32_t hi[SC / 2], lo[TERMS == 2 ? SC / 2 : 1];

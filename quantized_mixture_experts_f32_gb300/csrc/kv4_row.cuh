@@ -58,6 +58,13 @@ __device__ __forceinline__ float kv4_factor_of(const Kv4Factor& x, int e) {
     const int bits = (int)__float_as_uint(x.f), all = x.e + e, to = (bits >> 23) + all;
     return to < 1 ? 1e-38f : to > 254 ? 3.4e38f : __uint_as_float((uint32_t)(bits + all * (1 << 23)));
 }
+// The argument of a weight's exponential is q.k fac - m in one rounding, m itself rounded
+// to fp32.  Whether scores may be so large, past 2^21, that m's rounding is no small part
+// of it (|q.k| < 2^13 head_dim, q scaled): then q.k fac is rounded as m is first.
+template <int HD>
+__device__ __forceinline__ bool kv4_far(float fac) {
+    return fac > 0x1p8f / HD;
+}
 // whether that product is negative
 __device__ __forceinline__ bool kv4_negative(float scale, float global) {
     return (int)(__float_as_uint(scale) ^ __float_as_uint(global)) < 0;

@@ -562,6 +562,65 @@ def test_scores_of_zero_under_a_factor_past_the_range(q):
             kv.close()
 
 
+@pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("scale", [1e5, -1e8, 1e12, 1e30])
+@pytest.mark.parametrize("news", [[1, 1, 1], [33, 20, 3], [3, 150, 1]])
+def test_scores_far_past_the_exponential(q, news, scale, hd, dtype):
+    """Scores whose rounding alone is more than the exponential's whole range: the largest one takes all."""
+    lens = [40, 700, 9]
+    kv, x, cu, table = _filled(q, lens, news, 8, 2, hd, 16, dtype, 2)
+    try:
+        out, lse = kv.attention(x, cu, lens, table, dtype, scale=scale)
+        assert kv.status() == 0
+        t = x.shape[0]
+        xq = x.double().cpu().numpy().reshape(t, 8, hd)
+        k, v = kv.values()
+        want, wl, vmax, zabs, seen = R.attention(xq, (k, v), cu, lens, table, scale, kv.page)
+        got, gl = out.double().cpu().numpy().reshape(t, 8, hd), lse.double().cpu().numpy()
+        half = float(torch.finfo(out.dtype).eps) / 2
+        # two weights of a mean at least, each within 2^-22 + (seen + 8) roundings, one fp16 term of 16-bit rows' weights
+        w = 2.0 ** -22 + (seen[:, None] + 8) * R.EPS32 + (0 if dtype == "F32" else 2.0 ** -11 + seen[:, None] * 2.0 ** -25)
+        assert np.isfinite(got).all() and (np.abs(got) <= (vmax * (1 + 2 * w + half))[..., None]).all()
+        dz = (hd + 12) * R.EPS32 * zabs + 2.0 ** -22 * zabs
+        assert (np.abs(gl - wl) <= dz + 4 * R.EPS32 * zabs + 7).all()   # 7: ln(seen), which a row's rounding may lose
+        clear = 0
+        for s in range(3):
+            L = lens[s]
+            cols = table[s, :-(-L // 16)].astype(np.int64)
+            for i in range(news[s]):
+                r, n = int(cu[s]) + i, L - news[s] + i + 1
+                for h in range(8):
+                    kk, vv = k[cols, h // 4].reshape(-1, hd)[:n], v[cols, h // 4].reshape(-1, hd)[:n]
+                    z = np.sort(scale * (kk @ xq[r, h]))[::-1]
+                    if n == 1 or z[0] - z[1] > 2 * dz[r, h] + 40:  # no rounding makes another one the largest
+                        clear += 1
+                        top = vv[np.argmax(scale * (kk @ xq[r, h]))]
+                        assert (np.abs(got[r, h] - top) <= 2 * w[r] * vmax[r, h] + half * np.abs(top)).all(), (r, h)
+        assert clear > 0.8 * t * 8
+    finally:
+        kv.close()
+
+
+@pytest.mark.parametrize("dtype", ["F32", "BF16"])
+def test_scores_far_past_the_exponential_split_over_the_gpu(q, dtype):
+    """The same where parts of a context are joined: whichever the parts, one position takes all."""
+    for lens, news, nkv in (([9000], [1], 1), ([5000], [40], 1)):
+        kv, x, cu, table = _filled(q, lens, news, 8, nkv, 64, 16, dtype, 4)
+        try:
+            out, lse = kv.attention(x, cu, lens, table, dtype, scale=1e12)
+            assert kv.status() == 0 and torch.isfinite(out.float()).all()
+            t = x.shape[0]
+            xq = x.double().cpu().numpy().reshape(t, 8, 64)
+            want, wl, vmax, zabs, seen = R.attention(xq, kv.values(), cu, lens, table, 1e12, 16)
+            got = out.double().cpu().numpy().reshape(t, 8, 64)
+            same = (np.abs(got - want) <= 2.0 ** -7 * vmax[..., None]).all(-1)
+            assert same.mean() > 0.9                               # but for rows whose two largest are near each other
+            assert (np.abs(lse.double().cpu().numpy() - wl) <= (64 + 16) * R.EPS32 * zabs + 2.0 ** -22 * zabs + 10).all()
+        finally:
+            kv.close()
+
+
 @pytest.mark.parametrize("mag", [1e-6, 1e4, 1e18])
 @pytest.mark.parametrize("news", [[1, 1], [33, 20]])
 def test_rows_of_any_size(q, mag, news):
