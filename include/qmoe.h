@@ -330,7 +330,9 @@ typedef struct {
     void* v_scales;
     const float* k_global;  /* [n_kv_heads], finite; rows of a head whose global is not
                                positive are appended as zeros */
-    const float* v_global;  /* [n_kv_heads] */
+    const float* v_global;  /* [n_kv_heads], finite; attention's results lose bits where one
+                               is smaller than 2^-80 (divided by the weights' sum it may
+                               be subnormal) */
 } qmoe_kv4_cache;
 
 /* Create a handle on the current device and allocate its workspace (parts of

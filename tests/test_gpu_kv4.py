@@ -198,6 +198,25 @@ def test_plan_refuses_a_step_as_a_whole(q, what, status):
         kv.close()
 
 
+@pytest.mark.parametrize("n", [1024, 1025, 2047, 2048])
+def test_plan_of_a_thousand_requests_and_more(q, n):
+    """As many requests as a thread scans two and four of."""
+    rng = np.random.default_rng(n)
+    page, width = 32, 5
+    seq_len = rng.integers(0, 71, n).astype(np.int32)
+    new_len = rng.integers(-1, 40, n).astype(np.int32)
+    n_pages = int((-(-(seq_len + np.maximum(new_len, 0)) // page)).sum()) + 3
+    table, free, n_free = _tables(rng, seq_len, width, page, n_pages)
+    cap = int(np.maximum(new_len, 0).sum()) + 4
+    kv = Kv(q, 1, 1, 64, page, n_pages, n, cap, width)
+    try:
+        st, got = kv.plan(seq_len, new_len, table, free, n_free, cap)
+        assert st == 0
+        _same_plan(got, R.plan(seq_len, new_len, table, free, n_free, page, n_pages, cap), table)
+    finally:
+        kv.close()
+
+
 @pytest.mark.parametrize("n", [3, 700])
 @pytest.mark.parametrize("where", ["free", "returned", "returned and taken", "cached"])
 @pytest.mark.parametrize("bad", [-1, "n_pages", -2 ** 31, 2 ** 31 - 1])
@@ -351,6 +370,31 @@ def test_append_of_what_is_not_finite_keeps_scales_finite(q):
         assert ((kv.t["k_scales"].cpu().numpy()[0, 0, :4] & 0x7F) != 0x7F).all()
         c, s, _ = R.quantise(x[3:].cpu().numpy().reshape(1, 1, 64), kv.g[0])
         assert np.array_equal(kv.t["k_codes"].cpu().numpy()[0, 0, 3], c[0, 0])
+    finally:
+        kv.close()
+
+
+@pytest.mark.parametrize("dtype", ["F32", "BF16"])
+@pytest.mark.parametrize("nkv,hd", [(10, 256), (33, 64), (17, 128)])
+def test_append_of_rows_a_cta_takes_in_turns(q, nkv, hd, dtype):
+    """More than 2048 elements a row, the last turn of a row partly filled."""
+    rng = np.random.default_rng(hd)
+    t, page, n_pages = 7, 16, 2
+    kv = Kv(q, nkv, nkv, hd, page, n_pages, 1, t, n_pages, seed=3)
+    try:
+        x = torch.from_numpy(rng.normal(size=(2, t, nkv * hd))).cuda().to(TORCH[dtype])
+        slots = rng.permutation(n_pages * page)[:t].astype(np.int64)
+        hat = torch.full((2, t + 1, nkv * hd), 5.0, device="cuda")
+        kv.append(x[0], x[1], cuda(slots), dtype, hat[0], hat[1])
+        assert kv.status() == 0
+        p, o = slots // page, slots % page
+        for i, n in enumerate("kv"):
+            c, sc, val = R.quantise(x[i].float().cpu().numpy().reshape(t, nkv, hd), kv.g[i])
+            wc, ws = np.full((n_pages, nkv, page, hd // 2), 0x5A, np.uint8), np.full((n_pages, nkv, page, hd // 16), 0x7F, np.uint8)
+            wc[p, :, o], ws[p, :, o] = c, sc
+            assert np.array_equal(kv.t[n + "_codes"].cpu().numpy(), wc)
+            assert np.array_equal(kv.t[n + "_scales"].cpu().numpy(), ws)
+            assert np.array_equal(hat[i, :t].cpu().numpy(), val.reshape(t, -1).astype(np.float32)) and (hat[i, t] == 5.0).all()
     finally:
         kv.close()
 
@@ -525,6 +569,22 @@ def test_any_finite_scale(q, scale, news):
 
 
 @pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
+@pytest.mark.parametrize("scale,sign", [(-0.2, 1), (0.0, 1), (0.125, -1), (-0.125, -1)])
+@pytest.mark.parametrize("news", [[1, 1], [33, 20]])
+def test_signs_of_scale_and_global(q, scale, sign, news, dtype):
+    lens = [40, 70]
+    kv, x, cu, table = _filled(q, lens, news, 8, 2, 64, 16, dtype, 2)
+    try:
+        kv.g[0][1] *= sign                                         # the second kv head's keys
+        kv.kg.copy_(cuda(kv.g[0]))
+        out, lse = kv.attention(x, cu, lens, table, dtype, scale=scale)
+        assert kv.status() == 0
+        _check(kv, x, out, lse, cu, lens, table, scale=scale)
+    finally:
+        kv.close()
+
+
+@pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
 @pytest.mark.parametrize("kg,mag", [(3e38, 1.0), (1e-42, 1.0), (2.0 ** -100, 2.0 ** -14), (2.0 ** 126, 2.0 ** -14), (2.0 ** -149, 2.0 ** 10)])
 @pytest.mark.parametrize("news", [[1, 1], [33, 20]])
 def test_scale_and_global_at_opposite_ends(q, news, kg, mag, dtype):
@@ -619,6 +679,28 @@ def test_scores_far_past_the_exponential_split_over_the_gpu(q, dtype):
             assert (np.abs(lse.double().cpu().numpy() - wl) <= (64 + 16) * R.EPS32 * zabs + 2.0 ** -22 * zabs + 10).all()
         finally:
             kv.close()
+
+
+@pytest.mark.parametrize("dtype", ["F32", "F16", "BF16"])
+@pytest.mark.parametrize("vg", [2.0 ** -80, -0.01, 2.0 ** 100])
+@pytest.mark.parametrize("lens,news", [([40, 70], [1, 1]), ([40, 70], [33, 20]), ([6000], [24])])
+def test_small_large_and_negative_globals_of_v(q, lens, news, vg, dtype):
+    nq, nkv = (8, 1) if len(lens) == 1 else (8, 2)
+    kv, x, cu, table = _filled(q, lens, news, nq, nkv, 64, 16, dtype, 2)
+    try:
+        kv.g[1][:] = vg
+        kv.vg.copy_(cuda(kv.g[1]))
+        out, lse = kv.attention(x, cu, lens, table, dtype, "F32")
+        assert kv.status() == 0
+        t = x.shape[0]
+        xq = x.double().cpu().numpy().reshape(t, nq, 64)
+        want, wl, vmax, zabs, seen = R.attention(xq, kv.values(), cu, lens, table, 0.125, 16)
+        ob, lb = R.attention_bound(want / vg, vmax / abs(vg), zabs, seen, 64, dtype != "F32", 2.0 ** -24)
+        got = out.double().cpu().numpy().reshape(t, nq, 64)
+        assert (np.abs(got - want) <= ob * abs(vg)).all()
+        assert (np.abs(lse.double().cpu().numpy() - wl) <= lb).all()
+    finally:
+        kv.close()
 
 
 @pytest.mark.parametrize("mag", [1e-6, 1e4, 1e18])
