@@ -48,7 +48,8 @@ __device__ __forceinline__ void append_lane(const Kv4AppendArgs& a, int t, int c
 #pragma unroll
     for (int j = 0; j < 8; ++j) bmax = fmaxf(bmax, fabsf(v[j]));
     bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, 1));
-    const uint32_t s = g > 0.f ? __nv_cvt_float_to_fp8(bmax / (6.0f * g), __NV_SATFINITE, __NV_E4M3) : 0u;
+    // (448 for infinity over a 6 g that is infinite too: a scale is never NaN)
+    const uint32_t s = g > 0.f ? __nv_cvt_float_to_fp8(fminf(bmax / (6.0f * g), 448.f), __NV_SATFINITE, __NV_E4M3) : 0u;
     const float sf = e4m3_f(s), d = sf * g;
     uint32_t code = 0u;
     if (d >= 0x1p-90f && d <= 0x1p90f && bmax <= d * 0x1p30f) {

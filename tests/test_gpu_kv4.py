@@ -399,6 +399,23 @@ def test_append_of_rows_a_cta_takes_in_turns(q, nkv, hd, dtype):
         kv.close()
 
 
+def test_append_of_infinity_under_a_large_global_keeps_scales_finite(q):
+    """6 * global past fp32's range: infinity over infinity is no scale."""
+    kv = Kv(q, 1, 1, 64, 16, 1, 1, 8, 1)
+    try:
+        kv.kg.fill_(1e38)
+        kv.vg.fill_(3e38)
+        x = torch.randn(3, 64, device="cuda")
+        x[0, 3], x[1, 20] = float("inf"), float("-inf")
+        x[1, 40] = float("nan")
+        kv.append(x, x, cuda(np.arange(3)))
+        assert kv.status() == 0
+        for n in ("k_scales", "v_scales"):
+            assert ((kv.t[n].cpu().numpy()[0, 0, :3] & 0x7F) != 0x7F).all()
+    finally:
+        kv.close()
+
+
 # --------------------------------------------------------------------------- attention
 
 def _filled(q, lens, news, nq, nkv, hd, page, dtype, seed, width=None, extra=3, stream=0):
