@@ -441,8 +441,9 @@ qmoe_status qmoe_kv4_attention(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const 
  *  cu_tokens, seq_len, block_table, positions, slots : of the step, as
  *              qmoe_kv4_plan gives them; max_new as for qmoe_kv4_attention.
  *  ids_out   : nullable, int32 [n_layers][n_tokens][k] selected experts.
- * Rows behind cu_tokens[n_seqs] (a padded batch) are left as they were, their ids
- * unspecified.  Requires the attention geometry in the config and the shapes of
+ * Rows that qmoe_kv4_attention would not write (behind cu_tokens[n_seqs] in a padded
+ * batch, of a sequence that is skipped) are left as they were, their ids unspecified;
+ * their K and V go where slots says.  Requires the attention geometry in the config and the shapes of
  * qmoe_prefill; max_ctx does not bound the positions.  Device-side findings are in
  * the status words of both the context and the handle. */
 qmoe_status qmoe_step_kv4(qmoe_ctx* ctx, qmoe_kv4* kv, const qmoe_layer_weights* layers,

@@ -26,6 +26,7 @@
 #include <math.h>
 
 #include "kquant.cuh"
+#include "kv4.cuh"
 #include "pdl.cuh"
 #include "qmoe_internal.h"
 #include "umma.cuh"
@@ -165,12 +166,22 @@ __global__ void __launch_bounds__(128) qk_norm_rope_rows(float* __restrict__ qkv
     }
 }
 
-// rows behind the last token (*n_tokens of them are tokens): src -> dst
-__global__ void __launch_bounds__(NR_THREADS) copy_rows_behind(const float* __restrict__ src, float* __restrict__ dst,
-                                                               const int32_t* __restrict__ n_tokens, int H) {
+// rows that the cache's attention does not write: src -> dst.  A CTA looks its row up in all sequences.
+__global__ void __launch_bounds__(NR_THREADS) copy_rows_apart(const float* __restrict__ src, float* __restrict__ dst,
+                                                              const Kv4AttnArgs a, int H) {
     pdl_wait();
-    if ((int)blockIdx.x < *n_tokens) return;
-    const size_t base = (size_t)blockIdx.x * H;
+    const int t = blockIdx.x;
+    bool written = false, descends = false;
+    for (int s = threadIdx.x; s < a.n_seqs; s += NR_THREADS) {
+        Kv4Seq q;
+        kv4_seq(a, s, q);
+        written |= t >= q.q0 && t < q.q0 + q.n;        // n = 0: skipped
+        descends |= a.cu[s + 1] < a.cu[s];
+    }
+    written = __syncthreads_or(written);
+    descends = __syncthreads_or(descends);
+    if (written && !descends) return;
+    const size_t base = (size_t)t * H;
     for (int i = threadIdx.x; i < H; i += NR_THREADS) dst[base + i] = src[base + i];
 }
 
@@ -770,8 +781,8 @@ cudaError_t launch_step_layer_out(const PrefillLayerArgs& a, cudaStream_t st) {
     return launch_out(a, layer_scratch(a), st);
 }
 
-cudaError_t launch_copy_rows_behind(const float* src, float* dst, const int32_t* n_tokens, int T, int H, cudaStream_t st) {
-    return launch_pdl(copy_rows_behind, dim3(T), dim3(NR_THREADS), 0, st, src, dst, n_tokens, H);
+cudaError_t launch_copy_rows_apart(const float* src, float* dst, const Kv4AttnArgs& a, int H, cudaStream_t st) {
+    return launch_pdl(copy_rows_apart, dim3(a.n_tokens), dim3(NR_THREADS), 0, st, src, dst, a, H);
 }
 
 float* prefill_layer_x2(void* scratch, int T, int H, int nq, int nkv, int hd) {

@@ -856,8 +856,12 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* l
     if (dev.e != cudaSuccess) return cuda_fail(c, dev.e, "device select");
     v.w.stall_ns = *v.stall_ns;
     *v.stall_ns = 0;
-    // rows behind the last token are left as they were: the layers run over them, so they are kept aside
-    cudaError_t e = qmoe::launch_copy_rows_behind(hidden, c->hout, cu_tokens + n_seqs, n_tokens, k.hidden, c->stream);
+    const int64_t qd = (int64_t)k.n_heads * k.head_dim;
+    qmoe::Kv4AttnArgs at{v.s, {}, nullptr, qmoe::KV4_F16, qmoe::KV4_F16, qd, qd, n_seqs, n_tokens, max_new, cu_tokens,
+                         seq_len, block_table, 1.0f / sqrtf((float)k.head_dim), nullptr, nullptr, v.status};
+    // rows that no sequence has, or one that the attention skips, are left as they were: the layers run over
+    // them, so they are kept aside
+    cudaError_t e = qmoe::launch_copy_rows_apart(hidden, c->hout, at, k.hidden, c->stream);
     if (e != cudaSuccess) return cuda_fail(c, e, "row copy launch");
     float* x2 = qmoe::prefill_layer_x2(c->pl_scratch, n_tokens, k.hidden, k.n_heads, k.n_kv_heads, k.head_dim);
     for (int l = 0; l < n_layers; ++l) {
@@ -870,15 +874,13 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* l
         qmoe::StepRows r;
         e = qmoe::launch_step_layer_qkv(a, positions, l == 0, &r, c->stream);
         if (e != cudaSuccess) return cuda_fail(c, e, "Q/K/V launch");
-        const qmoe::Kv4Cache cache = qmoe::kv4_cache(caches + l);
-        const qmoe::Kv4AppendArgs ap{v.s, cache, r.k, r.v, qmoe::KV4_F32, n_tokens, r.kv_stride, r.kv_stride, slots,
+        at.c = qmoe::kv4_cache(caches + l);
+        at.q = r.q;
+        at.out = r.att;
+        const qmoe::Kv4AppendArgs ap{v.s, at.c, r.k, r.v, qmoe::KV4_F32, n_tokens, r.kv_stride, r.kv_stride, slots,
                                      nullptr, nullptr, v.status};
         e = qmoe::launch_kv4_append(ap, c->stream);
         if (e != cudaSuccess) return cuda_fail(c, e, "append launch");
-        const int64_t qd = (int64_t)k.n_heads * k.head_dim;
-        const qmoe::Kv4AttnArgs at{v.s, cache, r.q, qmoe::KV4_F16, qmoe::KV4_F16, qd, qd, n_seqs, n_tokens, max_new,
-                                   cu_tokens, seq_len, block_table, 1.0f / sqrtf((float)k.head_dim), r.att, nullptr,
-                                   v.status};
         e = qmoe::launch_kv4_attention(at, v.w, c->stream);
         v.w.stall_ns = 0;
         if (e != cudaSuccess) return cuda_fail(c, e, "attention launch");
@@ -890,7 +892,7 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* c, qmoe_kv4* kv, const qmoe_layer_weights* l
                                        QMOE_Q4_K, w.down_t, n_tokens, hidden, ids_l, nullptr);
         if (st != QMOE_OK) return st;
     }
-    e = qmoe::launch_copy_rows_behind(c->hout, hidden, cu_tokens + n_seqs, n_tokens, k.hidden, c->stream);
+    e = qmoe::launch_copy_rows_apart(c->hout, hidden, at, k.hidden, c->stream);
     if (e != cudaSuccess) return cuda_fail(c, e, "row copy launch");
     c->err[0] = 0;
     return QMOE_OK;

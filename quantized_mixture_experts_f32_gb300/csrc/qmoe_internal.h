@@ -302,8 +302,9 @@ struct StepRows {
 cudaError_t launch_step_layer_qkv(const PrefillLayerArgs& a, const int32_t* positions, bool table, StepRows* rows,
                                   cudaStream_t st);
 cudaError_t launch_step_layer_out(const PrefillLayerArgs& a, cudaStream_t st);
-// rows *n_tokens .. T-1 of src to dst
-cudaError_t launch_copy_rows_behind(const float* src, float* dst, const int32_t* n_tokens, int T, int H, cudaStream_t st);
+// the rows of src that the attention of these arguments leaves as they are, to dst
+struct Kv4AttnArgs;
+cudaError_t launch_copy_rows_apart(const float* src, float* dst, const Kv4AttnArgs& a, int H, cudaStream_t st);
 float* prefill_layer_x2(void* scratch, int T, int H, int nq, int nkv, int hd);
 
 // makes a handle's device current for a call (e: whether that went well), the one before it afterwards

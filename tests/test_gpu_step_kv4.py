@@ -187,6 +187,55 @@ def test_steps_of_whole_layers(q, name):
     print(f"{name}: rel err {worst:.2e}")
 
 
+@pytest.mark.parametrize("n", [4, 300])
+def test_rows_that_no_sequence_serves_stay(q, n):
+    """Sequences that the attention skips, rows before the first and behind the last one, offsets that descend:
+    their rows are left as they were, the others' are what they are without them."""
+    geo, page, width = SMALL, 16, 3
+    new = np.ones(n, np.int32)
+    new[:4] = [5, 3, 1, 9]
+    T = int(new.sum())
+    sv = Server(q, geo, n, page, width, n * 3, T + 4)
+    try:
+        sv.plan(torch.from_numpy(new).cuda())
+        sv.ok()
+        x = torch.from_numpy(synth.prefill_input(geo, T + 4)).cuda()
+        cu, lens = sv.cu.clone(), sv.len.clone()
+        want = x.clone()
+        sv.step(want, T + 4, 9)
+        sv.ok()
+        served = torch.ones(T + 4, dtype=torch.bool, device="cuda")
+        served[T:] = False
+        assert torch.equal(want[~served], x[~served]) and not torch.equal(want[:T], x[:T])
+
+        def stay(first, last, mx=9):
+            h = x.clone()
+            sv.step(h, T + 4, mx)
+            assert q.qmoe_get_status(sv.ctx) == 0 and q.qmoe_kv4_get_status(sv.kv) == 8
+            keep = ~served
+            keep[first:last] = True
+            assert torch.equal(h[keep], x[keep]) and torch.equal(h[~keep], want[~keep])
+            sv.cu.copy_(cu)
+            sv.len.copy_(lens)
+
+        sv.len[1] = -1                                             # sequence 1, rows 5 .. 7
+        stay(5, 8)
+        sv.len[n - 1] = width * page + 1                           # the last one
+        stay(T - new[n - 1], T)
+        stay(9, 18, 8)                                             # more new tokens than max_new says: sequence 3
+        sv.cu[0] = -1                                              # no such row
+        stay(0, 5)
+        sv.cu[2] = 4                                               # sequence 1 ends before it begins
+        stay(0, T)
+        sv.cu[:2] = 5                                              # rows before the first sequence's
+        h = x.clone()
+        sv.step(h, T + 4, 9)
+        sv.ok()
+        assert torch.equal(h[:5], x[:5]) and torch.equal(h[5:T], want[5:T])
+    finally:
+        sv.close()
+
+
 def test_a_captured_step_of_whole_layers(q):
     """plan and step captured once and replayed while the sequences grow equal the uncaptured calls."""
     geo, n, page, width, n_pages, cap = SMALL, 3, 16, 3, 9, 3
