@@ -416,9 +416,10 @@ qmoe_status qmoe_kv4_append(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const voi
  *  lse         : F32 [n_tokens][n_heads] or NULL: log of the sum of exp(scale * q.k_p).
  * A row that sees no position is 0 with lse -inf.  Rows behind cu_tokens[n_seqs] are
  * left as they were.  q head h reads kv head h / (n_heads/n_kv_heads).  Products
- * have fp32 accumulators and the running maximum and sum are fp32; F32 rows enter
- * the tensor cores as two fp16 terms each, F16 and BF16 rows as one (K and V are
- * exact in fp16).  A sequence whose offsets, length or new tokens are out of range
+ * have fp32 accumulators and the running maximum and sum are fp32; F32 rows and
+ * their softmax weights enter the tensor cores as two fp16 terms each (22 bits), F16
+ * and BF16 rows and their weights as one (11 bits, whatever out_t is; K and V are
+ * exact in fp16).  Scores have to be in fp32's range.  A sequence whose offsets, length or new tokens are out of range
  * (negative, past the table row, n_tokens or max_new) is skipped, a position whose
  * page id is out of range counts as not visible, and offsets that descend anywhere
  * leave all rows as they were; each sets QMOE_ERR_DEVICE_CHECK.  Row addresses,
@@ -435,7 +436,8 @@ qmoe_status qmoe_kv4_attention(qmoe_kv4* kv, const qmoe_kv4_cache* cache, const 
  * with its K and V rows appended (qmoe_kv4_append) and attended to
  * (qmoe_kv4_attention, q rows and output as fp16) in caches[l] instead of the
  * layers' own fp16 caches (k_cache and v_cache of the layers are not used and may
- * be NULL).  Decoding, draft tokens and prompt chunks may share a call.
+ * be NULL).  The caches' globals are the caller's choice, made before the rows are
+ * known: what is larger than 2688 globals is appended as that.  Decoding, draft tokens and prompt chunks may share a call.
  *  kv        : handle with the context's n_heads, n_kv_heads and head_dim, on its
  *              device (where the call runs, whichever is current) and stream.
  *  cu_tokens, seq_len, block_table, positions, slots : of the step, as

@@ -10,11 +10,15 @@
 // Both products are mma.sync m16n8k16 (fp16 in, fp32 out) with the cache as the
 // 16-row operand and the rows as the eight columns: S^T = K Q^T, O^T += V^T P^T.  K and
 // V are exact in fp16 (2 x 4 significant bits).  F32 rows enter as hi + lo (TERMS = 2,
-// 22 bits), two products into one accumulator.  tcgen05 would want the widened K and V
-// in shared memory, 4x the bytes the cache has, for 128 rows of which eight exist;
-// here a thread widens what it has loaded straight into operand registers.  Each row
-// of q is first scaled by the power of two of its largest element, so any fp32 or
-// bf16 range fits fp16.
+// 22 bits), two products into one accumulator, and so do their weights.  16-bit rows enter
+// as one term, and their weights too: 2^-11 of each at most, no more than the half step
+// that F16 results are off by themselves, where a second term would double the products of V;
+// l sums the weights as they are before that rounding.  (4 sequences of 131072 positions,
+// F16: 2.9e-4 from 64 bits, of which the result's own rounding is 2.1e-4.)  tcgen05 would
+// want the widened K and V in shared memory, 4x the bytes the cache has, for 128 rows of
+// which eight exist; here a thread widens what it has loaded straight into operand
+// registers.  Each row of q is first scaled by the power of two of its largest element, so
+// any fp32 or bf16 range fits fp16.
 //
 // The order of head elements in q.k and of positions in p.v is free: K and Q elements
 // are dealt to the four lanes of a position in contiguous runs (16-byte loads), and
@@ -22,10 +26,11 @@
 //
 // All positions of all items are dealt out evenly to two CTAs a multiprocessor, whatever
 // sequence they belong to.  Measured (32 q heads, 4 kv heads of 128, one token each): 4
-// sequences of 131072 positions, F16, 66.6 us, 4.5 TB/s, bound by issue (61% of the slots;
-// widening keeps the ALU at 50%, the tensor pipe at 23%); 64 of 100-8192, BF16, 28.7 us,
-// 2.5 TB/s, with a start and an end of about 9 us; 1 of 4096, F32, 11.3 us, of which the
-// positions are 2: lengths and shares take 1.8, the first bytes 1.8, the join 3.5.
+// sequences of 131072 positions, F16, 66.7 us, 4.5 TB/s: no pipe is full (issue 61%, ALU
+// 50% with the widening, tensor 23%, memory two thirds), and four warps a scheduler, all
+// that 122 registers leave room for, do not cover each other's waits; 64 of 100-8192,
+// BF16, 28.7 us, 2.4 TB/s, with a start and an end of about 9 us; 1 of 4096, F32, 11.4 us,
+// of which the positions are 2: lengths and shares take 1.8, the first bytes 1.8, the join 3.5.
 #include <limits.h>
 #include <math.h>
 
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(DT, HD == 256 ? 1 : 2)
         bool far = false;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) far |= kv4_far<HD>(fac[nr][0]) | kv4_far<HD>(fac[nr][1]);
-        far = __any_sync(0xffffffffu, far);            // z takes its factor in the branch of masks then
+        far = __any_sync(0xffffffffu, far);            // z takes its factor in the branch of masks, fac is 1 then
         if (far)
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) fac[nr][0] = fac[nr][1] = 1.f;
@@ -753,6 +758,8 @@ cudaError_t pick_rows(const Kv4AttnArgs& a, int few_rows, bool behind, const Kv4
     // 154 / 217).  So with few sequences 8.  Beside prompts too: requests bring one token there as a rule, and
     // what is smaller fills the multiprocessors that come free more evenly (24 requests of 300-6000 positions,
     // four with up to 500 new tokens, the others with one, 82.9 / 75.1; 23 with two and one with 500, 90.4 / 83.8).
+    // One rule for all types and head_dim, set at 128: at 256 it picks the slower one for one or two very long
+    // sequences (95 / 114 above).
     const int group = a.s.nq / a.s.nkv;
     const bool two = (long long)a.max_new * group > 8 &&
                      (behind ? group > 8 : (long long)a.n_seqs * a.s.nkv * 16 > w.num_sms);
@@ -801,7 +808,8 @@ int kv4_arrive_words(int num_sms) { return 2 * num_sms; }   // a CTA of the one 
 // 4096 positions, 16 rows 29.6 / 38.5, 24 rows 40.2 / 38.7, 64 rows 64 / 39; 64 of 1024, 16 rows
 // 33.8 / 42.3, 24 rows 49 / 42.  With few sequences the passes of the decode kernel run side by
 // side: 1 of 32768, 40 rows 36.0 / 40.2, 64 rows 39.4 / 40.4, 80 rows 45.6 / 50.2; 1 of 4096, 64
-// rows 19.4 / 26.8.
+// rows 19.4 / 26.8.  There 64 is on the decode kernel's side of the border, which lies past 80 rows
+// at 32768; other types and head_dim were not measured for it.
 //
 // The prompt kernel goes first: its CTAs do not end together, and the decode kernel's, smaller and
 // more, run where it has ended (bf16, 24 requests of 300-6000 positions, four of them with up to 500

@@ -18,15 +18,16 @@
 // longer than its softmax.  P overlays the S it came from; the next S into the slot is
 // issued after the product that reads P and runs after it.
 // O is rescaled only when a row's maximum rose by 2^8 since the last time.
-// F32 rows: q = hi + lo and p = hi + lo, two products each (TERMS = 2).
+// F32 rows: q = hi + lo and p = hi + lo, two products each (TERMS = 2).  16-bit rows: one
+// fp16 term of each, p's rounding 2^-11 of it at most, as in kv4_decode.cu.
 // Few items: the chunks of an item are split over CTAs; the one that comes last keeps its
 // part and joins the others' to it.
 //
 // Measured (32 q heads, 4 kv heads of 128): 4 sequences of 8192-16384 positions that bring
-// 2048 BF16 tokens each, 1174 us, 1380 TFLOP/s of visible products; the issue slots are
+// 2048 BF16 tokens each, 1172 us, 1380 TFLOP/s of visible products; the issue slots are
 // 61% taken (widening, exponentials, moves from and to TMEM) and the tensor pipe 58%: the
 // softmax of a step, its two products and the widening of its positions each take most of
-// the step's 900 ns.  777 F32 tokens from their first, 29.6 us: an item's start (lengths, q)
+// the step's 900 ns.  777 F32 tokens from their first, 29.9 us: an item's start (lengths, q)
 // and end take 10 of its 20 us, and 196 items are 1.3 waves.  Pieces taken in turn by CTAs
 // that stay were no faster (1173 us; the short calls 2 us slower).
 #include <limits.h>
