@@ -306,7 +306,10 @@ qmoe_status qmoe_prefill(qmoe_ctx* ctx, const qmoe_layer_weights* layers, int n_
  * its range is never followed, and sets the status word (QMOE_ERR_DEVICE_CHECK).
  * Waits between CTAs are bounded: one that runs out sets QMOE_ERR_TIMEOUT, the rows
  * it was for are not written, and the handle serves the next call. */
-typedef enum { QMOE_F32 = 0, QMOE_F16 = 1, QMOE_BF16 = 2 } qmoe_dtype;
+typedef enum {
+    QMOE_F32 = 0, QMOE_F16 = 1, QMOE_BF16 = 2,
+    QMOE_E4M3 = 3           /* only where an entry point names it */
+} qmoe_dtype;
 
 typedef struct qmoe_kv4 qmoe_kv4;
 
@@ -453,6 +456,146 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* ctx, qmoe_kv4* kv, const qmoe_layer_weights*
                           int max_new, const int32_t* cu_tokens, const int32_t* seq_len,
                           const int32_t* block_table, const int32_t* positions,
                           const int64_t* slots, float* hidden, int32_t* ids_out);
+
+/* ------------------------------------------------------------------ the 8-bit path's rows
+ *
+ * What a decoder layer over FP8 weights needs around qmoe_forward_fp8 and the paged
+ * cache: the norms, 8-bit activations, dense products on them, rotary positions and
+ * the append that rotates.  In the order of a layer:
+ *   qmoe_rmsnorm (residual added, 8 bits out), qmoe_linear_fp8 (Q/K/V),
+ *   qmoe_kv4_append_rope, qmoe_kv4_attention, qmoe_fp8_quantize, qmoe_linear_fp8 (O,
+ *   residual added), qmoe_rmsnorm, qmoe_forward_fp8.
+ *
+ * 8-bit rows: E4M3 codes [rows][cols], contiguous, and one F32 scale per 128
+ * consecutive elements of a row [rows][ceil(cols/128)]; value = e4m3(code) * scale.
+ * Made in fp32: scale = max|y| of the block / 448; code = E4M3 nearest to y / scale,
+ * ties to even, saturating; zero where the scale is 0 (max|y| / 448 may be too small
+ * for fp32).  A NaN has the NaN code and does not count for the maximum; in a block
+ * with an infinity the scale is infinite, the infinity's code NaN, the finite ones' 0.
+ *
+ * Conventions as above.  The calls on a qmoe_ctx use its stream and run on its device,
+ * whichever is current; none has a workspace, so max_tokens does not bound them.
+ * Strides are in elements of the rows' type, 0 for contiguous rows; row base
+ * addresses and strides in bytes are multiples of 16.  Unless said otherwise outputs
+ * must not overlap inputs. */
+
+/* h = x (+ residual); y = h / sqrt(mean(h^2) + eps) (* weight), for n_rows rows of dim
+ * elements (one launch).  The sum, its mean square and the quotient are fp32, from h
+ * before it is rounded to res_t; squares have to be in fp32's range.
+ *  x        : rows of x_t (F32, F16, BF16), x_stride apart.
+ *  residual : rows of res_t, res_stride apart, or NULL (then res_t and res_stride are
+ *             not used).
+ *  sum      : rows of res_t, res_stride apart, h itself, or NULL; may be the residual, or
+ *             x of that type and stride.  Only with a residual.
+ *  weight   : F32 [dim], 16-byte aligned, or NULL (1).
+ *  eps      : positive, finite.
+ *  n_rows 1..2^24, dim a multiple of 16 up to 65536.
+ *  y        : rows of y_t, y_stride apart (F32, F16, BF16; may be x of that type and
+ *             stride), or 8-bit rows (QMOE_E4M3; y_stride 0 or dim).
+ *  y_scale  : F32 [n_rows][ceil(dim/128)] for 8-bit rows, else NULL. */
+qmoe_status qmoe_rmsnorm(qmoe_ctx* ctx, const void* x, qmoe_dtype x_t, int64_t x_stride,
+                         const void* residual, qmoe_dtype res_t, int64_t res_stride, void* sum,
+                         const float* weight, float eps, int n_rows, int dim, void* y,
+                         qmoe_dtype y_t, int64_t y_stride, float* y_scale);
+
+/* n_rows rows of cols elements of x_t as 8-bit rows (one launch).  cols a multiple of
+ * 16 up to 65536, n_rows 1..2^24. */
+qmoe_status qmoe_fp8_quantize(qmoe_ctx* ctx, const void* x, qmoe_dtype x_t, int64_t x_stride,
+                              int n_rows, int cols, void* codes, float* scale);
+
+typedef enum {
+    QMOE_ACT_NONE = 0,
+    QMOE_ACT_RELU = 1,
+    QMOE_ACT_SILU = 2,     /* z / (1 + exp(-z)) */
+    QMOE_ACT_GELU = 3      /* z * (1 + erf(z / sqrt 2)) / 2 */
+} qmoe_act;
+
+/* out = act(x W^T + bias) + residual (one launch).
+ *  x_codes, x_scale : 8-bit rows [n_tokens][in_features] (codes 16-byte aligned).
+ *  w_codes : E4M3 [out_features][in_features], 16-byte aligned; w_scale: F32, one per
+ *            128 x 128 block, [ceil(out_features/128)][ceil(in_features/128)] (the weights
+ *            of qmoe_forward_fp8, with blocks cut at the edges).
+ *  bias    : F32 [out_features] or NULL.
+ *  residual: rows of out_t, res_stride apart, or NULL; may be out with the same stride.
+ *  out     : rows of out_t (F32, F16, BF16), out_stride apart, at least out_features.
+ *  in_features a multiple of 16 up to 2^20, n_tokens 1..2^24, out_features 1..2^24.
+ * Products of codes are accumulated in fp32 by blocks of 128, each block's sum scaled
+ * and added in fp32, in an order that the sizes alone decide.  The product of a
+ * token's and a block's scale has to be in fp32's range.  Only the out_features first
+ * elements of a row of out are written. */
+qmoe_status qmoe_linear_fp8(qmoe_ctx* ctx, const void* x_codes, const float* x_scale, int n_tokens,
+                            int in_features, const void* w_codes, const float* w_scale,
+                            int out_features, const float* bias, qmoe_act act, const void* residual,
+                            int64_t res_stride, void* out, qmoe_dtype out_t, int64_t out_stride);
+
+/* Rotary positions.  Pair j of a head (j < rot_dim/2) is turned by the angle p * f_j at
+ * position p; elements from rot_dim on stay as they are.
+ *   pairs: (j, j + rot_dim/2) in QMOE_ROPE_HALF, (2j, 2j + 1) in QMOE_ROPE_INTERLEAVED
+ *   f_j = base^(-2j/rot_dim), then
+ *     QMOE_ROPE_LINEAR: f_j / factor
+ *     QMOE_ROPE_PARTS : f_j (1 - r_j) + f_j / factor r_j, where r_j rises from 0 at pair
+ *       max(0, floor(d(beta_fast))) to 1 at min(rot_dim - 1, ceil(d(beta_slow))), at least
+ *       0.001 pairs further on, d(t) = rot_dim ln(orig_ctx / (2 pi t)) / (2 ln base) being the
+ *       pair that turns t times in orig_ctx positions (YaRN, Peng et al. 2023)
+ * mscale multiplies cosines and sines; 0 stands for 0.1 ln(factor) + 1 with
+ * QMOE_ROPE_PARTS (factor > 1), else 1. */
+typedef enum { QMOE_ROPE_HALF = 0, QMOE_ROPE_INTERLEAVED = 1 } qmoe_rope_layout;
+typedef enum { QMOE_ROPE_PLAIN = 0, QMOE_ROPE_LINEAR = 1, QMOE_ROPE_PARTS = 2 } qmoe_rope_scaling;
+typedef struct {
+    int layout;             /* qmoe_rope_layout */
+    int rot_dim;            /* elements of a head that are turned, a multiple of 16, 16..256 */
+    int scaling;            /* qmoe_rope_scaling */
+    int n_pos;              /* positions of the table, 1..2^24 */
+    double base;            /* > 1 */
+    double factor;          /* LINEAR, PARTS: > 0 */
+    double orig_ctx;        /* PARTS: > 0 */
+    double beta_fast;       /* PARTS: > beta_slow */
+    double beta_slow;       /* PARTS: > 0 */
+    double mscale;          /* >= 0 */
+    float* table;           /* F32 [n_pos][rot_dim/2][2], cosine and sine, 16-byte aligned */
+} qmoe_rope_config;
+
+/* Fill rope->table (angles, cosines and sines in 64 bits, rounded once): made once, and
+ * kept by the caller for the calls below. */
+qmoe_status qmoe_rope_table(qmoe_ctx* ctx, const qmoe_rope_config* rope);
+
+/* Rows of n_heads heads, each normalised on demand and turned (one launch):
+ *   n = x / sqrt(mean(x^2) + eps) * norm   over a head, where norm is not NULL
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * every product, sum and quotient fp32, rounded once (no fused multiply-add); the mean
+ * square of a head in more bits, its inverse root rounded to fp32.
+ *  rope      : layout, rot_dim (at most head_dim), n_pos and table are used.
+ *  x, out    : n_tokens rows of n_heads*head_dim elements of x_t, x_stride and out_stride
+ *              apart; out may be x with the same stride.
+ *  head_dim  : 64, 128 or 256.  n_tokens 1..2^20, n_heads 1..1024.
+ *  positions : int32 [n_tokens].  A row of a negative position (padding) is left as
+ *              it was in out, one of a position past the table too, and that sets
+ *              QMOE_ERR_DEVICE_CHECK.
+ *  norm      : F32 [head_dim], 16-byte aligned, or NULL (then eps is not used). */
+qmoe_status qmoe_rope(qmoe_ctx* ctx, const qmoe_rope_config* rope, const void* x, qmoe_dtype x_t,
+                      int64_t x_stride, int n_tokens, int n_heads, int head_dim,
+                      const int32_t* positions, const float* norm, float eps, void* out,
+                      int64_t out_stride);
+
+/* qmoe_kv4_append with qmoe_rope before it (one launch): the K rows are normalised (k_norm)
+ * and turned as there and appended with the V rows, and the q rows are turned (q_norm)
+ * into q_out; sizes and heads are the handle's.
+ *  rope     : rot_dim a multiple of 32 (at most head_dim).
+ *  q, q_out : rows of n_heads*head_dim elements of dtype, q_stride and q_out_stride apart;
+ *             q_out may be q with the same stride.  Both NULL: only K and V.
+ *  k, v     : rows of n_kv_heads*head_dim elements of dtype, as for qmoe_kv4_append.
+ *  positions: int32 [n_tokens], as for qmoe_rope; K and V of a row without a position go
+ *             nowhere, and its q_out, k_hat and v_hat are left as they were.
+ *  slots, k_hat, v_hat : as for qmoe_kv4_append (k_hat: the turned rows as the cache
+ *             holds them).
+ *  q_norm, k_norm : F32 [head_dim], 16-byte aligned, or NULL. */
+qmoe_status qmoe_kv4_append_rope(qmoe_kv4* kv, const qmoe_kv4_cache* cache,
+                                 const qmoe_rope_config* rope, const void* q, const void* k,
+                                 const void* v, qmoe_dtype dtype, int n_tokens, int64_t q_stride,
+                                 int64_t k_stride, int64_t v_stride, const int32_t* positions,
+                                 const int64_t* slots, const float* q_norm, const float* k_norm,
+                                 float eps, void* q_out, int64_t q_out_stride, float* k_hat,
+                                 float* v_hat);
 
 /* Allocation-free variant of qmoe_forward for decode-sized calls.  The pages
  * have no counterpart to this entry point; it exists for callers that cannot

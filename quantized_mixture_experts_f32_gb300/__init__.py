@@ -23,8 +23,12 @@ STATUS_NAMES = {0: "QMOE_OK", 1: "QMOE_ERR_INVALID_ARG", 2: "QMOE_ERR_MISALIGNED
                 6: "QMOE_ERR_CUDA", 7: "QMOE_ERR_TIMEOUT", 8: "QMOE_ERR_DEVICE_CHECK"}
 QMOE_Q4_K, QMOE_Q6_K = 1, 2
 QTYPE = {"Q4_K": QMOE_Q4_K, "Q6_K": QMOE_Q6_K}
-QMOE_F32, QMOE_F16, QMOE_BF16 = 0, 1, 2
-DTYPE = {"F32": QMOE_F32, "F16": QMOE_F16, "BF16": QMOE_BF16}
+QMOE_F32, QMOE_F16, QMOE_BF16, QMOE_E4M3 = 0, 1, 2, 3
+DTYPE = {"F32": QMOE_F32, "F16": QMOE_F16, "BF16": QMOE_BF16, "E4M3": QMOE_E4M3}
+ACT = {"NONE": 0, "RELU": 1, "SILU": 2, "GELU": 3}
+QMOE_ROPE_HALF, QMOE_ROPE_INTERLEAVED = 0, 1
+ROPE_LAYOUT = {"half": QMOE_ROPE_HALF, "interleaved": QMOE_ROPE_INTERLEAVED}
+QMOE_ROPE_PLAIN, QMOE_ROPE_LINEAR, QMOE_ROPE_PARTS = 0, 1, 2
 
 # kernels one qmoe_forward enqueues on the decode path (n_tokens <= 8): the
 # whole layer is one kernel (the batch-1 kernel for one token, the fused
@@ -69,7 +73,9 @@ EXPORTED = ["qmoe_create", "qmoe_destroy", "qmoe_set_stream", "qmoe_forward", "q
             "qmoe_debug_stall_next", "qmoe_debug_fail_alloc",
             "qmoe_kv4_create", "qmoe_kv4_destroy", "qmoe_kv4_set_stream", "qmoe_kv4_workspace_bytes",
             "qmoe_kv4_get_status", "qmoe_kv4_last_error", "qmoe_kv4_plan", "qmoe_kv4_append",
-            "qmoe_kv4_attention", "qmoe_step_kv4", "qmoe_kv4_debug_stall_next"]
+            "qmoe_kv4_attention", "qmoe_step_kv4", "qmoe_kv4_debug_stall_next",
+            "qmoe_rmsnorm", "qmoe_fp8_quantize", "qmoe_linear_fp8", "qmoe_rope_table", "qmoe_rope",
+            "qmoe_kv4_append_rope"]
 
 
 class qmoe_config(C.Structure):
@@ -97,6 +103,13 @@ class qmoe_kv4_config(C.Structure):
 class qmoe_kv4_cache(C.Structure):
     _fields_ = [("k_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_codes", C.c_void_p),
                 ("v_scales", C.c_void_p), ("k_global", C.c_void_p), ("v_global", C.c_void_p)]
+
+
+class qmoe_rope_config(C.Structure):
+    _fields_ = [("layout", C.c_int), ("rot_dim", C.c_int), ("scaling", C.c_int), ("n_pos", C.c_int),
+                ("base", C.c_double), ("factor", C.c_double), ("orig_ctx", C.c_double),
+                ("beta_fast", C.c_double), ("beta_slow", C.c_double), ("mscale", C.c_double),
+                ("table", C.c_void_p)]
 
 
 class QmoeError(RuntimeError):
@@ -179,6 +192,20 @@ def _load():
     L.qmoe_step_kv4.restype = i
     L.qmoe_kv4_debug_stall_next.argtypes = [vp, C.c_uint64]
     L.qmoe_kv4_debug_stall_next.restype = i
+    rope, f = C.POINTER(qmoe_rope_config), C.c_float
+    L.qmoe_rmsnorm.argtypes = [vp, vp, i, i64, vp, i, i64, vp, fp, f, i, i, vp, i, i64, fp]
+    L.qmoe_rmsnorm.restype = i
+    L.qmoe_fp8_quantize.argtypes = [vp, vp, i, i64, i, i, vp, fp]
+    L.qmoe_fp8_quantize.restype = i
+    L.qmoe_linear_fp8.argtypes = [vp, vp, fp, i, i, vp, fp, i, fp, i, vp, i64, vp, i, i64]
+    L.qmoe_linear_fp8.restype = i
+    L.qmoe_rope_table.argtypes = [vp, rope]
+    L.qmoe_rope_table.restype = i
+    L.qmoe_rope.argtypes = [vp, rope, vp, i, i64, i, i, i, ip, fp, f, vp, i64]
+    L.qmoe_rope.restype = i
+    L.qmoe_kv4_append_rope.argtypes = [vp, C.POINTER(qmoe_kv4_cache), rope, vp, vp, vp, i, i, i64, i64, i64, ip,
+                                       vp, fp, fp, f, vp, i64, fp, fp]
+    L.qmoe_kv4_append_rope.restype = i
     return L
 
 
@@ -378,6 +405,46 @@ def qmoe_step_kv4(ctx, kv, layers, caches, n_layers, n_seqs, n_tokens, max_new, 
 
 def qmoe_kv4_debug_stall_next(kv, wait_ns: int):
     _check_kv4(kv, lib.qmoe_kv4_debug_stall_next(kv, wait_ns))
+
+
+def qmoe_rmsnorm(ctx, x, x_t, x_stride, residual, res_t, res_stride, sum_out, weight, eps, n_rows, dim, y,
+                 y_t, y_stride, y_scale=None):
+    _check(ctx, lib.qmoe_rmsnorm(ctx, _ptr(x), x_t, x_stride, _ptr(residual), res_t, res_stride, _ptr(sum_out),
+                                 _ptr(weight), eps, n_rows, dim, _ptr(y), y_t, y_stride, _ptr(y_scale)))
+
+
+def qmoe_fp8_quantize(ctx, x, x_t, x_stride, n_rows, cols, codes, scale):
+    _check(ctx, lib.qmoe_fp8_quantize(ctx, _ptr(x), x_t, x_stride, n_rows, cols, _ptr(codes), _ptr(scale)))
+
+
+def qmoe_linear_fp8(ctx, x_codes, x_scale, n_tokens, in_features, w_codes, w_scale, out_features, bias, act,
+                    residual, res_stride, out, out_t, out_stride):
+    _check(ctx, lib.qmoe_linear_fp8(ctx, _ptr(x_codes), _ptr(x_scale), n_tokens, in_features, _ptr(w_codes),
+                                    _ptr(w_scale), out_features, _ptr(bias), act, _ptr(residual), res_stride,
+                                    _ptr(out), out_t, out_stride))
+
+
+def qmoe_rope_table(ctx, rope: qmoe_rope_config):
+    _check(ctx, lib.qmoe_rope_table(ctx, C.byref(rope)))
+
+
+def qmoe_rope(ctx, rope, x, x_t, x_stride, n_tokens, n_heads, head_dim, positions, norm, eps, out, out_stride):
+    _check(ctx, lib.qmoe_rope(ctx, C.byref(rope), _ptr(x), x_t, x_stride, n_tokens, n_heads, head_dim,
+                              _ptr(positions), _ptr(norm), eps, _ptr(out), out_stride))
+
+
+def qmoe_kv4_append_rope(kv, cache, rope, q, k, v, dtype, n_tokens, q_stride, k_stride, v_stride, positions,
+                         slots, q_norm, k_norm, eps, q_out, q_out_stride, k_hat=None, v_hat=None):
+    _check_kv4(kv, lib.qmoe_kv4_append_rope(kv, C.byref(cache), C.byref(rope), _ptr(q), _ptr(k), _ptr(v), dtype,
+                                            n_tokens, q_stride, k_stride, v_stride, _ptr(positions), _ptr(slots),
+                                            _ptr(q_norm), _ptr(k_norm), eps, _ptr(q_out), q_out_stride,
+                                            _ptr(k_hat), _ptr(v_hat)))
+
+
+def make_rope(rot_dim, base, n_pos, table, layout=QMOE_ROPE_HALF, scaling=QMOE_ROPE_PLAIN, factor=1.0,
+              orig_ctx=0.0, beta_fast=32.0, beta_slow=1.0, mscale=0.0) -> qmoe_rope_config:
+    return qmoe_rope_config(layout, rot_dim, scaling, n_pos, base, factor, orig_ctx, beta_fast, beta_slow, mscale,
+                            _ptr(table))
 
 
 def make_kv4_config(n_heads, n_kv_heads, head_dim, page_size, n_pages, max_seqs, max_tokens,

@@ -17,17 +17,6 @@ namespace {
 
 constexpr int AP_THREADS = 256;
 
-// v / d, correctly rounded, from r = 1 / d rounded: two of Markstein's corrections
-// (Computation of elementary functions on the IBM RISC System/6000 processor, 1990).
-// q = v r is within two units in the last place, the first correction brings it within
-// one, and from there q + r (v - q d), the remainder being exact, rounds as v / d does.
-// Exact while the remainder is a normal number; where |v| is too small for that, v / d
-// is far below the first code's border.
-__device__ __forceinline__ float quotient(float v, float d, float r) {
-    const float q = v * r, p = fmaf(fmaf(-q, d, v), r, q);
-    return copysignf(fmaf(fmaf(-p, d, v), r, p), v);          // the corrections lose the sign of -0
-}
-
 // The eight elements from c of row t (live: there are any; a block's lanes are live together).
 template <int F32>
 __device__ __forceinline__ void append_lane(const Kv4AppendArgs& a, int t, int c, bool live, int row, int hd_log2) {
@@ -48,32 +37,11 @@ __device__ __forceinline__ void append_lane(const Kv4AppendArgs& a, int t, int c
 #pragma unroll
     for (int j = 0; j < 8; ++j) bmax = fmaxf(bmax, fabsf(v[j]));
     bmax = fmaxf(bmax, __shfl_xor_sync(0xffffffffu, bmax, 1));
-    // (448 for infinity over a 6 g that is infinite too: a scale is never NaN)
-    const uint32_t s = g > 0.f ? __nv_cvt_float_to_fp8(fminf(bmax / (6.0f * g), 448.f), __NV_SATFINITE, __NV_E4M3) : 0u;
-    const float sf = e4m3_f(s), d = sf * g;
-    uint32_t code = 0u;
-    if (d >= 0x1p-90f && d <= 0x1p90f && bmax <= d * 0x1p30f) {
-        const float r = __frcp_rn(d);
-#pragma unroll
-        for (int j = 0; j < 8; j += 2)
-            code |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(quotient(v[j], d, r), quotient(v[j + 1], d, r)), __NV_E2M1,
-                                                       cudaRoundNearest) << (4 * j);
-    } else if (d > 0.f) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2)
-            code |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[j] / d, v[j + 1] / d), __NV_E2M1, cudaRoundNearest) << (4 * j);
-    }
+    uint32_t sc;
+    float sf;
+    const uint32_t code = kv4_encode8(v, bmax, g, sc, sf);
     float* hat = isv ? a.v_hat : a.k_hat;
-    if (hat && live) {
-        float4* o = reinterpret_cast<float4*>(hat + (size_t)t * row + c);
-        __half2 w[4];
-        kv4_widen8(code, w);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 x = __half22float2(w[2 * j]), y = __half22float2(w[2 * j + 1]);
-            o[j] = make_float4(x.x * sf * g, x.y * sf * g, y.x * sf * g, y.y * sf * g);
-        }
-    }
+    if (hat && live) kv4_store_values8(hat + (size_t)t * row + c, code, sf, g);
     if (slot < 0) return;
     const int64_t pg = slot >> a.s.page_log2;
     if (pg >= a.s.n_pages) {
@@ -82,7 +50,7 @@ __device__ __forceinline__ void append_lane(const Kv4AppendArgs& a, int t, int c
     }
     const size_t at = ((size_t)pg * a.s.nkv + h) * a.s.page + (size_t)(slot & (a.s.page - 1));
     *reinterpret_cast<uint32_t*>((isv ? a.c.vc : a.c.kc) + at * (a.s.hd / 2) + e / 2) = code;
-    if ((e & 15) == 0) (isv ? a.c.vs : a.c.ks)[at * (a.s.hd / 16) + e / 16] = (uint8_t)s;
+    if ((e & 15) == 0) (isv ? a.c.vs : a.c.ks)[at * (a.s.hd / 16) + e / 16] = (uint8_t)sc;
 }
 
 // blockIdx.y: 0 = K, 1 = V.  A CTA takes rows_cta whole rows where they fit its

@@ -113,6 +113,50 @@ __device__ __forceinline__ void kv4_store2(void* p, size_t at, int t, float x, f
     else *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + at) = __floats2bfloat162_rn(x, y);
 }
 
+// v / d, correctly rounded, from r = 1 / d rounded: two of Markstein's corrections
+// (Computation of elementary functions on the IBM RISC System/6000 processor, 1990).
+// q = v r is within two units in the last place, the first correction brings it within
+// one, and from there q + r (v - q d), the remainder being exact, rounds as v / d does.
+// Exact while the remainder is a normal number; where |v| is too small for that, v / d
+// is far below the first code's border.
+__device__ __forceinline__ float kv4_quotient(float v, float d, float r) {
+    const float q = v * r, p = fmaf(fmaf(-q, d, v), r, q);
+    return copysignf(fmaf(fmaf(-p, d, v), r, p), v);          // the corrections lose the sign of -0
+}
+
+// Eight elements of a 16-element block whose largest magnitude is bmax, under the head's
+// global g: the block's E4M3 scale code s and value sf, and the elements' E2M1 codes.
+__device__ __forceinline__ uint32_t kv4_encode8(const float (&v)[8], float bmax, float g, uint32_t& s, float& sf) {
+    // (448 for infinity over a 6 g that is infinite too: a scale is never NaN)
+    s = g > 0.f ? __nv_cvt_float_to_fp8(fminf(bmax / (6.0f * g), 448.f), __NV_SATFINITE, __NV_E4M3) : 0u;
+    sf = e4m3_f(s);
+    const float d = sf * g;
+    uint32_t code = 0u;
+    if (d >= 0x1p-90f && d <= 0x1p90f && bmax <= d * 0x1p30f) {
+        const float r = __frcp_rn(d);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+            code |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(kv4_quotient(v[j], d, r), kv4_quotient(v[j + 1], d, r)),
+                                                       __NV_E2M1, cudaRoundNearest) << (4 * j);
+    } else if (d > 0.f) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+            code |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[j] / d, v[j + 1] / d), __NV_E2M1, cudaRoundNearest) << (4 * j);
+    }
+    return code;
+}
+
+// the values that eight codes under a scale and a global stand for
+__device__ __forceinline__ void kv4_store_values8(float* to, uint32_t code, float sf, float g) {
+    __half2 w[4];
+    kv4_widen8(code, w);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const float2 x = __half22float2(w[2 * j]), y = __half22float2(w[2 * j + 1]);
+        reinterpret_cast<float4*>(to)[j] = make_float4(x.x * sf * g, x.y * sf * g, y.x * sf * g, y.y * sf * g);
+    }
+}
+
 // eight elements as they were loaded: F32 from two words of 16 bytes, else one
 template <int N>
 __device__ __forceinline__ void kv4_floats8(const uint4 (&u)[N], int t, float (&v)[8]) {

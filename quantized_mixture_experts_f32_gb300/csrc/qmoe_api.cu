@@ -11,6 +11,7 @@
 #include "../../include/qmoe.h"
 #include "kv4.cuh"
 #include "qmoe_internal.h"
+#include "rows.cuh"
 
 struct qmoe_ctx {
     qmoe_config cfg;
@@ -272,6 +273,8 @@ Kv4View kv4_view(qmoe_kv4* h);
 qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c);
 Kv4Cache kv4_cache(const qmoe_kv4_cache* c);
 
+CtxView ctx_view(qmoe_ctx* c) { return {c->stream, c->device, c->num_sms, c->status, c->err, sizeof(c->err)}; }
+
 void create_error(const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -362,6 +365,7 @@ qmoe_status qmoe_create(const qmoe_config* cfg, qmoe_ctx** out) {
     if (e == cudaSuccess) e = qmoe::t1_prepare();
     if (e == cudaSuccess) e = qmoe::route_prepare();
     if (e == cudaSuccess) e = qmoe::decode_step_prepare();
+    if (e == cudaSuccess) e = qmoe::linear_fp8_prepare();
     if (e == cudaSuccess && L.pl_ok) e = qmoe::prefill_layer_prepare();
     if (e != cudaSuccess) {
         create_fail("kernel set-up: %s", cudaGetErrorString(e));

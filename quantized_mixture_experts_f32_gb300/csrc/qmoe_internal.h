@@ -321,6 +321,15 @@ struct OnDevice {
     }
 };
 
+// What the row operators need of a context or a cache handle.
+struct CtxView {
+    cudaStream_t stream;
+    int device, num_sms;
+    int* status;
+    char* err;
+    size_t err_bytes;
+};
+
 // Text that qmoe_last_error(NULL) gives on this thread (a failed qmoe_kv4_create;
 // "" clears it), and whether the allocation-failure hook takes the next allocation.
 void create_error(const char* fmt, ...);

@@ -1,0 +1,98 @@
+// rows.cuh -- the 8-bit path's row operators: what their kernels and the C ABI share.
+#pragma once
+#include "kv4.cuh"
+
+namespace qmoe {
+
+enum : int { ROWS_E4M3 = 3 };                 // beside KV4_F32, KV4_F16, KV4_BF16
+constexpr int FP8_BLOCK = 128;                // elements of a row, and rows of W, that share a scale
+
+// y = h / sqrt(mean(h^2) + eps) * w with h = x + res; norm 0: y = x
+struct NormArgs {
+    const void* x;
+    const void* res;                          // or null
+    void* sum;                                // or null
+    const float* w;                           // or null
+    void* y;
+    float* scale;                             // of 8-bit rows
+    int64_t x_stride, res_stride, y_stride;   // elements between rows; sum's is res_stride
+    int x_t, res_t, y_t;
+    int rows, dim;
+    float eps;
+    int norm;
+};
+cudaError_t launch_rmsnorm_rows(const NormArgs& a, int num_sms, cudaStream_t st);
+
+struct LinearArgs {
+    const uint8_t* x;                         // [T][K]
+    const float* xs;                          // [T][ceil(K/128)]
+    const uint8_t* w;                         // [N][K]
+    const float* ws;                          // [ceil(N/128)][ceil(K/128)]
+    const float* bias;                        // or null
+    const void* res;                          // or null
+    void* out;
+    int64_t res_stride, out_stride;
+    int T, K, N, act, out_t;
+};
+enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
+cudaError_t linear_fp8_prepare();
+cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st);
+
+// Rotary positions on the heads of rows, and the append of K and V rows behind them.
+struct RopeArgs {
+    const float* table;                       // [n_pos][rot/2][2]
+    int n_pos, rot, interleaved;
+    int t, n_tokens, hd;                      // t: the rows' type
+    const int32_t* pos;
+    const void* q;
+    void* q_out;
+    int64_t q_stride, q_out_stride;
+    int nq;                                   // heads of a q row, 0: none
+    const float *q_norm, *k_norm;             // or null
+    float eps;
+    int* status;
+    // the append's: nkv 0 for none
+    int nkv;
+    const void* k;
+    const void* v;
+    int64_t k_stride, v_stride;
+    const int64_t* slots;
+    float* k_hat;
+    float* v_hat;
+    Kv4Cache c;
+    int page, page_log2, n_pages;
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+
+struct RopeFreq {                             // angle of each pair at position 1
+    double f[128];
+};
+cudaError_t launch_rope_rows_table(const RopeFreq& f, int half, int n_pos, double mscale, float* table, cudaStream_t st);
+
+// eight elements of a row of type t from element `at`, a multiple of eight
+__device__ __forceinline__ void rows_load8(const void* p, size_t at, int t, float (&v)[8]) {
+    if (t == KV4_F32) {
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
+        const uint4 u[2] = {s[0], s[1]};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[4 * i] = __uint_as_float(u[i].x);
+            v[4 * i + 1] = __uint_as_float(u[i].y);
+            v[4 * i + 2] = __uint_as_float(u[i].z);
+            v[4 * i + 3] = __uint_as_float(u[i].w);
+        }
+        return;
+    }
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t x = w[i];
+        const float2 f = t == KV4_F16 ? __half22float2(*reinterpret_cast<__half2*>(&x))
+                                      : make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
+}
+
+}  // namespace qmoe
