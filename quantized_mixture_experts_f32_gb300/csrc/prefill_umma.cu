@@ -1206,6 +1206,19 @@ bool tensor_map_half(CUtensorMap* m, const void* base, uint64_t cols, uint64_t r
     return map_half(m, base, cols, rows, box_rows);
 }
 
+// E4M3 codes [rows][cols] (cols % 16 == 0), box = 128 cols x box_rows, 128B swizzle
+bool tensor_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols};
+    cuuint32_t box[2] = {128, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool prefill_supported(const MoeShape& s, int gate_t, int up_t, int down_t) {
     if (gate_t != 1 || up_t != 1) return false;
     if (s.H % QK || s.F % QK || s.H % TILE_M || s.F % 64) return false;

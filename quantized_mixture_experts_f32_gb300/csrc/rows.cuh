@@ -33,6 +33,7 @@ struct LinearArgs {
     void* out;
     int64_t res_stride, out_stride;
     int T, K, N, act, out_t;
+    int* status;
 };
 enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 cudaError_t linear_fp8_prepare();
