@@ -552,7 +552,7 @@ typedef struct {
     double beta_fast;       /* PARTS: > beta_slow */
     double beta_slow;       /* PARTS: > 0 */
     double mscale;          /* >= 0 */
-    float* table;           /* F32 [n_pos][rot_dim/2][2], cosine and sine, 16-byte aligned */
+    float* table;           /* F32 [n_pos][2][rot_dim/2], cosines and sines, 16-byte aligned */
 } qmoe_rope_config;
 
 /* Fill rope->table (angles, cosines and sines in 64 bits, rounded once): made once, and

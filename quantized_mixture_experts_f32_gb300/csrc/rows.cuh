@@ -41,7 +41,7 @@ cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st)
 
 // Rotary positions on the heads of rows, and the append of K and V rows behind them.
 struct RopeArgs {
-    const float* table;                       // [n_pos][rot/2][2]
+    const float* table;                       // [n_pos][2][rot/2]: cosines, sines
     int n_pos, rot, interleaved;
     int t, n_tokens, hd;                      // t: the rows' type
     const int32_t* pos;
@@ -62,6 +62,7 @@ struct RopeArgs {
     float* v_hat;
     Kv4Cache c;
     int page, page_log2, n_pages;
+    float2 minus_zero;                        // launch_rope sets it
 };
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
 

@@ -98,9 +98,9 @@ def rope_heads(x, hd, norm, eps):
 
 
 def rope(x, cs, rot, layout):
-    """x [tokens, heads, hd] fp32 turned by cs [tokens, rot/2, 2] fp32, every step rounded once."""
+    """x [tokens, heads, hd] fp32 turned by cs [tokens, 2, rot/2] fp32, every step rounded once."""
     x = x.copy()
-    c, s = cs[:, None, :, 0], cs[:, None, :, 1]
+    c, s = cs[:, None, 0], cs[:, None, 1]
     a, b = (slice(0, rot // 2), slice(rot // 2, rot)) if layout == "half" else (slice(0, rot, 2), slice(1, rot, 2))
     p, q = x[..., a].copy(), x[..., b].copy()
     x[..., a] = p * c - q * s

@@ -309,7 +309,7 @@ def test_linear_results_do_not_change_from_run_to_run(q, ctx):
 # ---------------------------------------------------------------------------- rotary positions
 
 def make_table(q, ctx, rot, n_pos, layout="half", scaling="plain", base=1e6, **more):
-    table = torch.full((n_pos + 1, rot // 2, 2), 9.0, device=dev())
+    table = torch.full((n_pos + 1, 2, rot // 2), 9.0, device=dev())
     kind = {"plain": q.QMOE_ROPE_PLAIN, "linear": q.QMOE_ROPE_LINEAR, "parts": q.QMOE_ROPE_PARTS}[scaling]
     rope = q.make_rope(rot, base, n_pos, table, layout=q.ROPE_LAYOUT[layout], scaling=kind, **more)
     q.qmoe_rope_table(ctx, rope)
@@ -330,7 +330,7 @@ def test_rope_table(q, ctx, rot, n_pos, base, scaling, more):
     # half a step of a value in size at most m, and the frequency's and the product's rounding times the position
     tol = R.U * max(1.0, m) + n_pos * f.max() * 2.0 ** -50
     for j, fn in enumerate((np.cos, np.sin)):
-        assert np.abs(got[..., j] - (fn(ang) * m).astype(np.float64)).max() <= tol
+        assert np.abs(got[:, j] - (fn(ang) * m).astype(np.float64)).max() <= tol
 
 
 ROPE_CASES = [  # tokens, heads, hd, rot, layout, dtype, norm, stride beyond, in place
@@ -599,7 +599,7 @@ def test_linear_refusals(q, ctx):
 
 
 def test_rope_refusals(q, ctx):
-    table = torch.zeros(10, 32, 2, device=dev())
+    table = torch.zeros(10, 2, 32, device=dev())
     x, pos, w = torch.zeros(4, 128, device=dev()), torch.zeros(4, dtype=torch.int32, device=dev()), torch.ones(64, device=dev())
 
     def made(rot=64, base=1e4, n_pos=10, t=table, **k):

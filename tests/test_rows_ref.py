@@ -50,7 +50,7 @@ def test_rope_turns_pairs_and_keeps_their_distance(layout):
     f, m = R.rope_freq(32, 1e4)
     pos = np.array([0, 1, 77, 100000])
     ang = pos[:, None] * f
-    cs = np.stack([np.cos(ang) * m, np.sin(ang) * m], -1).astype(np.float32)
+    cs = np.stack([np.cos(ang) * m, np.sin(ang) * m], 1).astype(np.float32)
     y = R.rope(x, cs, 32, layout)
     assert np.array_equal(y[0], x[0]) and np.array_equal(y[..., 32:], x[..., 32:])
     a, b = (slice(0, 16), slice(16, 32)) if layout == "half" else (slice(0, 32, 2), slice(1, 32, 2))
