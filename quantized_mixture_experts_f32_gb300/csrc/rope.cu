@@ -13,7 +13,7 @@ namespace qmoe {
 
 namespace {
 
-constexpr int RO_THREADS = 256;
+constexpr int RO_THREADS = 64;
 
 // pairs of fp32 numbers in one instruction, each rounded as by itself
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -61,76 +61,85 @@ __device__ __forceinline__ float2 product2(float2 a, float2 b, float2 zero) {
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
-// sum over the `lanes` lanes of a head (a power of two)
-__device__ __forceinline__ float head_sum(float x, int lanes) {
-    for (int o = lanes >> 1; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+// sum over the LANES lanes of a head
+template <int LANES>
+__device__ __forceinline__ float head_sum(float x) {
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
 
-// 1 / sqrt(mean of the head's squares + eps), rounded to fp32; the head's lanes hold 16
-// elements each.  The squares are added to a power of two above their sum (which a first
-// pass bounds): every partial sum is then a multiple of that number's last place, so the
-// difference of two is exact, what a rounding lost is one more fused operation, and the
-// lanes' sums add up without loss.  Where the sum is so far from 1 that this leaves fp32's
-// range, once more from elements scaled by k.
-__device__ __forceinline__ float head_rms(const float2 (&v)[8], int lanes, float eps) {
-    const float inv = 1.0f / (float)(16 * lanes);            // exact: a power of two
-    float k = 1.f, h, l;
-    while (true) {
-        float2 f[8], s = both(0.f);
+// The mean of a head's squares, times k^2, plus p, in two words.  The squares are added to a
+// power of two above their sum (which a first pass bounds): every partial sum is then a
+// multiple of that number's last place, so the difference of two is exact, what a
+// rounding lost is one more fused operation, and the lanes' sums add up without loss.
+template <int LANES>
+__device__ __forceinline__ float2 mean_square(const float2 (&f)[8], float p, float& rough) {
+    constexpr float inv = 1.0f / (float)(16 * LANES);        // exact: a power of two
+    float2 s = mul2(f[0], f[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            f[i] = mul2(v[i], both(k));
-            s = sqr_add2(f[i], s);
-        }
-        const float rough = head_sum(s.x + s.y, lanes);
-        const float top = __uint_as_float((__float_as_uint(rough) & 0x7f800000u) + 0x01000000u);   // 2 to 4 times rough
-        float2 c = both(0.f);
-        s = both(top);
+    for (int i = 1; i < 8; ++i) s = sqr_add2(f[i], s);
+    rough = head_sum<LANES>(s.x + s.y);
+    const float top = __uint_as_float((__float_as_uint(rough) & 0x7f800000u) + 0x01000000u);   // 2 to 4 times rough
+    float2 c = both(0.f);
+    s = both(top);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 t = sqr_add2(f[i], s);
-            c = add2(c, sqr_add2(f[i], sub2(s, t)));
-            s = t;
-        }
-        h = head_sum(__fadd_rn(__fsub_rn(s.x, top), __fsub_rn(s.y, top)), lanes) * inv;
-        l = head_sum(__fadd_rn(c.x, c.y), lanes) * inv;
-        // h + eps, and what that rounding lost
-        const float p = eps * k * k, t = __fadd_rn(h, p), z = __fsub_rn(t, h);
-        l = __fadd_rn(l, __fadd_rn(__fsub_rn(h, __fsub_rn(t, z)), __fsub_rn(p, z)));
-        h = t;
-        const bool far = k == 1.f && !(rough < 1e30f && (rough > 1e-30f || rough == 0.f) && h > 1e-30f);
-        if (!__any_sync(0xffffffffu, far)) break;
-        k = !far ? k : rough < 1.f ? 0x1p70f : 0x1p-70f;
+    for (int i = 0; i < 8; ++i) {
+        const float2 t = sqr_add2(f[i], s), lost = sqr_add2(f[i], sub2(s, t));
+        c = i ? add2(c, lost) : lost;
+        s = t;
     }
-    const float y = rsqrtf(h);
+    const float h = head_sum<LANES>(__fadd_rn(__fsub_rn(s.x, top), __fsub_rn(s.y, top))) * inv;
+    const float l = head_sum<LANES>(__fadd_rn(c.x, c.y)) * inv;
+    // h + p, and what that rounding lost
+    const float t = __fadd_rn(h, p), z = __fsub_rn(t, h);
+    return make_float2(t, __fadd_rn(l, __fadd_rn(__fsub_rn(h, __fsub_rn(t, z)), __fsub_rn(p, z))));
+}
+
+// 1 / sqrt(mean of the head's squares + eps), rounded to fp32; the head's lanes hold 16
+// elements each.  Where the sum is so far from 1 that the two words leave fp32's range,
+// once more from elements scaled by k.
+template <int LANES>
+__device__ __forceinline__ float head_rms(const float2 (&v)[8], float eps) {
+    float rough, k = 1.f;
+    float2 m = mean_square<LANES>(v, eps, rough);
+    const bool far = !(rough < 1e30f && (rough > 1e-30f || rough == 0.f) && m.x > 1e-30f);
+    if (__any_sync(0xffffffffu, far)) {
+        k = !far ? 1.f : rough < 1.f ? 0x1p70f : 0x1p-70f;
+        float2 f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = make_float2(v[i].x * k, v[i].y * k);
+        m = mean_square<LANES>(f, eps * k * k, rough);
+    }
+    const float y = rsqrtf(m.x);
     // one step of Newton's iteration on 1 - (h + l) y^2, y^2 in two words
     const float q = __fmul_rn(y, y), ql = __fmaf_rn(y, y, -q);
-    float e = __fmaf_rn(-h, q, 1.0f);
-    e = __fsub_rn(e, __fmaf_rn(h, ql, __fmul_rn(l, q)));
+    float e = __fmaf_rn(-m.x, q, 1.0f);
+    e = __fsub_rn(e, __fmaf_rn(m.x, ql, __fmul_rn(m.y, q)));
     return (fabsf(e) < 1e-3f ? __fmaf_rn(y, __fmul_rn(e, __fmaf_rn(0.375f, e, 0.5f)), y) : y) * k;
 }
 
-// the words of eight elements at p, as pairs of floats
-template <int F32>
-__device__ __forceinline__ void widen(const uint4 (&u)[F32 + 1], int t, float2* v) {
-    float f[8];
-    kv4_floats8(u, t, f);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
-}
-
 // Sixteen elements of a head at ea and eb, eight each, as a lane holds them.
-template <int F32>
+template <int T>
 struct RopeUnit {
-    uint4 a[F32 + 1], b[F32 + 1];
-    __device__ __forceinline__ void load(const void* row, size_t at, int ea, int eb, bool live) {
-        const uint8_t* p = static_cast<const uint8_t*>(row) + at * (F32 ? 4 : 2);
+    static constexpr int N = T == KV4_F32 ? 2 : 1, BYTES = T == KV4_F32 ? 4 : 2;
+    uint4 a[N], b[N];
+    __device__ __forceinline__ void load(const void* row, size_t at, int ea, int eb) {
+        const uint8_t* p = static_cast<const uint8_t*>(row) + at * BYTES;
 #pragma unroll
-        for (int i = 0; i <= F32; ++i) {
-            a[i] = live ? *reinterpret_cast<const uint4*>(p + ea * (F32 ? 4 : 2) + 16 * i) : make_uint4(0, 0, 0, 0);
-            b[i] = live ? *reinterpret_cast<const uint4*>(p + eb * (F32 ? 4 : 2) + 16 * i) : make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < N; ++i) {
+            a[i] = *reinterpret_cast<const uint4*>(p + ea * BYTES + 16 * i);
+            b[i] = *reinterpret_cast<const uint4*>(p + eb * BYTES + 16 * i);
         }
+    }
+    __device__ __forceinline__ void widen(float2 (&v)[8]) const {
+        float f[8];
+        kv4_floats8(a, T, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = make_float2(f[2 * i], f[2 * i + 1]);
+        kv4_floats8(b, T, f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 + i] = make_float2(f[2 * i], f[2 * i + 1]);
     }
 };
 
@@ -145,9 +154,16 @@ __device__ __forceinline__ void normalise(float2 (&v)[8], float r, const float* 
 }
 
 // cosines and sines of eight pairs: in halves the pairs lie at ea and eb, else beside each other
-__device__ __forceinline__ void turn(float2 (&v)[8], const float4 (&c4)[2], const float4 (&s4)[2], bool apart, float2 zero) {
-    const float2 c[4] = {{c4[0].x, c4[0].y}, {c4[0].z, c4[0].w}, {c4[1].x, c4[1].y}, {c4[1].z, c4[1].w}};
-    const float2 s[4] = {{s4[0].x, s4[0].y}, {s4[0].z, s4[0].w}, {s4[1].x, s4[1].y}, {s4[1].z, s4[1].w}};
+__device__ __forceinline__ void turn(float2 (&v)[8], const float* cos8, const float* sin8, bool apart, float2 zero) {
+    float2 c[4], s[4];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 c4 = __ldg(reinterpret_cast<const float4*>(cos8) + i), s4 = __ldg(reinterpret_cast<const float4*>(sin8) + i);
+        c[2 * i] = make_float2(c4.x, c4.y);
+        c[2 * i + 1] = make_float2(c4.z, c4.w);
+        s[2 * i] = make_float2(s4.x, s4.y);
+        s[2 * i + 1] = make_float2(s4.z, s4.w);
+    }
     if (apart) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -166,9 +182,12 @@ __device__ __forceinline__ void turn(float2 (&v)[8], const float4 (&c4)[2], cons
     }
 }
 
-__device__ __forceinline__ void store8(void* p, size_t at, int t, const float2* v) {
-    const float f[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
-    kv4_store8(p, at, t, f);
+template <int T>
+__device__ __forceinline__ void store_unit(void* p, size_t at, int ea, int eb, const float2 (&v)[8]) {
+    const float x[8] = {v[0].x, v[0].y, v[1].x, v[1].y, v[2].x, v[2].y, v[3].x, v[3].y};
+    const float y[8] = {v[4].x, v[4].y, v[5].x, v[5].y, v[6].x, v[6].y, v[7].x, v[7].y};
+    kv4_store8(p, at + ea, T, x);
+    kv4_store8(p, at + eb, T, y);
 }
 
 // A K or V unit into its slot.  In halves a 16-element block is shared with the lane beside.
@@ -210,82 +229,134 @@ __device__ __forceinline__ void append_unit(const RopeArgs& a, const float2 (&v)
     if (apart && (eb & 15) == 0) scales[eb / 16] = (uint8_t)sy;
 }
 
-// A lane has the same unit of two heads, so that table and norm are read once: q heads
-// nq/2 apart, or a K head and its V head.  A unit of the part that turns is eight pairs,
-// so in halves its elements lie rot/2 apart; all other units are 16 neighbours.
-template <int F32, int NORM, int APPEND>
-__device__ __forceinline__ void rope_lane(const RopeArgs& a, int t, int lane, bool live, int hd_log2) {
-    const int lph_log2 = hd_log2 - 4, hp = lane >> lph_log2, u = lane - (hp << lph_log2), nq2 = (a.nq + 1) >> 1;
-    const bool isq = !APPEND || hp < nq2;
-    const int h0 = isq ? hp : hp - nq2, h1 = isq ? hp + nq2 : h0;
-    const bool turns = u < (a.rot >> 4), apart = turns && !a.interleaved;
-    const int ea = apart ? 8 * u : 16 * u, eb = apart ? (a.rot >> 1) + 8 * u : 16 * u + 8;
-    const int pos = live ? __ldg(a.pos + t) : -1;
-    const bool two = live && (!isq || h1 < a.nq);
-    RopeUnit<F32> r0, r1;
-    {
-        const size_t q0 = (size_t)t * a.q_stride, k0 = (size_t)t * a.k_stride, v0 = (size_t)t * a.v_stride;
-        r0.load(isq ? a.q : a.k, (isq ? q0 : k0) + ((size_t)h0 << hd_log2), ea, eb, live);
-        r1.load(isq ? a.q : a.v, (isq ? q0 : v0) + ((size_t)h1 << hd_log2), isq ? ea : 16 * u, isq ? eb : 16 * u + 8, two);
+// Where a lane's unit lies in a head.  A unit of the part that turns is eight pairs, so in
+// halves its elements lie rot/2 apart; all other units are 16 neighbours.
+struct RopePlace {
+    bool turns, apart;
+    int ea, eb;
+    __device__ __forceinline__ RopePlace(const RopeArgs& a, int u) {
+        turns = u < (a.rot >> 4);
+        apart = turns && !a.interleaved;
+        ea = apart ? 8 * u : 16 * u;
+        eb = apart ? (a.rot >> 1) + 8 * u : 16 * u + 8;
     }
-    const bool kv = APPEND && !isq && live;
-    const int64_t slot = kv ? __ldg(a.slots + t) : -1;
-    const float kg = kv ? __ldg(a.c.kg + h0) : 0.f, vg = kv ? __ldg(a.c.vg + h0) : 0.f;
-    const bool seen = pos >= 0 && pos < a.n_pos;
-    if (pos >= a.n_pos) atomicExch(a.status, ST_DEVICE_CHECK);
-    float4 c[2] = {}, s[2] = {};
-    if (seen && turns) {
-        const float4* p = reinterpret_cast<const float4*>(a.table + (size_t)pos * a.rot + 8 * u);
-        const float4* p2 = reinterpret_cast<const float4*>(a.table + (size_t)pos * a.rot + (a.rot >> 1) + 8 * u);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            c[i] = __ldg(p + i);
-            s[i] = __ldg(p2 + i);
-        }
-    }
-    const float* norm = isq ? a.q_norm : a.k_norm;
-    float2 v[8];
-    widen<F32>(r0.a, a.t, v);
-    widen<F32>(r0.b, a.t, v + 4);
+};
+
+// a unit's norm and turn at its row's table entries
+template <int LANES, int NORM>
+__device__ __forceinline__ void rope_unit(const RopeArgs& a, float2 (&v)[8], const RopePlace& w, const float* norm, const float* cs) {
     if (NORM) {
-        const float r = head_rms(v, 1 << lph_log2, a.eps);
-        if (norm) normalise(v, r, norm, ea, eb);
+        const float r = head_rms<LANES>(v, a.eps);
+        if (norm) normalise(v, r, norm, w.ea, w.eb);
     }
-    if (turns) turn(v, c, s, apart, a.minus_zero);
-    if (isq && seen) {
-        const size_t at = (size_t)t * a.q_out_stride + ((size_t)h0 << hd_log2);
-        store8(a.q_out, at + ea, a.t, v);
-        store8(a.q_out, at + eb, a.t, v + 4);
-    }
-    if (APPEND && __any_sync(0xffffffffu, !isq))
-        append_unit(a, v, false, !isq && seen, t, h0, ea, eb, apart, slot, kg, hd_log2);
-    widen<F32>(r1.a, a.t, v);
-    widen<F32>(r1.b, a.t, v + 4);
-    if (!APPEND || __any_sync(0xffffffffu, isq)) {
-        if (NORM) {
-            const float r = head_rms(v, 1 << lph_log2, a.eps);
-            if (norm && isq) normalise(v, r, norm, ea, eb);
-        }
-        if (isq && turns) turn(v, c, s, apart, a.minus_zero);
-        if (isq && seen && two) {
-            const size_t at = (size_t)t * a.q_out_stride + ((size_t)h1 << hd_log2);
-            store8(a.q_out, at + ea, a.t, v);
-            store8(a.q_out, at + eb, a.t, v + 4);
-        }
-    }
-    if (APPEND && __any_sync(0xffffffffu, !isq))
-        append_unit(a, v, true, !isq && seen, t, h0, 16 * u, 16 * u + 8, false, slot, vg, hd_log2);
+    if (w.turns) turn(v, cs, cs + (a.rot >> 1), w.apart, a.minus_zero);
 }
 
-// A CTA takes rows_cta whole rows where they fit its threads, else one row in turns.
-template <int F32, int NORM, int APPEND>
-__global__ void __launch_bounds__(512) rope_kernel(RopeArgs a, int lanes_row, int rows_cta, int hd_log2) {
+// The same unit of two q heads, nq/2 apart, so that a lane has two rows' loads in flight.
+// Lanes without work load the first row's and write nothing.
+template <int T, int HD, int NORM>
+__device__ __forceinline__ void rope_q(const RopeArgs& a, int t, int lane, bool live) {
+    constexpr int LANES = HD / 16;
+    t = live ? t : 0;
+    lane = live ? lane : 0;
+    const int h0 = lane / LANES, u = lane % LANES, nq2 = (a.nq + 1) >> 1;
+    const bool two = h0 + nq2 < a.nq;
+    const int h1 = two ? h0 + nq2 : h0;
+    const RopePlace w(a, u);
+    const int pos = __ldg(a.pos + t);
+    RopeUnit<T> r0, r1;
+    r0.load(a.q, (size_t)t * a.q_stride + h0 * HD, w.ea, w.eb);
+    r1.load(a.q, (size_t)t * a.q_stride + h1 * HD, w.ea, w.eb);
+    const bool seen = live && pos >= 0 && pos < a.n_pos;
+    if (live && pos >= a.n_pos) atomicExch(a.status, ST_DEVICE_CHECK);
+    const float* cs = a.table + (size_t)(seen ? pos : 0) * a.rot + (w.turns ? 8 * u : 0);
+    float2 v[8];
+    r0.widen(v);
+    rope_unit<LANES, NORM>(a, v, w, a.q_norm, cs);
+    if (seen) store_unit<T>(a.q_out, (size_t)t * a.q_out_stride + h0 * HD, w.ea, w.eb, v);
+    r1.widen(v);
+    rope_unit<LANES, NORM>(a, v, w, a.q_norm, cs);
+    if (seen && two) store_unit<T>(a.q_out, (size_t)t * a.q_out_stride + h1 * HD, w.ea, w.eb, v);
+}
+
+// A unit of a K head and of its V head.
+template <int T, int HD, int NORM>
+__device__ __forceinline__ void rope_kv(const RopeArgs& a, int t, int lane, bool live) {
+    constexpr int LANES = HD / 16, hd_log2 = HD == 64 ? 6 : HD == 128 ? 7 : 8;
+    t = live ? t : 0;
+    lane = live ? lane : 0;
+    const int h = lane / LANES, u = lane % LANES;
+    const RopePlace w(a, u);
+    const int pos = __ldg(a.pos + t);
+    RopeUnit<T> rk, rv;
+    rk.load(a.k, (size_t)t * a.k_stride + h * HD, w.ea, w.eb);
+    rv.load(a.v, (size_t)t * a.v_stride + h * HD, 16 * u, 16 * u + 8);
+    const int64_t slot = __ldg(a.slots + t);
+    const float kg = __ldg(a.c.kg + h), vg = __ldg(a.c.vg + h);
+    const bool seen = live && pos >= 0 && pos < a.n_pos;
+    if (live && pos >= a.n_pos) atomicExch(a.status, ST_DEVICE_CHECK);
+    const float* cs = a.table + (size_t)(seen ? pos : 0) * a.rot + (w.turns ? 8 * u : 0);
+    float2 v[8];
+    rk.widen(v);
+    rope_unit<LANES, NORM>(a, v, w, a.k_norm, cs);
+    append_unit(a, v, false, seen, t, h, w.ea, w.eb, w.apart, slot, kg, hd_log2);
+    rv.widen(v);
+    append_unit(a, v, true, seen, t, h, 16 * u, 16 * u + 8, false, slot, vg, hd_log2);
+}
+
+// How a kind's rows are dealt to CTAs: rows_cta whole rows where they fit a CTA's threads,
+// else `parts` CTAs a row.
+struct RopeDeal {
+    int lanes_row, rows_cta, parts, ctas;
+};
+
+// The CTAs of K and V rows first, which take longer; q's and theirs are apart, and small, so
+// that little waits for a CTA's slowest warp.
+template <int T, int HD, int NORM, int APPEND>
+__global__ void __launch_bounds__(RO_THREADS, 16) rope_kernel(const RopeArgs a, const RopeDeal dq, const RopeDeal dkv) {
     pdl_wait();
     pdl_launch_dependents();
-    const int r = rows_cta > 1 ? (int)threadIdx.x / lanes_row : 0;
-    const int t = (int)blockIdx.x * rows_cta + r;
-    for (int lane = (int)threadIdx.x - r * lanes_row; lane - (int)(threadIdx.x & 31) < lanes_row; lane += (int)blockDim.x)
-        rope_lane<F32, NORM, APPEND>(a, t, lane, r < rows_cta && t < a.n_tokens && lane < lanes_row, hd_log2);
+    const bool kv = APPEND && (int)blockIdx.x < dkv.ctas;
+    const RopeDeal d = kv ? dkv : dq;
+    const int cta = kv ? (int)blockIdx.x : (int)blockIdx.x - (APPEND ? dkv.ctas : 0);
+    int t, lane = (int)threadIdx.x;
+    bool live = true;
+    if (d.parts > 1) {
+        t = cta / d.parts;
+        lane += (cta - t * d.parts) * RO_THREADS;
+    } else {
+        const int r = lane / d.lanes_row;
+        t = cta * d.rows_cta + r;
+        lane -= r * d.lanes_row;
+        live = r < d.rows_cta;
+    }
+    live = live && t < a.n_tokens && lane < d.lanes_row;
+    if (kv) rope_kv<T, HD, NORM>(a, t, lane, live);
+    else rope_q<T, HD, NORM>(a, t, lane, live);
+}
+
+RopeDeal deal(int lanes_row, int n_tokens) {
+    if (!lanes_row) return {0, 1, 1, 0};
+    if (lanes_row > RO_THREADS) {
+        const int parts = (lanes_row + RO_THREADS - 1) / RO_THREADS;
+        return {lanes_row, 1, parts, n_tokens * parts};
+    }
+    const int rows_cta = RO_THREADS / lanes_row;
+    return {lanes_row, rows_cta, 1, (n_tokens + rows_cta - 1) / rows_cta};
+}
+
+using RopeKernel = void (*)(RopeArgs, RopeDeal, RopeDeal);
+
+template <int T, int HD>
+RopeKernel rope_kernel_of(bool norm, bool append) {
+    return norm ? append ? rope_kernel<T, HD, 1, 1> : rope_kernel<T, HD, 1, 0>
+                : append ? rope_kernel<T, HD, 0, 1> : rope_kernel<T, HD, 0, 0>;
+}
+template <int T>
+RopeKernel rope_kernel_of(int hd, bool norm, bool append) {
+    return hd == 64    ? rope_kernel_of<T, 64>(norm, append)
+           : hd == 128 ? rope_kernel_of<T, 128>(norm, append)
+                       : rope_kernel_of<T, 256>(norm, append);
 }
 
 // angles in 64 bits: a product and the range reduction lose 2^-53 of positions' worth
@@ -306,19 +377,14 @@ __global__ void rope_table_kernel(const __grid_constant__ RopeFreq f, int half, 
 }  // namespace
 
 cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
-    const int hd_log2 = a.hd == 64 ? 6 : a.hd == 128 ? 7 : 8;
-    const int lanes_row = ((a.nq + 1) / 2 + a.nkv) << (hd_log2 - 4);
-    // whole rows where two or more fit, else a row by as many threads as it has lanes
-    const int rows_cta = lanes_row <= RO_THREADS / 2 ? RO_THREADS / lanes_row : 1;
-    const int threads = rows_cta > 1 ? RO_THREADS : lanes_row < 512 ? (lanes_row + 31) / 32 * 32 : RO_THREADS;
-    const dim3 grid((unsigned)((a.n_tokens + rows_cta - 1) / rows_cta));
-    const int which = (a.t == KV4_F32 ? 4 : 0) + (a.q_norm || a.k_norm ? 2 : 0) + (a.nkv ? 1 : 0);
-    void (*const kernels[8])(RopeArgs, int, int, int) = {rope_kernel<0, 0, 0>, rope_kernel<0, 0, 1>, rope_kernel<0, 1, 0>,
-                                                         rope_kernel<0, 1, 1>, rope_kernel<1, 0, 0>, rope_kernel<1, 0, 1>,
-                                                         rope_kernel<1, 1, 0>, rope_kernel<1, 1, 1>};
+    const RopeDeal dq = deal((a.nq + 1) / 2 * (a.hd / 16), a.n_tokens), dkv = deal(a.nkv * (a.hd / 16), a.n_tokens);
+    const bool norm = a.q_norm || a.k_norm, append = a.nkv > 0;
+    const RopeKernel kernel = a.t == KV4_F32   ? rope_kernel_of<KV4_F32>(a.hd, norm, append)
+                              : a.t == KV4_F16 ? rope_kernel_of<KV4_F16>(a.hd, norm, append)
+                                               : rope_kernel_of<KV4_BF16>(a.hd, norm, append);
     RopeArgs b = a;
     b.minus_zero = make_float2(-0.f, -0.f);
-    return launch_pdl(kernels[which], grid, dim3(threads), 0, st, b, lanes_row, rows_cta, hd_log2);
+    return launch_pdl(kernel, dim3((unsigned)(dq.ctas + dkv.ctas)), dim3(RO_THREADS), 0, st, b, dq, dkv);
 }
 
 cudaError_t launch_rope_rows_table(const RopeFreq& f, int half, int n_pos, double mscale, float* table, cudaStream_t st) {
