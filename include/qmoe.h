@@ -489,7 +489,7 @@ qmoe_status qmoe_step_kv4(qmoe_ctx* ctx, qmoe_kv4* kv, const qmoe_layer_weights*
  *             x of that type and stride.  Only with a residual.
  *  weight   : F32 [dim], 16-byte aligned, or NULL (1).
  *  eps      : positive, finite.
- *  n_rows 1..2^24, dim a multiple of 16 up to 65536.
+ *  n_rows 1..2^24, dim a multiple of 16 up to 32768.
  *  y        : rows of y_t, y_stride apart (F32, F16, BF16; may be x of that type and
  *             stride), or 8-bit rows (QMOE_E4M3; y_stride 0 or dim).
  *  y_scale  : F32 [n_rows][ceil(dim/128)] for 8-bit rows, else NULL. */
@@ -499,7 +499,7 @@ qmoe_status qmoe_rmsnorm(qmoe_ctx* ctx, const void* x, qmoe_dtype x_t, int64_t x
                          qmoe_dtype y_t, int64_t y_stride, float* y_scale);
 
 /* n_rows rows of cols elements of x_t as 8-bit rows (one launch).  cols a multiple of
- * 16 up to 65536, n_rows 1..2^24. */
+ * 16 up to 32768, n_rows 1..2^24. */
 qmoe_status qmoe_fp8_quantize(qmoe_ctx* ctx, const void* x, qmoe_dtype x_t, int64_t x_stride,
                               int n_rows, int cols, void* codes, float* scale);
 

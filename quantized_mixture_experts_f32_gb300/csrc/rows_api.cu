@@ -44,7 +44,7 @@ bool valid_dtype(int t) { return t == QMOE_F32 || t == QMOE_F16 || t == QMOE_BF1
 int dtype_bytes(int t) { return t == QMOE_F32 ? 4 : 2; }
 
 constexpr int ROWS_MAX = 1 << 24;             // rows, tokens and features of a call
-constexpr int DIM_MAX = 65536;                // elements of a row that is normalised or quantised
+constexpr int DIM_MAX = 32768;                // elements of a row that is normalised or quantised
 constexpr int K_MAX = 1 << 20;                // in_features
 
 // rows of `row` elements: 0 stands for contiguous rows
