@@ -10,15 +10,9 @@
 // is a register and a warp's stores are neighbours.
 #include <limits.h>
 
-#include "kv4_row.cuh"
-#include "ptx_sync.cuh"
-#include "rows.cuh"
-#include "umma.cuh"
+#include "linear_fp8.cuh"
 
 namespace qmoe {
-
-// prefill_umma.cu
-bool tensor_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
 
 namespace {
 
@@ -27,23 +21,44 @@ constexpr int LN_GROUP = 4;                   // k blocks whose scales are stage
 constexpr int LN_SPLIT_MAX = 8;               // CTAs of a cluster that share a tile's k blocks
 constexpr int LN_STAGES_MAX = 12;
 
-__device__ __forceinline__ float activate(float z, int act) {
-    if (act == ACT_RELU) return z < 0.f ? 0.f : z;            // NaN stays
-    if (act == ACT_SILU) return z / (1.f + __expf(-z));
-    if (act == ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678118654752f));
-    return z;
+// Feature n of N tokens from t on: residual added, stored.  All residuals are read before
+// the first result is written, so that their latencies overlap and out may be residual.
+template <int T, int N>
+__device__ __forceinline__ void put(const LinearArgs& a, int t, int n, float (&v)[N]) {
+    using R = RowType<T>;
+    using type = typename R::type;
+    const int m = a.T - t;
+    if (m <= 0) return;
+    if (a.res) {
+        const type* p = static_cast<const type*>(a.res) + (size_t)t * a.res_stride + n;
+        type r[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += a.res_stride)
+            if (i < m) r[i] = *p;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < m) v[i] += R::load(r[i]);
+    }
+    type* p = static_cast<type*>(a.out) + (size_t)t * a.out_stride + n;
+    if (m >= N) {
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += a.out_stride) *p = R::store(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i, p += a.out_stride)
+            if (i < m) *p = R::store(v[i]);
+    }
 }
 
-__device__ __forceinline__ float row_load(const void* p, size_t at, int t) {
-    if (t == KV4_F32) return static_cast<const float*>(p)[at];
-    if (t == KV4_F16) return __half2float(static_cast<const __half*>(p)[at]);
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[at]);
-}
-
-__device__ __forceinline__ void row_store(void* p, size_t at, int t, float v) {
-    if (t == KV4_F32) static_cast<float*>(p)[at] = v;
-    else if (t == KV4_F16) static_cast<__half*>(p)[at] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(p)[at] = __float2bfloat16_rn(v);
+// z + bias through the activation, and out
+template <int N>
+__device__ __forceinline__ void finish(const LinearArgs& a, int t, int n, float bias, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += bias;
+    activate(v, a.act);
+    if (a.out_t == KV4_F32) put<KV4_F32>(a, t, n, v);
+    else if (a.out_t == KV4_F16) put<KV4_F16>(a, t, n, v);
+    else put<KV4_BF16>(a, t, n, v);
 }
 
 // D[tmem] (+)= A * B^T over E4M3 codes (M x 32 by N x 32), issued by one thread
@@ -55,31 +70,6 @@ __device__ __forceinline__ void umma_f8(uint32_t tmem_d, uint64_t adesc, uint64_
         : "memory");
 }
 
-// 16 columns of this thread's TMEM lane; tmem_arrived() before they are used
-__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
-
-// (x, y) += (a sx, b sy), two roundings in one instruction
-__device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, float sx, float sy) {
-    asm("{\n\t.reg .b64 d, v, s;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
-        "fma.rn.f32x2 d, v, s, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "+f"(acc.x), "+f"(acc.y)
-        : "r"(a), "r"(b), "f"(sx), "f"(sy));
-}
-
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
-}
 __device__ __forceinline__ float ld_cluster(uint32_t saddr, int rank) {
     float v;
     asm volatile("{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.f32 %0, [a];\n\t}"
@@ -91,7 +81,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t saddr, int rank) {
 // Shapes of a variant: TN tokens a tile, EW warps of the epilogue, TB products in TMEM.
 template <int TN>
 struct LinearTile {
-    static constexpr int EW = TN >= 128 ? 8 : 4;
+    static constexpr int EW = TN <= 64 ? 4 : TN / 16;            // at most 64 columns a thread
     static constexpr int EPI = EW * 32, THREADS = EPI + 64;
     static constexpr int COLS = TN * 4 / EW;                  // columns of a thread
     static constexpr int TB = TN >= 256 ? 2 : 4;
@@ -265,19 +255,11 @@ linear_umma_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
             if (ok && n < a.N) {
                 const float bias = a.bias ? a.bias[n] : 0.f;
 #pragma unroll
-                for (int c = 0; c < L::COLS; c += 16) {
-                    float v[16];
+                for (int c = 0; c < L::COLS; c += 8) {
+                    float v[8];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) v[i] = activate((i & 1 ? acc[(c + i) / 2].y : acc[(c + i) / 2].x) + bias, a.act);
-                    if (a.res) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (t0 + c0 + c + i < a.T)
-                                v[i] += row_load(a.res, (size_t)(t0 + c0 + c + i) * a.res_stride + n, a.out_t);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (t0 + c0 + c + i < a.T) row_store(a.out, (size_t)(t0 + c0 + c + i) * a.out_stride + n, a.out_t, v[i]);
+                    for (int i = 0; i < 8; ++i) v[i] = i & 1 ? acc[(c + i) / 2].y : acc[(c + i) / 2].x;
+                    finish(a, t0 + c0 + c, n, bias, v);
                 }
             }
             __syncwarp();
@@ -301,14 +283,11 @@ linear_umma_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant
 #pragma unroll
             for (int r = 0; r < LN_SPLIT_MAX; ++r) v[r] = r < split ? ld_cluster(red + 4 * i, r) : 0.f;
             if (n >= a.N) continue;
-            float z = v[0];
+            float z[1] = {v[0]};
 #pragma unroll
             for (int r = 1; r < LN_SPLIT_MAX; ++r)
-                if (r < split) z += v[r];
-            if (a.bias) z += a.bias[n];
-            z = activate(z, a.act);
-            if (a.res) z += row_load(a.res, (size_t)t * a.res_stride + n, a.out_t);
-            row_store(a.out, (size_t)t * a.out_stride + n, a.out_t, z);
+                if (r < split) z[0] += v[r];
+            finish(a, t, n, a.bias ? a.bias[n] : 0.f, z);
         }
         __syncwarp();
         cluster_sync();                                       // a part stays until all have read it
@@ -367,10 +346,12 @@ cudaError_t linear_fp8_prepare() {
     if (e == cudaSuccess) e = prepare_one<64>();
     if (e == cudaSuccess) e = prepare_one<128>();
     if (e == cudaSuccess) e = prepare_one<256>();
+    if (e == cudaSuccess) e = linear_pair_prepare();
     return e;
 }
 
 cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st) {
+    if (a.T > 256) return launch_linear_pair(a, num_sms, st);
     const int tn = a.T <= 16 ? 16 : a.T <= 32 ? 32 : a.T <= 64 ? 64 : a.T <= 128 ? 128 : 256;
     const int kb = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
     const int64_t tiles = (int64_t)((a.N + LN_M - 1) / LN_M) * ((a.T + tn - 1) / tn);

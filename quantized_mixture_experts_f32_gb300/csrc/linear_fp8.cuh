@@ -1,0 +1,101 @@
+// linear_fp8.cuh -- what the kernels of qmoe_linear_fp8 share.
+#pragma once
+#include "kv4_row.cuh"
+#include "ptx_sync.cuh"
+#include "rows.cuh"
+#include "umma.cuh"
+
+namespace qmoe {
+
+// prefill_umma.cu: tensor maps over E4M3 codes [rows][cols] (boxes of 128 columns) and over
+// rows of any type (boxes of 128 bytes), both with the 128-byte swizzle
+bool tensor_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
+bool tensor_map_rows(CUtensorMap* m, const void* base, int t, uint64_t cols, uint64_t rows, uint64_t stride, uint32_t box_rows);
+
+// linear_fp8_pair.cu
+cudaError_t linear_pair_prepare();
+cudaError_t launch_linear_pair(const LinearArgs& a, int num_sms, cudaStream_t st);
+
+__device__ __forceinline__ float relu(float z) { return z < 0.f ? 0.f : z; }                 // NaN stays
+__device__ __forceinline__ float silu(float z) { return z / (1.f + __expf(-z)); }
+__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.f + erff(z * 0.70710678118654752f)); }
+
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+    if (act == ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = relu(v[i]);
+    } else if (act == ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = silu(v[i]);
+    } else if (act == ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = gelu(v[i]);
+    }
+}
+
+// one element of a row
+template <int T>
+struct RowType {
+    using type = float;
+    static __device__ __forceinline__ float load(float v) { return v; }
+    static __device__ __forceinline__ float store(float v) { return v; }
+};
+template <>
+struct RowType<KV4_F16> {
+    using type = __half;
+    static __device__ __forceinline__ float load(__half v) { return __half2float(v); }
+    static __device__ __forceinline__ __half store(float v) { return __float2half_rn(v); }
+};
+template <>
+struct RowType<KV4_BF16> {
+    using type = __nv_bfloat16;
+    static __device__ __forceinline__ float load(__nv_bfloat16 v) { return __bfloat162float(v); }
+    static __device__ __forceinline__ __nv_bfloat16 store(float v) { return __float2bfloat16_rn(v); }
+};
+
+// element i of 16 bytes of a row of type T, and 16 bytes of elements
+template <int T>
+__device__ __forceinline__ float row_element(const uint32_t (&w)[4], int i) {
+    if (T == KV4_F32) return __uint_as_float(w[i & 3]);
+    uint32_t x = w[i / 2];
+    if (T == KV4_BF16) return __uint_as_float(i & 1 ? x & 0xffff0000u : x << 16);
+    const __half2 h = *reinterpret_cast<__half2*>(&x);
+    return i & 1 ? __high2float(h) : __low2float(h);
+}
+template <int T, int N>
+__device__ __forceinline__ void row_pack(const float (&v)[N], uint32_t (&w)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (T == KV4_F32) w[i] = __float_as_uint(v[i]);
+        else w[i] = kv4_pack16(v[2 * i], v[2 * i + 1], T);
+    }
+}
+
+// 16 columns of this thread's TMEM lane; tmem_arrived() before they are used
+__device__ __forceinline__ void tmem_fetch16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+
+// (x, y) += (a sx, b sy), two roundings in one instruction
+__device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, float sx, float sy) {
+    asm("{\n\t.reg .b64 d, v, s;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
+        "fma.rn.f32x2 d, v, s, d;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "r"(a), "r"(b), "f"(sx), "f"(sy));
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
+}  // namespace qmoe

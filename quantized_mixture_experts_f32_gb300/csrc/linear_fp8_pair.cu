@@ -1,0 +1,404 @@
+// linear_fp8_pair.cu -- qmoe_linear_fp8 for many tokens: pairs of CTAs on two SMs share a tile
+// of 256 tokens x 256 features (tcgen05 cta_group::2, kind::f8f6f4).
+//
+// Each CTA brings 128 rows of x and 128 of W, half of what the tile needs from either
+// side, and keeps the products of its 128 tokens: 32 KB a block of k, where a tile of
+// its own would take 48 and be bound by what L2 gives.  Tokens are TMEM's lanes, so that
+// a block's scale is one number a thread.  Sixteen warps scale the blocks' products into
+// fp32 registers, 64 features a thread, while the next two blocks' products run; rows
+// leave (and residuals come) through shared memory by TMA, a box a warp.
+#include <limits.h>
+
+#include "linear_fp8.cuh"
+
+namespace qmoe {
+
+namespace {
+
+constexpr int LP_EW = 16, LP_EPI = LP_EW * 32, LP_THREADS = LP_EPI + 128;
+constexpr int LP_TILE = 256;                  // tokens, and features, of a pair's tile
+constexpr int LP_COLS = 64;                   // features of a thread
+constexpr int LP_STAGE = 2 * 128 * 128;       // x and W rows of a block, of one CTA
+constexpr int LP_STAGES_MAX = 5;
+constexpr int LP_GROUP = 4, LP_SLOTS = 3;     // blocks of k whose scales are staged together, such groups
+
+struct PairBars {
+    uint64_t full[LP_STAGES_MAX], empty[LP_STAGES_MAX], tfull[2], tempty[2], sfull[LP_SLOTS], sempty[LP_SLOTS], res[LP_EW];
+    uint32_t tmem;
+    int failed;
+};
+
+struct PairScales {
+    float x[LP_SLOTS][LP_GROUP][128];         // of the CTA's tokens
+    float w[LP_SLOTS][2][LP_GROUP];           // of the tile's two blocks of features
+    __align__(16) float bias[2][4][LP_COLS];  // of the warps' features, in this tile and the next
+};
+
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+
+// a copy into this CTA whose bytes count on a barrier of the pair's first
+__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
+            "r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void umma_f8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// arrive on the barrier of both CTAs once the products issued so far are done
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, const void* src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+
+// Out types: a warp's 64 features of 32 tokens lie in boxes of 32 rows of 128 bytes.
+template <int OUT>
+struct PairOut {
+    static constexpr int SIZE = OUT == KV4_F32 ? 4 : 2;
+    static constexpr int BOXES = LP_COLS * SIZE / 128, BOX_COLS = 128 / SIZE;
+    static constexpr int E = 16 / SIZE;                       // elements of 16 bytes
+    static constexpr int BUF = 4096;                          // a warp's, for one box after the other
+    static constexpr int STAGES = 4;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * LP_STAGE + LP_EW * BUF;
+};
+
+template <int OUT>
+__global__ void __launch_bounds__(LP_THREADS, 1)
+linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+                   const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr, const LinearArgs a, int tiles_n,
+                   int tiles) {
+    using O = PairOut<OUT>;
+    constexpr int STAGES = O::STAGES;
+    extern __shared__ uint8_t dyn[];
+    __shared__ PairBars bars;
+    __shared__ PairScales sc;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
+    uint8_t* bufs = ring + (size_t)STAGES * LP_STAGE;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)blockIdx.x & 1, first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+    const int kb_all = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&bars.full[i], 1);
+            mbar_init(&bars.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars.tfull[i], 1);
+            mbar_init(&bars.tempty[i], 2 * LP_EW);
+        }
+        for (int i = 0; i < LP_SLOTS; ++i) {
+            mbar_init(&bars.sfull[i], 2);
+            mbar_init(&bars.sempty[i], LP_EW);
+        }
+        for (int i = 0; i < LP_EW; ++i) mbar_init(&bars.res[i], 1);
+        bars.failed = 0;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    if (warp == LP_EW + 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                           // both have their columns and barriers
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = bars.tmem;
+    volatile int* failed = &bars.failed;
+
+    if (warp == LP_EW) {
+        // ---- copies
+        if (lane == 0) {
+            int g = 0;
+            for (int tile = first; tile < tiles && !*failed; tile += step) {
+                const int t0 = tile / tiles_n * LP_TILE + rank * 128, n0 = tile % tiles_n * LP_TILE + rank * 128;
+                for (int kb = 0; kb < kb_all; ++kb, ++g) {
+                    const int st = g % STAGES;
+                    if (g >= STAGES && !mbar_wait(&bars.empty[st], (g / STAGES - 1) & 1)) {
+                        *failed = 1;
+                        break;
+                    }
+                    const uint32_t bar = cluster_addr(&bars.full[st], 0);
+                    uint8_t* to = ring + (size_t)st * LP_STAGE;
+                    if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * LP_STAGE);
+                    tma_load_pair(to, &mx, kb * FP8_BLOCK, t0, bar);
+                    tma_load_pair(to + 128 * 128, &mw, kb * FP8_BLOCK, n0, bar);
+                }
+            }
+            // copies in flight have landed before the pair ends (they count in the first CTA)
+            if (rank == 0)
+                for (int i = g > STAGES ? g - STAGES : 0; i < g; ++i) mbar_wait(&bars.full[i % STAGES], (i / STAGES) & 1);
+        }
+    } else if (warp == LP_EW + 1) {
+        // ---- products of both
+        if (lane == 0 && rank == 0) {
+            constexpr uint32_t idesc = umma_idesc_f16(LP_TILE, LP_TILE);  // E4M3 has F16's type number
+            int g = 0;
+            for (int tile = first; tile < tiles && !*failed; tile += step) {
+                for (int kb = 0; kb < kb_all; ++kb, ++g) {
+                    const int st = g % STAGES, tb = g & 1;
+                    if (!mbar_wait(&bars.full[st], (g / STAGES) & 1) ||
+                        (g >= 2 && !mbar_wait(&bars.tempty[tb], (g / 2 - 1) & 1))) {
+                        *failed = 1;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t s = smem_u32(ring + (size_t)st * LP_STAGE);
+                    const uint64_t da = umma_sdesc(s), db = umma_sdesc(s + 128 * 128);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + tb * LP_TILE, da + 2 * k, db + 2 * k, idesc, k > 0);
+                    umma_commit_pair(&bars.empty[st]);
+                    umma_commit_pair(&bars.tfull[tb]);
+                }
+            }
+            if (*failed && g > 0) mbar_wait(&bars.tfull[(g - 1) & 1], ((g - 1) / 2) & 1);   // products in flight
+        }
+    } else if (warp >= LP_EW + 2) {
+        // ---- scales: two warps, 64 tokens each
+        const int w2 = warp - LP_EW - 2, blocks_n = (a.N + FP8_BLOCK - 1) / FP8_BLOCK;
+        const bool quads = kb_all % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15) == 0;
+        int gr = 0;
+        for (int tile = first; tile < tiles && !*failed; tile += step) {
+            const int t0 = tile / tiles_n * LP_TILE + rank * 128 + w2 * 64 + lane, nb = tile % tiles_n * 2;
+            for (int kb = 0; kb < kb_all; kb += LP_GROUP, ++gr) {
+                float4 v[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float* p = a.xs + (size_t)min(t0 + 32 * i, a.T - 1) * kb_all;
+                    if (quads) v[i] = __ldg(reinterpret_cast<const float4*>(p + kb));
+                    else
+                        v[i] = make_float4(__ldg(p + kb), __ldg(p + min(kb + 1, kb_all - 1)), __ldg(p + min(kb + 2, kb_all - 1)),
+                                           __ldg(p + min(kb + 3, kb_all - 1)));
+                }
+                float w = 0.f;
+                if (w2 == 0 && lane < 2 * LP_GROUP)
+                    w = __ldg(a.ws + (size_t)min(nb + lane / LP_GROUP, blocks_n - 1) * kb_all + min(kb + lane % LP_GROUP, kb_all - 1));
+                const int slot = gr % LP_SLOTS;
+                if (gr >= LP_SLOTS && !mbar_wait(&bars.sempty[slot], (gr / LP_SLOTS - 1) & 1)) *failed = 1;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int at = w2 * 64 + 32 * i + lane;
+                    sc.x[slot][0][at] = v[i].x;
+                    sc.x[slot][1][at] = v[i].y;
+                    sc.x[slot][2][at] = v[i].z;
+                    sc.x[slot][3][at] = v[i].w;
+                }
+                if (w2 == 0 && lane < 2 * LP_GROUP) sc.w[slot][lane / LP_GROUP][lane % LP_GROUP] = w;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.sfull[slot]);
+                if (*failed) break;
+            }
+        }
+    } else {
+        // ---- sums and results.  After a wait that ran out (ok) the warp goes on to
+        // the end without waiting or writing, so that the barriers keep their counts.
+        const int c0 = (warp >> 2) * LP_COLS;
+        const uint32_t tcol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
+        const uint32_t empty0 = cluster_addr(&bars.tempty[0], 0), empty1 = cluster_addr(&bars.tempty[1], 0);
+        uint8_t* buf = bufs + warp * O::BUF;
+        // stores by TMA end on whole 16 bytes, whatever the map says: the features behind go one by one
+        const int whole = a.N / O::E * O::E;
+        int g = 0, gr = 0, turn = 0;                          // blocks, groups and residual boxes so far
+        const int my = (warp & 3) * 32 + lane, wb = c0 / FP8_BLOCK;
+        bool ok = true;
+        int par = 0;                                          // a warp is at most a tile ahead of another
+        for (int tile = first; tile < tiles; tile += step, par ^= 1) {
+            const int tw = tile / tiles_n * LP_TILE + rank * 128 + (warp & 3) * 32, t = tw + lane;   // the warp's rows, this one
+            const int n0 = tile % tiles_n * LP_TILE + c0;
+            const bool any = tw < a.T && n0 < a.N;            // the warp has something to write
+            if (a.res && any && ok && lane == 0) {
+                tma_stores_read();
+                mbar_arrive_expect_tx(&bars.res[warp], O::BUF);
+                tma_load_2d(buf, &mr, n0, tw, &bars.res[warp]);
+            }
+            float2 acc[LP_COLS / 2];
+#pragma unroll
+            for (int i = 0; i < LP_COLS / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+            if (a.bias) {
+#pragma unroll
+                for (int i = 0; i < LP_COLS; i += 32) sc.bias[par][warp >> 2][i + lane] = __ldg(a.bias + min(n0 + i + lane, a.N - 1));
+            }
+            for (int kb = 0; kb < kb_all; ++kb, ++g) {
+                const int in = kb % LP_GROUP, slot = gr % LP_SLOTS;
+                if (in == 0 && ok && !mbar_wait(&bars.sfull[slot], (gr / LP_SLOTS) & 1)) {
+                    *failed = 1;
+                    ok = false;
+                }
+                const float s = sc.x[slot][in][my] * sc.w[slot][wb][in];
+                const int tb = g & 1;
+                if (ok && !mbar_wait(&bars.tfull[tb], (g / 2) & 1)) {
+                    *failed = 1;
+                    ok = false;
+                }
+                ok = __all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                const uint32_t from = tcol + tb * LP_TILE;
+                uint32_t r[2][16];
+                tmem_fetch16(from, r[0]);
+#pragma unroll
+                for (int c = 0; c < LP_COLS / 16; ++c) {
+                    tmem_arrived(r[c & 1]);
+                    if (c + 1 < LP_COLS / 16) tmem_fetch16(from + 16 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s, s);
+                }
+                tc_fence_before();
+                __syncwarp();
+                const bool last = in == LP_GROUP - 1 || kb == kb_all - 1;
+                if (lane == 0) {
+                    arrive_cluster(tb ? empty1 : empty0);
+                    if (last) mbar_arrive(&bars.sempty[slot]);
+                }
+                gr += last;
+            }
+            if (!any || !ok) continue;                        // the same for the whole warp
+#pragma unroll
+            for (int b = 0; b < O::BOXES; ++b) {
+                if (a.res) {
+                    if (b && lane == 0) {
+                        tma_stores_read();
+                        mbar_arrive_expect_tx(&bars.res[warp], O::BUF);
+                        tma_load_2d(buf, &mr, n0 + b * O::BOX_COLS, tw, &bars.res[warp]);
+                    }
+                    if (ok && !mbar_wait(&bars.res[warp], turn & 1)) {
+                        *failed = 1;
+                        ok = false;
+                    }
+                    ++turn;
+                    ok = __all_sync(0xffffffffu, ok);
+                } else {
+                    if (lane == 0) tma_stores_read();
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {                 // 16 bytes a turn
+                    constexpr int E = O::E;
+                    const int c = b * O::BOX_COLS + i * E;
+                    float v[E];
+#pragma unroll
+                    for (int j = 0; j < E; ++j) v[j] = j & 1 ? acc[(c + j) / 2].y : acc[(c + j) / 2].x;
+                    if (a.bias) {
+#pragma unroll
+                        for (int j = 0; j < E; j += 4) {
+                            const float4 p = *reinterpret_cast<const float4*>(&sc.bias[par][warp >> 2][c + j]);
+                            v[j] += p.x;
+                            v[j + 1] += p.y;
+                            v[j + 2] += p.z;
+                            v[j + 3] += p.w;
+                        }
+                    }
+                    activate(v, a.act);
+                    uint4* at = reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4));
+                    if (a.res) {
+                        const uint4 u = *at;
+                        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int j = 0; j < E; ++j) v[j] += row_element<OUT>(w, j);
+                    }
+                    uint32_t w[4];
+                    row_pack<OUT>(v, w);
+                    *at = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (n0 + c == whole && ok && t < a.T) {
+                        using type = typename RowType<OUT>::type;
+                        type* p = static_cast<type*>(a.out) + (size_t)t * a.out_stride + whole;
+#pragma unroll
+                        for (int j = 0; j < E - 1; ++j)
+                            if (whole + j < a.N) p[j] = RowType<OUT>::store(v[j]);
+                    }
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0 && ok && n0 + b * O::BOX_COLS < whole) tma_store_2d(&mo, n0 + b * O::BOX_COLS, tw, buf);
+                __syncwarp();
+            }
+        }
+        if (lane == 0) tma_stores_read();
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *failed) atomicExch(a.status, ST_TIMEOUT);
+    cluster_sync();                                           // neither works in the other's memory any more
+    if (warp == LP_EW + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+template <int OUT>
+cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
+    using O = PairOut<OUT>;
+    CUtensorMap mx, mw, mo, mr;
+    if (!tensor_map_codes(&mx, a.x, (uint64_t)a.K, (uint64_t)a.T, 128) || !tensor_map_codes(&mw, a.w, (uint64_t)a.K, (uint64_t)a.N, 128) ||
+        !tensor_map_rows(&mo, a.out, OUT, (uint64_t)(a.N < O::E ? O::E : a.N / O::E * O::E), (uint64_t)a.T, (uint64_t)a.out_stride, 32) ||
+        !tensor_map_rows(&mr, a.res ? a.res : a.out, OUT, (uint64_t)a.N, (uint64_t)a.T, (uint64_t)(a.res ? a.res_stride : a.out_stride), 32))
+        return cudaErrorInvalidValue;
+    const int tiles_n = (a.N + LP_TILE - 1) / LP_TILE;
+    const int64_t tiles = (int64_t)tiles_n * ((a.T + LP_TILE - 1) / LP_TILE);
+    if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
+    const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * pairs);
+    cfg.blockDim = dim3(LP_THREADS);
+    cfg.dynamicSmemBytes = O::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OUT>, mx, mw, mo, mr, a, tiles_n, (int)tiles);
+}
+
+template <int OUT>
+cudaError_t prepare_out() {
+    return cudaFuncSetAttribute(linear_pair_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PairOut<OUT>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t linear_pair_prepare() {
+    cudaError_t e = prepare_out<KV4_F32>();
+    if (e == cudaSuccess) e = prepare_out<KV4_F16>();
+    if (e == cudaSuccess) e = prepare_out<KV4_BF16>();
+    return e;
+}
+
+cudaError_t launch_linear_pair(const LinearArgs& a, int num_sms, cudaStream_t st) {
+    return a.out_t == KV4_F32   ? launch_out<KV4_F32>(a, num_sms, st)
+           : a.out_t == KV4_F16 ? launch_out<KV4_F16>(a, num_sms, st)
+                                : launch_out<KV4_BF16>(a, num_sms, st);
+}
+
+}  // namespace qmoe

@@ -1219,6 +1219,21 @@ bool tensor_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// rows of type t (0 F32, 1 F16, 2 BF16), `stride` elements apart, box = 128 bytes x box_rows, 128B swizzle
+bool tensor_map_rows(CUtensorMap* m, const void* base, int t, uint64_t cols, uint64_t rows, uint64_t stride, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint32_t size = t == 0 ? 4 : 2;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {stride * size};
+    cuuint32_t box[2] = {128 / size, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    const CUtensorMapDataType dt = t == 0 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : t == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool prefill_supported(const MoeShape& s, int gate_t, int up_t, int down_t) {
     if (gate_t != 1 || up_t != 1) return false;
     if (s.H % QK || s.F % QK || s.H % TILE_M || s.F % 64) return false;
