@@ -94,6 +94,19 @@ __device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, float 
         : "r"(a), "r"(b), "f"(sx), "f"(sy));
 }
 
+// The warps that issue products and copies run their loops as a whole, so that descriptors
+// and addresses stay in uniform registers; only the instructions are one lane's (`one`).
+__device__ __forceinline__ uint32_t elected() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }   // known to be
+// a whole warp's bounded wait
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }

@@ -31,7 +31,7 @@ struct PairBars {
 struct PairScales {
     float x[LP_SLOTS][LP_GROUP][128];         // of the CTA's tokens
     float w[LP_SLOTS][2][LP_GROUP];           // of the tile's two blocks of features
-    __align__(16) float bias[2][4][LP_COLS];  // of the warps' features, in this tile and the next
+    __align__(16) float bias[LP_SLOTS][LP_TILE]; // of the tile's features, with its first group
 };
 
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
@@ -41,27 +41,32 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 }
 
 // a copy into this CTA whose bytes count on a barrier of the pair's first
-__device__ __forceinline__ void tma_load_pair(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void tma_load_pair(uint32_t one, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::
-            "r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::
+            "r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one)
         : "memory");
 }
 
-__device__ __forceinline__ void umma_f8_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// D[tmem] = A * B^T over E4M3 codes (256 x 32 by N x 32), or += it; descriptors by their low words
+template <int ADD>
+__device__ __forceinline__ void umma_f8_pair(uint32_t one, uint32_t d, uint32_t a, uint32_t b, uint32_t high, uint32_t idesc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(high), "r"(idesc), "n"(ADD), "r"(one)
         : "memory");
 }
 
 // arrive on the barrier of both CTAs once the products issued so far are done
-__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+__device__ __forceinline__ void umma_commit_pair(uint32_t one, uint32_t bar) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-        "h"((uint16_t)3)
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3), "r"(one)
         : "memory");
 }
 
@@ -89,7 +94,7 @@ struct PairOut {
     static constexpr size_t SMEM = 1024 + (size_t)STAGES * LP_STAGE + LP_EW * BUF;
 };
 
-template <int OUT>
+template <int OUT, int ACT>
 __global__ void __launch_bounds__(LP_THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                    const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr, const LinearArgs a, int tiles_n,
@@ -138,50 +143,62 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
 
     if (warp == LP_EW) {
         // ---- copies
-        if (lane == 0) {
-            int g = 0;
-            for (int tile = first; tile < tiles && !*failed; tile += step) {
-                const int t0 = tile / tiles_n * LP_TILE + rank * 128, n0 = tile % tiles_n * LP_TILE + rank * 128;
-                for (int kb = 0; kb < kb_all; ++kb, ++g) {
-                    const int st = g % STAGES;
-                    if (g >= STAGES && !mbar_wait(&bars.empty[st], (g / STAGES - 1) & 1)) {
-                        *failed = 1;
-                        break;
-                    }
-                    const uint32_t bar = cluster_addr(&bars.full[st], 0);
-                    uint8_t* to = ring + (size_t)st * LP_STAGE;
-                    if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * LP_STAGE);
-                    tma_load_pair(to, &mx, kb * FP8_BLOCK, t0, bar);
-                    tma_load_pair(to + 128 * 128, &mw, kb * FP8_BLOCK, n0, bar);
+        const uint32_t one = elected(), ring0 = uniform(smem_u32(ring)), full0 = uniform(cluster_addr(&bars.full[0], 0));
+        int st = 0, fresh = 1, phase = 1, left = 0;           // stage, whether never used, parity of its last emptying
+        bool go = true;
+        for (int tile = first; tile < tiles && go; tile += step) {
+            const int t0 = tile / tiles_n * LP_TILE + rank * 128, n0 = tile % tiles_n * LP_TILE + rank * 128;
+            for (int kb = 0; kb < kb_all; ++kb) {
+                go = fresh || warp_wait(&bars.empty[st], phase);
+                if (!go) break;
+                const uint32_t to = ring0 + st * LP_STAGE, bar = full0 + 8 * st;
+                if (rank == 0 && one) mbar_arrive_expect_tx(&bars.full[st], 2 * LP_STAGE);
+                tma_load_pair(one, to, &mx, kb * FP8_BLOCK, t0, bar);
+                tma_load_pair(one, to + 128 * 128, &mw, kb * FP8_BLOCK, n0, bar);
+                ++left;
+                if (++st == STAGES) {
+                    st = 0;
+                    fresh = 0;
+                    phase ^= 1;
                 }
             }
-            // copies in flight have landed before the pair ends (they count in the first CTA)
-            if (rank == 0)
-                for (int i = g > STAGES ? g - STAGES : 0; i < g; ++i) mbar_wait(&bars.full[i % STAGES], (i / STAGES) & 1);
         }
+        if (!go) *failed = 1;
+        // copies in flight have landed before the pair ends (they count in the first CTA)
+        if (rank == 0)
+            for (int i = left > STAGES ? left - STAGES : 0; i < left; ++i) warp_wait(&bars.full[i % STAGES], (i / STAGES) & 1);
     } else if (warp == LP_EW + 1) {
         // ---- products of both
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
+            const uint32_t one = elected(), tm = uniform(tmem), ring0 = uniform(smem_u32(ring));
+            const uint32_t high = (uint32_t)(umma_sdesc(0) >> 32), d0 = (uint32_t)umma_sdesc(ring0);
+            const uint32_t tfull0 = uniform(smem_u32(&bars.tfull[0])), empty0 = uniform(smem_u32(&bars.empty[0]));
             constexpr uint32_t idesc = umma_idesc_f16(LP_TILE, LP_TILE);  // E4M3 has F16's type number
-            int g = 0;
-            for (int tile = first; tile < tiles && !*failed; tile += step) {
+            int st = 0, phase = 0, g = 0;
+            bool go = true;
+            for (int tile = first; tile < tiles && go; tile += step) {
                 for (int kb = 0; kb < kb_all; ++kb, ++g) {
-                    const int st = g % STAGES, tb = g & 1;
-                    if (!mbar_wait(&bars.full[st], (g / STAGES) & 1) ||
-                        (g >= 2 && !mbar_wait(&bars.tempty[tb], (g / 2 - 1) & 1))) {
-                        *failed = 1;
-                        break;
-                    }
+                    const int tb = g & 1;
+                    go = warp_wait(&bars.full[st], phase) && (g < 2 || warp_wait(&bars.tempty[tb], (g / 2 - 1) & 1));
+                    if (!go) break;
                     tc_fence_after();
-                    const uint32_t s = smem_u32(ring + (size_t)st * LP_STAGE);
-                    const uint64_t da = umma_sdesc(s), db = umma_sdesc(s + 128 * 128);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) umma_f8_pair(tmem + tb * LP_TILE, da + 2 * k, db + 2 * k, idesc, k > 0);
-                    umma_commit_pair(&bars.empty[st]);
-                    umma_commit_pair(&bars.tfull[tb]);
+                    const uint32_t da = d0 + st * (LP_STAGE >> 4), db = da + (128 * 128 >> 4), d = tm + tb * LP_TILE;
+                    umma_f8_pair<0>(one, d, da, db, high, idesc);
+                    umma_f8_pair<1>(one, d, da + 2, db + 2, high, idesc);
+                    umma_f8_pair<1>(one, d, da + 4, db + 4, high, idesc);
+                    umma_f8_pair<1>(one, d, da + 6, db + 6, high, idesc);
+                    umma_commit_pair(one, tfull0 + 8 * tb);
+                    umma_commit_pair(one, empty0 + 8 * st);
+                    if (++st == STAGES) {
+                        st = 0;
+                        phase ^= 1;
+                    }
                 }
             }
-            if (*failed && g > 0) mbar_wait(&bars.tfull[(g - 1) & 1], ((g - 1) / 2) & 1);   // products in flight
+            if (!go) {
+                *failed = 1;
+                if (g > 0) warp_wait(&bars.tfull[(g - 1) & 1], ((g - 1) / 2) & 1);   // products in flight
+            }
         }
     } else if (warp >= LP_EW + 2) {
         // ---- scales: two warps, 64 tokens each
@@ -203,6 +220,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 float w = 0.f;
                 if (w2 == 0 && lane < 2 * LP_GROUP)
                     w = __ldg(a.ws + (size_t)min(nb + lane / LP_GROUP, blocks_n - 1) * kb_all + min(kb + lane % LP_GROUP, kb_all - 1));
+                float b4[4];
+                if (kb == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        b4[i] = a.bias ? __ldg(a.bias + min(tile % tiles_n * LP_TILE + w2 * 128 + 32 * i + lane, a.N - 1)) : 0.f;
+                }
                 const int slot = gr % LP_SLOTS;
                 if (gr >= LP_SLOTS && !mbar_wait(&bars.sempty[slot], (gr / LP_SLOTS - 1) & 1)) *failed = 1;
 #pragma unroll
@@ -212,6 +235,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     sc.x[slot][1][at] = v[i].y;
                     sc.x[slot][2][at] = v[i].z;
                     sc.x[slot][3][at] = v[i].w;
+                }
+                if (kb == 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sc.bias[slot][w2 * 128 + 32 * i + lane] = b4[i];
                 }
                 if (w2 == 0 && lane < 2 * LP_GROUP) sc.w[slot][lane / LP_GROUP][lane % LP_GROUP] = w;
                 __syncwarp();
@@ -231,8 +258,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         int g = 0, gr = 0, turn = 0;                          // blocks, groups and residual boxes so far
         const int my = (warp & 3) * 32 + lane, wb = c0 / FP8_BLOCK;
         bool ok = true;
-        int par = 0;                                          // a warp is at most a tile ahead of another
-        for (int tile = first; tile < tiles; tile += step, par ^= 1) {
+        for (int tile = first; tile < tiles; tile += step) {
             const int tw = tile / tiles_n * LP_TILE + rank * 128 + (warp & 3) * 32, t = tw + lane;   // the warp's rows, this one
             const int n0 = tile % tiles_n * LP_TILE + c0;
             const bool any = tw < a.T && n0 < a.N;            // the warp has something to write
@@ -242,17 +268,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 tma_load_2d(buf, &mr, n0, tw, &bars.res[warp]);
             }
             float2 acc[LP_COLS / 2];
-#pragma unroll
-            for (int i = 0; i < LP_COLS / 2; ++i) acc[i] = make_float2(0.f, 0.f);
-            if (a.bias) {
-#pragma unroll
-                for (int i = 0; i < LP_COLS; i += 32) sc.bias[par][warp >> 2][i + lane] = __ldg(a.bias + min(n0 + i + lane, a.N - 1));
-            }
             for (int kb = 0; kb < kb_all; ++kb, ++g) {
                 const int in = kb % LP_GROUP, slot = gr % LP_SLOTS;
                 if (in == 0 && ok && !mbar_wait(&bars.sfull[slot], (gr / LP_SLOTS) & 1)) {
                     *failed = 1;
                     ok = false;
+                }
+                if (kb == 0) {                                // sums begin with the bias
+#pragma unroll
+                    for (int i = 0; i < LP_COLS; i += 4) {
+                        const float4 p = *reinterpret_cast<const float4*>(&sc.bias[slot][c0 + i]);
+                        acc[i / 2] = make_float2(p.x, p.y);
+                        acc[i / 2 + 1] = make_float2(p.z, p.w);
+                    }
                 }
                 const float s = sc.x[slot][in][my] * sc.w[slot][wb][in];
                 const int tb = g & 1;
@@ -260,27 +288,30 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     *failed = 1;
                     ok = false;
                 }
-                ok = __all_sync(0xffffffffu, ok);
+                __syncwarp();
                 tc_fence_after();
                 const uint32_t from = tcol + tb * LP_TILE;
+                const bool last = in == LP_GROUP - 1 || kb == kb_all - 1;
                 uint32_t r[2][16];
                 tmem_fetch16(from, r[0]);
 #pragma unroll
                 for (int c = 0; c < LP_COLS / 16; ++c) {
                     tmem_arrived(r[c & 1]);
                     if (c + 1 < LP_COLS / 16) tmem_fetch16(from + 16 * (c + 1), r[(c + 1) & 1]);
+                    else {                                    // all read: the products after next may come
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            arrive_cluster(tb ? empty1 : empty0);
+                            if (last) mbar_arrive(&bars.sempty[slot]);
+                        }
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s, s);
                 }
-                tc_fence_before();
-                __syncwarp();
-                const bool last = in == LP_GROUP - 1 || kb == kb_all - 1;
-                if (lane == 0) {
-                    arrive_cluster(tb ? empty1 : empty0);
-                    if (last) mbar_arrive(&bars.sempty[slot]);
-                }
                 gr += last;
             }
+            ok = __all_sync(0xffffffffu, ok);
             if (!any || !ok) continue;                        // the same for the whole warp
 #pragma unroll
             for (int b = 0; b < O::BOXES; ++b) {
@@ -307,17 +338,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     float v[E];
 #pragma unroll
                     for (int j = 0; j < E; ++j) v[j] = j & 1 ? acc[(c + j) / 2].y : acc[(c + j) / 2].x;
-                    if (a.bias) {
-#pragma unroll
-                        for (int j = 0; j < E; j += 4) {
-                            const float4 p = *reinterpret_cast<const float4*>(&sc.bias[par][warp >> 2][c + j]);
-                            v[j] += p.x;
-                            v[j + 1] += p.y;
-                            v[j + 2] += p.z;
-                            v[j + 3] += p.w;
-                        }
-                    }
-                    activate(v, a.act);
+                    if (ACT) activate(v, a.act);
                     uint4* at = reinterpret_cast<uint4*>(buf + lane * 128 + ((i ^ (lane & 7)) << 4));
                     if (a.res) {
                         const uint4 u = *at;
@@ -352,7 +373,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     if (warp == LP_EW + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <int OUT>
+template <int OUT, int ACT>
 cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
     using O = PairOut<OUT>;
     CUtensorMap mx, mw, mo, mr;
@@ -378,12 +399,21 @@ cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OUT>, mx, mw, mo, mr, a, tiles_n, (int)tiles);
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OUT, ACT>, mx, mw, mo, mr, a, tiles_n, (int)tiles);
+}
+
+// the activations' code is long, and would be fetched past for every tile without one
+template <int OUT>
+cudaError_t launch_type(const LinearArgs& a, int num_sms, cudaStream_t st) {
+    return a.act == ACT_NONE ? launch_out<OUT, 0>(a, num_sms, st) : launch_out<OUT, 1>(a, num_sms, st);
 }
 
 template <int OUT>
 cudaError_t prepare_out() {
-    return cudaFuncSetAttribute(linear_pair_kernel<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PairOut<OUT>::SMEM);
+    cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<OUT, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PairOut<OUT>::SMEM);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(linear_pair_kernel<OUT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PairOut<OUT>::SMEM);
+    return e;
 }
 
 }  // namespace
@@ -396,9 +426,9 @@ cudaError_t linear_pair_prepare() {
 }
 
 cudaError_t launch_linear_pair(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    return a.out_t == KV4_F32   ? launch_out<KV4_F32>(a, num_sms, st)
-           : a.out_t == KV4_F16 ? launch_out<KV4_F16>(a, num_sms, st)
-                                : launch_out<KV4_BF16>(a, num_sms, st);
+    return a.out_t == KV4_F32   ? launch_type<KV4_F32>(a, num_sms, st)
+           : a.out_t == KV4_F16 ? launch_type<KV4_F16>(a, num_sms, st)
+                                : launch_type<KV4_BF16>(a, num_sms, st);
 }
 
 }  // namespace qmoe
