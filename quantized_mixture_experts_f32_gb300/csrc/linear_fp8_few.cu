@@ -1,0 +1,120 @@
+// linear_fp8_few.cu -- qmoe_linear_fp8 for a few tokens, on mma.sync (m16n8k16, F16).
+//
+// The call is W's bytes and latency, so everything that costs a wait is left out: codes go
+// from global memory through registers into the products (E4M3 is exact in F16, the
+// products in fp32), W's 16 rows as the first operand, eight tokens as the second.
+// tcgen05 would need W in shared memory, TMEM taken and given back, and three hand-overs.
+// A lane loads 16 neighbouring codes of a row; which k a product's position means is
+// free as long as both operands agree, so they serve four products of 16 as they lie.
+#include "linear_fp8.cuh"
+
+namespace qmoe {
+
+namespace {
+
+constexpr int LF_WARPS = 8;                   // of a CTA: 16 features, k dealt between them
+constexpr int LF_ROWS = 16;
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 16 codes -> eight pairs in F16
+__device__ __forceinline__ void widen16(const uint4& u, uint32_t (&h)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[2 * i] = kv4_u(kv4_scale2(w[i] & 0xffffu));
+        h[2 * i + 1] = kv4_u(kv4_scale2(w[i] >> 16));
+    }
+}
+
+// NT tiles of eight tokens.  A warp takes every eighth block of k, two at a time, with all
+// their loads on the way before the first is used.
+template <int NT>
+__global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearArgs a) {
+    constexpr int U = 2;
+    __shared__ float part[LF_WARPS][NT * 8][LF_ROWS];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int n0 = (int)blockIdx.x * LF_ROWS, kb_all = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
+    const uint8_t* w0 = a.w + (size_t)min(n0 + g, a.N - 1) * a.K;
+    const uint8_t* w1 = a.w + (size_t)min(n0 + g + 8, a.N - 1) * a.K;
+    const float* ws = a.ws + (size_t)(n0 / FP8_BLOCK) * kb_all;
+    float z[NT][4] = {};
+    for (int kb0 = warp; kb0 < kb_all; kb0 += U * LF_WARPS) {
+        uint4 wa[U][2], wb[U][2], x[U][2][NT];
+        float s[U], xs[U][NT][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int kb = kb0 + u * LF_WARPS;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kb * FP8_BLOCK + h * 64 + c * 16;
+                const bool in = k < a.K;
+                wa[u][h] = in ? ld_stream(w0 + k) : make_uint4(0, 0, 0, 0);
+                wb[u][h] = in ? ld_stream(w1 + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    x[u][h][j] = in ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)min(8 * j + g, a.T - 1) * a.K + k))
+                                    : make_uint4(0, 0, 0, 0);
+            }
+            const int at = min(kb, kb_all - 1);
+            s[u] = __ldg(ws + at);
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) xs[u][j][i] = __ldg(a.xs + (size_t)min(8 * j + 2 * c + i, a.T - 1) * kb_all + at);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (kb0 + u * LF_WARPS >= kb_all) break;          // the same for the whole warp
+            float d[NT][4] = {};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[8], q[8], r[8];
+                widen16(wa[u][h], p);
+                widen16(wb[u][h], q);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    widen16(x[u][h][j], r);
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) mma_f16(d[j], p[i], q[i], p[i + 1], q[i + 1], r[i], r[i + 1]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) z[j][i] = fmaf(d[j][i], s[u] * xs[u][j][i & 1], z[j][i]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][8 * j + 2 * c + (i & 1)][g + 8 * (i >> 1)] = z[j][i];
+    __syncthreads();
+    // the warps' sums in their order
+    for (int i = (int)threadIdx.x; i < LF_ROWS * a.T; i += LF_WARPS * 32) {
+        const int t = i / LF_ROWS, f = i % LF_ROWS, n = n0 + f;
+        if (n >= a.N) continue;
+        float v[1] = {0.f};
+#pragma unroll
+        for (int w = 0; w < LF_WARPS; ++w) v[0] += part[w][t][f];
+        if (a.bias) v[0] += a.bias[n];
+        activate(v, a.act);
+        put_one(a, t, n, v[0]);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st) {
+    const dim3 grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS));
+    return a.T <= 8 ? launch_pdl(linear_few_kernel<1>, grid, dim3(LF_WARPS * 32), 0, st, a)
+                    : launch_pdl(linear_few_kernel<2>, grid, dim3(LF_WARPS * 32), 0, st, a);
+}
+
+}  // namespace qmoe

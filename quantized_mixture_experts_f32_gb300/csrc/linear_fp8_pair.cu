@@ -34,12 +34,6 @@ struct PairScales {
     __align__(16) float bias[LP_SLOTS][LP_TILE]; // of the tile's features, with its first group
 };
 
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    return a;
-}
-
 // a copy into this CTA whose bytes count on a barrier of the pair's first
 __device__ __forceinline__ void tma_load_pair(uint32_t one, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
     asm volatile(
