@@ -31,15 +31,15 @@ __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&h)[8]) {
     }
 }
 
-// NT tiles of eight tokens.  A warp takes every eighth block of k, two at a time, with all
+// NT tiles of eight tokens.  A warp takes every eighth block of k, U at a time, with all
 // their loads on the way before the first is used.
-template <int NT>
+template <int NT, int U>
 __global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearArgs a) {
-    constexpr int U = 2;
     __shared__ float part[LF_WARPS][NT * 8][LF_ROWS];
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int t0 = (int)blockIdx.y * 8 * NT;                  // this CTA's tokens
     const int n0 = (int)blockIdx.x * LF_ROWS, kb_all = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
     const uint8_t* w0 = a.w + (size_t)min(n0 + g, a.N - 1) * a.K;
     const uint8_t* w1 = a.w + (size_t)min(n0 + g + 8, a.N - 1) * a.K;
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearA
                 wb[u][h] = in ? ld_stream(w1 + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
-                    x[u][h][j] = in ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)min(8 * j + g, a.T - 1) * a.K + k))
+                    x[u][h][j] = in ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)min(t0 + 8 * j + g, a.T - 1) * a.K + k))
                                     : make_uint4(0, 0, 0, 0);
             }
             const int at = min(kb, kb_all - 1);
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearA
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) xs[u][j][i] = __ldg(a.xs + (size_t)min(8 * j + 2 * c + i, a.T - 1) * kb_all + at);
+                for (int i = 0; i < 2; ++i) xs[u][j][i] = __ldg(a.xs + (size_t)min(t0 + 8 * j + 2 * c + i, a.T - 1) * kb_all + at);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -97,7 +97,8 @@ __global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearA
         for (int i = 0; i < 4; ++i) part[warp][8 * j + 2 * c + (i & 1)][g + 8 * (i >> 1)] = z[j][i];
     __syncthreads();
     // the warps' sums in their order
-    for (int i = (int)threadIdx.x; i < LF_ROWS * a.T; i += LF_WARPS * 32) {
+    const int rows = min(8 * NT, a.T - t0);
+    for (int i = (int)threadIdx.x; i < LF_ROWS * rows; i += LF_WARPS * 32) {
         const int t = i / LF_ROWS, f = i % LF_ROWS, n = n0 + f;
         if (n >= a.N) continue;
         float v[1] = {0.f};
@@ -105,16 +106,19 @@ __global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearA
         for (int w = 0; w < LF_WARPS; ++w) v[0] += part[w][t][f];
         if (a.bias) v[0] += a.bias[n];
         activate(v, a.act);
-        put_one(a, t, n, v[0]);
+        put_one(a, t0 + t, n, v[0]);
     }
 }
 
 }  // namespace
 
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st) {
-    const dim3 grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS));
-    return a.T <= 8 ? launch_pdl(linear_few_kernel<1>, grid, dim3(LF_WARPS * 32), 0, st, a)
-                    : launch_pdl(linear_few_kernel<2>, grid, dim3(LF_WARPS * 32), 0, st, a);
+    const unsigned ctas = (unsigned)((a.N + LF_ROWS - 1) / LF_ROWS);
+    const dim3 block(LF_WARPS * 32);
+    if (a.T <= 8) return launch_pdl(linear_few_kernel<1, 2>, dim3(ctas), block, 0, st, a);
+    if (a.T <= 16) return launch_pdl(linear_few_kernel<2, 2>, dim3(ctas), block, 0, st, a);
+    if (a.T <= 32) return launch_pdl(linear_few_kernel<4, 1>, dim3(ctas), block, 0, st, a);
+    return launch_pdl(linear_few_kernel<8, 1>, dim3(ctas, (unsigned)((a.T + 63) / 64)), block, 0, st, a);
 }
 
 }  // namespace qmoe

@@ -158,9 +158,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
         }
         if (!go) *failed = 1;
-        // copies in flight have landed before the pair ends (they count in the first CTA)
-        if (rank == 0)
-            for (int i = left > STAGES ? left - STAGES : 0; i < left; ++i) warp_wait(&bars.full[i % STAGES], (i / STAGES) & 1);
+        // before the pair ends copies in flight have landed (they count in the first CTA), and the
+        // last arrivals of products, which come to both
+        for (int i = left > STAGES ? left - STAGES : 0; i < left; ++i) {
+            if (rank == 0) warp_wait(&bars.full[i % STAGES], (i / STAGES) & 1);
+            if (go) warp_wait(&bars.empty[i % STAGES], (i / STAGES) & 1);
+        }
     } else if (warp == LP_EW + 1) {
         // ---- products of both
         if (rank == 0) {
