@@ -14,10 +14,10 @@ bool tensor_map_rows(CUtensorMap* m, const void* base, int t, uint64_t cols, uin
 
 // linear_fp8_pair.cu
 cudaError_t linear_pair_prepare();
-cudaError_t launch_linear_pair(const LinearArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int num_sms, cudaStream_t st);   // tile 128 or 256 features
 
-// linear_fp8_few.cu: up to LN_FEW tokens
-constexpr int LN_FEW = 16;
+// linear_fp8_few.cu: a group of at most 64 tokens at a time
+constexpr int LF_ROWS = 16;                   // features of a CTA
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st);
 
 __device__ __forceinline__ float relu(float z) { return z < 0.f ? 0.f : z; }                 // NaN stays

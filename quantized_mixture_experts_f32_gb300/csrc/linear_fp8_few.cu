@@ -13,7 +13,6 @@ namespace qmoe {
 namespace {
 
 constexpr int LF_WARPS = 8;                   // of a CTA: 16 features, k dealt between them
-constexpr int LF_ROWS = 16;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -34,7 +33,7 @@ __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&h)[8]) {
 // NT tiles of eight tokens.  A warp takes every eighth block of k, U at a time, with all
 // their loads on the way before the first is used.
 template <int NT, int U>
-__global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : NT <= 4 ? 2 : 1) linear_few_kernel(const LinearArgs a) {
     __shared__ float part[LF_WARPS][NT * 8][LF_ROWS];
     pdl_wait();
     pdl_launch_dependents();
@@ -103,7 +102,7 @@ __global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearA
         if (n >= a.N) continue;
         float v[1] = {0.f};
 #pragma unroll
-        for (int w = 0; w < LF_WARPS; ++w) v[0] += part[w][t][f];
+        for (int k = 0; k < LF_WARPS; ++k) v[0] += part[k][t][f];
         if (a.bias) v[0] += a.bias[n];
         activate(v, a.act);
         put_one(a, t0 + t, n, v[0]);
@@ -113,12 +112,11 @@ __global__ void __launch_bounds__(LF_WARPS * 32) linear_few_kernel(const LinearA
 }  // namespace
 
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st) {
-    const unsigned ctas = (unsigned)((a.N + LF_ROWS - 1) / LF_ROWS);
-    const dim3 block(LF_WARPS * 32);
-    if (a.T <= 8) return launch_pdl(linear_few_kernel<1, 2>, dim3(ctas), block, 0, st, a);
-    if (a.T <= 16) return launch_pdl(linear_few_kernel<2, 2>, dim3(ctas), block, 0, st, a);
-    if (a.T <= 32) return launch_pdl(linear_few_kernel<4, 1>, dim3(ctas), block, 0, st, a);
-    return launch_pdl(linear_few_kernel<8, 1>, dim3(ctas, (unsigned)((a.T + 63) / 64)), block, 0, st, a);
+    const dim3 block(LF_WARPS * 32), grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS), (unsigned)((a.T + 63) / 64));
+    return a.T <= 8    ? launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a)
+           : a.T <= 16 ? launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a)
+           : a.T <= 32 ? launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a)
+                       : launch_pdl(linear_few_kernel<8, 1>, grid, block, 0, st, a);
 }
 
 }  // namespace qmoe

@@ -15,15 +15,14 @@ namespace qmoe {
 
 namespace {
 
-constexpr int LP_EW = 16, LP_EPI = LP_EW * 32, LP_THREADS = LP_EPI + 128;
-constexpr int LP_TILE = 256;                  // tokens, and features, of a pair's tile
+constexpr int LP_TOKENS = 256;                // of a pair's tile
 constexpr int LP_COLS = 64;                   // features of a thread
-constexpr int LP_STAGE = 2 * 128 * 128;       // x and W rows of a block, of one CTA
-constexpr int LP_STAGES_MAX = 5;
+constexpr int LP_STAGES_MAX = 6;
+constexpr int LP_EW_MAX = 16;
 constexpr int LP_GROUP = 4, LP_SLOTS = 3;     // blocks of k whose scales are staged together, such groups
 
 struct PairBars {
-    uint64_t full[LP_STAGES_MAX], empty[LP_STAGES_MAX], tfull[2], tempty[2], sfull[LP_SLOTS], sempty[LP_SLOTS], res[LP_EW];
+    uint64_t full[LP_STAGES_MAX], empty[LP_STAGES_MAX], tfull[4], tempty[4], sfull[LP_SLOTS], sempty[LP_SLOTS], res[LP_EW_MAX];
     uint32_t tmem;
     int failed;
 };
@@ -31,7 +30,7 @@ struct PairBars {
 struct PairScales {
     float x[LP_SLOTS][LP_GROUP][128];         // of the CTA's tokens
     float w[LP_SLOTS][2][LP_GROUP];           // of the tile's two blocks of features
-    __align__(16) float bias[LP_SLOTS][LP_TILE]; // of the tile's features, with its first group
+    __align__(16) float bias[LP_SLOTS][256];  // of the tile's features, with its first group
 };
 
 // a copy into this CTA whose bytes count on a barrier of the pair's first
@@ -77,29 +76,33 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
 }
 __device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-// Out types: a warp's 64 features of 32 tokens lie in boxes of 32 rows of 128 bytes.
-template <int OUT>
-struct PairOut {
+// A variant: TILE features a pair's tile (256, or 128), OUT's type.  A warp's 64 features of
+// 32 tokens lie in boxes of 32 rows of 128 bytes.
+template <int OUT, int TILE>
+struct PairTile {
+    static constexpr int EW = TILE / 16, EPI = EW * 32, THREADS = EPI + 128;
+    static constexpr int TB = 512 / TILE;                     // products in TMEM
+    static constexpr int STAGE = 128 * 128 + TILE / 2 * 128;  // x and W rows of a block, of one CTA
     static constexpr int SIZE = OUT == KV4_F32 ? 4 : 2;
     static constexpr int BOXES = LP_COLS * SIZE / 128, BOX_COLS = 128 / SIZE;
     static constexpr int E = 16 / SIZE;                       // elements of 16 bytes
     static constexpr int BUF = 4096;                          // a warp's, for one box after the other
-    static constexpr int STAGES = 4;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * LP_STAGE + LP_EW * BUF;
+    static constexpr int STAGES = TILE == 256 ? 4 : 6;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + EW * BUF;
 };
 
-template <int OUT, int ACT>
-__global__ void __launch_bounds__(LP_THREADS, 1)
+template <int OUT, int ACT, int TILE>
+__global__ void __launch_bounds__(PairTile<OUT, TILE>::THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                    const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr, const LinearArgs a, int tiles_n,
                    int tiles) {
-    using O = PairOut<OUT>;
+    using O = PairTile<OUT, TILE>;
     constexpr int STAGES = O::STAGES;
     extern __shared__ uint8_t dyn[];
     __shared__ PairBars bars;
     __shared__ PairScales sc;
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
-    uint8_t* bufs = ring + (size_t)STAGES * LP_STAGE;
+    uint8_t* bufs = ring + (size_t)STAGES * O::STAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)blockIdx.x & 1, first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
     const int kb_all = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
@@ -109,20 +112,20 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             mbar_init(&bars.full[i], 1);
             mbar_init(&bars.empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < O::TB; ++i) {
             mbar_init(&bars.tfull[i], 1);
-            mbar_init(&bars.tempty[i], 2 * LP_EW);
+            mbar_init(&bars.tempty[i], 2 * O::EW);
         }
         for (int i = 0; i < LP_SLOTS; ++i) {
             mbar_init(&bars.sfull[i], 2);
-            mbar_init(&bars.sempty[i], LP_EW);
+            mbar_init(&bars.sempty[i], O::EW);
         }
-        for (int i = 0; i < LP_EW; ++i) mbar_init(&bars.res[i], 1);
+        for (int i = 0; i < O::EW; ++i) mbar_init(&bars.res[i], 1);
         bars.failed = 0;
         fence_barrier_init();
     }
     pdl_wait();
-    if (warp == LP_EW + 1) {
+    if (warp == O::EW + 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&bars.tmem)), "r"(512u)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -135,18 +138,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     const uint32_t tmem = bars.tmem;
     volatile int* failed = &bars.failed;
 
-    if (warp == LP_EW) {
+    if (warp == O::EW) {
         // ---- copies
         const uint32_t one = elected(), ring0 = uniform(smem_u32(ring)), full0 = uniform(cluster_addr(&bars.full[0], 0));
         int st = 0, fresh = 1, phase = 1, left = 0;           // stage, whether never used, parity of its last emptying
         bool go = true;
         for (int tile = first; tile < tiles && go; tile += step) {
-            const int t0 = tile / tiles_n * LP_TILE + rank * 128, n0 = tile % tiles_n * LP_TILE + rank * 128;
+            const int t0 = tile / tiles_n * LP_TOKENS + rank * 128, n0 = tile % tiles_n * TILE + rank * (TILE / 2);
             for (int kb = 0; kb < kb_all; ++kb) {
                 go = fresh || warp_wait(&bars.empty[st], phase);
                 if (!go) break;
-                const uint32_t to = ring0 + st * LP_STAGE, bar = full0 + 8 * st;
-                if (rank == 0 && one) mbar_arrive_expect_tx(&bars.full[st], 2 * LP_STAGE);
+                const uint32_t to = ring0 + st * O::STAGE, bar = full0 + 8 * st;
+                if (rank == 0 && one) mbar_arrive_expect_tx(&bars.full[st], 2 * O::STAGE);
                 tma_load_pair(one, to, &mx, kb * FP8_BLOCK, t0, bar);
                 tma_load_pair(one, to + 128 * 128, &mw, kb * FP8_BLOCK, n0, bar);
                 ++left;
@@ -164,22 +167,22 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             if (rank == 0) warp_wait(&bars.full[i % STAGES], (i / STAGES) & 1);
             if (go) warp_wait(&bars.empty[i % STAGES], (i / STAGES) & 1);
         }
-    } else if (warp == LP_EW + 1) {
+    } else if (warp == O::EW + 1) {
         // ---- products of both
         if (rank == 0) {
             const uint32_t one = elected(), tm = uniform(tmem), ring0 = uniform(smem_u32(ring));
             const uint32_t high = (uint32_t)(umma_sdesc(0) >> 32), d0 = (uint32_t)umma_sdesc(ring0);
             const uint32_t tfull0 = uniform(smem_u32(&bars.tfull[0])), empty0 = uniform(smem_u32(&bars.empty[0]));
-            constexpr uint32_t idesc = umma_idesc_f16(LP_TILE, LP_TILE);  // E4M3 has F16's type number
+            constexpr uint32_t idesc = umma_idesc_f16(LP_TOKENS, TILE);  // E4M3 has F16's type number
             int st = 0, phase = 0, g = 0;
             bool go = true;
             for (int tile = first; tile < tiles && go; tile += step) {
                 for (int kb = 0; kb < kb_all; ++kb, ++g) {
-                    const int tb = g & 1;
-                    go = warp_wait(&bars.full[st], phase) && (g < 2 || warp_wait(&bars.tempty[tb], (g / 2 - 1) & 1));
+                    const int tb = g % O::TB;
+                    go = warp_wait(&bars.full[st], phase) && (g < O::TB || warp_wait(&bars.tempty[tb], (g / O::TB - 1) & 1));
                     if (!go) break;
                     tc_fence_after();
-                    const uint32_t da = d0 + st * (LP_STAGE >> 4), db = da + (128 * 128 >> 4), d = tm + tb * LP_TILE;
+                    const uint32_t da = d0 + st * (O::STAGE >> 4), db = da + (128 * 128 >> 4), d = tm + tb * TILE;
                     umma_f8_pair<0>(one, d, da, db, high, idesc);
                     umma_f8_pair<1>(one, d, da + 2, db + 2, high, idesc);
                     umma_f8_pair<1>(one, d, da + 4, db + 4, high, idesc);
@@ -194,16 +197,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
             if (!go) {
                 *failed = 1;
-                if (g > 0) warp_wait(&bars.tfull[(g - 1) & 1], ((g - 1) / 2) & 1);   // products in flight
+                if (g > 0) warp_wait(&bars.tfull[(g - 1) % O::TB], ((g - 1) / O::TB) & 1);   // products in flight
             }
         }
-    } else if (warp >= LP_EW + 2) {
+    } else if (warp >= O::EW + 2) {
         // ---- scales: two warps, 64 tokens each
-        const int w2 = warp - LP_EW - 2, blocks_n = (a.N + FP8_BLOCK - 1) / FP8_BLOCK;
+        const int w2 = warp - O::EW - 2, blocks_n = (a.N + FP8_BLOCK - 1) / FP8_BLOCK;
         const bool quads = kb_all % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15) == 0;
         int gr = 0;
         for (int tile = first; tile < tiles && !*failed; tile += step) {
-            const int t0 = tile / tiles_n * LP_TILE + rank * 128 + w2 * 64 + lane, nb = tile % tiles_n * 2;
+            const int t0 = tile / tiles_n * LP_TOKENS + rank * 128 + w2 * 64 + lane, nb = tile % tiles_n * (TILE / 128);
             for (int kb = 0; kb < kb_all; kb += LP_GROUP, ++gr) {
                 float4 v[2];
 #pragma unroll
@@ -217,11 +220,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 float w = 0.f;
                 if (w2 == 0 && lane < 2 * LP_GROUP)
                     w = __ldg(a.ws + (size_t)min(nb + lane / LP_GROUP, blocks_n - 1) * kb_all + min(kb + lane % LP_GROUP, kb_all - 1));
-                float b4[4];
+                float b4[TILE / 64];
                 if (kb == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        b4[i] = a.bias ? __ldg(a.bias + min(tile % tiles_n * LP_TILE + w2 * 128 + 32 * i + lane, a.N - 1)) : 0.f;
+                    for (int i = 0; i < TILE / 64; ++i)
+                        b4[i] = a.bias ? __ldg(a.bias + min(tile % tiles_n * TILE + w2 * (TILE / 2) + 32 * i + lane, a.N - 1)) : 0.f;
                 }
                 const int slot = gr % LP_SLOTS;
                 if (gr >= LP_SLOTS && !mbar_wait(&bars.sempty[slot], (gr / LP_SLOTS - 1) & 1)) *failed = 1;
@@ -235,7 +238,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 }
                 if (kb == 0) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sc.bias[slot][w2 * 128 + 32 * i + lane] = b4[i];
+                    for (int i = 0; i < TILE / 64; ++i) sc.bias[slot][w2 * (TILE / 2) + 32 * i + lane] = b4[i];
                 }
                 if (w2 == 0 && lane < 2 * LP_GROUP) sc.w[slot][lane / LP_GROUP][lane % LP_GROUP] = w;
                 __syncwarp();
@@ -248,7 +251,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         // the end without waiting or writing, so that the barriers keep their counts.
         const int c0 = (warp >> 2) * LP_COLS;
         const uint32_t tcol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
-        const uint32_t empty0 = cluster_addr(&bars.tempty[0], 0), empty1 = cluster_addr(&bars.tempty[1], 0);
+        const uint32_t empty0 = cluster_addr(&bars.tempty[0], 0);
         uint8_t* buf = bufs + warp * O::BUF;
         // stores by TMA end on whole 16 bytes, whatever the map says: the features behind go one by one
         const int whole = a.N / O::E * O::E;
@@ -256,8 +259,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         const int my = (warp & 3) * 32 + lane, wb = c0 / FP8_BLOCK;
         bool ok = true;
         for (int tile = first; tile < tiles; tile += step) {
-            const int tw = tile / tiles_n * LP_TILE + rank * 128 + (warp & 3) * 32, t = tw + lane;   // the warp's rows, this one
-            const int n0 = tile % tiles_n * LP_TILE + c0;
+            const int tw = tile / tiles_n * LP_TOKENS + rank * 128 + (warp & 3) * 32, t = tw + lane;   // the warp's rows, this one
+            const int n0 = tile % tiles_n * TILE + c0;
             const bool any = tw < a.T && n0 < a.N;            // the warp has something to write
             if (a.res && any && ok && lane == 0) {
                 tma_stores_read();
@@ -280,14 +283,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     }
                 }
                 const float s = sc.x[slot][in][my] * sc.w[slot][wb][in];
-                const int tb = g & 1;
-                if (ok && !mbar_wait(&bars.tfull[tb], (g / 2) & 1)) {
+                const int tb = g % O::TB;
+                if (ok && !mbar_wait(&bars.tfull[tb], (g / O::TB) & 1)) {
                     *failed = 1;
                     ok = false;
                 }
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t from = tcol + tb * LP_TILE;
+                const uint32_t from = tcol + tb * TILE;
                 const bool last = in == LP_GROUP - 1 || kb == kb_all - 1;
                 uint32_t r[2][16];
                 tmem_fetch16(from, r[0]);
@@ -299,7 +302,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            arrive_cluster(tb ? empty1 : empty0);
+                            arrive_cluster(empty0 + 8 * tb);
                             if (last) mbar_arrive(&bars.sempty[slot]);
                         }
                     }
@@ -367,24 +370,24 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     __syncthreads();
     if (threadIdx.x == 0 && *failed) atomicExch(a.status, ST_TIMEOUT);
     cluster_sync();                                           // neither works in the other's memory any more
-    if (warp == LP_EW + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+    if (warp == O::EW + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <int OUT, int ACT>
+template <int OUT, int ACT, int TILE>
 cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    using O = PairOut<OUT>;
+    using O = PairTile<OUT, TILE>;
     CUtensorMap mx, mw, mo, mr;
-    if (!tensor_map_codes(&mx, a.x, (uint64_t)a.K, (uint64_t)a.T, 128) || !tensor_map_codes(&mw, a.w, (uint64_t)a.K, (uint64_t)a.N, 128) ||
+    if (!tensor_map_codes(&mx, a.x, (uint64_t)a.K, (uint64_t)a.T, 128) || !tensor_map_codes(&mw, a.w, (uint64_t)a.K, (uint64_t)a.N, TILE / 2) ||
         !tensor_map_rows(&mo, a.out, OUT, (uint64_t)(a.N < O::E ? O::E : a.N / O::E * O::E), (uint64_t)a.T, (uint64_t)a.out_stride, 32) ||
         !tensor_map_rows(&mr, a.res ? a.res : a.out, OUT, (uint64_t)a.N, (uint64_t)a.T, (uint64_t)(a.res ? a.res_stride : a.out_stride), 32))
         return cudaErrorInvalidValue;
-    const int tiles_n = (a.N + LP_TILE - 1) / LP_TILE;
-    const int64_t tiles = (int64_t)tiles_n * ((a.T + LP_TILE - 1) / LP_TILE);
+    const int tiles_n = (a.N + TILE - 1) / TILE;
+    const int64_t tiles = (int64_t)tiles_n * ((a.T + LP_TOKENS - 1) / LP_TOKENS);
     if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
     const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
-    cfg.blockDim = dim3(LP_THREADS);
+    cfg.blockDim = dim3(O::THREADS);
     cfg.dynamicSmemBytes = O::SMEM;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -396,21 +399,27 @@ cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OUT, ACT>, mx, mw, mo, mr, a, tiles_n, (int)tiles);
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OUT, ACT, TILE>, mx, mw, mo, mr, a, tiles_n, (int)tiles);
 }
 
 // the activations' code is long, and would be fetched past for every tile without one
 template <int OUT>
-cudaError_t launch_type(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    return a.act == ACT_NONE ? launch_out<OUT, 0>(a, num_sms, st) : launch_out<OUT, 1>(a, num_sms, st);
+cudaError_t launch_type(const LinearArgs& a, int tile, int num_sms, cudaStream_t st) {
+    if (tile == 256) return a.act == ACT_NONE ? launch_out<OUT, 0, 256>(a, num_sms, st) : launch_out<OUT, 1, 256>(a, num_sms, st);
+    return a.act == ACT_NONE ? launch_out<OUT, 0, 128>(a, num_sms, st) : launch_out<OUT, 1, 128>(a, num_sms, st);
+}
+
+template <int OUT, int TILE>
+cudaError_t prepare_tile() {
+    constexpr int smem = (int)PairTile<OUT, TILE>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<OUT, 0, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e == cudaSuccess ? cudaFuncSetAttribute(linear_pair_kernel<OUT, 1, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : e;
 }
 
 template <int OUT>
 cudaError_t prepare_out() {
-    cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<OUT, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PairOut<OUT>::SMEM);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(linear_pair_kernel<OUT, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PairOut<OUT>::SMEM);
-    return e;
+    const cudaError_t e = prepare_tile<OUT, 256>();
+    return e == cudaSuccess ? prepare_tile<OUT, 128>() : e;
 }
 
 }  // namespace
@@ -422,10 +431,10 @@ cudaError_t linear_pair_prepare() {
     return e;
 }
 
-cudaError_t launch_linear_pair(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    return a.out_t == KV4_F32   ? launch_type<KV4_F32>(a, num_sms, st)
-           : a.out_t == KV4_F16 ? launch_type<KV4_F16>(a, num_sms, st)
-                                : launch_type<KV4_BF16>(a, num_sms, st);
+cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int num_sms, cudaStream_t st) {
+    return a.out_t == KV4_F32   ? launch_type<KV4_F32>(a, tile, num_sms, st)
+           : a.out_t == KV4_F16 ? launch_type<KV4_F16>(a, tile, num_sms, st)
+                                : launch_type<KV4_BF16>(a, tile, num_sms, st);
 }
 
 }  // namespace qmoe
