@@ -114,7 +114,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         }
         for (int i = 0; i < O::TB; ++i) {
             mbar_init(&bars.tfull[i], 1);
-            mbar_init(&bars.tempty[i], 2 * O::EW);
+            mbar_init(&bars.tempty[i], O::EW + (rank == 0));
         }
         for (int i = 0; i < LP_SLOTS; ++i) {
             mbar_init(&bars.sfull[i], 2);
@@ -199,6 +199,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 *failed = 1;
                 if (g > 0) warp_wait(&bars.tfull[(g - 1) % O::TB], ((g - 1) / O::TB) & 1);   // products in flight
             }
+        } else {
+            // the second CTA's warps have read a product: one arrival tells the first
+            const uint32_t e0 = cluster_addr(&bars.tempty[0], 0);
+            int g = 0;
+            bool go = true;
+            for (int tile = first; tile < tiles && go; tile += step)
+                for (int kb = 0; kb < kb_all && go; ++kb, ++g) {
+                    go = warp_wait(&bars.tempty[g % O::TB], (g / O::TB) & 1);
+                    if (go && lane == 0) arrive_cluster(e0 + 8 * (g % O::TB));
+                }
         }
     } else if (warp >= O::EW + 2) {
         // ---- scales: two warps, 64 tokens each
@@ -206,7 +216,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         const bool quads = kb_all % 4 == 0 && (reinterpret_cast<uintptr_t>(a.xs) & 15) == 0;
         int gr = 0;
         for (int tile = first; tile < tiles && !*failed; tile += step) {
-            const int t0 = tile / tiles_n * LP_TOKENS + rank * 128 + w2 * 64 + lane, nb = tile % tiles_n * (TILE / 128);
+            const int t0 = tile / tiles_n * LP_TOKENS + rank * 128 + w2 * 64 + lane, nb = tile % tiles_n * TILE / 128;
             for (int kb = 0; kb < kb_all; kb += LP_GROUP, ++gr) {
                 float4 v[2];
 #pragma unroll
@@ -251,7 +261,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         // the end without waiting or writing, so that the barriers keep their counts.
         const int c0 = (warp >> 2) * LP_COLS;
         const uint32_t tcol = tmem + ((uint32_t)((warp & 3) * 32) << 16) + c0;
-        const uint32_t empty0 = cluster_addr(&bars.tempty[0], 0);
         uint8_t* buf = bufs + warp * O::BUF;
         // stores by TMA end on whole 16 bytes, whatever the map says: the features behind go one by one
         const int whole = a.N / O::E * O::E;
@@ -302,7 +311,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) {
-                            arrive_cluster(empty0 + 8 * tb);
+                            arrive_relaxed(&bars.tempty[tb]);
                             if (last) mbar_arrive(&bars.sempty[slot]);
                         }
                     }
