@@ -520,9 +520,10 @@ typedef enum {
  *  out     : rows of out_t (F32, F16, BF16), out_stride apart, at least out_features.
  *  in_features a multiple of 16 up to 2^20, n_tokens 1..2^24, out_features 1..2^24.
  * Products of codes are accumulated in fp32 by blocks of 128, each block's sum scaled
- * and added in fp32, in an order that the sizes alone decide.  The product of a
+ * and added in fp32, in an order that the sizes and the GPU decide.  The product of a
  * token's and a block's scale has to be in fp32's range.  Only the out_features first
- * elements of a row of out are written. */
+ * elements of a row of out are written.  A bounded wait that runs out sets
+ * QMOE_ERR_TIMEOUT, the call's results are then unspecified. */
 qmoe_status qmoe_linear_fp8(qmoe_ctx* ctx, const void* x_codes, const float* x_scale, int n_tokens,
                             int in_features, const void* w_codes, const float* w_scale,
                             int out_features, const float* bias, qmoe_act act, const void* residual,

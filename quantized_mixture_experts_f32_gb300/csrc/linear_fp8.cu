@@ -29,7 +29,7 @@ cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st)
     const double few = 2.0 + (a.T <= 32 ? waves(ctas, 2 * num_sms) * (0.3 + 0.11 * kb) : waves(ctas, num_sms) * (0.9 + 0.17 * kb));
     const double p128 = 3.7 + 0.33 * kb * waves(token_tiles * ((a.N + 127) / 128), num_sms / 2);
     const double p256 = 4.7 + 0.52 * kb * waves(token_tiles * ((a.N + 255) / 256), num_sms / 2);
-    if (few <= p128 && few <= p256) return launch_linear_few(a, st);
+    if (few <= p128 && few <= p256 && a.T <= 64 * 65535) return launch_linear_few(a, st);   // a grid's second size
     return launch_linear_pair(a, p128 < p256 ? 128 : 256, num_sms, st);
 }
 

@@ -173,6 +173,9 @@ qmoe_status qmoe_linear_fp8(qmoe_ctx* ctx, const void* x_codes, const float* x_s
     if (s == QMOE_OK) s = check_alias(c, "out and residual", out, out_t, out_stride, residual, out_t, res_stride);
     if (s != QMOE_OK) return s;
     if (out == x_codes || out == w_codes) return fail(c, QMOE_ERR_INVALID_ARG, "out must not overlap the codes");
+    // what a tensor map can hold
+    if (out_stride >= (int64_t)1 << 38 || (residual && res_stride >= (int64_t)1 << 38))
+        return fail(c, QMOE_ERR_SHAPE, "out and residual: strides of 2^38 elements and more are not served");
     qmoe::OnDevice dev(c.device);
     if (dev.e != cudaSuccess) return done(c, dev.e, "device select");
     const qmoe::LinearArgs a{static_cast<const uint8_t*>(x_codes), x_scale, static_cast<const uint8_t*>(w_codes), w_scale,

@@ -1,6 +1,4 @@
 """The 8-bit path's row operators on the GPU against their plain forms in 64 bits."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -17,6 +15,10 @@ EPS = 1e-6
 
 @pytest.fixture(scope="module")
 def q():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
     import quantized_mixture_experts_f32_gb300 as q
     return q
 
@@ -593,7 +595,7 @@ def test_linear_refusals(q, ctx):
                       (INVALID, dict(ot=3)), (MISALIGNED, dict(x=d[0].data_ptr() + 8)), (MISALIGNED, dict(w=d[2].data_ptr() + 1)),
                       (MISALIGNED, dict(b=b.data_ptr() + 2)), (MISALIGNED, dict(xs=d[1].data_ptr() + 2)), (SHAPE, dict(os=32)),
                       (MISALIGNED, dict(os=66)), (MISALIGNED, dict(N=63)), (INVALID, dict(r=out, rs=128)),
-                      (MISALIGNED, dict(r=out.data_ptr() + 4)), (INVALID, dict(o=d[0]))]:
+                      (MISALIGNED, dict(r=out.data_ptr() + 4)), (INVALID, dict(o=d[0])), (SHAPE, dict(os=1 << 38))]:
         refused(q, status, lambda: call(**k))
     call(b=None, r=out)
 
@@ -656,3 +658,138 @@ def test_append_rope_refusals(q, ctx):
     call(q=None, out=None, qn=None)
     assert q.qmoe_kv4_get_status(h) == q.QMOE_OK
     q.qmoe_kv4_destroy(h)
+
+
+# ---------------------------------------------------------------------------- streams, graphs, long strides
+
+LINEAR_PATHS = [(1, 512, 300), (12, 256, 200), (30, 640, 260), (64, 2048, 700), (150, 1024, 2048), (700, 512, 900), (1500, 768, 4096)]
+
+
+@pytest.mark.parametrize("T,K,N", LINEAR_PATHS)
+def test_linear_in_a_graph_follows_its_inputs(q, T, K, N):
+    """Captured once, replayed over other codes and scales: the results of calls of their own."""
+    st = torch.cuda.Stream()
+    ctx = make_ctx(q, st)
+    sets = []
+    for seed in (1, 2):
+        xc, xs, wc, ws = (torch.from_numpy(a).to(dev()) for a in linear_inputs(T, K, N, seed))
+        sets.append((xc, xs, wc, ws))
+    buf = [t.clone() for t in sets[0]]
+    wide = -(-N // 8) * 8
+    out = torch.zeros(T, wide, device=dev())[:, :N]
+    torch.cuda.synchronize()
+
+    def call():
+        q.qmoe_linear_fp8(ctx, buf[0], buf[1], T, K, buf[2], buf[3], N, None, q.ACT["SILU"], None, 0, out, q.QMOE_F32, wide)
+
+    with torch.cuda.stream(st):
+        call()
+        st.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            for _ in range(3):                               # kernels that overlap the ones before
+                call()
+        got = []
+        for s in (sets[1], sets[0], sets[1]):
+            for b, t in zip(buf, s):
+                b.copy_(t)
+            out.fill_(0)
+            g.replay()
+            got.append(out.clone())
+        for s, o in zip((sets[1], sets[0], sets[1]), got):
+            for b, t in zip(buf, s):
+                b.copy_(t)
+            out.fill_(0)
+            call()
+            assert torch.equal(out, o)
+        st.synchronize()
+    assert q.qmoe_get_status(ctx) == q.QMOE_OK
+    q.qmoe_destroy(ctx)
+
+
+def test_two_contexts_on_two_streams(q):
+    """Products, norms and turned rows of two contexts that run at the same time are those of each alone."""
+    T, K, N, dim = 600, 1024, 1300, 2048
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    ctxs = [make_ctx(q, s) for s in streams]
+    rope, _ = make_table(q, ctxs[0], 128, 4000)
+    work = []
+    for i in range(2):
+        d = [torch.from_numpy(a).to(dev()) for a in linear_inputs(T, K, N, 40 + i)]
+        x, pos = rand_rows(3000, dim, "BF16", 50 + i), torch.randint(0, 4000, (3000,), device=dev(), dtype=torch.int32)
+        work.append((d, x, pos, torch.zeros(T, 1304, device=dev())[:, :N], torch.zeros(3000, dim, dtype=torch.uint8, device=dev()),
+                     torch.zeros(3000, dim // 128, device=dev()), torch.zeros(3000, dim, dtype=torch.bfloat16, device=dev())))
+    torch.cuda.synchronize()
+
+    def go(i):
+        d, x, pos, out, codes, scale, turned = work[i]
+        q.qmoe_linear_fp8(ctxs[i], d[0], d[1], T, K, d[2], d[3], N, None, 0, None, 0, out, q.QMOE_F32, 1304)
+        q.qmoe_rmsnorm(ctxs[i], x, q.QMOE_BF16, 0, None, 0, 0, None, None, EPS, 3000, dim, codes, q.QMOE_E4M3, 0, scale)
+        q.qmoe_rope(ctxs[i], rope, x, q.QMOE_BF16, 0, 3000, dim // 128, 128, pos, None, 0.0, turned, 0)
+
+    alone = []
+    for i in range(2):
+        go(i)
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in work[i][3:]])
+        for t in work[i][3:]:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in range(2):
+            go(i)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert q.qmoe_get_status(ctxs[i]) == q.QMOE_OK
+        for a, b in zip(alone[i], work[i][3:]):
+            assert torch.equal(a, b)
+        q.qmoe_destroy(ctxs[i])
+
+
+def test_rows_further_apart_than_32_bits(q, ctx):
+    """Three rows 2^30 + 8 F32 elements apart: offsets past 2^32 bytes, and past 2^31 elements."""
+    stride, dim = (1 << 30) + 8, 128
+    buf = torch.empty(2 * stride + dim, device=dev())
+    x = torch.as_strided(buf, (3, dim), (stride, 1))
+    x.copy_(rand_rows(3, dim, "F32", 60))
+    want_c, want_s = R.quantise8(host(x))
+    codes, scale = torch.empty(3, dim, dtype=torch.uint8, device=dev()), torch.empty(3, 1, device=dev())
+    q.qmoe_fp8_quantize(ctx, x, q.QMOE_F32, stride, 3, dim, codes, scale)
+    assert np.array_equal(host(codes), want_c) and np.array_equal(host(scale), want_s)
+    rope, table = make_table(q, ctx, 64, 100)
+    pos = torch.tensor([3, 99, 50], dtype=torch.int32, device=dev())
+    want = R.rope(host(x).reshape(3, 2, 64), host(table)[host(pos)], 64, "half").reshape(3, dim)
+    q.qmoe_rope(ctx, rope, x, q.QMOE_F32, stride, 3, 2, 64, pos, None, 0.0, x, stride)
+    assert np.array_equal(host(x), want)
+    _, y = R.rmsnorm(host(x), None, None, EPS)
+    q.qmoe_rmsnorm(ctx, x, q.QMOE_F32, stride, None, 0, 0, None, None, EPS, 3, dim, x, q.QMOE_F32, stride, None)
+    assert (np.abs(host(x) - y) <= NORM_ERR * np.abs(y)).all()
+    # products into rows as far apart, from the kernel for few tokens
+    d = [torch.from_numpy(a).to(dev()) for a in linear_inputs(3, 256, 100, 61)]
+    want, size = R.linear(*linear_inputs(3, 256, 100, 61), None, "NONE", host(x)[:, :100])
+    q.qmoe_linear_fp8(ctx, d[0], d[1], 3, 256, d[2], d[3], 100, None, 0, x, stride, x, q.QMOE_F32, stride)
+    assert (np.abs(host(x)[:, :100] - want) <= linear_bound(size, 2, want, 0, "NONE") + 2 * R.U * np.abs(want)).all()
+
+
+def test_linear_rows_far_apart_on_pairs_of_ctas(q, ctx):
+    T, K, N, stride = 300, 128, 40, 1 << 23                 # the last rows' offsets are past 2^31 elements
+    buf = torch.empty((T - 1) * stride + N, dtype=torch.bfloat16, device=dev())
+    out = torch.as_strided(buf, (T, N), (stride, 1))
+    near = torch.empty(T, N, dtype=torch.bfloat16, device=dev())
+    d = [torch.from_numpy(a).to(dev()) for a in linear_inputs(T, K, N, 62)]
+    for o in (out, near):
+        q.qmoe_linear_fp8(ctx, d[0], d[1], T, K, d[2], d[3], N, None, 0, None, 0, o, q.QMOE_BF16, o.stride(0))
+    assert torch.equal(out, near)
+
+
+@pytest.mark.parametrize("T", [3, 20, 50, 300])
+def test_linear_scales_that_are_not_16_byte_aligned(q, ctx, T):
+    K, N = 512, 140
+    xc, xs, wc, ws = linear_inputs(T, K, N, 63)
+    pad = torch.zeros(T * 4 + 1, device=dev())
+    pad[1:] = torch.from_numpy(xs).to(dev()).flatten()
+    d = [torch.from_numpy(a).to(dev()) for a in (xc, wc, ws)]
+    out = torch.empty(T, N, device=dev())
+    q.qmoe_linear_fp8(ctx, d[0], pad.data_ptr() + 4, T, K, d[1], d[2], N, None, 0, None, 0, out, q.QMOE_F32, 0)
+    ref, size = R.linear(xc, xs, wc, ws, None, "NONE", None)
+    assert (np.abs(host(out) - ref) <= linear_bound(size, 4, ref, 0, "NONE")).all()

@@ -1,4 +1,7 @@
 """The plain forms of the row operators against definitions and library functions (CPU)."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -69,3 +72,28 @@ def test_frequencies_by_parts_are_between_plain_and_linear():
 def test_rmsnorm_of_constant_rows():
     h, y = R.rmsnorm(np.full((2, 32), 3.0), np.full((2, 32), -1.0), None, 1e-30)
     assert (h == 2).all() and np.allclose(y, 1, rtol=1e-15)
+
+
+def test_calls_select_their_device_before_they_reach_it():
+    src = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
+                            "quantized_mixture_experts_f32_gb300", "csrc", "rows_api.cu")).read()
+    bodies = {m.group(1): m.group(2) for m in re.finditer(r"^[\w ]+?[ *](\w+)\([^;{]*?\) \{\n(.*?)^\}", src, flags=re.S | re.M)}
+    names = [n for n in bodies if re.search(r"\blaunch_\w+\(", bodies[n])]
+    assert len(names) == 5                     # rmsnorm and quantise share one
+    for n in names:
+        guard = re.search(r"\bOnDevice dev\(\w+\.device\);", bodies[n])
+        assert guard and guard.start() < re.search(r"\blaunch_\w+\(", bodies[n]).start(), n
+
+
+def test_calls_without_a_handle_are_refused():
+    import __graft_entry__
+    __graft_entry__.build()
+    import quantized_mixture_experts_f32_gb300 as q
+    rope = q.make_rope(64, 1e4, 1, 16)
+    assert q.lib.qmoe_rmsnorm(None, 16, 0, 0, None, 0, 0, None, None, 1.0, 1, 16, 16, 0, 0, None) == 1
+    assert q.lib.qmoe_fp8_quantize(None, 16, 0, 0, 1, 16, 16, 16) == 1
+    assert q.lib.qmoe_linear_fp8(None, 16, 16, 1, 16, 16, 16, 1, None, 0, None, 0, 16, 0, 0) == 1
+    assert q.lib.qmoe_rope_table(None, rope) == 1
+    assert q.lib.qmoe_rope(None, rope, 16, 0, 0, 1, 1, 64, 16, None, 1.0, 16, 0) == 1
+    cache = q.make_kv4_cache(16, 16, 16, 16, 16, 16)
+    assert q.lib.qmoe_kv4_append_rope(None, cache, rope, None, 16, 16, 0, 1, 0, 0, 0, 16, 16, None, None, 1.0, None, 0, None, None) == 1
