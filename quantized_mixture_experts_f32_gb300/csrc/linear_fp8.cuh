@@ -16,8 +16,9 @@ bool tensor_map_rows(CUtensorMap* m, const void* base, int t, uint64_t cols, uin
 cudaError_t linear_pair_prepare();
 cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int num_sms, cudaStream_t st);   // tile 128 or 256 features
 
-// linear_fp8_few.cu: a group of at most 64 tokens at a time
-constexpr int LF_ROWS = 16;                   // features of a CTA
+// linear_fp8_few.cu: a CTA takes 16 features of a group of tokens
+constexpr int LF_ROWS = 16;
+inline int linear_few_group(int tokens) { return tokens <= 8 ? 8 : tokens <= 32 ? 16 : 32; }
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st);
 
 __device__ __forceinline__ float relu(float z) { return z < 0.f ? 0.f : z; }                 // NaN stays
@@ -53,21 +54,18 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
 template <int T>
 struct RowType {
     using type = float;
-    using word = float4;                      // four of them
     static __device__ __forceinline__ float load(float v) { return v; }
     static __device__ __forceinline__ float store(float v) { return v; }
 };
 template <>
 struct RowType<KV4_F16> {
     using type = __half;
-    using word = uint2;
     static __device__ __forceinline__ float load(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half store(float v) { return __float2half_rn(v); }
 };
 template <>
 struct RowType<KV4_BF16> {
     using type = __nv_bfloat16;
-    using word = uint2;
     static __device__ __forceinline__ float load(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 store(float v) { return __float2bfloat16_rn(v); }
 };
@@ -118,26 +116,6 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
                    "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 
-// the same of 32
-__device__ __forceinline__ void tmem_fetch(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
-          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-          "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
-                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
-                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-__device__ __forceinline__ void tmem_fetch(uint32_t taddr, uint32_t (&r)[16]) { tmem_fetch16(taddr, r); }
-
 // (x, y) += (a sx, b sy), two roundings in one instruction
 __device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, float sx, float sy) {
     asm("{\n\t.reg .b64 d, v, s;\n\tmov.b64 d, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\tmov.b64 s, {%4, %5};\n\t"
@@ -165,15 +143,9 @@ __device__ __forceinline__ void arrive_relaxed(uint64_t* bar) {
     asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
-    cluster_arrive();
-    cluster_wait();
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
     uint32_t a;

@@ -33,7 +33,7 @@ __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&h)[8]) {
 // NT tiles of eight tokens.  A warp takes every eighth block of k, U at a time, with all
 // their loads on the way before the first is used.
 template <int NT, int U>
-__global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : NT <= 4 ? 2 : 1) linear_few_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : 2) linear_few_kernel(const LinearArgs a) {
     __shared__ float part[LF_WARPS][NT * 8][LF_ROWS];
     pdl_wait();
     pdl_launch_dependents();
@@ -111,12 +111,17 @@ __global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : NT <= 4 ? 2 : 1) 
 
 }  // namespace
 
+// Groups of 16 tokens up to 32, of 32 beyond: more CTAs against W read (from L2) again.
+// In us, groups of 16 / 32 / 64 tokens:
+//   K 4096  N 2048   32 tokens   5.5   5.8   7.6      64 tokens    9.6    8.2    8.0
+//   K 2048  N 5120               7.3   7.4  11.6                  12.2   11.2   12.9
+//   K 2000  N 1003               2.8   3.9   4.8                   3.9    4.1    5.5
 cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st) {
-    const dim3 block(LF_WARPS * 32), grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS), (unsigned)((a.T + 63) / 64));
-    return a.T <= 8    ? launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a)
-           : a.T <= 16 ? launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a)
-           : a.T <= 32 ? launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a)
-                       : launch_pdl(linear_few_kernel<8, 1>, grid, block, 0, st, a);
+    const unsigned group = (unsigned)linear_few_group(a.T);
+    const dim3 block(LF_WARPS * 32), grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS), ((unsigned)a.T + group - 1) / group);
+    return group == 8    ? launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a)
+           : group == 16 ? launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a)
+                         : launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a);
 }
 
 }  // namespace qmoe

@@ -71,30 +71,4 @@ struct RopeFreq {                             // angle of each pair at position 
 };
 cudaError_t launch_rope_rows_table(const RopeFreq& f, int half, int n_pos, double mscale, float* table, cudaStream_t st);
 
-// eight elements of a row of type t from element `at`, a multiple of eight
-__device__ __forceinline__ void rows_load8(const void* p, size_t at, int t, float (&v)[8]) {
-    if (t == KV4_F32) {
-        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(p) + at);
-        const uint4 u[2] = {s[0], s[1]};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            v[4 * i] = __uint_as_float(u[i].x);
-            v[4 * i + 1] = __uint_as_float(u[i].y);
-            v[4 * i + 2] = __uint_as_float(u[i].z);
-            v[4 * i + 3] = __uint_as_float(u[i].w);
-        }
-        return;
-    }
-    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t x = w[i];
-        const float2 f = t == KV4_F16 ? __half22float2(*reinterpret_cast<__half2*>(&x))
-                                      : make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
-    }
-}
-
 }  // namespace qmoe
