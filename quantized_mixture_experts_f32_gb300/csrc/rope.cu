@@ -97,15 +97,15 @@ __device__ __forceinline__ float2 mean_square(const float2 (&f)[8], float p, flo
 }
 
 // 1 / sqrt(mean of the head's squares + eps), rounded to fp32; the head's lanes hold 16
-// elements each.  Where the sum is so far from 1 that the two words leave fp32's range,
-// once more from elements scaled by k.
+// elements each.  Once more from elements scaled by k where the squares or the root's leave fp32's range,
+// or mean and eps are so small that what they lose below it counts.
 template <int LANES>
 __device__ __forceinline__ float head_rms(const float2 (&v)[8], float eps) {
     float rough, k = 1.f;
     float2 m = mean_square<LANES>(v, eps, rough);
-    const bool far = !(rough < 1e30f && (rough > 1e-30f || rough == 0.f) && m.x > 1e-30f);
+    const bool far = !(rough < 1e30f && m.x > 1e-20f && m.x < 1e30f);
     if (__any_sync(0xffffffffu, far)) {
-        k = !far ? 1.f : rough < 1.f ? 0x1p70f : 0x1p-70f;
+        k = !far ? 1.f : m.x < 1.f ? 0x1p70f : 0x1p-70f;
         float2 f[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] = make_float2(v[i].x * k, v[i].y * k);

@@ -405,6 +405,21 @@ def test_rope_norm_of_small_large_and_zero_heads(q, ctx, dtype):
         assert (err <= (R.HALF[dtype] * 1.01 + 6 * R.U) * np.abs(want) + (2.0 ** -25 if dtype == "F16" else 1e-44)).all()
 
 
+@pytest.mark.parametrize("eps", [1e-44, 1e-25, 1e-3, 0.5, 1e10, 3e38])
+def test_rope_norm_of_any_eps(q, ctx, eps):
+    """eps far from 1, heads far from eps: the same inverse root as from 64 bits, to two steps."""
+    rope, _ = make_table(q, ctx, 64, 10)
+    x = rand_rows(8, 64, "F32", 16)
+    for i, f in enumerate((1e-30, 1e-22, 1e-18, 1e-15, 1.0, 1e10, 1e15, 1e18)):
+        x[i] *= f
+    pos = torch.zeros(8, dtype=torch.int32, device=dev())
+    out = torch.empty_like(x)
+    q.qmoe_rope(ctx, rope, x, q.QMOE_F32, 0, 8, 1, 64, pos, torch.ones(64, device=dev()), eps, out, 0)
+    d = host(x).astype(np.float64)
+    want = d / np.sqrt((d * d).mean(-1, keepdims=True) + np.float64(np.float32(eps)))
+    assert (np.abs(host(out) - want) <= 6 * R.U * np.abs(want) + 1e-44).all()
+
+
 # ---------------------------------------------------------------------------- the append
 
 APPEND_CASES = [  # tokens, heads, kv heads, hd, rot, layout, dtype, q norm, k norm, page, padded, with q
