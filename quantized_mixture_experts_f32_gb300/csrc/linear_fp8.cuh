@@ -14,7 +14,9 @@ bool tensor_map_rows(CUtensorMap* m, const void* base, int t, uint64_t cols, uin
 
 // linear_fp8_pair.cu
 cudaError_t linear_pair_prepare();
-cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int num_sms, cudaStream_t st);   // tile 128 or 256 features
+// tiles of 128 or 256 features; of 128, a tile's k may be shared by 2 to 4 pairs, each at least a
+// group of four blocks
+cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int parts, int num_sms, cudaStream_t st);
 
 // linear_fp8_few.cu: a CTA takes 16 features of a group of tokens
 constexpr int LF_ROWS = 16;

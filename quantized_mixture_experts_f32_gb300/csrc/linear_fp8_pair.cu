@@ -7,6 +7,16 @@
 // a block's scale is one number a thread.  Sixteen warps scale the blocks' products into
 // fp32 registers, 64 features a thread, while the next two blocks' products run; rows
 // leave (and residuals come) through shared memory by TMA, a box a warp.
+//
+// 16384 tokens, 2048 x 5120, BF16: 166 us, 2070 TFLOP/s, 1.08 of the measured bf16 rate of a
+// library product, the tensor pipe 44% active.  A scale for each block of 128 takes every
+// product through registers, by barriers between both SMs and with the two products that
+// TMEM holds at this size; products and copies without that take 114 us.
+// Tiles of 128 features (four products in TMEM, 0.33 us a block of k instead of 0.52) are
+// for calls with few tiles; tiles of 64 were slower than either.
+// Where even these leave most SMs idle, two to four pairs in a cluster share a tile's k, and
+// send their sums to one another's shared memory (256 tokens, 4096 x 2048: 14.6 us by one
+// pair a tile, 11.4 by two, 10.6 by three; 16384 x 512: 45, 27, 20, 17 by four).
 #include <limits.h>
 
 #include "linear_fp8.cuh"
@@ -20,6 +30,7 @@ constexpr int LP_COLS = 64;                   // features of a thread
 constexpr int LP_STAGES_MAX = 6;
 constexpr int LP_EW_MAX = 16;
 constexpr int LP_GROUP = 4, LP_SLOTS = 3;     // blocks of k whose scales are staged together, such groups
+constexpr int LP_SLOTS_SUM = 6;               // warps' sums that come from other pairs: 8 warps' from 1 to 3
 
 struct PairBars {
     uint64_t full[LP_STAGES_MAX], empty[LP_STAGES_MAX], tfull[4], tempty[4], sfull[LP_SLOTS], sempty[LP_SLOTS], res[LP_EW_MAX];
@@ -55,12 +66,20 @@ __device__ __forceinline__ void umma_f8_pair(uint32_t one, uint32_t d, uint32_t 
 }
 
 // arrive on the barrier of both CTAs once the products issued so far are done
-__device__ __forceinline__ void umma_commit_pair(uint32_t one, uint32_t bar) {
+template <int MASK>
+__device__ __forceinline__ void umma_commit_mask(uint32_t one, uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
         "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"((uint16_t)3), "r"(one)
+        "h"((uint16_t)MASK), "r"(one)
         : "memory");
+}
+template <bool SPLIT>
+__device__ __forceinline__ void umma_commit_pair(uint32_t one, uint32_t bar, int part) {
+    if (!SPLIT || part == 0) umma_commit_mask<3>(one, bar);
+    else if (part == 1) umma_commit_mask<12>(one, bar);
+    else if (part == 2) umma_commit_mask<48>(one, bar);
+    else umma_commit_mask<192>(one, bar);
 }
 
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
@@ -74,11 +93,21 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int 
                  : "memory");
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+__device__ __forceinline__ float4 load_shared(const float4* at) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(smem_u32(at)) : "memory");
+    return v;
+}
+// into another CTA of the cluster
+__device__ __forceinline__ void store_cluster(uint32_t at, float2 p, float2 q) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(p.x), "f"(p.y), "f"(q.x), "f"(q.y) : "memory");
+}
 __device__ __forceinline__ void tma_stores_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
-// A variant: TILE features a pair's tile (256, or 128), OUT's type.  A warp's 64 features of
-// 32 tokens lie in boxes of 32 rows of 128 bytes.
-template <int OUT, int TILE>
+// A variant: TILE features a pair's tile (256, or 128), OUT's type, SPLIT where 2 to 4 pairs
+// of a cluster share a tile's k.  A warp's 64 features of 32 tokens lie in boxes of 32 rows
+// of 128 bytes.
+template <int OUT, int TILE, bool SPLIT>
 struct PairTile {
     static constexpr int EW = TILE / 16, EPI = EW * 32, THREADS = EPI + 128;
     static constexpr int TB = 512 / TILE;                     // products in TMEM
@@ -87,16 +116,16 @@ struct PairTile {
     static constexpr int BOXES = LP_COLS * SIZE / 128, BOX_COLS = 128 / SIZE;
     static constexpr int E = 16 / SIZE;                       // elements of 16 bytes
     static constexpr int BUF = 4096;                          // a warp's, for one box after the other
-    static constexpr int STAGES = TILE == 256 ? 4 : 6;
-    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + EW * BUF;
+    static constexpr int STAGES = TILE == 256 ? 4 : SPLIT ? 5 : 6;
+    static constexpr size_t SMEM = 1024 + (size_t)STAGES * STAGE + EW * BUF + (SPLIT ? LP_SLOTS_SUM * 32 * LP_COLS * 4 : 0);
 };
 
-template <int OUT, int ACT, int TILE>
-__global__ void __launch_bounds__(PairTile<OUT, TILE>::THREADS, 1)
+template <int OUT, int ACT, int TILE, bool SPLIT>
+__global__ void __launch_bounds__(PairTile<OUT, TILE, SPLIT>::THREADS, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                    const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap mr, const LinearArgs a, int tiles_n,
-                   int tiles) {
-    using O = PairTile<OUT, TILE>;
+                   int tiles, int pairs) {
+    using O = PairTile<OUT, TILE, SPLIT>;
     constexpr int STAGES = O::STAGES;
     extern __shared__ uint8_t dyn[];
     __shared__ PairBars bars;
@@ -104,8 +133,14 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~uintptr_t(1023));
     uint8_t* bufs = ring + (size_t)STAGES * O::STAGE;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)blockIdx.x & 1, first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
-    const int kb_all = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
+    const int rank = (int)blockIdx.x & 1, kb_all = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
+    // a cluster's tiles, and this pair's part of k: whole groups of blocks
+    const int n_parts = SPLIT ? pairs : 1, part = SPLIT ? ((int)blockIdx.x >> 1) % pairs : 0;
+    const int first = ((int)blockIdx.x >> 1) / n_parts, step = ((int)gridDim.x >> 1) / n_parts;
+    const int groups = (kb_all + LP_GROUP - 1) / LP_GROUP;
+    const int kb0 = SPLIT ? groups * part / n_parts * LP_GROUP : 0;
+    const int kb_n = SPLIT ? min(groups * (part + 1) / n_parts * LP_GROUP, kb_all) - kb0 : kb_all;
+    const uint32_t lead = SPLIT ? 2 * part : 0;           // the pair's first CTA in the cluster
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
@@ -140,18 +175,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
 
     if (warp == O::EW) {
         // ---- copies
-        const uint32_t one = elected(), ring0 = uniform(smem_u32(ring)), full0 = uniform(cluster_addr(&bars.full[0], 0));
+        const uint32_t one = elected(), ring0 = uniform(smem_u32(ring)), full0 = uniform(cluster_addr(&bars.full[0], lead));
         int st = 0, fresh = 1, phase = 1, left = 0;           // stage, whether never used, parity of its last emptying
         bool go = true;
         for (int tile = first; tile < tiles && go; tile += step) {
             const int t0 = tile / tiles_n * LP_TOKENS + rank * 128, n0 = tile % tiles_n * TILE + rank * (TILE / 2);
-            for (int kb = 0; kb < kb_all; ++kb) {
+            for (int kb = 0; kb < kb_n; ++kb) {
                 go = fresh || warp_wait(&bars.empty[st], phase);
                 if (!go) break;
                 const uint32_t to = ring0 + st * O::STAGE, bar = full0 + 8 * st;
                 if (rank == 0 && one) mbar_arrive_expect_tx(&bars.full[st], 2 * O::STAGE);
-                tma_load_pair(one, to, &mx, kb * FP8_BLOCK, t0, bar);
-                tma_load_pair(one, to + 128 * 128, &mw, kb * FP8_BLOCK, n0, bar);
+                tma_load_pair(one, to, &mx, (kb0 + kb) * FP8_BLOCK, t0, bar);
+                tma_load_pair(one, to + 128 * 128, &mw, (kb0 + kb) * FP8_BLOCK, n0, bar);
                 ++left;
                 if (++st == STAGES) {
                     st = 0;
@@ -177,7 +212,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             int st = 0, phase = 0, g = 0;
             bool go = true;
             for (int tile = first; tile < tiles && go; tile += step) {
-                for (int kb = 0; kb < kb_all; ++kb, ++g) {
+                for (int kb = 0; kb < kb_n; ++kb, ++g) {
                     const int tb = g % O::TB;
                     go = warp_wait(&bars.full[st], phase) && (g < O::TB || warp_wait(&bars.tempty[tb], (g / O::TB - 1) & 1));
                     if (!go) break;
@@ -187,8 +222,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     umma_f8_pair<1>(one, d, da + 2, db + 2, high, idesc);
                     umma_f8_pair<1>(one, d, da + 4, db + 4, high, idesc);
                     umma_f8_pair<1>(one, d, da + 6, db + 6, high, idesc);
-                    umma_commit_pair(one, tfull0 + 8 * tb);
-                    umma_commit_pair(one, empty0 + 8 * st);
+                    umma_commit_pair<SPLIT>(one, tfull0 + 8 * tb, part);
+                    umma_commit_pair<SPLIT>(one, empty0 + 8 * st, part);
                     if (++st == STAGES) {
                         st = 0;
                         phase ^= 1;
@@ -201,11 +236,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             }
         } else {
             // the second CTA's warps have read a product: one arrival tells the first
-            const uint32_t e0 = cluster_addr(&bars.tempty[0], 0);
+            const uint32_t e0 = cluster_addr(&bars.tempty[0], lead);
             int g = 0;
             bool go = true;
             for (int tile = first; tile < tiles && go; tile += step)
-                for (int kb = 0; kb < kb_all && go; ++kb, ++g) {
+                for (int kb = 0; kb < kb_n && go; ++kb, ++g) {
                     go = warp_wait(&bars.tempty[g % O::TB], (g / O::TB) & 1);
                     if (go && lane == 0) arrive_cluster(e0 + 8 * (g % O::TB));
                 }
@@ -217,24 +252,24 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         int gr = 0;
         for (int tile = first; tile < tiles && !*failed; tile += step) {
             const int t0 = tile / tiles_n * LP_TOKENS + rank * 128 + w2 * 64 + lane, nb = tile % tiles_n * TILE / 128;
-            for (int kb = 0; kb < kb_all; kb += LP_GROUP, ++gr) {
+            for (int kb = 0; kb < kb_n; kb += LP_GROUP, ++gr) {
                 float4 v[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const float* p = a.xs + (size_t)min(t0 + 32 * i, a.T - 1) * kb_all;
+                    const float* p = a.xs + (size_t)min(t0 + 32 * i, a.T - 1) * kb_all + kb0;
                     if (quads) v[i] = __ldg(reinterpret_cast<const float4*>(p + kb));
                     else
-                        v[i] = make_float4(__ldg(p + kb), __ldg(p + min(kb + 1, kb_all - 1)), __ldg(p + min(kb + 2, kb_all - 1)),
-                                           __ldg(p + min(kb + 3, kb_all - 1)));
+                        v[i] = make_float4(__ldg(p + kb), __ldg(p + min(kb + 1, kb_n - 1)), __ldg(p + min(kb + 2, kb_n - 1)),
+                                           __ldg(p + min(kb + 3, kb_n - 1)));
                 }
                 float w = 0.f;
                 if (w2 == 0 && lane < 2 * LP_GROUP)
-                    w = __ldg(a.ws + (size_t)min(nb + lane / LP_GROUP, blocks_n - 1) * kb_all + min(kb + lane % LP_GROUP, kb_all - 1));
+                    w = __ldg(a.ws + (size_t)min(nb + lane / LP_GROUP, blocks_n - 1) * kb_all + kb0 + min(kb + lane % LP_GROUP, kb_n - 1));
                 float b4[TILE / 64];
                 if (kb == 0) {
 #pragma unroll
                     for (int i = 0; i < TILE / 64; ++i)
-                        b4[i] = a.bias ? __ldg(a.bias + min(tile % tiles_n * TILE + w2 * (TILE / 2) + 32 * i + lane, a.N - 1)) : 0.f;
+                        b4[i] = a.bias && part == 0 ? __ldg(a.bias + min(tile % tiles_n * TILE + w2 * (TILE / 2) + 32 * i + lane, a.N - 1)) : 0.f;
                 }
                 const int slot = gr % LP_SLOTS;
                 if (gr >= LP_SLOTS && !mbar_wait(&bars.sempty[slot], (gr / LP_SLOTS - 1) & 1)) *failed = 1;
@@ -270,14 +305,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         for (int tile = first; tile < tiles; tile += step) {
             const int tw = tile / tiles_n * LP_TOKENS + rank * 128 + (warp & 3) * 32, t = tw + lane;   // the warp's rows, this one
             const int n0 = tile % tiles_n * TILE + c0;
-            const bool any = tw < a.T && n0 < a.N;            // the warp has something to write
+            // the warp has something to write; the pairs of a cluster share a tile's results by warps
+            const bool any = tw < a.T && n0 < a.N && warp % n_parts == part;
             if (a.res && any && ok && lane == 0) {
                 tma_stores_read();
                 mbar_arrive_expect_tx(&bars.res[warp], O::BUF);
                 tma_load_2d(buf, &mr, n0, tw, &bars.res[warp]);
             }
             float2 acc[LP_COLS / 2];
-            for (int kb = 0; kb < kb_all; ++kb, ++g) {
+            for (int kb = 0; kb < kb_n; ++kb, ++g) {
                 const int in = kb % LP_GROUP, slot = gr % LP_SLOTS;
                 if (in == 0 && ok && !mbar_wait(&bars.sfull[slot], (gr / LP_SLOTS) & 1)) {
                     *failed = 1;
@@ -300,7 +336,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                 __syncwarp();
                 tc_fence_after();
                 const uint32_t from = tcol + tb * TILE;
-                const bool last = in == LP_GROUP - 1 || kb == kb_all - 1;
+                const bool last = in == LP_GROUP - 1 || kb == kb_n - 1;
                 uint32_t r[2][16];
                 tmem_fetch16(from, r[0]);
 #pragma unroll
@@ -319,6 +355,35 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
                     for (int i = 0; i < 8; ++i) fma2(acc[8 * c + i], r[c & 1][2 * i], r[c & 1][2 * i + 1], s, s);
                 }
                 gr += last;
+            }
+            if (SPLIT) {
+                // (one tile a cluster) a warp's sums go to the pair that has its results, which adds
+                // the others' in their order; slots by the owner's warps, then by senders.  As pairs of
+                // registers and four loads at a time: sums that are moved, or spilled, cost the
+                // loop above 0.05 us a block.
+                const int owner = warp % n_parts;
+                float4* slots = reinterpret_cast<float4*>(bufs + O::EW * O::BUF) + warp / n_parts * (n_parts - 1) * (LP_COLS / 4 * 32) + lane;
+                if (owner != part) {
+                    const uint32_t to = cluster_addr(slots + (part - (part > owner)) * (LP_COLS / 4 * 32), 2 * owner + rank);
+#pragma unroll
+                    for (int i = 0; i < LP_COLS / 4; ++i) store_cluster(to + 512 * i, acc[2 * i], acc[2 * i + 1]);
+                }
+                __syncwarp();
+                cluster_sync();
+#pragma unroll 1
+                for (int p = 0; p < n_parts - 1 && any; ++p) {
+#pragma unroll
+                    for (int i = 0; i < LP_COLS / 4; i += 4) {
+                        float4 v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = load_shared(slots + p * (LP_COLS / 4 * 32) + 32 * (i + j));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            fma2(acc[2 * (i + j)], __float_as_uint(v[j].x), __float_as_uint(v[j].y), 1.f, 1.f);
+                            fma2(acc[2 * (i + j) + 1], __float_as_uint(v[j].z), __float_as_uint(v[j].w), 1.f, 1.f);
+                        }
+                    }
+                }
             }
             ok = __all_sync(0xffffffffu, ok);
             if (!any || !ok) continue;                        // the same for the whole warp
@@ -375,6 +440,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
         if (lane == 0) tma_stores_read();
         __syncwarp();
     }
+    if (SPLIT && warp >= O::EW) {
+        __syncwarp();
+        cluster_sync();                                       // where the sums meet
+    }
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0 && *failed) atomicExch(a.status, ST_TIMEOUT);
@@ -382,9 +451,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
     if (warp == O::EW + 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-template <int OUT, int ACT, int TILE>
-cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    using O = PairTile<OUT, TILE>;
+template <int OUT, int ACT, int TILE, bool SPLIT>
+cudaError_t launch_out(const LinearArgs& a, int parts, int num_sms, cudaStream_t st) {
+    using O = PairTile<OUT, TILE, SPLIT>;
     CUtensorMap mx, mw, mo, mr;
     if (!tensor_map_codes(&mx, a.x, (uint64_t)a.K, (uint64_t)a.T, 128) || !tensor_map_codes(&mw, a.w, (uint64_t)a.K, (uint64_t)a.N, TILE / 2) ||
         !tensor_map_rows(&mo, a.out, OUT, (uint64_t)(a.N < O::E ? O::E : a.N / O::E * O::E), (uint64_t)a.T, (uint64_t)a.out_stride, 32) ||
@@ -392,8 +461,9 @@ cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
         return cudaErrorInvalidValue;
     const int tiles_n = (a.N + TILE - 1) / TILE;
     const int64_t tiles = (int64_t)tiles_n * ((a.T + LP_TOKENS - 1) / LP_TOKENS);
-    if (tiles > INT_MAX / 2) return cudaErrorInvalidValue;
-    const int pairs = (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    if (tiles > INT_MAX / 8) return cudaErrorInvalidValue;
+    if (SPLIT != (parts > 1) || parts > 4 || (SPLIT && a.K <= FP8_BLOCK * LP_GROUP * (parts - 1))) return cudaErrorInvalidValue;
+    const int pairs = SPLIT ? (int)tiles * parts : (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(O::THREADS);
@@ -403,32 +473,38 @@ cudaError_t launch_out(const LinearArgs& a, int num_sms, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.x = 2 * parts;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OUT, ACT, TILE>, mx, mw, mo, mr, a, tiles_n, (int)tiles);
+    return cudaLaunchKernelEx(&cfg, linear_pair_kernel<OUT, ACT, TILE, SPLIT>, mx, mw, mo, mr, a, tiles_n, (int)tiles, parts);
 }
 
 // the activations' code is long, and would be fetched past for every tile without one
+template <int OUT, int TILE, bool SPLIT>
+cudaError_t launch_act(const LinearArgs& a, int parts, int num_sms, cudaStream_t st) {
+    return a.act == ACT_NONE ? launch_out<OUT, 0, TILE, SPLIT>(a, parts, num_sms, st) : launch_out<OUT, 1, TILE, SPLIT>(a, parts, num_sms, st);
+}
 template <int OUT>
-cudaError_t launch_type(const LinearArgs& a, int tile, int num_sms, cudaStream_t st) {
-    if (tile == 256) return a.act == ACT_NONE ? launch_out<OUT, 0, 256>(a, num_sms, st) : launch_out<OUT, 1, 256>(a, num_sms, st);
-    return a.act == ACT_NONE ? launch_out<OUT, 0, 128>(a, num_sms, st) : launch_out<OUT, 1, 128>(a, num_sms, st);
+cudaError_t launch_type(const LinearArgs& a, int tile, int parts, int num_sms, cudaStream_t st) {
+    return tile == 256 ? launch_act<OUT, 256, false>(a, 1, num_sms, st)
+           : parts > 1 ? launch_act<OUT, 128, true>(a, parts, num_sms, st)
+                       : launch_act<OUT, 128, false>(a, 1, num_sms, st);
 }
 
-template <int OUT, int TILE>
+template <int OUT, int TILE, bool SPLIT>
 cudaError_t prepare_tile() {
-    constexpr int smem = (int)PairTile<OUT, TILE>::SMEM;
-    const cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<OUT, 0, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e == cudaSuccess ? cudaFuncSetAttribute(linear_pair_kernel<OUT, 1, TILE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : e;
+    constexpr int smem = (int)PairTile<OUT, TILE, SPLIT>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(linear_pair_kernel<OUT, 0, TILE, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e == cudaSuccess ? cudaFuncSetAttribute(linear_pair_kernel<OUT, 1, TILE, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : e;
 }
 
 template <int OUT>
 cudaError_t prepare_out() {
-    const cudaError_t e = prepare_tile<OUT, 256>();
-    return e == cudaSuccess ? prepare_tile<OUT, 128>() : e;
+    cudaError_t e = prepare_tile<OUT, 256, false>();
+    if (e == cudaSuccess) e = prepare_tile<OUT, 128, false>();
+    return e == cudaSuccess ? prepare_tile<OUT, 128, true>() : e;
 }
 
 }  // namespace
@@ -440,10 +516,10 @@ cudaError_t linear_pair_prepare() {
     return e;
 }
 
-cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int num_sms, cudaStream_t st) {
-    return a.out_t == KV4_F32   ? launch_type<KV4_F32>(a, tile, num_sms, st)
-           : a.out_t == KV4_F16 ? launch_type<KV4_F16>(a, tile, num_sms, st)
-                                : launch_type<KV4_BF16>(a, tile, num_sms, st);
+cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int parts, int num_sms, cudaStream_t st) {
+    return a.out_t == KV4_F32   ? launch_type<KV4_F32>(a, tile, parts, num_sms, st)
+           : a.out_t == KV4_F16 ? launch_type<KV4_F16>(a, tile, parts, num_sms, st)
+                                : launch_type<KV4_BF16>(a, tile, parts, num_sms, st);
 }
 
 }  // namespace qmoe

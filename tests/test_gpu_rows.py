@@ -264,6 +264,40 @@ def test_linear(q, ctx, T, K, N, out_t, act, bias, residual, pad):
     run_linear(q, ctx, T, K, N, out_t, act, bias, residual, T + K + N, pad)
 
 
+SHARED_CASES = [  # tiles whose k is shared by two to four pairs of CTAs: tokens, K, N as above
+    (100, 2048, 2500, "BF16", "NONE", False, "", 0), (777, 2000, 1100, "F32", "SILU", True, "place", 0),
+    (256, 4096, 2048, "F32", "NONE", False, "place", 0), (199, 4112, 2047, "F16", "GELU", True, "apart", 0),
+    (200, 4096, 1400, "BF16", "RELU", True, "", 8), (256, 16368, 513, "F32", "GELU", True, "apart", 4),
+    (257, 6160, 1001, "BF16", "NONE", True, "place", 0), (513, 8208, 300, "F16", "NONE", False, "", 0),
+    (1500, 10000, 129, "BF16", "SILU", False, "apart", 0), (140, 1552, 2560, "F32", "NONE", True, "", 0)]
+
+
+@pytest.mark.parametrize("T,K,N,out_t,act,bias,residual,pad", SHARED_CASES)
+def test_linear_shared_k(q, ctx, T, K, N, out_t, act, bias, residual, pad):
+    run_linear(q, ctx, T, K, N, out_t, act, bias, residual, T + K + N, pad)
+
+
+@pytest.mark.parametrize("T,K,N", [(256, 4096, 2048), (200, 4096, 1400), (100, 2048, 2500)])
+def test_linear_shared_k_on_two_streams_and_again(q, T, K, N):
+    """Two handles at once, many calls, the results the same bits each time."""
+    st = [torch.cuda.Stream(), torch.cuda.Stream()]
+    ctx = [make_ctx(q, s) for s in st]
+    d = [torch.from_numpy(a).to(dev()) for a in linear_inputs(T, K, N, 3)]
+    out = [[torch.zeros(T, -(-N // 4) * 4, device=dev())[:, :N] for _ in range(8)] for _ in st]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for c, o in zip(ctx, out):
+            q.qmoe_linear_fp8(c, d[0], d[1], T, K, d[2], d[3], N, None, 0, None, 0, o[i], q.QMOE_F32, o[i].stride(0))
+    torch.cuda.synchronize()
+    for c, o in zip(ctx, out):
+        assert q.qmoe_get_status(c) == q.QMOE_OK
+        assert all(torch.equal(out[0][0], x) for x in o)
+    want, size = R.linear(*linear_inputs(T, K, N, 3), None, "NONE", None)
+    assert (np.abs(host(out[0][0]) - want) <= linear_bound(size, -(-K // 128), want, 0, "NONE")).all()
+    for c in ctx:
+        q.qmoe_destroy(c)
+
+
 def test_linear_products_are_summed_in_32_bits(q, ctx):
     """Blocks whose large products cancel: what is left is exact where 24 bits hold every partial sum."""
     T, K, N = 40, 256, 160
