@@ -298,6 +298,23 @@ def test_linear_shared_k_on_two_streams_and_again(q, T, K, N):
         q.qmoe_destroy(c)
 
 
+@pytest.mark.parametrize("T", [1, 300])
+@pytest.mark.parametrize("act", ["RELU", "SILU", "GELU"])
+def test_linear_activations_over_their_range(q, ctx, act, T):
+    """Products of zeros, so that a bias is what is activated: tiny, ordinary, huge."""
+    z = np.concatenate([np.linspace(-12, 12, 1501), np.geomspace(1e-38, 1e30, 300), -np.geomspace(1e-38, 1e30, 300)]).astype(np.float32)
+    N, K = len(z), 128
+    zero = torch.zeros(max(T, N), K, dtype=torch.uint8, device=dev())
+    one = torch.ones(max(T, N), device=dev())
+    bias = torch.from_numpy(z).to(dev())
+    wide = -(-N // 4) * 4
+    out = torch.zeros(T, wide, device=dev())[:, :N]
+    q.qmoe_linear_fp8(ctx, zero, one, T, K, zero, one, N, bias, q.ACT[act], None, 0, out, q.QMOE_F32, wide)
+    want = R.activate(z.astype(np.float64), act)
+    # exponentials and their arguments to some four steps, times a slope below 1.2
+    assert (np.abs(host(out) - want) <= 8 * R.U * np.abs(z) + 1e-37).all()
+
+
 def test_linear_products_are_summed_in_32_bits(q, ctx):
     """Blocks whose large products cancel: what is left is exact where 24 bits hold every partial sum."""
     T, K, N = 40, 256, 160
