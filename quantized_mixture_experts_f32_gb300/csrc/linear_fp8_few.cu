@@ -9,8 +9,8 @@
 //
 // One token, W of 2048 x 5120: 3.3 us, 3.1 TB/s (2048 x 40000: 16.8 us, 4.9 TB/s; x 151936:
 // 53.5 us, 5.8 TB/s), bound by one chain of load, products and join.  64 tokens, 4096 x
-// 2048: 7.9 us, bound by the rate of mma.sync, which neither copies by cp.async (9.2) nor
-// products on E4M3 directly (12.9, emulated) nor 32 features a CTA (slower) got past.
+// 2048: 7.8 us, bound by the rate of mma.sync, which neither copies by cp.async (9.2) nor
+// products on E4M3 directly (12.9, emulated) nor 32 features a CTA (15.2) got past.
 #include "linear_fp8.cuh"
 
 namespace qmoe {
@@ -33,6 +33,13 @@ __device__ __forceinline__ void widen16(const uint4& u, uint32_t (&h)[8]) {
         h[2 * i] = kv4_u(kv4_scale2(w[i] & 0xffffu));
         h[2 * i + 1] = kv4_u(kv4_scale2(w[i] >> 16));
     }
+}
+
+// (out of line: it keeps the products' registers to themselves, 3.35 -> 3.25 us one token, 2048 x 5120)
+__device__ __noinline__ float activate1(float z, int act) {
+    float v[1] = {z};
+    activate(v, act);
+    return v[0];
 }
 
 // NT tiles of eight tokens.  A warp takes every eighth block of k, U at a time, with all
@@ -105,12 +112,12 @@ __global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : 2) linear_few_ker
     for (int i = (int)threadIdx.x; i < LF_ROWS * rows; i += LF_WARPS * 32) {
         const int t = i / LF_ROWS, f = i % LF_ROWS, n = n0 + f;
         if (n >= a.N) continue;
-        float v[1] = {0.f};
+        float v = 0.f;
 #pragma unroll
-        for (int k = 0; k < LF_WARPS; ++k) v[0] += part[k][t][f];
-        if (a.bias) v[0] += a.bias[n];
-        activate(v, a.act);
-        put_one(a, t0 + t, n, v[0]);
+        for (int k = 0; k < LF_WARPS; ++k) v += part[k][t][f];
+        if (a.bias) v += a.bias[n];
+        if (a.act) v = activate1(v, a.act);
+        put_one(a, t0 + t, n, v);
     }
 }
 
