@@ -30,7 +30,7 @@ cudaError_t linear_fp8_prepare() { return linear_pair_prepare(); }
 //                    192            6.5            7.3           5.7
 //   K   256  N  256 2000            7.0            6.4           5.0
 cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    if (a.T <= 16) return launch_linear_few(a, st);
+    if (a.T <= 16) return launch_linear_few(a, num_sms, st);
     auto waves = [](int64_t work, int at_once) { return (double)((work + at_once - 1) / at_once); };
     const double kb = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
     const int group = linear_few_group(a.T);
@@ -53,7 +53,7 @@ cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st)
         }
     }
     const double pairs = fmin(fmin(p128, p256), split);
-    if (few <= pairs && a.T <= 32 * 65535) return launch_linear_few(a, st);   // a grid's second size
+    if (few <= pairs && a.T <= 32 * 65535) return launch_linear_few(a, num_sms, st);   // a grid's second size
     if (split < p128 && split < p256) return launch_linear_pair(a, 128, parts, num_sms, st);
     return launch_linear_pair(a, p128 < p256 ? 128 : 256, 1, num_sms, st);
 }

@@ -21,7 +21,7 @@ cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int parts, int num
 // linear_fp8_few.cu: a CTA takes 16 features of a group of tokens
 constexpr int LF_ROWS = 16;
 inline int linear_few_group(int tokens) { return tokens <= 8 ? 8 : tokens <= 32 ? 16 : 32; }
-cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st);
+cudaError_t launch_linear_few(const LinearArgs& a, int num_sms, cudaStream_t st);
 
 // (x, y) += (a sx, b sy), two roundings in one instruction
 __device__ __forceinline__ void fma2(float2& acc, uint32_t a, uint32_t b, float sx, float sy) {

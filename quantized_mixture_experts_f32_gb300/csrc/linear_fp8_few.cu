@@ -45,8 +45,12 @@ __device__ __noinline__ float activate1(float z, int act) {
 // NT tiles of eight tokens.  A warp takes every eighth block of k, U at a time, with all
 // their loads on the way before the first is used.
 template <int NT, int U>
-__global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : 2) linear_few_kernel(const LinearArgs a) {
+__global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : 2) linear_few_kernel(const LinearArgs a, bool ahead) {
     __shared__ float part[LF_WARPS][NT * 8][LF_ROWS];
+    if (ahead && threadIdx.x < LF_ROWS && blockIdx.y == 0) {  // W's rows into L2, whatever runs before
+        const uint8_t* row = a.w + (size_t)min((int)blockIdx.x * LF_ROWS + (int)threadIdx.x, a.N - 1) * a.K;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(row), "r"(a.K) : "memory");
+    }
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -128,12 +132,17 @@ __global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : 2) linear_few_ker
 //   K 4096  N 2048   32 tokens   5.5   5.8   7.6      64 tokens    9.6    8.2    8.0
 //   K 2048  N 5120               7.3   7.4  11.6                  12.2   11.2   12.9
 //   K 2000  N 1003               2.8   3.9   4.8                   3.9    4.1    5.5
-cudaError_t launch_linear_few(const LinearArgs& a, cudaStream_t st) {
+//
+// Where all CTAs run at once they ask for their rows of W before they wait for the kernel before
+// (W from HBM, in us: one token 2048 x 5120 4.1 -> 3.3, 4096 x 2048 4.3 -> 3.95, 64 tokens 9.1 ->
+// 8.4); in several waves it only adds requests (8192 x 8192, one token 15.9 -> 16.9).
+cudaError_t launch_linear_few(const LinearArgs& a, int num_sms, cudaStream_t st) {
     const unsigned group = (unsigned)linear_few_group(a.T);
     const dim3 block(LF_WARPS * 32), grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS), ((unsigned)a.T + group - 1) / group);
-    return group == 8    ? launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a)
-           : group == 16 ? launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a)
-                         : launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a);
+    const bool ahead = (uint64_t)grid.x * grid.y <= (group == 8 ? 3u : 2u) * (unsigned)num_sms;
+    return group == 8    ? launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a, ahead)
+           : group == 16 ? launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a, ahead)
+                         : launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a, ahead);
 }
 
 }  // namespace qmoe
