@@ -334,6 +334,23 @@ def test_linear_products_are_summed_in_32_bits(q, ctx):
     assert np.array_equal(host(out), ref.astype(np.float32))
 
 
+@pytest.mark.parametrize("T,K,N", [(2000, 256, 256), (600, 1024, 5120), (256, 4096, 2048), (16, 4096, 128)])
+def test_linear_products_are_summed_in_32_bits_by_every_kernel(q, ctx, T, K, N):
+    """As above on tcgen05, both tiles, k shared or not: 448 * 448 and its negative beside ones."""
+    rng = np.random.default_rng(7)
+    x = np.full((1, K), 0x38, np.uint8)
+    x[:, 0::2] = 0x7e
+    w = np.full((N, K), 0x38, np.uint8)
+    w[:, 0::4], w[:, 2::4] = 0x7e, 0x7e | 0x80
+    w[:, 1::2] |= rng.integers(0, 2, (N, K // 2)).astype(np.uint8) << 7
+    ref = (1 - 2 * (w[:, 1::2] >> 7).astype(np.float64)).sum(1).astype(np.float32)
+    d = [torch.from_numpy(a).to(dev()) for a in (np.repeat(x, T, 0), w)]
+    xs, ws = torch.ones(T, -(-K // 128), device=dev()), torch.ones(-(-N // 128), -(-K // 128), device=dev())
+    out = torch.empty(T, N, device=dev())
+    q.qmoe_linear_fp8(ctx, d[0], xs, T, K, d[1], ws, N, None, 0, None, 0, out, q.QMOE_F32, 0)
+    assert (host(out) == ref).all()
+
+
 def test_linear_not_finite_stays_in_its_row(q, ctx):
     T, K, N = 20, 256, 200
     xc, xs, wc, ws = linear_inputs(T, K, N, 9)
