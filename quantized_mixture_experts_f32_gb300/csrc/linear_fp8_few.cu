@@ -7,8 +7,8 @@
 // A lane loads 16 neighbouring codes of a row; which k a product's position means is
 // free as long as both operands agree, so they serve four products of 16 as they lie.
 //
-// One token, W of 2048 x 5120: 3.3 us, 3.1 TB/s (2048 x 40000: 16.8 us, 4.9 TB/s; x 151936:
-// 53.5 us, 5.8 TB/s), bound by one chain of load, products and join.  64 tokens, 4096 x
+// One token, W of 2048 x 5120: 3.3 us, 3.1 TB/s (2048 x 40000: 16.1 us, 5.1 TB/s; x 151936:
+// 52.5 us, 5.9 TB/s), bound by one chain of load, products and join.  64 tokens, 4096 x
 // 2048: 7.8 us, bound by the rate of mma.sync, which neither copies by cp.async (9.2) nor
 // products on E4M3 directly (12.9, emulated) nor 32 features a CTA (15.2) got past.
 #include "linear_fp8.cuh"
@@ -45,7 +45,7 @@ __device__ __noinline__ float activate1(float z, int act) {
 // NT tiles of eight tokens.  A warp takes every eighth block of k, U at a time, with all
 // their loads on the way before the first is used.
 template <int NT, int U>
-__global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : 2) linear_few_kernel(const LinearArgs a, bool ahead) {
+__global__ void __launch_bounds__(LF_WARPS * 32, NT > 1 ? 2 : U > 1 ? 3 : 4) linear_few_kernel(const LinearArgs a, bool ahead) {
     __shared__ float part[LF_WARPS][NT * 8][LF_ROWS];
     if (ahead && threadIdx.x < LF_ROWS && blockIdx.y == 0) {  // W's rows into L2, whatever runs before
         const uint8_t* row = a.w + (size_t)min((int)blockIdx.x * LF_ROWS + (int)threadIdx.x, a.N - 1) * a.K;
@@ -136,10 +136,15 @@ __global__ void __launch_bounds__(LF_WARPS * 32, NT == 1 ? 3 : 2) linear_few_ker
 // Where all CTAs run at once they ask for their rows of W before they wait for the kernel before
 // (W from HBM, in us: one token 2048 x 5120 4.1 -> 3.3, 4096 x 2048 4.3 -> 3.95, 64 tokens 9.1 ->
 // 8.4); in several waves it only adds requests (8192 x 8192, one token 15.9 -> 16.9).
+//
+// Up to eight tokens a block of k at a time, and four CTAs an SM instead of three, where there
+// are many waves (one token, 2048 x 40000: 16.1 us instead of 17.3, x 151936: 52.5 for 56; the
+// other way at 2048 x 5120: 3.9 for 3.35; at 8192 x 8192 and 2048 x 10240 neither wins).
 cudaError_t launch_linear_few(const LinearArgs& a, int num_sms, cudaStream_t st) {
     const unsigned group = (unsigned)linear_few_group(a.T);
     const dim3 block(LF_WARPS * 32), grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS), ((unsigned)a.T + group - 1) / group);
     const bool ahead = (uint64_t)grid.x * grid.y <= (group == 8 ? 3u : 2u) * (unsigned)num_sms;
+    if (group == 8 && grid.x > 8u * (unsigned)num_sms) return launch_pdl(linear_few_kernel<1, 1>, grid, block, 0, st, a, ahead);
     return group == 8    ? launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a, ahead)
            : group == 16 ? launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a, ahead)
                          : launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a, ahead);

@@ -264,6 +264,12 @@ def test_linear(q, ctx, T, K, N, out_t, act, bias, residual, pad):
     run_linear(q, ctx, T, K, N, out_t, act, bias, residual, T + K + N, pad)
 
 
+@pytest.mark.parametrize("T,K,N,out_t,act,bias,residual", [(1, 528, 20011, "F32", "SILU", True, "place"), (7, 144, 40001, "BF16", "NONE", False, ""),
+                                                          (8, 1040, 20000, "F16", "GELU", True, "apart")])
+def test_linear_few_tokens_many_features(q, ctx, T, K, N, out_t, act, bias, residual):
+    run_linear(q, ctx, T, K, N, out_t, act, bias, residual, T + K + N)
+
+
 SHARED_CASES = [  # tiles whose k is shared by two to four pairs of CTAs: tokens, K, N as above
     (100, 2048, 2500, "BF16", "NONE", False, "", 0), (777, 2000, 1100, "F32", "SILU", True, "place", 0),
     (256, 4096, 2048, "F32", "NONE", False, "place", 0), (199, 4112, 2047, "F16", "GELU", True, "apart", 0),
