@@ -18,6 +18,9 @@
  * qmoe_forward_fp8 and qmoe_forward_nvfp4 run it over FP8 block-scaled and
  * NVFP4 experts instead of k-quants (qmoe_nvfp4_quantize makes NVFP4 weights
  * from BF16 ones).
+ * qmoe_rmsnorm, qmoe_fp8_quantize, qmoe_linear_fp8, qmoe_rope and
+ * qmoe_kv4_append_rope are what a decoder layer over FP8 weights needs around
+ * qmoe_forward_fp8 and the paged cache (qmoe_kv4_*).
  *
  * Conventions shared by every entry point:
  *  - Every tensor pointer is a DEVICE pointer that the caller allocated and owns
@@ -507,7 +510,7 @@ typedef enum {
     QMOE_ACT_NONE = 0,
     QMOE_ACT_RELU = 1,
     QMOE_ACT_SILU = 2,     /* z / (1 + exp(-z)) */
-    QMOE_ACT_GELU = 3      /* z * (1 + erf(z / sqrt 2)) / 2 */
+    QMOE_ACT_GELU = 3      /* z * (1 + erf(z / sqrt 2)) / 2, to 2e-7 |z| */
 } qmoe_act;
 
 /* out = act(x W^T + bias) + residual (one launch).

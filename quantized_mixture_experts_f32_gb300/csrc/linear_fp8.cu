@@ -8,7 +8,7 @@ namespace qmoe {
 cudaError_t linear_fp8_prepare() { return linear_pair_prepare(); }
 
 // Up to 16 tokens go to mma.sync, whose CTAs read W once and wait for nothing else (W of
-// 2048 x 5120, one token: 3.3 us, 9 on a pair of CTAs; of 2048 x 40000, 16 tokens: 24, 32).
+// 2048 x 5120, one token: 3.3 us, 9 on a pair of CTAs; of 2048 x 40000, 16 tokens: 21, 32).
 // Beyond, the sizes decide, by what the kernels were measured to take in us: a start, and
 // so much a CTA and block of k that an SM takes, or a block of k for each wave of pairs.
 //                                 mma.sync  pairs, 256 features  128   k shared by 2     3     4

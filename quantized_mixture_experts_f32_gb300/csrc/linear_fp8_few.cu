@@ -42,10 +42,13 @@ __device__ __noinline__ float activate1(float z, int act) {
     return v[0];
 }
 
+// CTAs that an SM holds
+constexpr int lf_ctas(int nt, int u) { return nt == 4 ? 2 : (nt == 1 ? 4 : 3) - (u == 2); }
+
 // NT tiles of eight tokens.  A warp takes every eighth block of k, U at a time, with all
 // their loads on the way before the first is used.
 template <int NT, int U>
-__global__ void __launch_bounds__(LF_WARPS * 32, NT > 1 ? 2 : U > 1 ? 3 : 4) linear_few_kernel(const LinearArgs a, bool ahead) {
+__global__ void __launch_bounds__(LF_WARPS * 32, lf_ctas(NT, U)) linear_few_kernel(const LinearArgs a, bool ahead) {
     __shared__ float part[LF_WARPS][NT * 8][LF_ROWS];
     if (ahead && threadIdx.x < LF_ROWS && blockIdx.y == 0) {  // W's rows into L2, whatever runs before
         const uint8_t* row = a.w + (size_t)min((int)blockIdx.x * LF_ROWS + (int)threadIdx.x, a.N - 1) * a.K;
@@ -133,21 +136,26 @@ __global__ void __launch_bounds__(LF_WARPS * 32, NT > 1 ? 2 : U > 1 ? 3 : 4) lin
 //   K 2048  N 5120               7.3   7.4  11.6                  12.2   11.2   12.9
 //   K 2000  N 1003               2.8   3.9   4.8                   3.9    4.1    5.5
 //
+// Up to 32 tokens two blocks of k at a time, or one with one more CTA an SM where that saves a
+// wave of CTAs.  In us: 16 tokens 2048 x 5120 5.9 / 4.85, x 40000 24.2 / 21.3, one token x 40000
+// 17.3 / 16.1, x 151936 56 / 52.5; where it saves none 4096 x 2048 4.3 / 5.2, 8192 x 8192 19.3 / 21.2
+// (16 tokens), 2048 x 5120 3.35 / 3.9 (one).
+//
 // Where all CTAs run at once they ask for their rows of W before they wait for the kernel before
 // (W from HBM, in us: one token 2048 x 5120 4.1 -> 3.3, 4096 x 2048 4.3 -> 3.95, 64 tokens 9.1 ->
 // 8.4); in several waves it only adds requests (8192 x 8192, one token 15.9 -> 16.9).
-//
-// Up to eight tokens a block of k at a time, and four CTAs an SM instead of three, where there
-// are many waves (one token, 2048 x 40000: 16.1 us instead of 17.3, x 151936: 52.5 for 56; the
-// other way at 2048 x 5120: 3.9 for 3.35; at 8192 x 8192 and 2048 x 10240 neither wins).
 cudaError_t launch_linear_few(const LinearArgs& a, int num_sms, cudaStream_t st) {
     const unsigned group = (unsigned)linear_few_group(a.T);
     const dim3 block(LF_WARPS * 32), grid((unsigned)((a.N + LF_ROWS - 1) / LF_ROWS), ((unsigned)a.T + group - 1) / group);
-    const bool ahead = (uint64_t)grid.x * grid.y <= (group == 8 ? 3u : 2u) * (unsigned)num_sms;
-    if (group == 8 && grid.x > 8u * (unsigned)num_sms) return launch_pdl(linear_few_kernel<1, 1>, grid, block, 0, st, a, ahead);
-    return group == 8    ? launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a, ahead)
-           : group == 16 ? launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a, ahead)
-                         : launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a, ahead);
+    const uint64_t ctas = (uint64_t)grid.x * grid.y;
+    auto waves = [&](int u) { return (ctas - 1) / ((uint64_t)lf_ctas((int)group / 8, u) * (uint64_t)num_sms) + 1; };
+    const int u = group == 32 || waves(1) < waves(2) ? 1 : 2;
+    const bool ahead = waves(u) == 1;
+    if (group == 8)
+        return u == 1 ? launch_pdl(linear_few_kernel<1, 1>, grid, block, 0, st, a, ahead) : launch_pdl(linear_few_kernel<1, 2>, grid, block, 0, st, a, ahead);
+    if (group == 16)
+        return u == 1 ? launch_pdl(linear_few_kernel<2, 1>, grid, block, 0, st, a, ahead) : launch_pdl(linear_few_kernel<2, 2>, grid, block, 0, st, a, ahead);
+    return launch_pdl(linear_few_kernel<4, 1>, grid, block, 0, st, a, ahead);
 }
 
 }  // namespace qmoe

@@ -265,7 +265,9 @@ def test_linear(q, ctx, T, K, N, out_t, act, bias, residual, pad):
 
 
 @pytest.mark.parametrize("T,K,N,out_t,act,bias,residual", [(1, 528, 20011, "F32", "SILU", True, "place"), (7, 144, 40001, "BF16", "NONE", False, ""),
-                                                          (8, 1040, 20000, "F16", "GELU", True, "apart")])
+                                                          (8, 1040, 20000, "F16", "GELU", True, "apart"),
+                                                          (16, 400, 5121, "F32", "RELU", False, "apart"), (30, 2064, 4999, "BF16", "SILU", True, "place"),
+                                                          (1, 2048, 8192, "BF16", "NONE", False, ""), (12, 272, 30001, "F16", "NONE", True, "")])
 def test_linear_few_tokens_many_features(q, ctx, T, K, N, out_t, act, bias, residual):
     run_linear(q, ctx, T, K, N, out_t, act, bias, residual, T + K + N)
 
