@@ -97,3 +97,16 @@ def test_calls_without_a_handle_are_refused():
     assert q.lib.qmoe_rope(None, rope, 16, 0, 0, 1, 1, 64, 16, None, 1.0, 16, 0) == 1
     cache = q.make_kv4_cache(16, 16, 16, 16, 16, 16)
     assert q.lib.qmoe_kv4_append_rope(None, cache, rope, None, 16, 16, 0, 1, 0, 0, 0, 16, 16, None, None, 1.0, None, 0, None, None) == 1
+
+
+def test_cluster_barriers_are_met_by_whole_warps():
+    """barrier.cluster's aligned forms want every lane of a warp at the same instruction: a lane that had something
+    of its own to do (the status of a wait that ran out) meets the others first."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_mixture_experts_f32_gb300", "csrc")
+    seen = 0
+    for f in os.listdir(csrc):
+        src = re.sub(r"//[^\n]*", "", open(os.path.join(csrc, f)).read())
+        for m in re.finditer(r'asm volatile\("barrier\.cluster\.arrive\.aligned', src):
+            assert re.search(r"__syncwarp\(\);\s*$", src[:m.start()]), f
+            seen += 1
+    assert seen == 1
