@@ -658,7 +658,7 @@ qmoe_status qmoe_get_status(qmoe_ctx* ctx);
  * QMOE_ERR_NO_MEMORY the bytes the workspace needs and the bytes free). */
 const char* qmoe_last_error(qmoe_ctx* ctx);
 
-/* Test hooks of the failure paths (no counterpart on the pages).
+/* Test hooks (no counterpart on the pages).
  * qmoe_debug_stall_next: the next fused decode launch on this context (a
  *   qmoe_forward / qmoe_forward_ex of n_tokens <= 8 at a fused shape) waits for
  *   router logits carrying a launch tag that no CTA writes, gives up after
@@ -671,10 +671,16 @@ const char* qmoe_last_error(qmoe_ctx* ctx);
  *   gives up: QMOE_ERR_TIMEOUT, the item's rows left unwritten.
  * qmoe_debug_fail_alloc: the next n workspace allocations of qmoe_create and
  *   qmoe_kv4_create, in any thread, fail as if the device were out of memory
- *   (QMOE_ERR_NO_MEMORY). */
+ *   (QMOE_ERR_NO_MEMORY).
+ * qmoe_debug_linear_choice: which kernel qmoe_linear_fp8 takes for these sizes on a GPU of
+ *   num_sms multiprocessors: the features of a tile of a pair of CTAs (128 or 256) and how
+ *   many pairs share its k (1 to 4), or tile 0 for the kernel of few tokens.  Pure host
+ *   query; a test of a kernel asks it whether its sizes still go there. */
 qmoe_status qmoe_debug_stall_next(qmoe_ctx* ctx, uint64_t wait_ns);
 qmoe_status qmoe_kv4_debug_stall_next(qmoe_kv4* kv, uint64_t wait_ns);
 void qmoe_debug_fail_alloc(int n);
+qmoe_status qmoe_debug_linear_choice(int num_sms, int n_tokens, int in_features, int out_features,
+                                     int* tile, int* parts);
 
 /* Bytes of workspace a context with this config allocates (0 on bad config). */
 size_t qmoe_workspace_bytes(const qmoe_config* cfg);

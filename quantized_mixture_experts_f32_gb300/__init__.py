@@ -75,7 +75,7 @@ EXPORTED = ["qmoe_create", "qmoe_destroy", "qmoe_set_stream", "qmoe_forward", "q
             "qmoe_kv4_get_status", "qmoe_kv4_last_error", "qmoe_kv4_plan", "qmoe_kv4_append",
             "qmoe_kv4_attention", "qmoe_step_kv4", "qmoe_kv4_debug_stall_next",
             "qmoe_rmsnorm", "qmoe_fp8_quantize", "qmoe_linear_fp8", "qmoe_rope_table", "qmoe_rope",
-            "qmoe_kv4_append_rope"]
+            "qmoe_kv4_append_rope", "qmoe_debug_linear_choice"]
 
 
 class qmoe_config(C.Structure):
@@ -199,6 +199,8 @@ def _load():
     L.qmoe_fp8_quantize.restype = i
     L.qmoe_linear_fp8.argtypes = [vp, vp, fp, i, i, vp, fp, i, fp, i, vp, i64, vp, i, i64]
     L.qmoe_linear_fp8.restype = i
+    L.qmoe_debug_linear_choice.argtypes = [i, i, i, i, C.POINTER(i), C.POINTER(i)]
+    L.qmoe_debug_linear_choice.restype = i
     L.qmoe_rope_table.argtypes = [vp, rope]
     L.qmoe_rope_table.restype = i
     L.qmoe_rope.argtypes = [vp, rope, vp, i, i64, i, i, i, ip, fp, f, vp, i64]
@@ -422,6 +424,13 @@ def qmoe_linear_fp8(ctx, x_codes, x_scale, n_tokens, in_features, w_codes, w_sca
     _check(ctx, lib.qmoe_linear_fp8(ctx, _ptr(x_codes), _ptr(x_scale), n_tokens, in_features, _ptr(w_codes),
                                     _ptr(w_scale), out_features, _ptr(bias), act, _ptr(residual), res_stride,
                                     _ptr(out), out_t, out_stride))
+
+
+def qmoe_debug_linear_choice(num_sms, n_tokens, in_features, out_features):
+    """(tile, parts): features of a pair's tile, 0 for the kernel of few tokens, and pairs that share its k."""
+    tile, parts = C.c_int(), C.c_int()
+    _check(None, lib.qmoe_debug_linear_choice(num_sms, n_tokens, in_features, out_features, C.byref(tile), C.byref(parts)))
+    return tile.value, parts.value
 
 
 def qmoe_rope_table(ctx, rope: qmoe_rope_config):

@@ -29,19 +29,19 @@ cudaError_t linear_fp8_prepare() { return linear_pair_prepare(); }
 //   K   512  N 2048  100            4.5            7.1           5.7
 //                    192            6.5            7.3           5.7
 //   K   256  N  256 2000            7.0            6.4           5.0
-cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    if (a.T <= 16) return launch_linear_few(a, num_sms, st);
+LinearChoice linear_fp8_choice(int T, int K, int N, int num_sms) {
+    if (T <= 16) return {0, 1};
     auto waves = [](int64_t work, int at_once) { return (double)((work + at_once - 1) / at_once); };
-    const double kb = (a.K + FP8_BLOCK - 1) / FP8_BLOCK;
-    const int group = linear_few_group(a.T);
-    const int64_t token_tiles = (a.T + 255) / 256, ctas = (int64_t)((a.N + LF_ROWS - 1) / LF_ROWS) * ((a.T + group - 1) / group);
+    const double kb = (K + FP8_BLOCK - 1) / FP8_BLOCK;
+    const int group = linear_few_group(T);
+    const int64_t token_tiles = (T + 255) / 256, ctas = (int64_t)((N + LF_ROWS - 1) / LF_ROWS) * ((T + group - 1) / group);
     const double each = group == 16 ? 0.35 + 0.057 * kb : 0.45 + 0.095 * kb;
     const double few = 2.0 + each * (ctas < num_sms ? 1.0 : (double)ctas / num_sms);
-    const double p128 = 3.7 + 0.33 * kb * waves(token_tiles * ((a.N + 127) / 128), num_sms / 2);
-    const double p256 = 4.7 + 0.52 * kb * waves(token_tiles * ((a.N + 255) / 256), num_sms / 2);
+    const double p128 = 3.7 + 0.33 * kb * waves(token_tiles * ((N + 127) / 128), num_sms / 2);
+    const double p256 = 4.7 + 0.52 * kb * waves(token_tiles * ((N + 255) / 256), num_sms / 2);
     // a tile's k shared by 2, 3 or 4 pairs, where such clusters fit the GPU at once (36, 21 and 15 on
     // 152 SMs): 5.2 us, 0.3 a pair, and its blocks of k, in groups of four
-    const int64_t tiles = token_tiles * ((a.N + 127) / 128), groups = ((int64_t)kb + 3) / 4;
+    const int64_t tiles = token_tiles * ((N + 127) / 128), groups = ((int64_t)kb + 3) / 4;
     double split = 1e30;
     int parts = 1;
     for (int p = 2; p <= 4; ++p) {
@@ -53,9 +53,14 @@ cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st)
         }
     }
     const double pairs = fmin(fmin(p128, p256), split);
-    if (few <= pairs && a.T <= 32 * 65535) return launch_linear_few(a, num_sms, st);   // a grid's second size
-    if (split < p128 && split < p256) return launch_linear_pair(a, 128, parts, num_sms, st);
-    return launch_linear_pair(a, p128 < p256 ? 128 : 256, 1, num_sms, st);
+    if (few <= pairs && T <= 32 * 65535) return {0, 1};       // a grid's second size
+    if (split < p128 && split < p256) return {128, parts};
+    return {p128 < p256 ? 128 : 256, 1};
+}
+
+cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st) {
+    const LinearChoice c = linear_fp8_choice(a.T, a.K, a.N, num_sms);
+    return c.tile ? launch_linear_pair(a, c.tile, c.parts, num_sms, st) : launch_linear_few(a, num_sms, st);
 }
 
 }  // namespace qmoe

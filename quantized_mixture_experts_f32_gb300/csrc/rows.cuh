@@ -36,6 +36,11 @@ struct LinearArgs {
     int* status;
 };
 enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
+struct LinearChoice {
+    int tile;                                 // features of a pair of CTAs' tile, 0: mma.sync
+    int parts;                                // pairs that share a tile's k
+};
+LinearChoice linear_fp8_choice(int T, int K, int N, int num_sms);
 cudaError_t linear_fp8_prepare();
 cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st);
 

@@ -184,6 +184,16 @@ qmoe_status qmoe_linear_fp8(qmoe_ctx* ctx, const void* x_codes, const float* x_s
     return done(c, qmoe::launch_linear_fp8(a, c.num_sms, c.stream), "linear launch");
 }
 
+qmoe_status qmoe_debug_linear_choice(int num_sms, int n_tokens, int in_features, int out_features, int* tile, int* parts) {
+    if (!tile || !parts || num_sms < 2 || n_tokens < 1 || n_tokens > ROWS_MAX || in_features < 16 || in_features > K_MAX ||
+        in_features % 16 || out_features < 1 || out_features > ROWS_MAX)
+        return QMOE_ERR_INVALID_ARG;
+    const qmoe::LinearChoice c = qmoe::linear_fp8_choice(n_tokens, in_features, out_features, num_sms);
+    *tile = c.tile;
+    *parts = c.parts;
+    return QMOE_OK;
+}
+
 qmoe_status qmoe_rope_table(qmoe_ctx* ctx, const qmoe_rope_config* r) {
     if (!ctx) return QMOE_ERR_INVALID_ARG;
     const CtxView c = qmoe::ctx_view(ctx);
