@@ -669,6 +669,9 @@ const char* qmoe_last_error(qmoe_ctx* ctx);
  *   first layer) on this handle the CTAs that share an item of a prompt chunk hand
  *   their parts over wait_ns late (1..10^9); past 200 ms the CTA that joins them
  *   gives up: QMOE_ERR_TIMEOUT, the item's rows left unwritten.
+ * qmoe_debug_stall_linear_next: in the next qmoe_linear_fp8 on this context, where pairs of
+ *   CTAs take it and it has F32 rows and no activation, one CTA gets its scales wait_ns late
+ *   (1..10^9); past 200 ms its pair gives up: QMOE_ERR_TIMEOUT, the call's results are unspecified.
  * qmoe_debug_fail_alloc: the next n workspace allocations of qmoe_create and
  *   qmoe_kv4_create, in any thread, fail as if the device were out of memory
  *   (QMOE_ERR_NO_MEMORY).
@@ -678,6 +681,7 @@ const char* qmoe_last_error(qmoe_ctx* ctx);
  *   query; a test of a kernel asks it whether its sizes still go there. */
 qmoe_status qmoe_debug_stall_next(qmoe_ctx* ctx, uint64_t wait_ns);
 qmoe_status qmoe_kv4_debug_stall_next(qmoe_kv4* kv, uint64_t wait_ns);
+qmoe_status qmoe_debug_stall_linear_next(qmoe_ctx* ctx, uint64_t wait_ns);
 void qmoe_debug_fail_alloc(int n);
 qmoe_status qmoe_debug_linear_choice(int num_sms, int n_tokens, int in_features, int out_features,
                                      int* tile, int* parts);

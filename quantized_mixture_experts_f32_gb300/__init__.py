@@ -75,7 +75,8 @@ EXPORTED = ["qmoe_create", "qmoe_destroy", "qmoe_set_stream", "qmoe_forward", "q
             "qmoe_kv4_get_status", "qmoe_kv4_last_error", "qmoe_kv4_plan", "qmoe_kv4_append",
             "qmoe_kv4_attention", "qmoe_step_kv4", "qmoe_kv4_debug_stall_next",
             "qmoe_rmsnorm", "qmoe_fp8_quantize", "qmoe_linear_fp8", "qmoe_rope_table", "qmoe_rope",
-            "qmoe_kv4_append_rope", "qmoe_debug_linear_choice"]
+            "qmoe_kv4_append_rope", "qmoe_debug_linear_choice",
+            "qmoe_debug_stall_linear_next"]
 
 
 class qmoe_config(C.Structure):
@@ -199,6 +200,8 @@ def _load():
     L.qmoe_fp8_quantize.restype = i
     L.qmoe_linear_fp8.argtypes = [vp, vp, fp, i, i, vp, fp, i, fp, i, vp, i64, vp, i, i64]
     L.qmoe_linear_fp8.restype = i
+    L.qmoe_debug_stall_linear_next.argtypes = [vp, C.c_uint64]
+    L.qmoe_debug_stall_linear_next.restype = i
     L.qmoe_debug_linear_choice.argtypes = [i, i, i, i, C.POINTER(i), C.POINTER(i)]
     L.qmoe_debug_linear_choice.restype = i
     L.qmoe_rope_table.argtypes = [vp, rope]
@@ -424,6 +427,10 @@ def qmoe_linear_fp8(ctx, x_codes, x_scale, n_tokens, in_features, w_codes, w_sca
     _check(ctx, lib.qmoe_linear_fp8(ctx, _ptr(x_codes), _ptr(x_scale), n_tokens, in_features, _ptr(w_codes),
                                     _ptr(w_scale), out_features, _ptr(bias), act, _ptr(residual), res_stride,
                                     _ptr(out), out_t, out_stride))
+
+
+def qmoe_debug_stall_linear_next(ctx, wait_ns: int):
+    _check(ctx, lib.qmoe_debug_stall_linear_next(ctx, wait_ns))
 
 
 def qmoe_debug_linear_choice(num_sms, n_tokens, in_features, out_features):

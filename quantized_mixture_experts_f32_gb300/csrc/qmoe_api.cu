@@ -47,6 +47,7 @@ struct qmoe_ctx {
     int attn_splits;
     void* pl_scratch; // batched prefill layer scratch (null: shape not served)
     unsigned long long stall_ns; // test hook: the next fused launch stalls for this long (0: off)
+    unsigned long long stall_linear_ns; // test hook: scales of the next qmoe_linear_fp8 come this late (0: off)
 };
 
 namespace {
@@ -273,7 +274,7 @@ Kv4View kv4_view(qmoe_kv4* h);
 qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c);
 Kv4Cache kv4_cache(const qmoe_kv4_cache* c);
 
-CtxView ctx_view(qmoe_ctx* c) { return {c->stream, c->device, c->num_sms, c->status, c->err, sizeof(c->err)}; }
+CtxView ctx_view(qmoe_ctx* c) { return {c->stream, c->device, c->num_sms, c->status, c->err, sizeof(c->err), &c->stall_linear_ns}; }
 
 void create_error(const char* fmt, ...) {
     va_list ap;
@@ -921,6 +922,12 @@ const char* qmoe_last_error(qmoe_ctx* c) { return c ? c->err : g_create_err; }
 qmoe_status qmoe_debug_stall_next(qmoe_ctx* c, uint64_t wait_ns) {
     if (!c || wait_ns == 0) return QMOE_ERR_INVALID_ARG;
     c->stall_ns = wait_ns;
+    return QMOE_OK;
+}
+
+qmoe_status qmoe_debug_stall_linear_next(qmoe_ctx* c, uint64_t wait_ns) {
+    if (!c || wait_ns == 0 || wait_ns > 1000000000ull) return QMOE_ERR_INVALID_ARG;
+    c->stall_linear_ns = wait_ns;
     return QMOE_OK;
 }
 

@@ -328,6 +328,7 @@ struct CtxView {
     int* status;
     char* err;
     size_t err_bytes;
+    unsigned long long* stall_linear_ns;      // of a context: what the next product's scales are late by
 };
 
 // Text that qmoe_last_error(NULL) gives on this thread (a failed qmoe_kv4_create;

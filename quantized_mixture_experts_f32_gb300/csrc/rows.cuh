@@ -34,6 +34,7 @@ struct LinearArgs {
     int64_t res_stride, out_stride;
     int T, K, N, act, out_t;
     int* status;
+    unsigned long long stall_ns;              // test hook: scales of one CTA of a pair come this late
 };
 enum : int { ACT_NONE = 0, ACT_RELU = 1, ACT_SILU = 2, ACT_GELU = 3 };
 struct LinearChoice {

@@ -180,7 +180,8 @@ qmoe_status qmoe_linear_fp8(qmoe_ctx* ctx, const void* x_codes, const float* x_s
     if (dev.e != cudaSuccess) return done(c, dev.e, "device select");
     const qmoe::LinearArgs a{static_cast<const uint8_t*>(x_codes), x_scale, static_cast<const uint8_t*>(w_codes), w_scale,
                              bias, residual, out, res_stride, out_stride, n_tokens, in_features, out_features, (int)act,
-                             (int)out_t, c.status};
+                             (int)out_t, c.status, *c.stall_linear_ns};
+    *c.stall_linear_ns = 0;
     return done(c, qmoe::launch_linear_fp8(a, c.num_sms, c.stream), "linear launch");
 }
 

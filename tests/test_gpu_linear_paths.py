@@ -1,13 +1,15 @@
 """qmoe_linear_fp8 on pairs of CTAs: both tiles, k shared or not, one and several tiles a pair, every type and
 activation of each, against the plain form in 64 bits.  Each size says which kernel it is for, and the test asks
 whether it still goes there."""
+import time
+
 import numpy as np
 import pytest
 import torch
 
 from tests import rows_ref as R
 from tests.gpu_util import dev
-from tests.test_gpu_rows import ctx, guarded, assert_guard, host, linear_bound, linear_inputs, q, run_linear  # noqa: F401
+from tests.test_gpu_rows import assert_guard, ctx, guarded, host, linear_bound, linear_inputs, make_ctx, q, run_linear  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +126,51 @@ def test_rows_far_apart(q, ctx, size, stride):  # noqa: F811
     q.qmoe_linear_fp8(ctx, d[0], d[1], T, K, d[2], d[3], N, bias, 0, out, stride, out, q.QMOE_BF16, stride)
     assert (np.abs(host(out) - ref) <= linear_bound(size, -(-K // 128), ref, R.HALF["BF16"], "NONE")).all()
     assert (wide[:, N:] == 7).all()
+
+
+# ---------------------------------------------------------------------------- waits that run out
+
+LATE = [(128, 128, 2500, (128, 1)), (1281, 464, 4999, (256, 1)), (3000, 640, 2051, (128, 1)), T128, T256, SHARED,
+        (300, 1536, 1003, (128, 3)), (257, 4096, 700, (128, 4))]
+
+
+@pytest.mark.parametrize("T,K,N,want", LATE)
+def test_scales_that_come_late(q, T, K, N, want):  # noqa: F811
+    """One CTA's scales later than the limit: the status says so, and the next call on the context is right; later than
+    usual within it: nothing but time."""
+    check_path(q, T, K, N, want)
+    c = make_ctx(q)
+    data = linear_inputs(T, K, N, 71)
+    d = [torch.from_numpy(a).to(dev()) for a in data]
+    res = torch.randn(T, -(-N // 4) * 4, device=dev())[:, :N]
+    ref, size = R.linear(*data, None, "NONE", host(res))
+    out, guard = guarded(T, N, torch.float32, -(-N // 4) * 4)
+
+    def call():
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        q.qmoe_linear_fp8(c, d[0], d[1], T, K, d[2], d[3], N, None, 0, res, res.stride(0), out, q.QMOE_F32, out.stride(0))
+        torch.cuda.synchronize()
+        return time.perf_counter() - t0
+
+    def right():
+        assert q.qmoe_get_status(c) == q.QMOE_OK, q.qmoe_last_error(c)
+        assert (np.abs(host(out) - ref) <= linear_bound(size, -(-K // 128), ref, 0, "NONE")).all()
+        assert_guard(guard, T, N)
+
+    for wait in (400_000_000, 20_000_000, 250_000_000):
+        q.qmoe_debug_stall_linear_next(c, wait)
+        took = call()
+        print(f"{wait / 1e9} s late: {took:.3f} s")
+        assert took > 0.9e-9 * wait
+        if wait > 200_000_000:
+            assert q.qmoe_get_status(c) == 7 and "status 7" in q.qmoe_last_error(c)
+            assert_guard(guard, T, N)
+            call()                                       # the hook is spent
+        right()
+    for bad in (0, 1_000_000_001):
+        with pytest.raises(q.QmoeError):
+            q.qmoe_debug_stall_linear_next(c, bad)
+    assert q.lib.qmoe_debug_stall_linear_next(None, 5) == 1
+    q.qmoe_destroy(c)
