@@ -118,7 +118,7 @@ Kv4View kv4_view(qmoe_kv4* h) {
     return {shape(h), h->work, h->status, &h->stall_ns, h->stream, h->device, h->cfg.max_seqs, h->cfg.max_tokens};
 }
 
-CtxView kv4_ctx_view(qmoe_kv4* h) { return {h->stream, h->device, h->num_sms, h->status, h->err, sizeof(h->err), nullptr}; }
+CtxView kv4_ctx_view(qmoe_kv4* h) { return {h->stream, h->device, h->num_sms, h->status, h->err, sizeof(h->err), nullptr, nullptr}; }
 
 qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c) { return check_cache(h, c); }
 

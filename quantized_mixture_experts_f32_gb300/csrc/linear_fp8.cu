@@ -5,8 +5,6 @@
 
 namespace qmoe {
 
-cudaError_t linear_fp8_prepare() { return linear_pair_prepare(); }
-
 // Up to 16 tokens go to mma.sync, whose CTAs read W once and wait for nothing else (W of
 // 2048 x 5120, one token: 3.3 us, 9 on a pair of CTAs; of 2048 x 40000, 16 tokens: 21, 32).
 // Beyond, the sizes decide, by what the kernels were measured to take in us: a start, and
@@ -58,9 +56,9 @@ LinearChoice linear_fp8_choice(int T, int K, int N, int num_sms) {
     return {p128 < p256 ? 128 : 256, 1};
 }
 
-cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st) {
-    const LinearChoice c = linear_fp8_choice(a.T, a.K, a.N, num_sms);
-    return c.tile ? launch_linear_pair(a, c.tile, c.parts, num_sms, st) : launch_linear_few(a, num_sms, st);
+cudaError_t launch_linear_fp8(const LinearArgs& a, const LinearRun& run) {
+    const LinearChoice c = linear_fp8_choice(a.T, a.K, a.N, run.num_sms);
+    return c.tile ? launch_linear_pair(a, c.tile, c.parts, run) : launch_linear_few(a, run.num_sms, run.st);
 }
 
 }  // namespace qmoe

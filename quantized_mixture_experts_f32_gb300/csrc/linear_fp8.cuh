@@ -13,10 +13,9 @@ bool tensor_map_codes(CUtensorMap* m, const void* base, uint64_t cols, uint64_t 
 bool tensor_map_rows(CUtensorMap* m, const void* base, int t, uint64_t cols, uint64_t rows, uint64_t stride, uint32_t box_rows);
 
 // linear_fp8_pair.cu
-cudaError_t linear_pair_prepare();
 // tiles of 128 or 256 features; of 128, a tile's k may be shared by 2 to 4 pairs, each at least a
 // group of four blocks
-cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int parts, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int parts, const LinearRun& run);
 
 // linear_fp8_few.cu: a CTA takes 16 features of a group of tokens
 constexpr int LF_ROWS = 16;

@@ -463,7 +463,7 @@ auto pair_kernel(bool late) {
 }
 
 template <int OUT, int ACT, int TILE, bool SPLIT>
-cudaError_t launch_out(const LinearArgs& a, int parts, int num_sms, cudaStream_t st) {
+cudaError_t launch_out(const LinearArgs& a, int parts, const LinearRun& run) {
     using O = PairTile<OUT, TILE, SPLIT>;
     CUtensorMap mx, mw, mo, mr;
     if (!tensor_map_codes(&mx, a.x, (uint64_t)a.K, (uint64_t)a.T, 128) || !tensor_map_codes(&mw, a.w, (uint64_t)a.K, (uint64_t)a.N, TILE / 2) ||
@@ -474,12 +474,20 @@ cudaError_t launch_out(const LinearArgs& a, int parts, int num_sms, cudaStream_t
     const int64_t tiles = (int64_t)tiles_n * ((a.T + LP_TOKENS - 1) / LP_TOKENS);
     if (tiles > INT_MAX / 8) return cudaErrorInvalidValue;
     if (SPLIT != (parts > 1) || parts > 4 || (SPLIT && a.K <= FP8_BLOCK * LP_GROUP * (parts - 1))) return cudaErrorInvalidValue;
-    const int pairs = SPLIT ? (int)tiles * parts : (int)(tiles < num_sms / 2 ? tiles : num_sms / 2);
+    const int pairs = SPLIT ? (int)tiles * parts : (int)(tiles < run.num_sms / 2 ? tiles : run.num_sms / 2);
+    const bool late = OUT == KV4_F32 && ACT == ACT_NONE && a.stall_ns;
+    const auto kernel = pair_kernel<OUT, ACT, TILE, SPLIT>(late);
+    const uint64_t bit = 1ull << (((late ? 3 : OUT) * 4 + ACT) * 3 + (TILE == 256 ? 0 : SPLIT ? 1 : 2));
+    if (!(*run.ready & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)O::SMEM);
+        if (e != cudaSuccess) return e;
+        *run.ready |= bit;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * pairs);
     cfg.blockDim = dim3(O::THREADS);
     cfg.dynamicSmemBytes = O::SMEM;
-    cfg.stream = st;
+    cfg.stream = run.st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -489,57 +497,32 @@ cudaError_t launch_out(const LinearArgs& a, int parts, int num_sms, cudaStream_t
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, pair_kernel<OUT, ACT, TILE, SPLIT>(a.stall_ns != 0), mx, mw, mo, mr, a, tiles_n, (int)tiles, parts);
+    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, mo, mr, a, tiles_n, (int)tiles, parts);
 }
 
 // A kernel an activation: 64 results' code for each is long, and is fetched past or branched
 // around otherwise (16384 tokens, 2048 x 5120: none 166 us, SiLU 184, GELU 193; with one kernel for
 // the three 166, 196, 203; with one for all four 191 and more).
 template <int OUT, int TILE, bool SPLIT>
-cudaError_t launch_act(const LinearArgs& a, int parts, int num_sms, cudaStream_t st) {
-    return a.act == ACT_NONE   ? launch_out<OUT, ACT_NONE, TILE, SPLIT>(a, parts, num_sms, st)
-           : a.act == ACT_RELU ? launch_out<OUT, ACT_RELU, TILE, SPLIT>(a, parts, num_sms, st)
-           : a.act == ACT_SILU ? launch_out<OUT, ACT_SILU, TILE, SPLIT>(a, parts, num_sms, st)
-                               : launch_out<OUT, ACT_GELU, TILE, SPLIT>(a, parts, num_sms, st);
+cudaError_t launch_act(const LinearArgs& a, int parts, const LinearRun& run) {
+    return a.act == ACT_NONE   ? launch_out<OUT, ACT_NONE, TILE, SPLIT>(a, parts, run)
+           : a.act == ACT_RELU ? launch_out<OUT, ACT_RELU, TILE, SPLIT>(a, parts, run)
+           : a.act == ACT_SILU ? launch_out<OUT, ACT_SILU, TILE, SPLIT>(a, parts, run)
+                               : launch_out<OUT, ACT_GELU, TILE, SPLIT>(a, parts, run);
 }
 template <int OUT>
-cudaError_t launch_type(const LinearArgs& a, int tile, int parts, int num_sms, cudaStream_t st) {
-    return tile == 256 ? launch_act<OUT, 256, false>(a, 1, num_sms, st)
-           : parts > 1 ? launch_act<OUT, 128, true>(a, parts, num_sms, st)
-                       : launch_act<OUT, 128, false>(a, 1, num_sms, st);
-}
-
-template <int OUT, int TILE, bool SPLIT>
-cudaError_t prepare_tile() {
-    constexpr int smem = (int)PairTile<OUT, TILE, SPLIT>::SMEM;
-    cudaError_t e = cudaSuccess;
-    for (auto k : {pair_kernel<OUT, ACT_NONE, TILE, SPLIT>(false), pair_kernel<OUT, ACT_RELU, TILE, SPLIT>(false),
-                   pair_kernel<OUT, ACT_SILU, TILE, SPLIT>(false), pair_kernel<OUT, ACT_GELU, TILE, SPLIT>(false),
-                   pair_kernel<OUT, ACT_NONE, TILE, SPLIT>(true)})
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e;
-}
-
-template <int OUT>
-cudaError_t prepare_out() {
-    cudaError_t e = prepare_tile<OUT, 256, false>();
-    if (e == cudaSuccess) e = prepare_tile<OUT, 128, false>();
-    return e == cudaSuccess ? prepare_tile<OUT, 128, true>() : e;
+cudaError_t launch_type(const LinearArgs& a, int tile, int parts, const LinearRun& run) {
+    return tile == 256 ? launch_act<OUT, 256, false>(a, 1, run)
+           : parts > 1 ? launch_act<OUT, 128, true>(a, parts, run)
+                       : launch_act<OUT, 128, false>(a, 1, run);
 }
 
 }  // namespace
 
-cudaError_t linear_pair_prepare() {
-    cudaError_t e = prepare_out<KV4_F32>();
-    if (e == cudaSuccess) e = prepare_out<KV4_F16>();
-    if (e == cudaSuccess) e = prepare_out<KV4_BF16>();
-    return e;
-}
-
-cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int parts, int num_sms, cudaStream_t st) {
-    return a.out_t == KV4_F32   ? launch_type<KV4_F32>(a, tile, parts, num_sms, st)
-           : a.out_t == KV4_F16 ? launch_type<KV4_F16>(a, tile, parts, num_sms, st)
-                                : launch_type<KV4_BF16>(a, tile, parts, num_sms, st);
+cudaError_t launch_linear_pair(const LinearArgs& a, int tile, int parts, const LinearRun& run) {
+    return a.out_t == KV4_F32   ? launch_type<KV4_F32>(a, tile, parts, run)
+           : a.out_t == KV4_F16 ? launch_type<KV4_F16>(a, tile, parts, run)
+                                : launch_type<KV4_BF16>(a, tile, parts, run);
 }
 
 }  // namespace qmoe

@@ -48,6 +48,7 @@ struct qmoe_ctx {
     void* pl_scratch; // batched prefill layer scratch (null: shape not served)
     unsigned long long stall_ns; // test hook: the next fused launch stalls for this long (0: off)
     unsigned long long stall_linear_ns; // test hook: scales of the next qmoe_linear_fp8 come this late (0: off)
+    uint64_t linear_ready; // the kernels of qmoe_linear_fp8 that are set up
 };
 
 namespace {
@@ -274,7 +275,7 @@ Kv4View kv4_view(qmoe_kv4* h);
 qmoe_status kv4_check_cache(qmoe_kv4* h, const qmoe_kv4_cache* c);
 Kv4Cache kv4_cache(const qmoe_kv4_cache* c);
 
-CtxView ctx_view(qmoe_ctx* c) { return {c->stream, c->device, c->num_sms, c->status, c->err, sizeof(c->err), &c->stall_linear_ns}; }
+CtxView ctx_view(qmoe_ctx* c) { return {c->stream, c->device, c->num_sms, c->status, c->err, sizeof(c->err), &c->stall_linear_ns, &c->linear_ready}; }
 
 void create_error(const char* fmt, ...) {
     va_list ap;
@@ -366,7 +367,6 @@ qmoe_status qmoe_create(const qmoe_config* cfg, qmoe_ctx** out) {
     if (e == cudaSuccess) e = qmoe::t1_prepare();
     if (e == cudaSuccess) e = qmoe::route_prepare();
     if (e == cudaSuccess) e = qmoe::decode_step_prepare();
-    if (e == cudaSuccess) e = qmoe::linear_fp8_prepare();
     if (e == cudaSuccess && L.pl_ok) e = qmoe::prefill_layer_prepare();
     if (e != cudaSuccess) {
         create_fail("kernel set-up: %s", cudaGetErrorString(e));

@@ -328,7 +328,9 @@ struct CtxView {
     int* status;
     char* err;
     size_t err_bytes;
-    unsigned long long* stall_linear_ns;      // of a context: what the next product's scales are late by
+    // of a context: what the next product's scales are late by, and the products' kernels set up
+    unsigned long long* stall_linear_ns;
+    uint64_t* linear_ready;
 };
 
 // Text that qmoe_last_error(NULL) gives on this thread (a failed qmoe_kv4_create;

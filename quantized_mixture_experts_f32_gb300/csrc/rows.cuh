@@ -42,8 +42,14 @@ struct LinearChoice {
     int parts;                                // pairs that share a tile's k
 };
 LinearChoice linear_fp8_choice(int T, int K, int N, int num_sms);
-cudaError_t linear_fp8_prepare();
-cudaError_t launch_linear_fp8(const LinearArgs& a, int num_sms, cudaStream_t st);
+// Where a product runs, and which kernels this context has set up: each with its first call, as
+// there are many, and most contexts use few or none.
+struct LinearRun {
+    int num_sms;
+    cudaStream_t st;
+    uint64_t* ready;
+};
+cudaError_t launch_linear_fp8(const LinearArgs& a, const LinearRun& run);
 
 // Rotary positions on the heads of rows, and the append of K and V rows behind them.
 struct RopeArgs {

@@ -182,7 +182,7 @@ qmoe_status qmoe_linear_fp8(qmoe_ctx* ctx, const void* x_codes, const float* x_s
                              bias, residual, out, res_stride, out_stride, n_tokens, in_features, out_features, (int)act,
                              (int)out_t, c.status, *c.stall_linear_ns};
     *c.stall_linear_ns = 0;
-    return done(c, qmoe::launch_linear_fp8(a, c.num_sms, c.stream), "linear launch");
+    return done(c, qmoe::launch_linear_fp8(a, {c.num_sms, c.stream, c.linear_ready}), "linear launch");
 }
 
 qmoe_status qmoe_debug_linear_choice(int num_sms, int n_tokens, int in_features, int out_features, int* tile, int* parts) {

@@ -1,6 +1,9 @@
 """qmoe_linear_fp8 on pairs of CTAs: both tiles, k shared or not, one and several tiles a pair, every type and
 activation of each, against the plain form in 64 bits.  Each size says which kernel it is for, and the test asks
 whether it still goes there."""
+import os
+import subprocess
+import sys
 import time
 
 import numpy as np
@@ -174,3 +177,39 @@ def test_scales_that_come_late(q, T, K, N, want):  # noqa: F811
             q.qmoe_debug_stall_linear_next(c, bad)
     assert q.lib.qmoe_debug_stall_linear_next(None, 5) == 1
     q.qmoe_destroy(c)
+
+
+# ---------------------------------------------------------------------------- the first call
+
+FIRST = """
+import sys
+import torch
+sys.path.insert(0, {root!r})
+import quantized_mixture_experts_f32_gb300 as q
+from tests.test_gpu_rows import linear_inputs, make_ctx
+T, K, N = {size}
+st = torch.cuda.Stream()
+c, other = make_ctx(q, st), make_ctx(q, st)
+d = [torch.from_numpy(a).cuda() for a in linear_inputs(T, K, N, 5)]
+out = [torch.zeros(T, -(-N // 4) * 4, device="cuda") for _ in range(3)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=st):
+    q.qmoe_linear_fp8(c, d[0], d[1], T, K, d[2], d[3], N, None, 0, None, 0, out[0], 0, out[0].stride(0))
+g.replay()
+q.qmoe_linear_fp8(c, d[0], d[1], T, K, d[2], d[3], N, None, 0, None, 0, out[1], 0, out[1].stride(0))
+q.qmoe_linear_fp8(other, d[0], d[1], T, K, d[2], d[3], N, None, 0, None, 0, out[2], 0, out[2].stride(0))
+torch.cuda.synchronize()
+assert q.qmoe_get_status(c) == 0 and q.qmoe_get_status(other) == 0
+assert out[0].abs().sum() > 0 and torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
+print("first call right")
+"""
+
+
+@pytest.mark.parametrize("size", [T128, T256, SHARED], ids=["128", "256", "shared"])
+def test_a_kernels_first_call_may_be_captured(q, size):  # noqa: F811
+    """A process's first call of a kernel, which sets it up, inside a graph's capture; then calls of two contexts."""
+    check_path(q, *size)
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root, size=size[:3])], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first call right" in r.stdout, r.stderr[-2000:]

@@ -1,4 +1,7 @@
 """Which kernel of qmoe_linear_fp8 takes which sizes (CPU; the query is pure host code)."""
+import os
+import re
+
 import pytest
 
 from tests import test_gpu_linear_paths as P
@@ -40,3 +43,12 @@ def test_choice_refusals(q):
             q.qmoe_debug_linear_choice(*bad)
         assert e.value.status == 1
     assert q.lib.qmoe_debug_linear_choice(SMS, 1, 16, 1, None, None) == 1
+
+
+def test_a_context_sets_up_no_kernels_of_products():
+    """There are 36 on pairs of CTAs: each is set up by its first call, not by every qmoe_create."""
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "quantized_mixture_experts_f32_gb300", "csrc")
+    api = open(os.path.join(csrc, "qmoe_api.cu")).read()
+    create = re.search(r"^qmoe_status qmoe_create\(.*?^}", api, flags=re.S | re.M).group(0)
+    assert "_prepare(" in create and "linear" not in create
+    assert not re.search(r"linear\w*prepare", "".join(open(os.path.join(csrc, f)).read() for f in os.listdir(csrc)))
