@@ -34,11 +34,6 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return c;
 }
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 __device__ __forceinline__ float relu(float z) {                                             // NaN stays
     float y;
@@ -52,10 +47,10 @@ __device__ __forceinline__ float silu(float z) {
     return z * r;
 }
 // z Phi(z) = max(z, 0) - m erfc(m / sqrt 2) / 2, m = |z|, erfc as 2^-q(m) with q a polynomial without a
-// constant, fitted to log2 erfc for the least largest error of the result over |z|: 2.8e-8 for
-// m up to 6, where the second term is 6e-9 and stays.  Two results at a time: 9 instructions
-// each, where a form with a quotient (1.5e-7) took 20 and 16384 tokens, 2048 x 5120, 242 us
-// instead of 203.
+// constant, fitted to log2 erfc for the least largest error of the result over |z|, m up to 6, where the
+// second term is 6e-9 and stays.  The fit alone is off by 1.3e-8 |z| and by 3.5e-8 at most; in fp32, with
+// the exponential's error and the result rounded, 8.5e-8 |z| was the most found (2e-7 |z| is promised).
+// Two results at a time: 9 instructions each, where a form with a quotient (1.5e-7 |z|) took 20.
 __device__ __forceinline__ float2 gelu(float2 z) {
     const float2 m = make_float2(fminf(fabsf(z.x), 6.f), fminf(fabsf(z.y), 6.f));
     float2 p = both(-2.8349129e-06f);
@@ -67,7 +62,7 @@ __device__ __forceinline__ float2 gelu(float2 z) {
     p = fma2(p, m, both(-4.59208190e-01f));
     p = fma2(p, m, both(-1.15110517f));
     p = make_float2(p.x * m.x, p.y * m.y);
-    const float2 e = make_float2(exp2_fast(p.x), exp2_fast(p.y));
+    const float2 e = make_float2(kv4_ex2(p.x), kv4_ex2(p.y));
     return fma2(make_float2(-0.5f * m.x, -0.5f * m.y), e, make_float2(relu(z.x), relu(z.y)));
 }
 

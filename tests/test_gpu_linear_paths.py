@@ -131,6 +131,30 @@ def test_rows_far_apart(q, ctx, size, stride):  # noqa: F811
     assert (wide[:, N:] == 7).all()
 
 
+@pytest.mark.parametrize("size", [FEW, T128, T256, SHARED], ids=["few", "128", "256", "shared"])
+def test_gelu_is_as_exact_as_it_says(q, ctx, size):  # noqa: F811
+    """2e-7 |z|, over a fine grid: one product of ones under a token's scale, a bias a feature, z their rounded sum."""
+    T, K, N, want = size
+    check_path(q, T, K, N, want)
+    xc, wc = torch.zeros(T, K, dtype=torch.uint8, device=dev()), torch.zeros(N, K, dtype=torch.uint8, device=dev())
+    xc[:, 5], wc[:, 5] = 0x38, 0x38
+    ws = torch.ones(-(-N // 128), -(-K // 128), device=dev())
+    out = torch.empty(T, -(-N // 4) * 4, device=dev())[:, :N]
+    half = np.geomspace(1e-30, 1e4, N // 2)
+    for scales, bias in [(np.linspace(0, 16 / N, T), np.linspace(-8, 8, N)), (np.zeros(T), np.append(half, -half)),
+                         (np.geomspace(1e-6, 1, T), np.append(half, -half))]:
+        bias = np.resize(bias.astype(np.float32), N)
+        xs = torch.zeros(T, -(-K // 128), device=dev())
+        xs[:, 0] = torch.from_numpy(scales.astype(np.float32))
+        q.qmoe_linear_fp8(ctx, xc, xs, T, K, wc, ws, N, torch.from_numpy(bias).to(dev()), q.ACT["GELU"], None, 0, out, q.QMOE_F32, out.stride(0))
+        z = (scales.astype(np.float32)[:, None] + bias[None]).astype(np.float64)      # rounded to fp32 once
+        ref = z * 0.5 * torch.erfc(torch.from_numpy(-z / np.sqrt(2))).numpy()
+        err = np.abs(host(out) - ref)
+        with np.errstate(divide="ignore", invalid="ignore"):
+            print("largest error over |z|", np.nanmax(err / np.abs(z)), "absolute below 0", err[z < 0].max())
+        assert (err <= 2e-7 * np.abs(z)).all()
+
+
 # ---------------------------------------------------------------------------- waits that run out
 
 LATE = [(128, 128, 2500, (128, 1)), (1281, 464, 4999, (256, 1)), (3000, 640, 2051, (128, 1)), T128, T256, SHARED,
