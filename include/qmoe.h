@@ -567,7 +567,8 @@ qmoe_status qmoe_rope_table(qmoe_ctx* ctx, const qmoe_rope_config* rope);
  *   n = x / sqrt(mean(x^2) + eps) * norm   over a head, where norm is not NULL
  *   (a, b) -> (a cos - b sin, b cos + a sin)
  * every product, sum and quotient fp32, rounded once (no fused multiply-add); the mean
- * square of a head in more bits, its inverse root rounded to fp32.
+ * square of a head in more bits, its inverse root rounded to fp32 (to the nearest, or the
+ * other where the root lies within 2^-34 of the border between two: one head in a million).
  *  rope      : layout, rot_dim (at most head_dim), n_pos and table are used.
  *  x, out    : n_tokens rows of n_heads*head_dim elements of x_t, x_stride and out_stride
  *              apart; out may be x with the same stride.

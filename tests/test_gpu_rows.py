@@ -496,6 +496,37 @@ def test_rope_norm_of_any_eps(q, ctx, eps):
     assert (np.abs(host(out) - want) <= 6 * R.U * np.abs(want) + 1e-44).all()
 
 
+@pytest.mark.parametrize("hd,eps,chunks", [(64, 1e-6, 20), (64, 1e-12, 16), (128, 1e-6, 10), (128, 1e-3, 10), (256, 1e-6, 6)])
+@pytest.mark.parametrize("constant", [False, True])
+def test_rope_roots_are_nearest_or_next_to_a_border(q, ctx, hd, eps, chunks, constant):
+    """2^20 F32 heads a chunk at position 0: every inverse root is the fp32 number nearest to the one in 64 bits, or
+    the other where that lies within 2^-34 of the border between the two.
+
+    The mean of n squares in two words, relative to it: a square's loss is at most 2^-22 (half a step of a
+    power of two up to four times the sum) and is rounded itself (n 2^-46); eight of one sign add up to
+    35 2^-46 of rounding in each of n/8 sums (n 4.4 2^-46); pairs, lanes (four levels at most) and the two
+    last sums another n 2^-46 each, 7 at most.  n 12.4 2^-46 is below 2^-34 at n = 256; half of it in the
+    root, and 2^-44 of its last step.  Constant heads are those where losses have one sign."""
+    heads = 1 << 20
+    rope, table = make_table(q, ctx, 16, 1)
+    g = torch.Generator(device=dev())
+    g.manual_seed(hd)
+    w, pos = torch.ones(hd, device=dev()), torch.zeros(heads // 16, dtype=torch.int32, device=dev())
+    others = 0
+    for chunk in range(2 if constant else chunks):
+        x = torch.randn(heads, 1 if constant else hd, device=dev(), generator=g) * torch.exp(2 * torch.randn(heads, 1, device=dev(), generator=g))
+        x = x.expand(heads, hd).contiguous()
+        out = torch.empty_like(x)
+        q.qmoe_rope(ctx, rope, x, q.QMOE_F32, 0, heads // 16, 16, hd, pos, w, eps, out, 0)
+        d = x.double()
+        r = 1 / torch.sqrt((d * d).sum(1, keepdim=True) / hd + float(np.float32(eps)))
+        low, high = (x * (r * (1 + o)).float() for o in (-2.0 ** -34, 2.0 ** -34))
+        assert ((out == low).all(1) | (out == high).all(1)).all(), chunk
+        others += int((out != x * r.float()).any(1).sum())
+    print("not the nearest:", others, "of", (chunk + 1) * heads)
+    assert (table[0, 0] == 1).all() and not table[0, 1].any()
+
+
 # ---------------------------------------------------------------------------- the append
 
 APPEND_CASES = [  # tokens, heads, kv heads, hd, rot, layout, dtype, q norm, k norm, page, padded, with q
