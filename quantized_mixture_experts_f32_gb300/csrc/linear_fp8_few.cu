@@ -8,9 +8,12 @@
 // free as long as both operands agree, so they serve four products of 16 as they lie.
 //
 // One token, W of 2048 x 5120: 3.3 us, 3.1 TB/s (2048 x 40000: 16.1 us, 5.1 TB/s; x 151936:
-// 52.5 us, 5.9 TB/s), bound by one chain of load, products and join.  64 tokens, 4096 x
-// 2048: 7.8 us, bound by the rate of mma.sync, which neither copies by cp.async (9.2) nor
-// products on E4M3 directly (12.9, emulated) nor 32 features a CTA (15.2) got past.
+// 52.5 us, 5.9 TB/s), bound by one chain of load, products and join.  Long rows are that chain
+// several times, as k is not shared by CTAs and a warp's next loads begin behind its products:
+// 8192 x 8192 from HBM 16.4 us (10.0 for W's bytes), 16384 x 512 7.5 us on 32 CTAs (1.3), x 128 7.2.
+// 64 tokens, 4096 x 2048: 8.0 us (8.4 with a residual), bound by its loads' latency with two CTAs an SM (21%
+// of the warps; long_scoreboard 5.9 an issue, math_pipe_throttle 0.8, tensor pipe 22%).  Copies by
+// cp.async (9.2 when this took 8.0), products on E4M3 directly (12.9, emulated) and 32 features a CTA (15.2) were no faster.
 #include "linear_fp8.cuh"
 
 namespace qmoe {

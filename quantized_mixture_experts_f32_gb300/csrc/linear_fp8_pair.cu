@@ -8,8 +8,9 @@
 // fp32 registers, 64 features a thread, while the next two blocks' products run; rows
 // leave (and residuals come) through shared memory by TMA, a box a warp.
 //
-// 16384 tokens, 2048 x 5120, BF16: 166 us, 2070 TFLOP/s, 1.08 of the measured bf16 rate of a
-// library product, the tensor pipe 44% active.  A scale for each block of 128 takes every
+// 16384 tokens, 2048 x 5120, BF16, bias: 164.5 us back to back in a graph, 2089 TFLOP/s, 1.09 of the
+// measured bf16 rate of a library product (170 to 173 us, 1.03 to 1.05, called one by one), the tensor
+// pipe 44% active.  A scale for each block of 128 takes every
 // product through registers, by barriers between both SMs and with the two products that
 // TMEM holds at this size; products and copies without that take 114 us.
 // Tiles of 128 features (four products in TMEM, 0.33 us a block of k instead of 0.52) are
@@ -363,8 +364,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant
             if (SPLIT) {
                 // (one tile a cluster) a warp's sums go to the pair that has its results, which adds
                 // the others' in their order; slots by the owner's warps, then by senders.  As pairs of
-                // registers and four loads at a time: sums that are moved, or spilled, cost the
-                // loop above 0.05 us a block.
+                // registers and four loads at a time: with the sums moved as quads in one batch the loop
+                // above lost 0.05 us a block.  (Rows of 16 bits still spill 20 to 48 bytes here, F32
+                // rows none: 256 tokens, 4096 x 2048, 10.5 and 10.15 us.)
                 const int owner = warp % n_parts;
                 float4* slots = reinterpret_cast<float4*>(bufs + O::EW * O::BUF) + warp / n_parts * (n_parts - 1) * (LP_COLS / 4 * 32) + lane;
                 if (owner != part) {
@@ -501,7 +503,7 @@ cudaError_t launch_out(const LinearArgs& a, int parts, const LinearRun& run) {
 }
 
 // A kernel an activation: 64 results' code for each is long, and is fetched past or branched
-// around otherwise (16384 tokens, 2048 x 5120: none 166 us, SiLU 184, GELU 193; with one kernel for
+// around otherwise (16384 tokens, 2048 x 5120: none 164 us, SiLU 182, GELU 192; with one kernel for
 // the three 166, 196, 203; with one for all four 191 and more).
 template <int OUT, int TILE, bool SPLIT>
 cudaError_t launch_act(const LinearArgs& a, int parts, const LinearRun& run) {
